@@ -7,6 +7,7 @@ rejected, an exception is raised.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 
@@ -31,6 +32,8 @@ EXPORTS = [
     "w4a8g_linear_grouped", "w4a8g_plan_info",
     "index_softmax_lut", "index_softmax_c_int", "index_softmax_u8",
     "w4_interleave_rows", "w4a8_gate_up_silu_workspace_bytes", "w4a8_gate_up_silu", "w4a8_silu_mul",
+    "add_norm", "rope_frequencies", "rope_rotate", "kvq_write", "kvq_read", "kvq_keep",
+    "kvq_attention_workspace_bytes", "kvq_attention",
 ]
 
 
@@ -49,7 +52,19 @@ class _Tuning(ctypes.Structure):
                 ("qmma_operands", ctypes.c_int)]
 
 
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ks", ctypes.c_void_p), ("vs", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("page", ctypes.c_int), ("heads", ctypes.c_int), ("dim", ctypes.c_int),
+                ("bits", ctypes.c_int)]
+
+
+class _Batch(ctypes.Structure):
+    _fields_ = [("cu", ctypes.c_void_p), ("start", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("seqs", ctypes.c_int64), ("tokens", ctypes.c_int64), ("max_pages", ctypes.c_int64)]
+
+
 _i64, _p, _u = ctypes.c_int64, ctypes.c_void_p, ctypes.c_uint
+_int, _f, _d = ctypes.c_int, ctypes.c_float, ctypes.c_double
 _SIGS = {
     "w4_quantize_weights": (ctypes.c_int, [_p, _i64, _i64, _p, _p, _p]),
     "w8_quantize_weights": (ctypes.c_int, [_p, _i64, _i64, _p, _p, _p]),
@@ -88,6 +103,15 @@ _SIGS = {
     "w4a8_gate_up_silu_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
     "w4a8_gate_up_silu": (ctypes.c_int, [_p, _i64, _i64, _p, _p, _i64, _p, _p, _p, ctypes.c_size_t, _u, _p]),
     "w4a8_silu_mul": (ctypes.c_int, [_p, _p, _i64, _i64, _p, _u, _p]),
+    "add_norm": (ctypes.c_int, [_p, _int, _p, _int, _p, _p, _i64, _p, _i64, _i64, _f, _f, _f, _p, _p, _p, _p, _u, _p]),
+    "rope_frequencies": (ctypes.c_int, [_int, _d, _int, _d, _d, _d, _d, _p, _p]),
+    "rope_rotate": (ctypes.c_int, [_p, _int, _i64, _i64, _int, _int, _p, _p, _int, _int, _f, _p, _int, _i64, _u, _p]),
+    "kvq_write": (ctypes.c_int, [_p, _p, _p, _i64, _p, _i64, _p, _i64, _int, _int, _p, _p, _int, _int, _f, _p, _u,
+                                 _p]),
+    "kvq_read": (ctypes.c_int, [_p, _p, _p, _p, _int, _u, _p]),
+    "kvq_keep": (ctypes.c_int, [_p, _p, _p, _u, _p]),
+    "kvq_attention_workspace_bytes": (ctypes.c_size_t, [_p, _p, _int]),
+    "kvq_attention": (ctypes.c_int, [_p, _p, _p, _int, _p, _f, _p, _p, ctypes.c_size_t, _u, _p]),
 }
 
 _lib = None
@@ -517,6 +541,270 @@ def index_softmax_u8(A, c_int: int, b: int = ISX_DEFAULT_B, lut: bytes = None, P
     _check(lib().index_softmax_u8(_ptr(A), rows, cols, c_int, b,
                                   ctypes.cast(lut_buf, ctypes.c_void_p), _ptr(P), _stream(A)))
     return P
+
+
+# -- the decoder layer around the linears --------------------------------------
+
+_F32, _F16 = 0, 1
+_TYPES = {torch.float32: _F32, torch.float16: _F16}
+
+
+def _want_type(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.dtype not in _TYPES:
+        raise TypeError("%s must be float32 or float16, got %s" % (name, t.dtype))
+    return _TYPES[t.dtype]
+
+
+def add_norm(r, w=None, y=None, post_w=None, gate=None, alpha: float = 1.0, beta: float = 1.0, eps: float = 1e-6,
+             r_out=None, X=None, Xq=None, sa=None, codes: bool = False, flags: int = 0):
+    """Residual update with the norms on both sides of it:
+    r' = alpha * r + beta * gate * u, u = y or rmsnorm(y) * post_w;
+    X = fp16(rmsnorm(r') * w).
+
+    r [M][N] fp32 or fp16; y (a linear's output) alike, any of the two types;
+    post_w, w [N] fp32; gate [N] or [M][N] fp32.  Returns (r', X), r' of r's
+    type (r_out may be r); with codes=True (r', X, Xq, sa), the INT8
+    activation of X as act_quantize_i8 gives it.  Without w: (r', None)."""
+    rt = _want_type(r, "r")
+    if r.dim() != 2:
+        raise ValueError("r must have two dimensions")
+    M, N = shape = r.shape
+    _want(r, r.dtype, "r")
+    yt = 0
+    if y is not None:
+        yt = _want_type(y, "y")
+        _want(y, y.dtype, "y", shape)
+    elif post_w is not None or gate is not None:
+        raise ValueError("post_w and gate need y")
+    if post_w is not None:
+        _want(post_w, torch.float32, "post_w", (N,))
+    ld_gate = 0
+    if gate is not None:
+        _want(gate, torch.float32, "gate", (N,) if gate.dim() == 1 else shape)
+        ld_gate = N if gate.dim() == 2 else 0
+    r_out = torch.empty_like(r) if r_out is None else r_out
+    _want(r_out, r.dtype, "r_out", shape)
+    if w is not None:
+        _want(w, torch.float32, "w", (N,))
+        X = torch.empty(shape, dtype=torch.float16, device=r.device) if X is None else X
+        _want(X, torch.float16, "X", shape)
+        if codes or Xq is not None or sa is not None:
+            Xq = torch.empty(shape, dtype=torch.int8, device=r.device) if Xq is None else Xq
+            sa = torch.empty((M,), dtype=torch.float32, device=r.device) if sa is None else sa
+            _want(Xq, torch.int8, "Xq", shape)
+            _want(sa, torch.float32, "sa", (M,))
+    elif X is not None or codes or Xq is not None or sa is not None:
+        raise ValueError("X and its codes need w")
+    _check(lib().add_norm(_ptr(r), rt, _ptr(y), yt, _ptr(post_w), _ptr(gate), ld_gate, _ptr(w), M, N, alpha, beta,
+                          eps, _ptr(r_out), _ptr(X), _ptr(Xq), _ptr(sa), flags, _stream(r)))
+    return (r_out, X) if Xq is None else (r_out, X, Xq, sa)
+
+
+ROPE_SCALINGS = {None: 0, "plain": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling=None, factor: float = 1.0, old_ctx: float = 0.0,
+                     low: float = 1.0, high: float = 32.0, device=None):
+    """(freqs [rot/2] float64 tensor, mscale): the rotary frequencies, plain or
+    scaled for long contexts ("linear", "ntk", "yarn", "bands").  Computed on
+    the host; `device` places the tensor."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError("scaling must be one of %s" % ", ".join(str(k) for k in ROPE_SCALINGS))
+    buf = (ctypes.c_double * 128)()
+    ms = ctypes.c_float(1.0)
+    _check(lib().rope_frequencies(rot, base, ROPE_SCALINGS[scaling], factor, old_ctx, low, high,
+                                  ctypes.cast(buf, ctypes.c_void_p), ctypes.byref(ms)))
+    return torch.tensor(buf[:rot // 2], dtype=torch.float64, device=device), float(ms.value)
+
+
+def _want_heads(t, name, shape=None):
+    """[tokens][heads][dim], the last two dimensions contiguous, rows at any
+    distance (a slice of a fused projection); returns the row distance."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dim() != 3:
+        raise ValueError("%s must be [tokens][heads][dim]" % name)
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    n, h, d = t.shape
+    st = t.stride()
+    if st[2] != 1 or (st[1] != d and h > 1):
+        raise ValueError("%s: the heads of a row must be contiguous" % name)
+    return st[0] if n > 1 else max(st[0], h * d)
+
+
+def _want_rope(pos, freqs, tokens):
+    _want(pos, torch.int32, "pos", (tokens,))
+    _want(freqs, torch.float64, "freqs")
+    if freqs.dim() != 1:
+        raise ValueError("freqs must have one dimension")
+    return 2 * freqs.shape[0]
+
+
+def rope_rotate(X, pos, freqs, interleaved: bool = False, mscale: float = 1.0, Y=None, dtype=None, flags: int = 0):
+    """Rotary positions on X [tokens][heads][dim] (fp32 or fp16, rows at any
+    distance): pairs (i, i + rot/2), or (2i, 2i + 1) when interleaved, turned by
+    pos * freqs[i]; rot = 2 * len(freqs).  Returns Y (Y may be X)."""
+    xt = _want_type(X, "X")
+    ld = _want_heads(X, "X")
+    n, h, d = X.shape
+    rot = _want_rope(pos, freqs, n)
+    Y = torch.empty((n, h, d), dtype=dtype or X.dtype, device=X.device) if Y is None else Y
+    yt = _want_type(Y, "Y")
+    ld_y = _want_heads(Y, "Y", (n, h, d))
+    _check(lib().rope_rotate(_ptr(X), xt, ld, n, h, d, _ptr(pos), _ptr(freqs), rot, int(interleaved), mscale,
+                             _ptr(Y), yt, ld_y, flags, _stream(X)))
+    return Y
+
+
+# Pages of quantized keys and values: k, v int8 [pages][heads][page][dim] (8
+# bits) or uint8 [pages][heads][page][dim/2] (4 bits), ks, vs fp32
+# [pages][heads][page].
+KVQCache = collections.namedtuple("KVQCache", "k v ks vs")
+# The tokens of a call: cu int32 [seqs + 1], start int32 [seqs], table int32
+# [seqs][max_pages] (kvq_batch_t in the C header).
+KVQBatch = collections.namedtuple("KVQBatch", "cu start table")
+
+
+def kvq_cache(pages: int, page: int, heads: int, dim: int, bits: int = 8, device="cuda") -> KVQCache:
+    """An empty cache."""
+    if bits not in (8, 4):
+        raise ValueError("bits must be 8 or 4")
+    dt, width = (torch.int8, dim) if bits == 8 else (torch.uint8, dim // 2)
+    k, v = (torch.zeros((pages, heads, page, width), dtype=dt, device=device) for _ in range(2))
+    ks, vs = (torch.zeros((pages, heads, page), dtype=torch.float32, device=device) for _ in range(2))
+    return KVQCache(k, v, ks, vs)
+
+
+def _cache_arg(c):
+    k, v, ks, vs = c
+    if not isinstance(k, torch.Tensor) or k.dtype not in (torch.int8, torch.uint8):
+        raise TypeError("the cache's codes must be int8 (8 bits) or uint8 (4 bits) tensors")
+    if k.dim() != 4:
+        raise ValueError("the cache's codes must be [pages][heads][page][dim]")
+    _want(k, k.dtype, "k")
+    _want(v, k.dtype, "v", k.shape)
+    pages, heads, page, width = k.shape
+    _want(ks, torch.float32, "ks", (pages, heads, page))
+    _want(vs, torch.float32, "vs", (pages, heads, page))
+    bits = 8 if k.dtype == torch.int8 else 4
+    return _Cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, page, heads, width * 8 // bits,
+                  bits)
+
+
+def _batch_arg(b, tokens):
+    cu, start, table = b
+    _want(cu, torch.int32, "cu")
+    _want(start, torch.int32, "start")
+    _want(table, torch.int32, "table")
+    if cu.dim() != 1 or start.dim() != 1 or table.dim() != 2 or cu.shape[0] != start.shape[0] + 1 or \
+            table.shape[0] != start.shape[0]:
+        raise ValueError("the batch must be cu [seqs + 1], start [seqs], table [seqs][max_pages]")
+    return _Batch(cu.data_ptr(), start.data_ptr(), table.data_ptr(), start.shape[0], tokens, table.shape[1])
+
+
+def kvq_write(cache, batch, K, V, Q=None, pos=None, freqs=None, interleaved: bool = False, mscale: float = 1.0,
+              Q_out=None, flags: int = 0):
+    """Writes K, V [tokens][heads][dim] (fp32 or fp16, rows at any distance) into
+    the cache, rotated first when freqs is given, and rotates Q
+    [tokens][heads_q][dim] in the same launch; returns Q_out (fp16; None without Q)."""
+    ca = _cache_arg(cache)
+    xt = _want_type(K, "K")
+    n = K.shape[0]
+    shape = (n, ca.heads, ca.dim)
+    ld_k, ld_v = _want_heads(K, "K", shape), _want_heads(V, "V", shape)
+    if V.dtype != K.dtype or (Q is not None and Q.dtype != K.dtype):
+        raise TypeError("Q, K and V must have one type")
+    ba = _batch_arg(batch, n)
+    rot = _want_rope(pos, freqs, n) if freqs is not None else 0
+    hq = ld_q = 0
+    if Q is not None:
+        hq = Q.shape[1]
+        ld_q = _want_heads(Q, "Q", (n, hq, ca.dim))
+        Q_out = torch.empty((n, hq, ca.dim), dtype=torch.float16, device=K.device) if Q_out is None else Q_out
+        _want(Q_out, torch.float16, "Q_out", (n, hq, ca.dim))
+    elif Q_out is not None:
+        raise ValueError("Q_out needs Q")
+    _check(lib().kvq_write(ctypes.byref(ca), ctypes.byref(ba), _ptr(K), ld_k, _ptr(V), ld_v, _ptr(Q), ld_q, hq, xt,
+                           _ptr(pos), _ptr(freqs), rot, int(interleaved), mscale, _ptr(Q_out), flags, _stream(K)))
+    return Q_out
+
+
+def kvq_read(cache, batch, tokens: int, dtype=torch.float16, K=None, V=None, flags: int = 0):
+    """The batch's keys and values (tokens = cu[-1]) as values:
+    (K, V) [tokens][heads][dim], fp16 or fp32."""
+    ca = _cache_arg(cache)
+    ba = _batch_arg(batch, tokens)
+    shape = (tokens, ca.heads, ca.dim)
+    K = torch.empty(shape, dtype=dtype, device=cache[0].device) if K is None else K
+    V = torch.empty(shape, dtype=K.dtype, device=cache[0].device) if V is None else V
+    yt = _want_type(K, "K")
+    _want(K, K.dtype, "K", shape)
+    _want(V, K.dtype, "V", shape)
+    _check(lib().kvq_read(ctypes.byref(ca), ctypes.byref(ba), _ptr(K), _ptr(V), yt, flags, _stream(K)))
+    return K, V
+
+
+def kvq_keep(cache, batch, keep, flags: int = 0):
+    """Moves a drafted tree's accepted tokens together: slot start[b] + i takes
+    what slot start[b] + keep[cu[b] + i] held, until an entry is negative."""
+    ca = _cache_arg(cache)
+    _want(keep, torch.int32, "keep")
+    if keep.dim() != 1:
+        raise ValueError("keep must have one dimension")
+    ba = _batch_arg(batch, keep.shape[0])
+    _check(lib().kvq_keep(ctypes.byref(ca), ctypes.byref(ba), _ptr(keep), flags, _stream(keep)))
+
+
+def kvq_attention_workspace_bytes(cache, batch, tokens: int, heads_q: int) -> int:
+    ca, ba = _cache_arg(cache), _batch_arg(batch, tokens)
+    return int(lib().kvq_attention_workspace_bytes(ctypes.byref(ca), ctypes.byref(ba), heads_q))
+
+
+_attn_ws = {}
+
+
+def _stream_workspace(nbytes: int, device, stream: int):
+    """A zero-filled workspace per stream; under graph capture one of the graph's
+    own, so that replays share nothing with eager calls."""
+    if nbytes == 0:
+        return None
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    buf = _attn_ws.get((device, stream))
+    if buf is None or buf.numel() < nbytes:
+        buf = _attn_ws[(device, stream)] = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+    return buf
+
+
+def kvq_attention(Q, cache, batch, mask=None, scale: float = None, out=None, ws=None, flags: int = 0):
+    """Attention of Q [tokens][heads_q][dim] fp16 over the cache; returns out
+    (same shape, fp16).  Every token sees its sequence's start[b] cached slots and
+    of the call's own tokens those whose bit is set in mask [tokens] (int64 as 64
+    bits; a tree's ancestors and itself), or without mask those up to itself.
+    scale: 1 / sqrt(dim) by default."""
+    ca = _cache_arg(cache)
+    _want(Q, torch.float16, "Q")
+    if Q.dim() != 3 or Q.shape[2] != ca.dim:
+        raise ValueError("Q must be [tokens][heads_q][%d]" % ca.dim)
+    n, hq, d = Q.shape
+    ba = _batch_arg(batch, n)
+    if mask is not None:
+        _want(mask, torch.int64, "mask", (n,))
+    out = torch.empty_like(Q) if out is None else out
+    _want(out, torch.float16, "out", Q.shape)
+    L = lib()
+    stream = _stream(Q)
+    ca_p, ba_p = ctypes.byref(ca), ctypes.byref(ba)
+    if ws is None:
+        ws = _stream_workspace(int(L.kvq_attention_workspace_bytes(ca_p, ba_p, hq)), Q.device, stream)
+    _check(L.kvq_attention(ca_p, ba_p, _ptr(Q), hq, _ptr(mask), d ** -0.5 if scale is None else scale, _ptr(out),
+                           _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), flags, stream))
+    return out
 
 
 def w4a8_last_error() -> str:

@@ -12,6 +12,7 @@
 #include <string>
 
 #include "../../include/w4a8.h"
+#include "abi_status.h"
 #include "kernels.h"
 #include "plan.h"
 
@@ -37,6 +38,16 @@ int ok() {
 int cuda_fail(cudaError_t e, const char* what) {
     return fail(W4A8_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
 }
+
+}  // namespace
+
+// The same for the entry points of abi_layer.cu.
+namespace w4a8 {
+int status_fail(int code, const char* message) { return fail(code, "%s", message); }
+int status_done(cudaError_t e, const char* what) { return e == cudaSuccess ? ok() : cuda_fail(e, what); }
+}  // namespace w4a8
+
+namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -109,6 +120,12 @@ int sm_count(int* out) {
     *out = n;
     return W4A8_OK;
 }
+
+}  // namespace
+
+int w4a8::status_sm_count(int* out) { return sm_count(out); }
+
+namespace {
 
 w4a8::Tuning tuning() {
     w4a8::Tuning t;
@@ -714,6 +731,8 @@ int w4a8_device_error(unsigned* flags, void* stream) {
     if (e == cudaSuccess) e = w4a8::read_and_clear_mma_error(flags, static_cast<cudaStream_t>(stream));
     if (e == cudaSuccess) e = w4a8::read_and_clear_rowdot_error(flags, static_cast<cudaStream_t>(stream));
     if (e == cudaSuccess) e = w4a8::read_and_clear_qmma_error(flags, static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) e = w4a8::read_and_clear_kvq_error(flags, static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) e = w4a8::read_and_clear_attn_error(flags, static_cast<cudaStream_t>(stream));
     // a wait that gave up may leave split-K arrival counters non-zero; the
     // static scratch of w4a8_linear_noalloc is cleared here (caller-owned
     // workspaces must be re-zeroed by the caller)

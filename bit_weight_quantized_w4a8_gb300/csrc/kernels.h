@@ -5,6 +5,7 @@
 
 #include <cstdint>
 
+#include "../../include/w4a8.h"
 #include "plan.h"
 #include "qmma_plan.h"
 #include "rowdot_plan.h"
@@ -97,5 +98,29 @@ int isx_kernel_kind(int64_t cols, bool vec_ok, int* q_needed);
 cudaError_t launch_index_softmax(const int32_t* A, int64_t rows, int64_t cols, uint32_t c_int,
                                  int b, const uint8_t* lut, const uint32_t* thr, uint8_t* P,
                                  cudaStream_t stream);
+
+// The decoder layer around the linears: residual and norms (norm.cu), rotary
+// positions and the quantized cache (kvq.cu), attention over it (kvq_attn.cu).
+cudaError_t launch_add_norm(const void* r, int r_f16, const void* y, int y_f16, const float* post_w,
+                            const float* gate, int64_t ld_gate, const float* w, int64_t M, int N, float alpha,
+                            float beta, float eps, void* r_out, uint16_t* X, int8_t* Xq, float* sa, bool vec,
+                            unsigned flags, cudaStream_t stream);
+cudaError_t launch_rope_rotate(const void* X, int x_f16, int64_t ld_x, int64_t tokens, int heads, int dim,
+                               const int32_t* pos, const double* freqs, int rot, int inter, float mscale, void* Y,
+                               int y_f16, int64_t ld_y, int sms, unsigned flags, cudaStream_t stream);
+cudaError_t launch_kvq_write(const kvq_cache_t& c, const kvq_batch_t& b, const void* K, int64_t ld_k, const void* V,
+                             int64_t ld_v, const void* Q, int64_t ld_q, int heads_q, int x_f16, const int32_t* pos,
+                             const double* freqs, int rot, int inter, float mscale, uint16_t* Q_out, int sms,
+                             unsigned flags, cudaStream_t stream);
+cudaError_t launch_kvq_read(const kvq_cache_t& c, const kvq_batch_t& b, void* K, void* V, int y_f16, unsigned flags,
+                            cudaStream_t stream);
+cudaError_t launch_kvq_keep(const kvq_cache_t& c, const kvq_batch_t& b, const int32_t* keep, unsigned flags,
+                            cudaStream_t stream);
+size_t kvq_attn_workspace(const kvq_cache_t& c, const kvq_batch_t& b, int heads_q, int sms);
+cudaError_t launch_kvq_attention(const kvq_cache_t& c, const kvq_batch_t& b, const uint16_t* Q, int heads_q,
+                                 const uint64_t* mask, float scale, uint16_t* out, void* ws, int sms, unsigned flags,
+                                 cudaStream_t stream);
+cudaError_t read_and_clear_kvq_error(unsigned* flags, cudaStream_t stream);
+cudaError_t read_and_clear_attn_error(unsigned* flags, cudaStream_t stream);
 
 }  // namespace w4a8

@@ -1,0 +1,63 @@
+// kvq_index.h -- where a token's key and value lie in the paged cache: the
+// look-ups of kvq_batch_t and their range checks, for the kernels and for
+// host tests.
+#pragma once
+
+#include <cstdint>
+
+#ifdef __CUDACC__
+#define KVQ_HD __host__ __device__ __forceinline__
+#else
+#define KVQ_HD inline
+#endif
+
+namespace w4a8 {
+
+// Sequence of token i: the b with cu[b] <= i < cu[b + 1], or -1 when the
+// offsets hold none (they do not cover i, or are not in order).
+KVQ_HD int kvq_find_seq(const int32_t* cu, int seqs, int i) {
+    int lo = 0, hi = seqs;  // cu[lo] <= i would hold, cu[hi] > i
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (cu[mid] <= i)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return cu[lo] <= i && i < cu[lo + 1] ? lo : -1;
+}
+
+// Row of the pool (page * page_size + offset) of slot s of sequence b, or -1
+// when the slot lies past the table or its page outside the pool.  page_size
+// = 1 << shift.
+KVQ_HD int64_t kvq_slot_row(const int32_t* table, int64_t max_pages, int64_t pages, int shift, int b,
+                            int64_t s) {
+    if (s < 0 || (s >> shift) >= max_pages) return -1;
+    const int64_t p = table[b * max_pages + (s >> shift)];
+    if (p < 0 || p >= pages) return -1;
+    return (p << shift) + (s & ((1 << shift) - 1));
+}
+
+// Sequence b's tokens [first, first + count) and start, from arrays that may
+// hold anything: count and start are 0 unless 0 <= cu[b] <= cu[b + 1] <= tokens
+// and 0 <= start.  end, the slots in use, is cut to what the table holds; ok
+// tells whether all was in range.
+struct KvqSeq {
+    int first, count;
+    int64_t start, end;
+    bool ok;
+};
+KVQ_HD KvqSeq kvq_seq(const int32_t* cu, const int32_t* start, int b, int64_t tokens, int64_t max_pages,
+                      int shift) {
+    KvqSeq q;
+    const int64_t lo = cu[b], hi = cu[b + 1], s = start[b], slots = max_pages << shift;
+    const bool sound = lo >= 0 && lo <= hi && hi <= tokens && s >= 0;
+    q.first = (int)lo;
+    q.count = sound ? (int)(hi - lo) : 0;
+    q.start = sound ? s : 0;
+    q.end = q.start + q.count < slots ? q.start + q.count : slots;
+    q.ok = sound && s + (hi - lo) <= slots;
+    return q;
+}
+
+}  // namespace w4a8

@@ -447,6 +447,179 @@ int index_softmax_u8(const int32_t* A, int64_t rows, int64_t cols, int64_t c_int
                      const uint8_t* lut, uint8_t* P, void* stream);
 
 /* ---------------------------------------------------------------------- */
+/* The decoder layer around the linears: residual and norms, rotary         */
+/* positions, the quantized paged key/value cache and attention over it     */
+/* ---------------------------------------------------------------------- */
+
+/* Types of the tensors that these calls take in more than one type. */
+#define W4A8_T_F32 0
+#define W4A8_T_F16 1
+
+/* Residual update with the norms on both sides of it, per row:
+ *   u  = y, or y / sqrt(mean(y^2) + eps) * post_w   (the norm after a block)
+ *   r' = alpha * r + beta * gate * u                (no gate: beta * u)
+ *   x  = binary16(r' / sqrt(mean(r'^2) + eps) * w)  (the norm before the next)
+ * in fp32 (sums of squares in fp32, by a tree over the row; the x norm reads
+ * the unrounded r'), r' rounded once to its type.
+ *   r [M][N] residual in, r_type; y [M][N] block output, y_type (a linear's
+ *   fp32 Y), or NULL: r' = alpha * r; post_w [N] fp32 or NULL; gate fp32: row m
+ *   at gate + m * ld_gate (0: one gate [N] for all rows), or NULL; w [N] fp32.
+ *   r_out [M][N] (r_type; may be r itself, NULL to skip), X [M][N] binary16
+ *   (NULL to skip).
+ *   Xq [M][N] int8 and sa [M] fp32 (both or neither): what act_quantize_i8
+ *   gives for X, for w4a8_gemv; needs N % 8 == 0.
+ *   flags: 0 or W4A8_LAUNCH_PDL (the kernel waits before it reads anything).
+ * Requires 1 <= M <= 2^31 - 1, 1 <= N <= W4A8_NORM_MAX_N, eps >= 0, finite
+ * alpha and beta, ld_gate 0 or >= N, at least one output; tensors aligned to
+ * their element.  N % 8 == 0 with all pointers (and ld_gate * 4) 16-byte aligned
+ * takes the vector path. */
+#define W4A8_NORM_MAX_N 32768
+int add_norm(const void* r, int r_type, const void* y, int y_type, const float* post_w,
+                  const float* gate, int64_t ld_gate, const float* w, int64_t M, int64_t N, float alpha,
+                  float beta, float eps, void* r_out, uint16_t* X, int8_t* Xq, float* sa, unsigned flags,
+                  void* stream);
+
+/* Host-only: rotary frequencies in radians per position, binary64,
+ * freqs[i] = base^(-2 i / rot) for i < rot / 2, rescaled for long contexts:
+ *   ROPE_PLAIN   as they are;
+ *   ROPE_LINEAR  divided by factor (positions interpolated);
+ *   ROPE_NTK     base raised to base * factor^(rot / (rot - 2)): the lowest
+ *                frequency is divided by factor, the highest kept;
+ *   ROPE_YARN    by parts: a pair that turns at least high times within
+ *                old_ctx positions keeps its frequency, one that turns at most
+ *                low times is divided by factor, a linear ramp over the pair index
+ *                between the two (rounded outwards to whole pairs); *mscale =
+ *                0.1 ln(factor) + 1 (cos and sin are multiplied by it);
+ *   ROPE_BANDS   by wavelength: longer than old_ctx / low divided by factor,
+ *                shorter than old_ctx / high kept, linear in old_ctx /
+ *                wavelength between.
+ * *mscale (NULL to skip) is 1 for all but ROPE_YARN.
+ * Requires rot % 8 == 0, 8 <= rot <= 256, base > 1, factor >= 1 and, for the
+ * last two, old_ctx >= 1 and 0 < low < high. */
+#define ROPE_PLAIN 0
+#define ROPE_LINEAR 1
+#define ROPE_NTK 2
+#define ROPE_YARN 3
+#define ROPE_BANDS 4
+int rope_frequencies(int rot, double base, int scaling, double factor, double old_ctx, double low,
+                     double high, double* freqs, float* mscale);
+
+/* Rotary positions on the first `rot` values of every head:
+ *   (a, b) -> mscale * (a cos t - b sin t, b cos t + a sin t), t = pos * freq[i],
+ * the pair i being values (2i, 2i + 1) (interleaved != 0) or (i, i + rot / 2);
+ * the other values are copied.  fp32 arithmetic.  The angle is exact: freq /
+ * (2 pi) is held as a 64-bit fraction of a turn, whose product with an integer
+ * position, modulo one turn, takes no rounding; what cos and sin are taken of
+ * is within 2^-23 + 2^-52 |pos| rad of pos * freq for frequencies up to 1.
+ *   X [tokens][heads][dim], x_type, rows ld_x elements apart; Y likewise (Y may
+ *   be X when both have the same type and row distance).
+ *   pos [tokens] int32, freqs [rot / 2] binary64 (rope_frequencies), device.
+ * Requires tokens, heads >= 1, tokens * heads <= 2^40, dim 64, 128 or 256, rot a
+ * multiple of 8 from 8 to dim, ld >= heads * dim, ld % 4 == 0; X and Y 16-byte
+ * (binary16: 8-byte) aligned. */
+int rope_rotate(const void* X, int x_type, int64_t ld_x, int64_t tokens, int heads, int dim,
+                const int32_t* pos, const double* freqs, int rot, int interleaved, float mscale, void* Y,
+                int y_type, int64_t ld_y, unsigned flags, void* stream);
+
+/* The quantized paged key/value cache.  A pool of `pages` pages of `page`
+ * slots; one slot holds the key and the value of one token for `heads` heads,
+ * each head's vector of `dim` values as codes with one fp32 scale:
+ *   k, v   bits 8: int8 [pages][heads][page][dim]; bits 4: uint8
+ *          [pages][heads][page][dim / 2], two codes a byte as in Wq (low nibble
+ *          first, two's complement);
+ *   ks, vs fp32 [pages][heads][page].
+ * Quantization of a vector, in fp32: scale = max|x| * fl(1 / top), top = 127 or
+ * 7 (one multiply by the rounded reciprocal, within one unit in the last place
+ * of max|x| / top); code = clamp(round_half_away(x / scale), -top, top) with
+ * the IEEE quotient by that stored scale, so code * scale is within half a step of x.
+ * A zero vector gets scale 0 and codes 0.  A page of one head is contiguous: the attention
+ * streams it.  Requires page 16, 32, 64, 128 or 256, dim 64, 128 or 256, 1 <=
+ * heads <= 1024, 1 <= pages <= 2^31 - 1; k, v 16-byte, ks, vs 4-byte aligned. */
+typedef struct {
+    void* k;
+    void* v;
+    float* ks;
+    float* vs;
+    int64_t pages;
+    int page, heads, dim, bits;
+} kvq_cache_t;
+
+/* The tokens of a call, sequence by sequence (all device arrays of int32, so
+ * that a captured graph follows them):
+ *   cu [seqs + 1]: tokens cu[b] .. cu[b + 1] - 1 are sequence b's (none is
+ *     fine); cu[0] = 0, not decreasing, cu[seqs] = tokens;
+ *   start [seqs]: token cu[b] + i sits in (goes to, comes from) the
+ *     sequence's slot start[b] + i;
+ *   table [seqs][max_pages]: slot s lies in page table[b][s / page].
+ * Requires 1 <= seqs <= 65536, 1 <= tokens <= 2^31 - 1, 1 <= max_pages <= 2^31
+ * - 1.  What the arrays hold is checked on the device: a token whose
+ * slot or page is out of range is neither written nor read, its keys are
+ * seen by nobody, and bit 3 of the device error word is set
+ * (w4a8_device_error); no address outside the cache is touched. */
+typedef struct {
+    const int32_t* cu;
+    const int32_t* start;
+    const int32_t* table;
+    int64_t seqs, tokens, max_pages;
+} kvq_batch_t;
+
+/* Writes the batch's keys and values into the cache, rotating first when
+ * freqs is given, and rotates the queries in the same launch.
+ *   K, V [tokens][heads][dim], x_type, rows ld_k, ld_v elements apart;
+ *   Q [tokens][heads_q][dim], x_type, rows ld_q apart, or NULL; Q_out
+ *   [tokens][heads_q][dim] binary16 (Q as it is when freqs is NULL).
+ *   pos, freqs, rot, interleaved, mscale: as in rope_rotate (freqs NULL: no
+ *   rotation, the others are not read).
+ * The key is quantized from its rotated fp32 values.  Tokens must have
+ * distinct slots.  Requires what rope_rotate does of rot, ld and alignment; 1 <= heads_q <=
+ * 16384 with Q. */
+int kvq_write(const kvq_cache_t* cache, const kvq_batch_t* batch, const void* K, int64_t ld_k, const void* V,
+              int64_t ld_v, const void* Q, int64_t ld_q, int heads_q, int x_type, const int32_t* pos,
+              const double* freqs, int rot, int interleaved, float mscale, uint16_t* Q_out, unsigned flags,
+              void* stream);
+
+/* Reads the batch's keys and values back: code * scale in fp32, rounded once
+ * to the output type.  K, V [tokens][heads][dim], y_type, 16-byte aligned.  Rows of
+ * tokens out of range are left as they are. */
+int kvq_read(const kvq_cache_t* cache, const kvq_batch_t* batch, void* K, void* V, int y_type,
+             unsigned flags, void* stream);
+
+/* Moves the accepted tokens of a drafted tree together: for every sequence b
+ * and i = 0, 1, ... while keep[cu[b] + i] >= 0 (and i < its token count), slot
+ * start[b] + i takes what slot start[b] + keep[cu[b] + i] held before the call.
+ * keep [tokens] int32.  A sequence of more than KVQ_MAX_TREE tokens or an entry
+ * past its tokens is left alone and sets bit 3 of the device error word. */
+#define KVQ_MAX_TREE 64
+int kvq_keep(const kvq_cache_t* cache, const kvq_batch_t* batch, const int32_t* keep, unsigned flags,
+             void* stream);
+
+/* Attention of the batch's tokens over the cache (their own keys and
+ * values, already written, included), grouped heads: query head h reads cache
+ * head h / (heads_q / heads).
+ *   out[t][h] = sum_j p_j vs_j vc_j,  p = softmax_j(scale * ks_j * (Q[t][h] . kc_j))
+ * over the slots j that token t = cu[b] + i sees: every j < start[b], and of the
+ * drafted tokens those whose bit j - start[b] is set in mask[t] (the
+ * token's ancestors and itself, for a tree), or, with mask NULL, j <= start[b]
+ * + i.  A token that sees nothing gets zeros.  A key whose scale is NaN or
+ * infinite harms only the rows that see it.
+ * Arithmetic: the products of binary16 queries and integer codes are summed in
+ * fp32; softmax statistics, their merge over the pieces of a long cache and the
+ * output sums are fp32; p_j vs_j is rounded to binary16 for the second product
+ * (2^-11 relative at most above 2^-27 of the row's largest).  The pieces
+ * depend on cu and start alone and are merged in their order: the same
+ * call gives the same bits.
+ *   Q, out [tokens][heads_q][dim] binary16; mask [tokens] uint64 or NULL.
+ *   ws, ws_bytes: kvq_attention_workspace_bytes, rules of
+ *   w4a8_workspace_bytes (zeroed once, left ready, one call at a time).
+ * Requires heads_q a multiple of heads, at most 1024 times heads; with a mask
+ * at most KVQ_MAX_TREE tokens a sequence (more: bit 3 of the device error
+ * word, zeros); finite scale; Q and out 16-byte, mask 8-byte aligned. */
+size_t kvq_attention_workspace_bytes(const kvq_cache_t* cache, const kvq_batch_t* batch, int heads_q);
+int kvq_attention(const kvq_cache_t* cache, const kvq_batch_t* batch, const uint16_t* Q, int heads_q,
+                  const uint64_t* mask, float scale, uint16_t* out, void* ws, size_t ws_bytes,
+                  unsigned flags, void* stream);
+
+/* ---------------------------------------------------------------------- */
 /* Diagnostics                                                             */
 /* ---------------------------------------------------------------------- */
 
@@ -457,7 +630,8 @@ const char* w4a8_last_error(void);
 
 /* Copies the current device's error word into *flags and clears it.  Bit 0:
  * a wait for weight data ran out; bit 1: unused; bit 2: a wait for
- * in-flight copies at exit ran out.  A non-zero word means that some call's
+ * in-flight copies at exit ran out; bit 3: a cache call met a slot or page out
+ * of range (kvq_batch_t), which touches no workspace.  A non-zero word means that some call's
  * outputs are unspecified and that the split-K arrival counters of the
  * workspace it used may be left non-zero: zero-fill that workspace again
  * before reusing it.  (The static scratch of w4a8_linear_noalloc is cleared
