@@ -142,11 +142,20 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it (2 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(t: torch.Tensor) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _want(t, dtype, name, shape=None):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous() and \
+            (shape is None or t.shape == shape):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
     if not t.is_cuda:
@@ -568,37 +577,48 @@ def add_norm(r, w=None, y=None, post_w=None, gate=None, alpha: float = 1.0, beta
     type (r_out may be r); with codes=True (r', X, Xq, sa), the INT8
     activation of X as act_quantize_i8 gives it.  Without w: (r', None)."""
     rt = _want_type(r, "r")
-    if r.dim() != 2:
-        raise ValueError("r must have two dimensions")
-    M, N = shape = r.shape
     _want(r, r.dtype, "r")
-    yt = 0
+    shape = r.shape
+    if len(shape) != 2:
+        raise ValueError("r must have two dimensions")
+    M, N = shape
+    yt = ld_gate = 0
+    yp = pp = gp = wp = xp = qp = sp = None
     if y is not None:
         yt = _want_type(y, "y")
         _want(y, y.dtype, "y", shape)
+        yp = y.data_ptr()
     elif post_w is not None or gate is not None:
         raise ValueError("post_w and gate need y")
     if post_w is not None:
         _want(post_w, torch.float32, "post_w", (N,))
-    ld_gate = 0
+        pp = post_w.data_ptr()
     if gate is not None:
         _want(gate, torch.float32, "gate", (N,) if gate.dim() == 1 else shape)
         ld_gate = N if gate.dim() == 2 else 0
-    r_out = torch.empty_like(r) if r_out is None else r_out
-    _want(r_out, r.dtype, "r_out", shape)
+        gp = gate.data_ptr()
+    if r_out is None:
+        r_out = torch.empty_like(r)
+    else:
+        _want(r_out, r.dtype, "r_out", shape)
     if w is not None:
         _want(w, torch.float32, "w", (N,))
-        X = torch.empty(shape, dtype=torch.float16, device=r.device) if X is None else X
-        _want(X, torch.float16, "X", shape)
+        wp = w.data_ptr()
+        if X is None:
+            X = torch.empty_like(r, dtype=torch.float16)
+        else:
+            _want(X, torch.float16, "X", shape)
+        xp = X.data_ptr()
         if codes or Xq is not None or sa is not None:
-            Xq = torch.empty(shape, dtype=torch.int8, device=r.device) if Xq is None else Xq
+            Xq = torch.empty_like(r, dtype=torch.int8) if Xq is None else Xq
             sa = torch.empty((M,), dtype=torch.float32, device=r.device) if sa is None else sa
             _want(Xq, torch.int8, "Xq", shape)
             _want(sa, torch.float32, "sa", (M,))
+            qp, sp = Xq.data_ptr(), sa.data_ptr()
     elif X is not None or codes or Xq is not None or sa is not None:
         raise ValueError("X and its codes need w")
-    _check(lib().add_norm(_ptr(r), rt, _ptr(y), yt, _ptr(post_w), _ptr(gate), ld_gate, _ptr(w), M, N, alpha, beta,
-                          eps, _ptr(r_out), _ptr(X), _ptr(Xq), _ptr(sa), flags, _stream(r)))
+    _check(lib().add_norm(r.data_ptr(), rt, yp, yt, pp, gp, ld_gate, wp, M, N, alpha, beta, eps, r_out.data_ptr(), xp,
+                          qp, sp, flags, _stream(r)))
     return (r_out, X) if Xq is None else (r_out, X, Xq, sa)
 
 
@@ -626,11 +646,14 @@ def _want_heads(t, name, shape=None):
         raise TypeError("%s must be a torch tensor" % name)
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if t.dim() != 3:
+    have = t.shape
+    if len(have) != 3:
         raise ValueError("%s must be [tokens][heads][dim]" % name)
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    n, h, d = t.shape
+    if shape is not None and have != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(have)))
+    n, h, d = have
+    if t.is_contiguous():
+        return h * d
     st = t.stride()
     if st[2] != 1 or (st[1] != d and h > 1):
         raise ValueError("%s: the heads of a row must be contiguous" % name)
@@ -653,9 +676,10 @@ def rope_rotate(X, pos, freqs, interleaved: bool = False, mscale: float = 1.0, Y
     ld = _want_heads(X, "X")
     n, h, d = X.shape
     rot = _want_rope(pos, freqs, n)
-    Y = torch.empty((n, h, d), dtype=dtype or X.dtype, device=X.device) if Y is None else Y
+    if Y is None:
+        Y = torch.empty((n, h, d), dtype=dtype or X.dtype, device=X.device)
     yt = _want_type(Y, "Y")
-    ld_y = _want_heads(Y, "Y", (n, h, d))
+    ld_y = _want_heads(Y, "Y", X.shape)
     _check(lib().rope_rotate(_ptr(X), xt, ld, n, h, d, _ptr(pos), _ptr(freqs), rot, int(interleaved), mscale,
                              _ptr(Y), yt, ld_y, flags, _stream(X)))
     return Y
@@ -768,16 +792,16 @@ def kvq_attention_workspace_bytes(cache, batch, tokens: int, heads_q: int) -> in
 _attn_ws = {}
 
 
-def _stream_workspace(nbytes: int, device, stream: int):
-    """A zero-filled workspace per stream; under graph capture one of the graph's
-    own, so that replays share nothing with eager calls."""
+def _stream_workspace(device, stream: int, nbytes: int = 0):
+    """The zero-filled workspace of a stream, made anew when `nbytes` asks for
+    more; under graph capture one of the graph's own, so that replays share
+    nothing with eager calls."""
+    capturing = torch.cuda.is_current_stream_capturing()
     if nbytes == 0:
-        return None
-    if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
-    buf = _attn_ws.get((device, stream))
-    if buf is None or buf.numel() < nbytes:
-        buf = _attn_ws[(device, stream)] = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+        return None if capturing else _attn_ws.get((device, stream))
+    buf = torch.zeros(nbytes if capturing else max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+    if not capturing:
+        _attn_ws[(device, stream)] = buf
     return buf
 
 
@@ -795,15 +819,25 @@ def kvq_attention(Q, cache, batch, mask=None, scale: float = None, out=None, ws=
     ba = _batch_arg(batch, n)
     if mask is not None:
         _want(mask, torch.int64, "mask", (n,))
-    out = torch.empty_like(Q) if out is None else out
-    _want(out, torch.float16, "out", Q.shape)
+    if out is None:
+        out = torch.empty_like(Q)
+    else:
+        _want(out, torch.float16, "out", Q.shape)
     L = lib()
     stream = _stream(Q)
     ca_p, ba_p = ctypes.byref(ca), ctypes.byref(ba)
-    if ws is None:
-        ws = _stream_workspace(int(L.kvq_attention_workspace_bytes(ca_p, ba_p, hq)), Q.device, stream)
-    _check(L.kvq_attention(ca_p, ba_p, _ptr(Q), hq, _ptr(mask), d ** -0.5 if scale is None else scale, _ptr(out),
-                           _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), flags, stream))
+    mine = ws is None
+    if mine:
+        ws = _stream_workspace(Q.device, stream)
+    mp = None if mask is None else mask.data_ptr()
+    scale = d ** -0.5 if scale is None else scale
+    while True:
+        st = L.kvq_attention(ca_p, ba_p, Q.data_ptr(), hq, mp, scale, out.data_ptr(), _ptr(ws),
+                             0 if ws is None else ws.numel() * ws.element_size(), flags, stream)
+        if st != ERR_WORKSPACE or not mine:
+            break
+        ws, mine = _stream_workspace(Q.device, stream, int(L.kvq_attention_workspace_bytes(ca_p, ba_p, hq))), False
+    _check(st)
     return out
 
 

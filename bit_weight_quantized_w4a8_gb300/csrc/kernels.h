@@ -100,7 +100,7 @@ cudaError_t launch_index_softmax(const int32_t* A, int64_t rows, int64_t cols, u
                                  cudaStream_t stream);
 
 // The decoder layer around the linears: residual and norms (norm.cu), rotary
-// positions and the quantized cache (kvq.cu), attention over it (kvq_attn.cu).
+// positions and the quantized cache (kvq.cu), attention over it.
 cudaError_t launch_add_norm(const void* r, int r_f16, const void* y, int y_f16, const float* post_w,
                             const float* gate, int64_t ld_gate, const float* w, int64_t M, int N, float alpha,
                             float beta, float eps, void* r_out, uint16_t* X, int8_t* Xq, float* sa, bool vec,
@@ -116,6 +116,13 @@ cudaError_t launch_kvq_read(const kvq_cache_t& c, const kvq_batch_t& b, void* K,
                             cudaStream_t stream);
 cudaError_t launch_kvq_keep(const kvq_cache_t& c, const kvq_batch_t& b, const int32_t* keep, unsigned flags,
                             cudaStream_t stream);
+// Rows of a (sequence, cache head) in blocks of 8 or 16 (kvq_attn.cu); many of
+// them on tcgen05 (kvq_tree.cu), which routes the calls of kvq_attention.
+size_t attn_rows_workspace(const kvq_cache_t& c, const kvq_batch_t& b, int heads_q, int sms);
+cudaError_t launch_attn_rows(const kvq_cache_t& c, const kvq_batch_t& b, const uint16_t* Q, int heads_q,
+                             const uint64_t* mask, float scale, uint16_t* out, void* ws, int sms, unsigned flags,
+                             cudaStream_t stream);
+cudaError_t read_and_clear_attn_rows_error(unsigned* flags, cudaStream_t stream);
 size_t kvq_attn_workspace(const kvq_cache_t& c, const kvq_batch_t& b, int heads_q, int sms);
 cudaError_t launch_kvq_attention(const kvq_cache_t& c, const kvq_batch_t& b, const uint16_t* Q, int heads_q,
                                  const uint64_t* mask, float scale, uint16_t* out, void* ws, int sms, unsigned flags,

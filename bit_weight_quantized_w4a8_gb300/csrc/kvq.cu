@@ -18,7 +18,6 @@ namespace {
 __device__ unsigned g_kvq_error;
 
 constexpr int kLayerThreads = 256;
-constexpr int kMaxRot = 256;
 
 __device__ __forceinline__ uint64_t turn_fraction(double freq) {
     const double t = freq * 0.15915494309189533577;  // 1 / (2 pi)

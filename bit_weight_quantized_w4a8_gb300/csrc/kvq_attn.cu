@@ -5,44 +5,27 @@
 // The rows that share a cache head (tokens x heads_q / heads of them) are taken
 // in blocks of 8 or 16; a CTA of four warps walks the keys of one (sequence,
 // head, row block) in units of 128, each warp its own 32, and the warps' and
-// CTAs' pieces are joined by their softmax statistics.  The work of the whole
-// batch, in units, is cut into equal runs for the CTAs on the device, from the
-// lengths that it finds there: long and short sequences fill the GPU alike, and
-// a captured graph follows its lengths.
+// CTAs' pieces are joined by their softmax statistics (kvq_attn.cuh cuts the
+// batch's units into runs).
 //
 // Both products run on mma.sync m16n8k16 with the cache as the M operand, so
 // that 8 rows are enough to fill an instruction: S^T = K Q^T, then O^T = V^T W^T,
 // W^T being S^T's weights transposed by movmatrix.  Codes are integers of
 // at most 7 bits and sign, exact in binary16, and the scales stay outside the products:
 // ks_j multiplies the fp32 logit, vs_j the fp32 weight before its rounding.
+#include <atomic>
 #include <type_traits>
 
 #include "kernels.h"
-#include "layer.cuh"
+#include "kvq_attn.cuh"
 
 namespace w4a8 {
 namespace {
-
-__device__ unsigned g_attn_error;
 
 constexpr int kAttnThreads = 128;
 constexpr int kWarps = 4;
 constexpr int kStep = 32;                 // keys of a warp's step
 constexpr int kUnit = kStep * kWarps;     // keys of a CTA's unit of work
-constexpr int kTicketBytesAttn = 4096;    // arrival counters, one per CTA
-constexpr int kMaxCtas = kTicketBytesAttn / 4;
-
-struct AttnArgs {
-    KvqCacheArg c;
-    KvqBatchArg b;
-    const __half* Q;
-    const uint64_t* mask;
-    __half* out;
-    int heads_q, group;  // query heads of a cache head
-    float scale_log2;
-    unsigned* tickets;
-    float* parts;
-};
 
 __device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -82,36 +65,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-__device__ __forceinline__ float exp2_fast(float x) {  // within 2^-22 relative
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t hsub2_u(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-__device__ __forceinline__ uint32_t hfma2_u(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t d;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-    return d;
-}
-
-// 8-bit codes: bytes u = code + 128 (an xor) under the exponent byte 0x64 read
-// as 1024 + u, so subtracting 1152 leaves the code exactly.
-__device__ __forceinline__ void widen8(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    const uint32_t u = w ^ 0x80808080u;
-    lo = hsub2_u(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u);
-    hi = hsub2_u(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
-}
-// 4-bit codes, nibbles i and i + 4 of a word: 1032 + code and 1024 + 16 (code +
-// 8) in the low and high nibble of a byte, then - 1032, or / 16 - 72.
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t& n0, uint32_t& n1) {
-    n0 = hsub2_u((w & 0x000F000Fu) ^ 0x64086408u, 0x64086408u);
-    n1 = hfma2_u((w & 0x00F000F0u) ^ 0x64806480u, 0x2C002C00u, 0xD480D480u);
-}
-
 // Layout of a warp's stage in shared memory: 32 keys, then 32 values, each
 // vector W bytes, then their scales.  The 16-byte chunks of a vector are permuted
 // by its key so that the reads below meet each bank once: keys are read
@@ -144,20 +97,6 @@ struct Cfg {
     static constexpr int kPart = kRows * (DIM + 2);          // floats of a CTA's piece
 };
 
-// Units of sequence b: row blocks x heads x units of keys (at least one, which
-// writes the zeros of rows that see nothing).
-struct SeqWork {
-    int blocks;
-    int64_t units;  // per (row block, head)
-};
-__device__ __forceinline__ SeqWork seq_work(const AttnArgs& a, const KvqSeq& s, int rows) {
-    SeqWork w;
-    w.blocks = (int)(((int64_t)s.count * a.group + rows - 1) / rows);
-    const int64_t end = a.mask != nullptr && s.count > KVQ_MAX_TREE ? 0 : s.end;
-    w.units = end > 0 ? (end + kUnit - 1) / kUnit : 1;
-    return w;
-}
-
 template <int DIM, int BITS, int NR>
 __global__ void __launch_bounds__(kAttnThreads) attn_kernel(const AttnArgs a) {
     using C = Cfg<DIM, BITS, NR>;
@@ -166,7 +105,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(const AttnArgs a) {
     constexpr int KW = W == 32 ? 2 : 4;          // words of a run
     constexpr int MT = DIM / 16;                 // 16-dim tiles of the output
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t s_units[kWarps], s_find[2];
+    using Walk = AttnWalk<kAttnThreads, ROWS, 1, kUnit>;
+    __shared__ typename Walk::Shared s_walk;
     __shared__ float s_stat[3][kWarps][ROWS];
     __shared__ unsigned s_last;
     griddep_launch_dependents();
@@ -174,92 +114,24 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(const AttnArgs a) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
 
-    // total work, then the run of this CTA: units [begin, end)
-    int64_t total = 0;
-    for (int b0 = 0; b0 < a.b.seqs; b0 += kAttnThreads) {
-        if (b0 + tid < a.b.seqs) {
-            const KvqSeq s = kvq_seq(a.b.cu, a.b.start, b0 + tid, a.b.tokens, a.b.max_pages, a.c.shift);
-            if (!s.ok || (a.mask != nullptr && s.count > KVQ_MAX_TREE)) atomicOr(&g_attn_error, kErrCacheRange);
-            const SeqWork w = seq_work(a, s, ROWS);
-            total += w.units * w.blocks * a.c.heads;
-        }
-    }
-    #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-    if (lane == 0) s_units[warp] = total;
-    __syncthreads();
-    total = 0;
-    #pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += s_units[w];
-    const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    int64_t at = per * blockIdx.x;  // next unit of the batch
-    const int64_t run_end = min(at + per, total);
-    if (at >= run_end) return;
-
-    // the sequence that holds unit `at`: found by warp 0, 32 sequences a time
-    if (warp == 0) {
-        int64_t before = 0;
-        for (int b0 = 0; b0 < a.b.seqs; b0 += 32) {
-            int64_t n = 0;
-            if (b0 + lane < a.b.seqs) {
-                const KvqSeq s = kvq_seq(a.b.cu, a.b.start, b0 + lane, a.b.tokens, a.b.max_pages, a.c.shift);
-                const SeqWork w = seq_work(a, s, ROWS);
-                n = w.units * w.blocks * a.c.heads;
-            }
-            int64_t sum = n;
-            #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t x = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-                if (lane >= o) sum += x;
-            }
-            const unsigned past = __ballot_sync(0xFFFFFFFFu, before + sum > at);
-            if (past) {
-                if (lane == __ffs(past) - 1) {
-                    s_find[0] = b0 + lane;
-                    s_find[1] = before + sum - n;
-                }
-                break;
-            }
-            before += __shfl_sync(0xFFFFFFFFu, sum, 31);
-        }
-    }
-    __syncthreads();
-    int b = (int)s_find[0];
-    int64_t seq_first = s_find[1];  // first unit of sequence b
+    Walk walk;
+    if (!walk.init(a, s_walk)) return;
 
     const uint32_t ring = smem_u32(smem) + warp * (C::kStages * C::kStageBytes);
-    const int64_t page_mask = (1 << a.c.shift) - 1;
+    const int page_mask = (1 << a.c.shift) - 1;
 
-    while (at < run_end) {
-        const KvqSeq s = kvq_seq(a.b.cu, a.b.start, b, a.b.tokens, a.b.max_pages, a.c.shift);
-        const SeqWork sw = seq_work(a, s, ROWS);
-        const int64_t seq_units = sw.units * sw.blocks * a.c.heads;
-        if (at >= seq_first + seq_units) {
-            seq_first += seq_units;
-            ++b;
-            continue;
-        }
-        // tile: units [tile_first, tile_first + units) are head h, row block rb
-        const int64_t tile = (at - seq_first) / sw.units;
-        const int64_t tile_first = seq_first + tile * sw.units;
-        const int h = (int)(tile / sw.blocks), rb = (int)(tile - (int64_t)h * sw.blocks);
-        const int u0 = (int)(at - tile_first);
-        const int u1 = (int)(min(run_end, tile_first + sw.units) - tile_first);
-        at = tile_first + u1;
-        const int n_rows = min(ROWS, s.count * a.group - rb * ROWS);
-        // slots that some row of the block may see end here
-        int64_t key_end = a.mask != nullptr && s.count > KVQ_MAX_TREE ? 0 : s.end;
-        if (a.mask == nullptr) {
-            const int64_t last = s.start + (rb * ROWS + n_rows - 1) / a.group + 1;
-            if (last < key_end) key_end = last;
-        }
+    AttnTile t;
+    while (walk.next(a, t)) {
+        const KvqSeq& s = t.s;
+        const int b = t.b, h = t.h, u0 = t.u0, u1 = t.u1, n_rows = t.rows;
+        const int key_end = t.key_end;
 
         // queries: B operands, row 8 nr + g, in the order in which the key's runs
         // are widened
         uint32_t qf[NR][DIM / 16][2];
         #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-            const int r = rb * ROWS + 8 * nr + g;
+            const int r = t.row0 + 8 * nr + g;
             const bool live = 8 * nr + g < n_rows;
             const int tok = s.first + r / a.group;
             const __half* q = a.Q + ((int64_t)tok * a.heads_q + h * a.group + r % a.group) * DIM;
@@ -307,7 +179,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(const AttnArgs a) {
 
         // page of this lane's key (lane = key of the step) for step u
         auto page_of = [&](int u) -> int {
-            const int64_t k = (int64_t)u * kUnit + warp * kStep + lane;
+            const int k = u * kUnit + warp * kStep + lane;
             if (u >= u1 || k >= key_end) return -2;  // no key
             const int p = a.b.table[b * a.b.max_pages + (k >> a.c.shift)];
             if (p < 0 || p >= a.c.pages) {
@@ -318,7 +190,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(const AttnArgs a) {
         };
         auto issue = [&](int u, int page) {
             if (u < u1) {
-                const int64_t k0 = (int64_t)u * kUnit + warp * kStep;
+                const int k0 = u * kUnit + warp * kStep;
                 const uint32_t st = ring + ((u - u0) % C::kStages) * C::kStageBytes;
                 const int64_t vec = page >= 0 ? ((((int64_t)page * a.c.heads + h) << a.c.shift) + ((k0 + lane) & page_mask)) : 0;
                 constexpr int CPV = W / 16, KPI = 32 / CPV;  // chunks of a vector, keys of one warp-wide copy
@@ -353,7 +225,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(const AttnArgs a) {
             valid[C::kStages - 2] = __ballot_sync(0xFFFFFFFFu, pg >= 0);
             issue(u + C::kStages - 1, pg);
             pg = page_of(u + C::kStages);
-            const int64_t k0 = (int64_t)u * kUnit + warp * kStep;
+            const int k0 = u * kUnit + warp * kStep;
             if (ok_keys == 0) continue;
             const uint32_t st = ring + ((u - u0) % C::kStages) * C::kStageBytes;
             const uint32_t sk = st + 2 * kStep * W, sv = sk + 4 * kStep;
@@ -422,14 +294,14 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(const AttnArgs a) {
                     #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int r = 8 * nr + 2 * t4 + e;
-                        const int tok = (rb * ROWS + min(r, n_rows - 1)) / a.group;
+                        const int tok = (t.row0 + min(r, n_rows - 1)) / a.group;
                         const uint64_t word = a.mask != nullptr ? a.mask[s.first + tok] : 0;
                         #pragma unroll
                         for (int mt = 0; mt < 2; ++mt)
                             #pragma unroll
                             for (int hf = 0; hf < 2; ++hf) {
                                 const int kk = 16 * mt + 8 * hf + g;
-                                const int64_t w = k0 + kk - s.start;
+                                const int w = k0 + kk - s.start;
                                 bool see = (ok_keys >> kk) & 1;
                                 if (w >= 0) see = see && (a.mask != nullptr ? w < 64 && ((word >> w) & 1) : w <= tok);
                                 if (!see) {
@@ -597,7 +469,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(const AttnArgs a) {
             }
         __syncthreads();
 
-        const bool whole = u0 == 0 && u1 == (int)sw.units;
+        const bool whole = u0 == 0 && u1 == t.units;
         float* part = a.parts + ((int64_t)blockIdx.x * 2 + (u0 == 0 ? 1 : 0)) * C::kPart;
         for (int e = tid; e < ROWS * DIM / 4; e += kAttnThreads) {
             const int r = e / (DIM / 4), d = (e % (DIM / 4)) * 4;
@@ -617,7 +489,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(const AttnArgs a) {
             }
             if (whole) {
                 if (r < n_rows) {
-                    const int row = rb * ROWS + r;
+                    const int row = t.row0 + r;
                     const float inv = top == -INFINITY && sum == 0.f ? 0.f : 1.f / sum;
                     __half* out = a.out + ((int64_t)(s.first + row / a.group) * a.heads_q + h * a.group + row % a.group) * DIM + d;
                     store4(out, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
@@ -631,7 +503,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(const AttnArgs a) {
             // the last CTA of the tile to arrive joins the pieces in their order
             __threadfence();
             __syncthreads();
-            const int64_t c0 = tile_first / per, c1 = (tile_first + sw.units - 1) / per;
+            const int64_t c0 = walk.first_cta(t), c1 = walk.last_cta(t);
             if (tid == 0) {
                 const unsigned n = atomicAdd(a.tickets + c0, 1u);
                 s_last = n == (unsigned)(c1 - c0);
@@ -661,7 +533,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(const AttnArgs a) {
                         o.w = fmaf(x.w, f, o.w);
                         sum = fmaf(st.y, f, sum);
                     }
-                    const int row = rb * ROWS + r;
+                    const int row = t.row0 + r;
                     const float inv = top == -INFINITY && sum == 0.f ? 0.f : 1.f / sum;
                     __half* out = a.out + ((int64_t)(s.first + row / a.group) * a.heads_q + h * a.group + row % a.group) * DIM + d;
                     store4(out, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
@@ -677,7 +549,7 @@ int attn_ctas(int sms) {
     // two CTAs an SM where their rings fit
     const int per_sm = 2 * (Cfg<DIM, BITS, NR>::kSmem + 2048) <= 227 * 1024 ? 2 : 1;
     const int n = sms * per_sm;
-    return n < kMaxCtas ? n : kMaxCtas;
+    return n < kAttnMaxCtas ? n : kAttnMaxCtas;
 }
 
 // Row blocks of 8 when the rows that share a cache head fill no more on average.
@@ -701,30 +573,31 @@ auto by_config(const kvq_cache_t& c, const kvq_batch_t& b, int heads_q, F f) {
 
 }  // namespace
 
-size_t kvq_attn_workspace(const kvq_cache_t& c, const kvq_batch_t& b, int heads_q, int sms) {
+size_t attn_rows_workspace(const kvq_cache_t& c, const kvq_batch_t& b, int heads_q, int sms) {
     return by_config(c, b, heads_q, [&](auto dim, auto bits, auto nr) -> size_t {
         constexpr int D = decltype(dim)::value, B = decltype(bits)::value, N = decltype(nr)::value;
-        return kTicketBytesAttn + (size_t)attn_ctas<D, B, N>(sms) * 2 * Cfg<D, B, N>::kPart * sizeof(float);
+        return kAttnTicketBytes + (size_t)attn_ctas<D, B, N>(sms) * 2 * Cfg<D, B, N>::kPart * sizeof(float);
     });
 }
 
-cudaError_t launch_kvq_attention(const kvq_cache_t& c, const kvq_batch_t& b, const uint16_t* Q, int heads_q,
+cudaError_t launch_attn_rows(const kvq_cache_t& c, const kvq_batch_t& b, const uint16_t* Q, int heads_q,
                                  const uint64_t* mask, float scale, uint16_t* out, void* ws, int sms, unsigned flags,
                                  cudaStream_t stream) {
     const AttnArgs a = {cache_arg(c), batch_arg(b), reinterpret_cast<const __half*>(Q), mask,
                         reinterpret_cast<__half*>(out), heads_q, heads_q / c.heads, scale * 1.4426950408889634f,
                         static_cast<unsigned*>(ws),
-                        reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kTicketBytesAttn)};
+                        reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kAttnTicketBytes)};
     return by_config(c, b, heads_q, [&](auto dim, auto bits, auto nr) {
         constexpr int D = decltype(dim)::value, B = decltype(bits)::value, N = decltype(nr)::value;
         auto* f = attn_kernel<D, B, N>;
-        cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, B, N>::kSmem);
+        static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is set
+        const cudaError_t e = layer_smem(f, Cfg<D, B, N>::kSmem, ready);
         if (e != cudaSuccess) return e;
         return layer_launch(f, dim3((unsigned)attn_ctas<D, B, N>(sms)), kAttnThreads, Cfg<D, B, N>::kSmem, flags, stream, a);
     });
 }
 
-cudaError_t read_and_clear_attn_error(unsigned* flags, cudaStream_t stream) {
+cudaError_t read_and_clear_attn_rows_error(unsigned* flags, cudaStream_t stream) {
     unsigned v = 0, z = 0;
     cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_attn_error, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
     if (e != cudaSuccess) return e;

@@ -40,22 +40,25 @@ KVQ_HD int64_t kvq_slot_row(const int32_t* table, int64_t max_pages, int64_t pag
 
 // Sequence b's tokens [first, first + count) and start, from arrays that may
 // hold anything: count and start are 0 unless 0 <= cu[b] <= cu[b + 1] <= tokens
-// and 0 <= start.  end, the slots in use, is cut to what the table holds; ok
+// and 0 <= start.  end, the slots in use, is cut to what the table holds (and to
+// kKvqMaxSlots, so that slots and the blocks past them are 32-bit numbers); ok
 // tells whether all was in range.
+constexpr int kKvqMaxSlots = 0x7FFFF000;
 struct KvqSeq {
-    int first, count;
-    int64_t start, end;
+    int first, count, start, end;
     bool ok;
 };
 KVQ_HD KvqSeq kvq_seq(const int32_t* cu, const int32_t* start, int b, int64_t tokens, int64_t max_pages,
                       int shift) {
     KvqSeq q;
-    const int64_t lo = cu[b], hi = cu[b + 1], s = start[b], slots = max_pages << shift;
+    const int64_t lo = cu[b], hi = cu[b + 1], s = start[b];
+    const int64_t room = max_pages << shift, slots = room < kKvqMaxSlots ? room : kKvqMaxSlots;
     const bool sound = lo >= 0 && lo <= hi && hi <= tokens && s >= 0;
     q.first = (int)lo;
     q.count = sound ? (int)(hi - lo) : 0;
-    q.start = sound ? s : 0;
-    q.end = q.start + q.count < slots ? q.start + q.count : slots;
+    q.start = sound ? (int)s : 0;
+    const int64_t e = (int64_t)q.start + q.count;
+    q.end = (int)(e < slots ? e : slots);
     q.ok = sound && s + (hi - lo) <= slots;
     return q;
 }

@@ -1,0 +1,714 @@
+// kvq_tree.cu -- attention of many rows over the quantized paged cache (trees of
+// drafted tokens times the query heads of a cache head) on the 5th-generation
+// tensor cores; formulas and rounding as in kvq_attn.cu.
+//
+// With hundreds of rows on each key the work is the two products, which only
+// tcgen05 runs at full rate, so the codes are widened to binary16 once
+// per CTA, in shared memory, for up to 256 rows:
+//   warps 8-11 load the codes of 128 keys and values, widen them and store them
+//     in the tensor core's 128-byte swizzled layout (two stages each);
+//   warps 0-3 and 4-7 are two slots of softmax: S is read from TMEM, the
+//     weights go back over it as binary16;
+//   the first warp of a slot issues its products: S = Q K^T into TMEM (128 rows x
+//     128 keys), and O += W V with the weights W as the TMEM operand and V with its
+//     dimensions contiguous (the transposed B operand), so nothing is transposed.
+// The slots take two tiles of 128 rows in turn; when a row block has only one
+// tile, they take alternate keys of the same rows and are joined like two CTAs.  While
+// one slot computes weights the tensor core works for the other.
+//
+// Softmax: row r keeps a reference M; p_j = 2^(t_j - M) is summed in fp32 and w_j
+// = p_j vs_j rounded to binary16.  M is the row's maximum so far plus e - 10,
+// 2^e being a bound of the value scales, and is raised (and O and the sum
+// rescaled) only when a weight would pass 2^14: so seldom that O stays in TMEM.
+#include <atomic>
+#include <cstddef>
+#include <type_traits>
+
+#include "kernels.h"
+#include "kvq_attn.cuh"
+#include "tc.cuh"
+
+namespace w4a8 {
+namespace {
+
+constexpr int kSoftWarps = 8, kLoadWarps = 4;
+// 12 warps: three to a scheduler, 168 registers a thread (softmax holds a row's
+// 128 weights and two batches of logits); a 13th would cost all of them 40
+constexpr int kTreeThreads = (kSoftWarps + kLoadWarps) * 32;
+constexpr int kRowsTile = 128;   // rows of a tile, TMEM lanes
+constexpr int kBlock = 128;      // keys of a unit
+constexpr int kScaleRing = 4;    // blocks whose scales are held
+constexpr float kTop = 10.f;     // log2 of the weight of a fresh maximum
+constexpr float kSlack = 4.f;    // log2 of what it may grow by before O is rescaled
+
+struct alignas(16) BlockScales {  // read as 16-byte vectors
+    float k[kBlock];        // ks * scale * log2(e)
+    float v[kBlock];
+    uint32_t valid[4];      // bit i of word w: key 32 w + i is there
+};
+
+struct TreeShared {
+    uint64_t kfull[2], kfree[2], vfull[2], vfree[2], sfull[2], pready[2], pvdone[2], scfull[kScaleRing], drain[2];
+    BlockScales sc[kScaleRing];
+    AttnWalk<kTreeThreads, kRowsTile, 2, kBlock>::Shared find;
+    AttnWalk<kTreeThreads, kRowsTile, 2, kBlock> walk;  // thread 0's
+    AttnTile tile;                                      // and where it is
+    float stat[2][2][kRowsTile];  // [reference, sum][slot][row]
+    int more;
+    uint32_t tmem;
+    volatile int abort;
+};
+
+static_assert(offsetof(TreeShared, sc) % 16 == 0 && sizeof(BlockScales) % 16 == 0 && offsetof(BlockScales, v) % 16 == 0,
+              "scales are read as 16-byte vectors");
+
+template <int DIM, int BITS>
+struct TreeCfg {
+    static constexpr int W = DIM * BITS / 8;
+    static constexpr int kHalf = kRowsTile * 128;            // 128 rows of 64 binary16 values
+    static constexpr int kTileBytes = kHalf * (DIM / 64);
+    static constexpr int kOffQ = 0, kOffK = 2 * kTileBytes, kOffV = 4 * kTileBytes, kOffShared = 6 * kTileBytes;
+    static constexpr int kSmem = kOffShared + (int)sizeof(TreeShared) + 1024;  // + alignment
+    static constexpr int kPiece = kRowsTile * (DIM + 2);     // floats: O [DIM][128], M, sum
+    static constexpr uint32_t kS = 0, kO = 256;              // TMEM columns: S of slot i at 128 i, O at 256 + DIM i
+    static constexpr uint32_t kCols = 512;
+};
+
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    #pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    for (;;) {
+        #pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            *abort_flag = 1;
+            atomicOr(&g_attn_error, kErrFullWait);
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Byte of 16-byte chunk c (8 values) of row r in a tile of 128 rows: halves of 64
+// values, rows of 128 bytes, chunks permuted by chunk ^ (r % 8).
+__device__ __forceinline__ uint32_t tile_off(int r, int c) {
+    return (uint32_t)((c >> 3) * (kRowsTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// Draft tokens d0 .. d0 + 31 (negative: cached ones) that a row sees.
+__device__ __forceinline__ uint32_t seen_bits(int d0, bool tree, uint64_t word, int tok) {
+    if (d0 <= -32) return 0xFFFFFFFFu;
+    if (!tree) {
+        const int n = tok + 1 - d0;  // the first n
+        return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+    }
+    if (d0 >= 0) return d0 < 64 ? (uint32_t)(word >> d0) : 0u;
+    return (uint32_t)(word << -d0) | ((1u << -d0) - 1u);
+}
+
+// Column of dimension y in a group of eight: the widened 4-bit codes come in the
+// order 0, 4, 1, 5, 2, 6, 3, 7.
+template <int BITS>
+__device__ __forceinline__ constexpr int column_of(int y) {
+    return BITS == 8 ? y : (y < 4 ? 2 * y : 2 * y - 7);
+}
+__device__ __forceinline__ void store8(__half* p, const float* f) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
+}
+
+template <int DIM, int BITS>
+__global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a) {
+    using C = TreeCfg<DIM, BITS>;
+    constexpr int KSTEPS = DIM / 16;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    const uint32_t base = smem_u32(smem);
+    TreeShared& sh = *reinterpret_cast<TreeShared*>(smem + C::kOffShared);
+    griddep_launch_dependents();
+    griddep_wait();
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // one value for the warp, known to the compiler as such
+
+    {
+        AttnWalk<kTreeThreads, kRowsTile, 2, kBlock> walk;
+        if (!walk.init(a, sh.find)) return;
+        if (tid == 0) sh.walk = walk;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.kfull[i]), kLoadWarps);
+            mbar_init(smem_u32(&sh.vfull[i]), kLoadWarps);
+            mbar_init(smem_u32(&sh.kfree[i]), 2);
+            mbar_init(smem_u32(&sh.vfree[i]), 2);
+            mbar_init(smem_u32(&sh.drain[i]), 1);
+            mbar_init(smem_u32(&sh.sfull[i]), 1);
+            mbar_init(smem_u32(&sh.pready[i]), 4);
+            mbar_init(smem_u32(&sh.pvdone[i]), 1);
+        }
+        for (int i = 0; i < kScaleRing; ++i) mbar_init(smem_u32(&sh.scfull[i]), kLoadWarps);
+        fence_mbar_init();
+        sh.abort = 0;
+    }
+    if (warp == kSoftWarps) tmem_alloc(smem_u32(&sh.tmem), C::kCols);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = sh.tmem;
+    const uint32_t u_tmem = __shfl_sync(0xFFFFFFFFu, tmem, 0), u_base = __shfl_sync(0xFFFFFFFFu, base, 0);
+    const bool leader = elect_one();
+
+    int blocks_done = 0;             // key blocks of earlier tiles: stage and phase go on
+    int jobs_done[2] = {0, 0};       // S tiles of earlier row blocks, per slot
+    for (;;) {
+        if (tid == 0) sh.more = sh.walk.next(a, sh.tile);
+        __syncthreads();
+        if (!sh.more) break;
+        const AttnTile& t = sh.tile;  // the roles take what they need of it into registers
+        const int nb = t.u1 - t.u0;
+        const bool two = t.tiles == 2;
+        // the queries of the block's rows, widened keys' order of dimensions
+        for (int e = tid; e < t.tiles * kRowsTile * (DIM / 8); e += kTreeThreads) {
+            const int r = e / (DIM / 8), c = e % (DIM / 8);
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (r < t.rows) {
+                const int row = t.row0 + r, tok = t.s.first + row / a.group;
+                x = *reinterpret_cast<const uint4*>(a.Q + ((int64_t)tok * a.heads_q + t.h * a.group + row % a.group) * DIM + 8 * c);
+            }
+            if constexpr (BITS == 4)
+                x = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
+                               __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
+            sts16(base + C::kOffQ + (r / kRowsTile) * C::kTileBytes + tile_off(r % kRowsTile, c), x.x, x.y, x.z, x.w);
+        }
+        fence_async_shared();
+        __syncthreads();
+
+        if (warp >= kSoftWarps) {
+            // codes of this warp's 32 keys of every block, widened
+            constexpr int CPR = C::W / 16;  // 16-byte chunks of codes per vector
+            const int lw = warp - kSoftWarps;
+            const int u0 = t.u0, u1 = t.u1, key_end = t.key_end, h = t.h;
+            const int32_t* table = a.b.table + t.b * a.b.max_pages;
+            uint4 xk[CPR], xv[CPR];
+            float sk = 0.f, sv = 0.f;
+            uint32_t there = 0u;  // keys of the block being loaded that are in range
+            int64_t row_a = 0, row_b = 0;  // vectors of the first and second 16 keys (one page each)
+            const int pmask = (1 << a.c.shift) - 1;
+            // nothing here waits for what it has just loaded: page numbers are
+            // fetched two blocks ahead, codes and scales one
+            auto page_of = [&](int u) -> int {  // of this lane's key, as the table has it
+                const int k = u * kBlock + 32 * lw + lane;
+                return u < u1 && k < key_end ? table[k >> a.c.shift] : -1;
+            };
+            auto row_of = [&](int i) -> int {
+                return CPR >= 4 ? 8 * (i / (CPR / 4 > 0 ? CPR / 4 : 1)) + (lane & 7) : 16 * i + 8 * (lane >> 4) + (lane & 7);
+            };
+            auto chunk_of = [&](int i) -> int {
+                return CPR >= 4 ? (lane >> 3) + 4 * (i % (CPR / 4 > 0 ? CPR / 4 : 1)) : (lane >> 3) & 1;
+            };
+            auto load = [&](const uint8_t* codes, uint4* x) {
+                #pragma unroll
+                for (int i = 0; i < CPR; ++i) {
+                    const int r = row_of(i);
+                    const int64_t v = (r < 16 ? row_a : row_b - 16) + r;
+                    x[i] = (there >> r) & 1 ? ld_global_nc_v4(codes + v * C::W + 16 * chunk_of(i)) : make_uint4(0u, 0u, 0u, 0u);
+                }
+            };
+            auto load_k = [&](int u, int page) {
+                const int k = u * kBlock + 32 * lw + lane;
+                const bool ok = page >= 0 && page < a.c.pages;
+                if (!ok && u < u1 && k < key_end) atomicOr(&g_attn_error, kErrCacheRange);
+                const int64_t vec = ok ? ((((int64_t)page * a.c.heads + h) << a.c.shift) + (k & pmask)) : 0;
+                there = __ballot_sync(0xFFFFFFFFu, ok);
+                row_a = __shfl_sync(0xFFFFFFFFu, vec, 0);
+                row_b = __shfl_sync(0xFFFFFFFFu, vec, 16);
+                load(a.c.k, xk);
+                sk = ok ? a.c.ks[vec] : 0.f;
+                sv = ok ? a.c.vs[vec] : 0.f;
+            };
+            auto store = [&](uint32_t dst, const uint4* x) {
+                #pragma unroll
+                for (int i = 0; i < CPR; ++i) {
+                    const int r = 32 * lw + row_of(i), c = chunk_of(i);
+                    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    if constexpr (BITS == 8) {
+                        uint32_t h[8];
+                        #pragma unroll
+                        for (int j = 0; j < 4; ++j) widen8(w[j], h[2 * j], h[2 * j + 1]);
+                        sts16(dst + tile_off(r, 2 * c), h[0], h[1], h[2], h[3]);
+                        sts16(dst + tile_off(r, 2 * c + 1), h[4], h[5], h[6], h[7]);
+                    } else {
+                        #pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t h[4];
+                            widen4(w[j], h[0], h[1]);
+                            widen4(w[j] >> 8, h[2], h[3]);
+                            sts16(dst + tile_off(r, 4 * c + j), h[0], h[1], h[2], h[3]);
+                        }
+                    }
+                }
+            };
+            load_k(u0, page_of(u0));
+            load(a.c.v, xv);
+            int page = page_of(u0 + 1);
+            for (int j = 0; j < nb; ++j) {
+                const int blk = blocks_done + j, st = blk & 1;
+                if (blk >= 2 && !__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.kfree[st]), ((blk >> 1) - 1) & 1, &sh.abort))) break;
+                store(base + C::kOffK + st * C::kTileBytes, xk);
+                BlockScales& bs = sh.sc[blk % kScaleRing];
+                bs.k[32 * lw + lane] = sk * a.scale_log2;
+                bs.v[32 * lw + lane] = sv;
+                if (lane == 0) bs.valid[lw] = there;
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&sh.scfull[blk % kScaleRing]));
+                    mbar_arrive(smem_u32(&sh.kfull[st]));
+                }
+                if (j + 1 < nb) load_k(u0 + j + 1, page);
+                page = page_of(u0 + j + 2);
+                if (blk >= 2 && !__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.vfree[st]), ((blk >> 1) - 1) & 1, &sh.abort))) break;
+                store(base + C::kOffV + st * C::kTileBytes, xv);
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.vfull[st]));
+                if (j + 1 < nb) load(a.c.v, xv);
+            }
+        } else {
+            // softmax: this thread's row of its slot
+            const int slot = warp >> 2, quad = warp & 3;
+            // S, W and O are held in fragments: rows 8 k + lane / 4 of the warp's 32 (k < 4),
+            // columns 2 (lane % 4), + 1 of every 8.  A thread so needs the scales of a
+            // quarter of the keys: read for whole rows they took half of the
+            // shared-memory bandwidth that the products of Q and K leave nothing of.
+            const int tile_rows = two ? min(kRowsTile, t.rows - slot * kRowsTile) : t.rows;
+            const int u0 = t.u0, start = t.s.start;
+            const bool idle = 32 * quad >= tile_rows;             // the whole warp has no row
+            const int row_base = t.row0 + (two ? slot * kRowsTile : 0);
+            const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+            const uint32_t ts = lanes + C::kS + 128 * slot, to = lanes + C::kO + DIM * slot;
+            constexpr uint32_t kHalfLanes = 16u << 16;
+            float M[4], l[4];
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) M[k] = -INFINITY, l[k] = 0.f;
+            const int my_jobs = two ? nb : (nb + 1 - slot) / 2;
+            const int u_q = __shfl_sync(0xFFFFFFFFu, two ? slot : 0, 0);
+            auto block_of = [&](int i) -> int { return blocks_done + (two ? i : 2 * i + slot); };
+            // products of job i, issued by the slot's first warp (all of it in step, so
+            // that descriptors live in uniform registers; one lane issues)
+            auto qk = [&](int i) -> bool {
+                const int blk = block_of(i), st = blk & 1;
+                if (!__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.kfull[st]), (blk >> 1) & 1, &sh.abort))) return false;
+                tc_fence_after_sync();
+                const int u_st = __shfl_sync(0xFFFFFFFFu, st, 0);
+                const uint64_t qd = sw128_desc(u_base + C::kOffQ) + u_q * (C::kTileBytes >> 4);
+                const uint64_t kd = sw128_desc(u_base + C::kOffK) + u_st * (C::kTileBytes >> 4);
+                if (leader) {
+                    #pragma unroll
+                    for (int k = 0; k < KSTEPS; ++k) {
+                        const uint64_t off = ((k >> 2) * C::kHalf + (k & 3) * 32) >> 4;
+                        tc_mma_f16(u_tmem + C::kS + 128 * slot, qd + off, kd + off, f16_idesc(kRowsTile, kBlock), k > 0);
+                    }
+                    tc_commit(smem_u32(&sh.sfull[slot]));
+                    tc_commit(smem_u32(&sh.kfree[st]));
+                    if (!two) tc_commit(smem_u32(&sh.kfree[st]));  // the one user arrives for both
+                }
+                __syncwarp();
+                return true;
+            };
+            auto pv = [&](int i) -> bool {
+                const int blk = block_of(i), st = blk & 1, q = jobs_done[slot] + i;
+                if (!__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.pready[slot]), q & 1, &sh.abort) &&
+                                                 wait_bounded(smem_u32(&sh.vfull[st]), (blk >> 1) & 1, &sh.abort))) return false;
+                tc_fence_after_sync();
+                const int u_st = __shfl_sync(0xFFFFFFFFu, st, 0);
+                const uint64_t vd = sw128_desc_mn(u_base + C::kOffV, C::kHalf) + u_st * (C::kTileBytes >> 4);
+                if (leader) {
+                    #pragma unroll
+                    for (int k = 0; k < kBlock / 16; ++k)
+                        tc_mma_f16_tmem_a(u_tmem + C::kO + DIM * slot, u_tmem + C::kS + 128 * slot + 8 * k,
+                                          vd + k * (2048 >> 4), f16_idesc(kRowsTile, DIM) | kIdescTransposeB, i > 0 || k > 0);
+                    tc_commit(smem_u32(&sh.vfree[st]));
+                    if (!two) tc_commit(smem_u32(&sh.vfree[st]));
+                    tc_commit(smem_u32(&sh.pvdone[slot]));
+                }
+                __syncwarp();
+                return true;
+            };
+            bool ok = quad != 0 || my_jobs == 0 || qk(0);
+            for (int i = 0; ok && i < my_jobs; ++i) {
+                const int u = u0 + (two ? i : 2 * i + slot);
+                const int blk = block_of(i), q = jobs_done[slot] + i;
+                ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.scfull[blk % kScaleRing]), (blk / kScaleRing) & 1, &sh.abort)) &&
+                     __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.sfull[slot]), q & 1, &sh.abort));
+                if (!ok) break;
+                if (!idle) {
+                    tc_fence_after_sync();
+                    const BlockScales& bs = sh.sc[blk % kScaleRing];
+                    const int k0 = u * kBlock;
+                    // bound 2^ve of the block's finite value scales
+                    float ve;
+                    {
+                        const float4 v = reinterpret_cast<const float4*>(bs.v)[lane];
+                        const float top = fmaxf(fmaxf(fabsf(v.x) < INFINITY ? fabsf(v.x) : 0.f, fabsf(v.y) < INFINITY ? fabsf(v.y) : 0.f),
+                                                fmaxf(fabsf(v.z) < INFINITY ? fabsf(v.z) : 0.f, fabsf(v.w) < INFINITY ? fabsf(v.w) : 0.f));
+                        const unsigned bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
+                        ve = fmaxf((float)((int)(bits >> 23) - 126), -100.f);
+                    }
+                    const bool plain = k0 + kBlock <= start &&
+                                       (bs.valid[0] & bs.valid[1] & bs.valid[2] & bs.valid[3]) == 0xFFFFFFFFu;
+                    // what row k sees of keys 32 c .. 32 c + 31
+                    auto seen = [&](int k, int c) -> uint32_t {
+                        const int tok = (row_base + min(32 * quad + 8 * k + (lane >> 2), tile_rows - 1)) / a.group;
+                        const uint64_t word = a.mask != nullptr ? a.mask[t.s.first + tok] : 0;
+                        return bs.valid[c] & seen_bits(k0 + 32 * c - start, a.mask != nullptr, word, tok);
+                    };
+                    uint32_t p[2][32];  // weights: rows k = 2 hb (even places) and 2 hb + 1, pairs of keys
+                    float add[4], grow;
+                    auto weights = [&](auto masked) {  // p and its sums, against M
+                        constexpr bool MASKED = decltype(masked)::value;
+                        uint64_t sum[4] = {0, 0, 0, 0}, nm[4];
+                        grow = -INFINITY;
+                        #pragma unroll
+                        for (int k = 0; k < 4; ++k) nm[k] = pack2(-M[k], -M[k]);
+                        uint32_t sb[2][16];
+                        tmem_ld_frag32(ts, sb[0]);
+                        #pragma unroll
+                        for (int e = 0; e < 8; ++e) {  // 32 columns c of rows 2 hb, 2 hb + 1
+                            const int c = e >> 1, hb = e & 1;
+                            uint32_t see[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+                            if constexpr (MASKED) see[0] = seen(2 * hb, c), see[1] = seen(2 * hb + 1, c);
+                            tmem_ld_wait();
+                            if (e < 7) tmem_ld_frag32(ts + 32 * ((e + 1) >> 1) + ((e + 1) & 1) * kHalfLanes, sb[(e + 1) & 1]);
+                            const uint32_t* s = sb[e & 1];
+                            #pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int key = 8 * j + 2 * (lane & 3);
+                                const uint64_t kf = *reinterpret_cast<const uint64_t*>(bs.k + 32 * c + key);
+                                const uint64_t vf = *reinterpret_cast<const uint64_t*>(bs.v + 32 * c + key);
+                                #pragma unroll
+                                for (int rr = 0; rr < 2; ++rr) {
+                                    const int k = 2 * hb + rr;
+                                    float2 d = unpack2(fma2(pack2(__uint_as_float(s[4 * j + 2 * rr]), __uint_as_float(s[4 * j + 2 * rr + 1])), kf, nm[k]));
+                                    if constexpr (MASKED) {
+                                        if (!((see[rr] >> key) & 1)) d.x = -INFINITY;
+                                        if (!((see[rr] >> (key + 1)) & 1)) d.y = -INFINITY;
+                                    }
+                                    grow = fmaxf(grow, fmaxf(d.x, d.y));
+                                    const uint64_t x = pack2(exp2_fast(d.x), exp2_fast(d.y));
+                                    sum[k] = add2(sum[k], x);
+                                    float2 w = unpack2(mul2(x, vf));
+                                    if constexpr (MASKED) {  // an unseen key's scale may be anything
+                                        if (!((see[rr] >> key) & 1)) w.x = 0.f;
+                                        if (!((see[rr] >> (key + 1)) & 1)) w.y = 0.f;
+                                    }
+                                    p[hb][2 * (4 * c + j) + rr] = pack_half2(w.x, w.y);
+                                }
+                            }
+                        }
+                        #pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 f = unpack2(sum[k]);
+                            add[k] = f.x + f.y;
+                        }
+                    };
+                    for (int pass = 0;; ++pass) {
+                        if (plain) weights(std::false_type());
+                        else weights(std::true_type());
+                        if (pass == 1 || !__any_sync(0xFFFFFFFFu, grow + ve > kTop + kSlack)) break;
+                        // raise the references that are too low: the rows' maxima
+                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, f[4];
+                        #pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            #pragma unroll
+                            for (int hb = 0; hb < 2; ++hb) {
+                                uint32_t s[16];
+                                tmem_ld_frag32(ts + 32 * c + hb * kHalfLanes, s);
+                                uint32_t see[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+                                if (!plain) see[0] = seen(2 * hb, c), see[1] = seen(2 * hb + 1, c);
+                                tmem_ld_wait();
+                                #pragma unroll
+                                for (int x = 0; x < 16; ++x) {
+                                    const int key = 8 * (x >> 2) + 2 * (lane & 3) + (x & 1), rr = (x >> 1) & 1;
+                                    if ((see[rr] >> key) & 1)
+                                        top[2 * hb + rr] = fmaxf(top[2 * hb + rr], __uint_as_float(s[x]) * bs.k[32 * c + key]);
+                                }
+                            }
+                        }
+                        #pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            top[k] = fmaxf(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], 1));
+                            top[k] = fmaxf(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], 2));
+                            const bool up = top[k] - M[k] + ve > kTop + kSlack;
+                            const float Mn = up ? top[k] + ve - kTop : M[k];
+                            f[k] = !up ? 1.f : M[k] == -INFINITY ? 0.f : exp2_fast(M[k] - Mn);
+                            M[k] = Mn;
+                            l[k] *= f[k];
+                        }
+                        if (i > 0) {
+                            ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.pvdone[slot]), (q - 1) & 1, &sh.abort));
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                            #pragma unroll 1
+                            for (int c = 0; c < DIM / 32; ++c) {
+                                #pragma unroll
+                                for (int hb = 0; hb < 2; ++hb) {
+                                    uint32_t o[16];
+                                    tmem_ld_frag32(to + 32 * c + hb * kHalfLanes, o);
+                                    tmem_ld_wait();
+                                    #pragma unroll
+                                    for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f[2 * hb + ((x >> 1) & 1)]);
+                                    tmem_st_frag32(to + 32 * c + hb * kHalfLanes, o);
+                                }
+                            }
+                            tmem_st_wait();
+                        }
+                    }
+                    if (!ok) break;
+                    #pragma unroll
+                    for (int k = 0; k < 4; ++k) l[k] += add[k];
+                    tmem_st_pairs64(ts, p[0]);
+                    tmem_st_pairs64(ts + kHalfLanes, p[1]);
+                    tmem_st_wait();
+                    tc_fence_before_sync();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.pready[slot]));
+                if (quad == 0) ok = pv(i) && (i + 1 >= my_jobs || qk(i + 1));
+            }
+            // settled: the slot's last product, and what its rows' sums are relative to
+            if (ok && !idle && my_jobs > 0)
+                ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.pvdone[slot]), (jobs_done[slot] + my_jobs - 1) & 1, &sh.abort));
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                l[k] += __shfl_xor_sync(0xFFFFFFFFu, l[k], 1);
+                l[k] += __shfl_xor_sync(0xFFFFFFFFu, l[k], 2);
+                if ((lane & 3) == 0) {
+                    sh.stat[0][slot][32 * quad + 8 * k + (lane >> 2)] = M[k];
+                    sh.stat[1][slot][32 * quad + 8 * k + (lane >> 2)] = l[k];
+                }
+            }
+        }
+        blocks_done += nb;
+        jobs_done[0] += two ? nb : (nb + 1) / 2;
+        jobs_done[1] += two ? nb : nb / 2;
+
+        tc_fence_before_sync();
+        __syncthreads();  // roles done: operands, TMEM and statistics are settled
+        tc_fence_after_sync();
+        if (sh.abort) break;
+        // the tile's sums go out, normalized, or to this CTA's piece: a thread per
+        // row (TMEM lane); of one tile's two slots each takes half of the
+        // dimensions of both
+        if (warp < kSoftWarps) {
+            const int slot = warp >> 2, r = 32 * (warp & 3) + lane;
+            const int tile_rows = two ? min(kRowsTile, t.rows - slot * kRowsTile) : t.rows;
+            if (32 * (warp & 3) < tile_rows) {
+                const int tl = two ? slot : 0;
+                const bool whole = t.u0 == 0 && t.u1 == t.units;
+                float m, sum, f0 = 1.f, f1 = 0.f;
+                if (two) {
+                    m = sh.stat[0][slot][r];
+                    sum = sh.stat[1][slot][r];
+                } else {
+                    const float m0 = sh.stat[0][0][r], m1 = sh.stat[0][1][r];
+                    m = fmaxf(m0, m1);
+                    f0 = m0 == -INFINITY ? 0.f : exp2_fast(m0 - m);  // a slot of which nothing is seen: its sums are 0 or not written
+                    f1 = m1 == -INFINITY ? 0.f : exp2_fast(m1 - m);
+                    sum = sh.stat[1][0][r] * (m0 == -INFINITY ? 1.f : f0) + sh.stat[1][1][r] * (m1 == -INFINITY ? 1.f : f1);
+                }
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const int row = t.row0 + tl * kRowsTile + min(r, tile_rows - 1);
+                __half* out = a.out + ((int64_t)(t.s.first + row / a.group) * a.heads_q + t.h * a.group + row % a.group) * DIM;
+                float* piece = a.parts + (((int64_t)blockIdx.x * 2 + (t.u0 == 0 ? 1 : 0)) * 2 + tl) * C::kPiece;
+                const uint32_t to = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + C::kO;
+                const int c0 = two ? 0 : slot * (DIM / 64), c1 = two ? DIM / 32 : c0 + DIM / 64;
+                #pragma unroll 1
+                for (int c = c0; c < c1; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(to + (two ? DIM * slot : 0) + 32 * c, o);
+                    tmem_ld_wait();
+                    if (!two) {
+                        uint32_t x[32];
+                        if (nb > 1) {
+                            tmem_ld32(to + DIM + 32 * c, x);
+                            tmem_ld_wait();
+                        }
+                        #pragma unroll
+                        for (int y = 0; y < 32; ++y) {
+                            float z = __uint_as_float(o[y]) * f0;
+                            if (nb > 1) z = fmaf(__uint_as_float(x[y]), f1, z);
+                            o[y] = __float_as_uint(z);
+                        }
+                    }
+                    if (whole) {
+                        #pragma unroll
+                        for (int x = 0; x < 32; x += 8) {
+                            float f[8];
+                            #pragma unroll
+                            for (int y = 0; y < 8; ++y) f[y] = __uint_as_float(o[x + column_of<BITS>(y)]) * inv;
+                            if (r < tile_rows) store8(out + 32 * c + x, f);
+                        }
+                    } else {
+                        #pragma unroll
+                        for (int x = 0; x < 32; ++x) piece[(32 * c + x) * kRowsTile + r] = __uint_as_float(o[x]);
+                    }
+                }
+                if (!whole && (two || slot == 0)) {
+                    piece[DIM * kRowsTile + r] = m;
+                    piece[(DIM + 1) * kRowsTile + r] = sum;
+                }
+            }
+            tc_fence_before_sync();
+        }
+        __syncthreads();  // the tile and TMEM have been read
+        tc_fence_after_sync();
+    }
+    // the tensor core is idle before its memory is given back
+    if (warp == 0 || warp == 4) {
+        if (leader) {
+            tc_commit(smem_u32(&sh.drain[warp >> 2]));
+            if (!mbar_wait(smem_u32(&sh.drain[warp >> 2]), 0)) atomicOr(&g_attn_error, kErrDrainWait);
+        }
+        __syncwarp();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kSoftWarps) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, C::kCols);
+    }
+}
+
+// Joins the pieces of the row block that began in the run of CTA blockIdx.x and
+// went on in the next ones, in their order: 8 dimensions of one tile a CTA,
+// a thread per row.  As its own launch it has the whole GPU for what the last
+// CTA to arrive would read alone (up to 2 MB).
+template <int DIM, int BITS>
+__global__ void __launch_bounds__(kRowsTile) tree_join_kernel(const AttnArgs a) {
+    using C = TreeCfg<DIM, BITS>;
+    using Walk = AttnWalk<kRowsTile, kRowsTile, 2, kBlock>;
+    __shared__ typename Walk::Shared find;
+    griddep_launch_dependents();
+    griddep_wait();
+    Walk walk;
+    if (!walk.init(a, find, true)) return;
+    AttnTile t;
+    const int64_t c0 = blockIdx.x;
+    if (!walk.next(a, t, true) || walk.first_cta(t) != c0) return;
+    const int64_t c1 = walk.last_cta(t);
+    const int tl = blockIdx.y / (DIM / 8), c8 = blockIdx.y % (DIM / 8), r = threadIdx.x, rt = tl * kRowsTile + r;
+    if (c1 == c0 || rt >= t.rows) return;
+    auto piece = [&](int64_t c) { return a.parts + ((c * 2 + (c == c0 ? 1 : 0)) * 2 + tl) * C::kPiece; };
+    float top = -INFINITY;
+    #pragma unroll 4
+    for (int64_t c = c0; c <= c1; ++c) top = fmaxf(top, piece(c)[DIM * kRowsTile + r]);
+    float o[8] = {}, sum = 0.f;
+    #pragma unroll 2
+    for (int64_t c = c0; c <= c1; ++c) {
+        const float* p = piece(c);
+        const float m = p[DIM * kRowsTile + r];
+        const float f = m == -INFINITY ? 1.f : exp2_fast(m - top);  // nothing seen: zeros (or NaN)
+        sum = fmaf(p[(DIM + 1) * kRowsTile + r], f, sum);
+        #pragma unroll
+        for (int y = 0; y < 8; ++y) o[y] = fmaf(p[(8 * c8 + column_of<BITS>(y)) * kRowsTile + r], f, o[y]);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    #pragma unroll
+    for (int y = 0; y < 8; ++y) o[y] *= inv;
+    const int row = t.row0 + rt;
+    store8(a.out + ((int64_t)(t.s.first + row / a.group) * a.heads_q + t.h * a.group + row % a.group) * DIM + 8 * c8, o);
+}
+
+template <typename F>
+auto by_config(const kvq_cache_t& c, F f) {
+    auto bits = [&](auto dim) {
+        return c.bits == 8 ? f(dim, std::integral_constant<int, 8>()) : f(dim, std::integral_constant<int, 4>());
+    };
+    return c.dim == 64 ? bits(std::integral_constant<int, 64>()) : bits(std::integral_constant<int, 128>());
+}
+
+int tree_ctas(int sms) { return sms < kAttnMaxCtas ? sms : kAttnMaxCtas; }
+
+// Rows that share a cache head, on average, from which this kernel serves a call.
+constexpr int64_t kTreeMinRows = 17;
+
+bool tree_serves(const kvq_cache_t& c, const kvq_batch_t& b, int heads_q) {
+    return c.dim <= 128 && (b.tokens * (heads_q / c.heads) + b.seqs - 1) / b.seqs >= kTreeMinRows;
+}
+
+}  // namespace
+
+size_t kvq_attn_workspace(const kvq_cache_t& c, const kvq_batch_t& b, int heads_q, int sms) {
+    if (!tree_serves(c, b, heads_q)) return attn_rows_workspace(c, b, heads_q, sms);
+    return by_config(c, [&](auto dim, auto bits) -> size_t {
+        return kAttnTicketBytes +
+               (size_t)tree_ctas(sms) * 4 * TreeCfg<decltype(dim)::value, decltype(bits)::value>::kPiece * sizeof(float);
+    });
+}
+
+cudaError_t launch_kvq_attention(const kvq_cache_t& c, const kvq_batch_t& b, const uint16_t* Q, int heads_q,
+                                 const uint64_t* mask, float scale, uint16_t* out, void* ws, int sms, unsigned flags,
+                                 cudaStream_t stream) {
+    if (!tree_serves(c, b, heads_q)) return launch_attn_rows(c, b, Q, heads_q, mask, scale, out, ws, sms, flags, stream);
+    const AttnArgs a = {cache_arg(c), batch_arg(b), reinterpret_cast<const __half*>(Q), mask,
+                        reinterpret_cast<__half*>(out), heads_q, heads_q / c.heads, scale * 1.4426950408889634f,
+                        static_cast<unsigned*>(ws),
+                        reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kAttnTicketBytes)};
+    return by_config(c, [&](auto dim, auto bits) {
+        constexpr int D = decltype(dim)::value, B = decltype(bits)::value;
+        static std::atomic<uint64_t> ready{0};
+        cudaError_t e = layer_smem(tree_kernel<D, B>, TreeCfg<D, B>::kSmem, ready);
+        if (e != cudaSuccess) return e;
+        const unsigned ctas = (unsigned)tree_ctas(sms);
+        e = layer_launch(tree_kernel<D, B>, dim3(ctas), kTreeThreads, TreeCfg<D, B>::kSmem, flags, stream, a);
+        if (e != cudaSuccess) return e;
+        return layer_launch(tree_join_kernel<D, B>, dim3(ctas, 2 * D / 8), kRowsTile, 0, W4A8_LAUNCH_PDL, stream, a);
+    });
+}
+
+cudaError_t read_and_clear_attn_error(unsigned* flags, cudaStream_t stream) {
+    unsigned v = 0, z = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_attn_error, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
+    if (e != cudaSuccess) return e;
+    e = cudaMemcpyToSymbolAsync(g_attn_error, &z, sizeof(z), 0, cudaMemcpyHostToDevice, stream);
+    if (e != cudaSuccess) return e;
+    e = cudaStreamSynchronize(stream);
+    *flags |= v;
+    return e == cudaSuccess ? read_and_clear_attn_rows_error(flags, stream) : e;
+}
+
+}  // namespace w4a8

@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/w4a8.h"
@@ -69,6 +70,20 @@ inline KvqBatchArg batch_arg(const kvq_batch_t& b) {
 __device__ __forceinline__ int64_t kvq_vec(const KvqCacheArg& c, int64_t row, int h) {
     const int64_t page = row >> c.shift;
     return ((page * c.heads + h) << c.shift) + (row & ((1 << c.shift) - 1));
+}
+
+// Raises a kernel's dynamic shared-memory limit, once per device (`ready`: the
+// kernel's own word of devices done; past 64 of them every time).
+template <typename F>
+inline cudaError_t layer_smem(F* f, int bytes, std::atomic<uint64_t>& ready) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 // One launch, with programmatic dependent launch when the flag asks for it.
