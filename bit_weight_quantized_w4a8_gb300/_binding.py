@@ -790,16 +790,18 @@ def kvq_attention_workspace_bytes(cache, batch, tokens: int, heads_q: int) -> in
 
 
 _attn_ws = {}
+_TICKET_BYTES = 4096  # arrival counters at a workspace's start (w4a8_workspace_bytes)
 
 
 def _stream_workspace(device, stream: int, nbytes: int = 0):
-    """The zero-filled workspace of a stream, made anew when `nbytes` asks for
-    more; under graph capture one of the graph's own, so that replays share
-    nothing with eager calls."""
+    """A stream's workspace (its arrival counters zeroed), made anew when
+    `nbytes` asks for more; under graph capture one of the graph's own, so that
+    replays share nothing with eager calls."""
     capturing = torch.cuda.is_current_stream_capturing()
     if nbytes == 0:
         return None if capturing else _attn_ws.get((device, stream))
-    buf = torch.zeros(nbytes if capturing else max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+    buf = torch.empty(nbytes if capturing else max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+    buf[:_TICKET_BYTES].zero_()
     if not capturing:
         _attn_ws[(device, stream)] = buf
     return buf

@@ -5,9 +5,9 @@
 // With hundreds of rows on each key the work is the two products, which only
 // tcgen05 runs at full rate, so the codes are widened to binary16 once
 // per CTA, in shared memory, for up to 256 rows:
-//   warps 8-11 load the codes of 128 keys and values, widen them and store them
+//   warps 16-19 load the codes of 128 keys and values, widen them and store them
 //     in the tensor core's 128-byte swizzled layout (two stages each);
-//   warps 0-3 and 4-7 are two slots of softmax: S is read from TMEM, the
+//   warps 0-7 and 8-15 are two slots of softmax: S is read from TMEM, the
 //     weights go back over it as binary16;
 //   the first warp of a slot issues its products: S = Q K^T into TMEM (128 rows x
 //     128 keys), and O += W V with the weights W as the TMEM operand and V with its
@@ -31,9 +31,10 @@
 namespace w4a8 {
 namespace {
 
-constexpr int kSoftWarps = 8, kLoadWarps = 4;
-// 12 warps: three to a scheduler, 168 registers a thread (softmax holds a row's
-// 128 weights and two batches of logits); a 13th would cost all of them 40
+// Two slots of eight softmax warps and four that load: five warps to a scheduler.
+// Everything here waits for something (loads, TMEM, barriers), and with half
+// the softmax warps, each with twice the keys, a block took half as long again.
+constexpr int kSlotWarps = 8, kSoftWarps = 2 * kSlotWarps, kLoadWarps = 4;
 constexpr int kTreeThreads = (kSoftWarps + kLoadWarps) * 32;
 constexpr int kRowsTile = 128;   // rows of a tile, TMEM lanes
 constexpr int kBlock = 128;      // keys of a unit
@@ -42,18 +43,27 @@ constexpr float kTop = 10.f;     // log2 of the weight of a fresh maximum
 constexpr float kSlack = 4.f;    // log2 of what it may grow by before O is rescaled
 
 struct alignas(16) BlockScales {  // read as 16-byte vectors
-    float k[kBlock];        // ks * scale * log2(e)
-    float v[kBlock];
+    float k[kBlock];        // ks * scale * log2(e), never 0
+    float v[kBlock];        // vs, 0 where one of the two is not finite
     uint32_t valid[4];      // bit i of word w: key 32 w + i is there
+    uint32_t bad[4];        // it has a scale that is not finite
 };
 
 struct TreeShared {
-    uint64_t kfull[2], kfree[2], vfull[2], vfree[2], sfull[2], pready[2], pvdone[2], scfull[kScaleRing], drain[2];
+    uint64_t kfull[2], vfull[2];   // [stage]: a block's keys, values are in place
+    uint64_t scfull[kScaleRing];   // [block % 4]: its scales are
+    uint64_t sfull[2];             // [slot]: S of a job is there, and the product before it done
+    uint64_t kfree[2], vfree[2];   // [stage]: both slots' products have used them
+    uint64_t drain[2];
     BlockScales sc[kScaleRing];
     AttnWalk<kTreeThreads, kRowsTile, 2, kBlock>::Shared find;
     AttnWalk<kTreeThreads, kRowsTile, 2, kBlock> walk;  // thread 0's
     AttnTile tile;                                      // and where it is
-    float stat[2][2][kRowsTile];  // [reference, sum][slot][row]
+    float ref[2][kRowsTile];      // [slot][row]: reference
+    float sum[2][2][kRowsTile];   // [slot][half of the keys][row]
+    float top[2][2][kRowsTile];   // a block's maxima, exchanged when a reference is raised
+    uint64_t word[2][kRowsTile];  // [tile][row]: what its token sees of the drafted ones
+    int tok[2][kRowsTile];        // and its place among them
     int more;
     uint32_t tmem;
     volatile int abort;
@@ -174,10 +184,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
             mbar_init(smem_u32(&sh.vfull[i]), kLoadWarps);
             mbar_init(smem_u32(&sh.kfree[i]), 2);
             mbar_init(smem_u32(&sh.vfree[i]), 2);
-            mbar_init(smem_u32(&sh.drain[i]), 1);
             mbar_init(smem_u32(&sh.sfull[i]), 1);
-            mbar_init(smem_u32(&sh.pready[i]), 4);
-            mbar_init(smem_u32(&sh.pvdone[i]), 1);
+            mbar_init(smem_u32(&sh.drain[i]), 1);
         }
         for (int i = 0; i < kScaleRing; ++i) mbar_init(smem_u32(&sh.scfull[i]), kLoadWarps);
         fence_mbar_init();
@@ -192,7 +200,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
     const bool leader = elect_one();
 
     int blocks_done = 0;             // key blocks of earlier tiles: stage and phase go on
-    int jobs_done[2] = {0, 0};       // S tiles of earlier row blocks, per slot
+    int s_phase[2] = {0, 0};         // phases of sfull in earlier row blocks
     for (;;) {
         if (tid == 0) sh.more = sh.walk.next(a, sh.tile);
         __syncthreads();
@@ -200,18 +208,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
         const AttnTile& t = sh.tile;  // the roles take what they need of it into registers
         const int nb = t.u1 - t.u0;
         const bool two = t.tiles == 2;
-        // the queries of the block's rows, widened keys' order of dimensions
+        // the queries of the block's rows, in the widened keys' order of dimensions, and
+        // what the rows see of the drafted tokens
+        #pragma unroll 4
         for (int e = tid; e < t.tiles * kRowsTile * (DIM / 8); e += kTreeThreads) {
             const int r = e / (DIM / 8), c = e % (DIM / 8);
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
             if (r < t.rows) {
-                const int row = t.row0 + r, tok = t.s.first + row / a.group;
-                x = *reinterpret_cast<const uint4*>(a.Q + ((int64_t)tok * a.heads_q + t.h * a.group + row % a.group) * DIM + 8 * c);
+                const int row = t.row0 + r, tok = row / a.group;
+                x = *reinterpret_cast<const uint4*>(a.Q + ((int64_t)(t.s.first + tok) * a.heads_q + t.h * a.group + row - tok * a.group) * DIM + 8 * c);
             }
             if constexpr (BITS == 4)
                 x = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
                                __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
             sts16(base + C::kOffQ + (r / kRowsTile) * C::kTileBytes + tile_off(r % kRowsTile, c), x.x, x.y, x.z, x.w);
+        }
+        if (tid < t.tiles * kRowsTile) {
+            const int tok = (t.row0 + min(tid, t.rows - 1)) / a.group;
+            sh.tok[tid / kRowsTile][tid % kRowsTile] = tok;
+            sh.word[tid / kRowsTile][tid % kRowsTile] = a.mask != nullptr ? a.mask[t.s.first + tok] : 0;
         }
         fence_async_shared();
         __syncthreads();
@@ -244,7 +259,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                 for (int i = 0; i < CPR; ++i) {
                     const int r = row_of(i);
                     const int64_t v = (r < 16 ? row_a : row_b - 16) + r;
-                    x[i] = (there >> r) & 1 ? ld_global_nc_v4(codes + v * C::W + 16 * chunk_of(i)) : make_uint4(0u, 0u, 0u, 0u);
+                    x[i] = ld_global_nc_v4_if(codes + v * C::W + 16 * chunk_of(i), (there >> r) & 1);
                 }
             };
             auto load_k = [&](int u, int page) {
@@ -289,9 +304,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                 if (blk >= 2 && !__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.kfree[st]), ((blk >> 1) - 1) & 1, &sh.abort))) break;
                 store(base + C::kOffK + st * C::kTileBytes, xk);
                 BlockScales& bs = sh.sc[blk % kScaleRing];
-                bs.k[32 * lw + lane] = sk * a.scale_log2;
-                bs.v[32 * lw + lane] = sv;
-                if (lane == 0) bs.valid[lw] = there;
+                {
+                    // a factor of 0 would make NaN of an unseen key's -inf; a key of zeros
+                    // has logit 0 with any
+                    const float kk = sk * a.scale_log2;
+                    const bool fine = fabsf(kk) < INFINITY && fabsf(sv) < INFINITY;
+                    bs.k[32 * lw + lane] = fine && kk != 0.f ? kk : 1e-30f;
+                    bs.v[32 * lw + lane] = fine ? sv : 0.f;
+                    const unsigned bad = __ballot_sync(0xFFFFFFFFu, !fine);
+                    if (lane == 0) {
+                        bs.valid[lw] = there;
+                        bs.bad[lw] = bad;
+                    }
+                }
                 fence_async_shared();
                 __syncwarp();
                 if (lane == 0) {
@@ -308,286 +333,325 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                 if (j + 1 < nb) load(a.c.v, xv);
             }
         } else {
-            // softmax: this thread's row of its slot
-            const int slot = warp >> 2, quad = warp & 3;
-            // S, W and O are held in fragments: rows 8 k + lane / 4 of the warp's 32 (k < 4),
-            // columns 2 (lane % 4), + 1 of every 8.  A thread so needs the scales of a
-            // quarter of the keys: read for whole rows they took half of the
-            // shared-memory bandwidth that the products of Q and K leave nothing of.
+            // Softmax.  A slot's eight warps are its tile's four quarters of rows times
+            // two halves of a block's keys.  S, W and O are held in fragments: rows 8 k +
+            // lane / 4 of the warp's 32 (k < 4), columns 2 (lane % 4), + 1 of every 8.  A
+            // thread so needs the scales of a quarter of its keys: read for whole rows
+            // they took half of the shared-memory bandwidth, of which the product of Q
+            // and K leaves nothing (LDS 34 cycles instead of 4).
+            const int slot = warp / kSlotWarps, half = (warp >> 2) & 1, quad = warp & 3;
+            const bool first = warp % kSlotWarps == 0;            // issues the slot's products
+            const int tl = two ? slot : 0;
             const int tile_rows = two ? min(kRowsTile, t.rows - slot * kRowsTile) : t.rows;
             const int u0 = t.u0, start = t.s.start;
             const bool idle = 32 * quad >= tile_rows;             // the whole warp has no row
-            const int row_base = t.row0 + (two ? slot * kRowsTile : 0);
             const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-            const uint32_t ts = lanes + C::kS + 128 * slot, to = lanes + C::kO + DIM * slot;
+            const uint32_t ts = lanes + C::kS + 128 * slot + 64 * half;  // S of its keys; W goes over its first half
+            const uint32_t to = lanes + C::kO + DIM * slot + (DIM / 2) * half;
             constexpr uint32_t kHalfLanes = 16u << 16;
             float M[4], l[4];
             #pragma unroll
             for (int k = 0; k < 4; ++k) M[k] = -INFINITY, l[k] = 0.f;
             const int my_jobs = two ? nb : (nb + 1 - slot) / 2;
-            const int u_q = __shfl_sync(0xFFFFFFFFu, two ? slot : 0, 0);
+            const int u_q = __shfl_sync(0xFFFFFFFFu, tl, 0);
             auto block_of = [&](int i) -> int { return blocks_done + (two ? i : 2 * i + slot); };
-            // products of job i, issued by the slot's first warp (all of it in step, so
-            // that descriptors live in uniform registers; one lane issues)
-            auto qk = [&](int i) -> bool {
-                const int blk = block_of(i), st = blk & 1;
-                if (!__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.kfull[st]), (blk >> 1) & 1, &sh.abort))) return false;
-                tc_fence_after_sync();
-                const int u_st = __shfl_sync(0xFFFFFFFFu, st, 0);
+            // products, issued by the slot's first warp (all of it in step, so that
+            // descriptors live in uniform registers; one lane issues)
+            auto qk = [&](int i) {
+                const int st = __shfl_sync(0xFFFFFFFFu, block_of(i) & 1, 0);
                 const uint64_t qd = sw128_desc(u_base + C::kOffQ) + u_q * (C::kTileBytes >> 4);
-                const uint64_t kd = sw128_desc(u_base + C::kOffK) + u_st * (C::kTileBytes >> 4);
+                const uint64_t kd = sw128_desc(u_base + C::kOffK) + st * (C::kTileBytes >> 4);
                 if (leader) {
                     #pragma unroll
                     for (int k = 0; k < KSTEPS; ++k) {
                         const uint64_t off = ((k >> 2) * C::kHalf + (k & 3) * 32) >> 4;
                         tc_mma_f16(u_tmem + C::kS + 128 * slot, qd + off, kd + off, f16_idesc(kRowsTile, kBlock), k > 0);
                     }
-                    tc_commit(smem_u32(&sh.sfull[slot]));
-                    tc_commit(smem_u32(&sh.kfree[st]));
-                    if (!two) tc_commit(smem_u32(&sh.kfree[st]));  // the one user arrives for both
                 }
-                __syncwarp();
-                return true;
             };
-            auto pv = [&](int i) -> bool {
-                const int blk = block_of(i), st = blk & 1, q = jobs_done[slot] + i;
-                if (!__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.pready[slot]), q & 1, &sh.abort) &&
-                                                 wait_bounded(smem_u32(&sh.vfull[st]), (blk >> 1) & 1, &sh.abort))) return false;
-                tc_fence_after_sync();
-                const int u_st = __shfl_sync(0xFFFFFFFFu, st, 0);
-                const uint64_t vd = sw128_desc_mn(u_base + C::kOffV, C::kHalf) + u_st * (C::kTileBytes >> 4);
+            auto pv = [&](int i) {
+                const int st = __shfl_sync(0xFFFFFFFFu, block_of(i) & 1, 0);
+                const uint64_t vd = sw128_desc_mn(u_base + C::kOffV, C::kHalf) + st * (C::kTileBytes >> 4);
                 if (leader) {
                     #pragma unroll
                     for (int k = 0; k < kBlock / 16; ++k)
-                        tc_mma_f16_tmem_a(u_tmem + C::kO + DIM * slot, u_tmem + C::kS + 128 * slot + 8 * k,
+                        tc_mma_f16_tmem_a(u_tmem + C::kO + DIM * slot, u_tmem + C::kS + 128 * slot + 64 * (k >> 2) + 8 * (k & 3),
                                           vd + k * (2048 >> 4), f16_idesc(kRowsTile, DIM) | kIdescTransposeB, i > 0 || k > 0);
-                    tc_commit(smem_u32(&sh.vfree[st]));
-                    if (!two) tc_commit(smem_u32(&sh.vfree[st]));
-                    tc_commit(smem_u32(&sh.pvdone[slot]));
                 }
-                __syncwarp();
-                return true;
             };
-            bool ok = quad != 0 || my_jobs == 0 || qk(0);
-            for (int i = 0; ok && i < my_jobs; ++i) {
-                const int u = u0 + (two ? i : 2 * i + slot);
-                const int blk = block_of(i), q = jobs_done[slot] + i;
-                ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.scfull[blk % kScaleRing]), (blk / kScaleRing) & 1, &sh.abort)) &&
-                     __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.sfull[slot]), q & 1, &sh.abort));
-                if (!ok) break;
-                if (!idle) {
+            // a stage is free when both slots have used it; of one tile, its one user
+            // arrives for both
+            auto release = [&](uint64_t* bars, int i) {
+                if (leader) {
+                    tc_commit(smem_u32(&bars[block_of(i) & 1]));
+                    if (!two) tc_commit(smem_u32(&bars[block_of(i) & 1]));
+                }
+            };
+            auto commit = [&]() {
+                if (leader) tc_commit(smem_u32(&sh.sfull[slot]));
+            };
+            auto wait = [&](uint64_t& bar, int phase) -> bool {
+                return __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bar), phase & 1, &sh.abort));
+            };
+            auto wait_keys = [&](int i) -> bool {
+                const int blk = block_of(i);
+                return wait(sh.kfull[blk & 1], blk >> 1);
+            };
+            // a wait that gave up (ok false) skips the work of what follows, but each
+            // warp still meets the slot's barrier once a job
+            bool ok = true;
+            if (first && my_jobs > 0) {
+                ok = wait_keys(0);
+                if (ok) {
                     tc_fence_after_sync();
-                    const BlockScales& bs = sh.sc[blk % kScaleRing];
-                    const int k0 = u * kBlock;
-                    // bound 2^ve of the block's finite value scales
-                    float ve;
-                    {
-                        const float4 v = reinterpret_cast<const float4*>(bs.v)[lane];
-                        const float top = fmaxf(fmaxf(fabsf(v.x) < INFINITY ? fabsf(v.x) : 0.f, fabsf(v.y) < INFINITY ? fabsf(v.y) : 0.f),
-                                                fmaxf(fabsf(v.z) < INFINITY ? fabsf(v.z) : 0.f, fabsf(v.w) < INFINITY ? fabsf(v.w) : 0.f));
-                        const unsigned bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
-                        ve = fmaxf((float)((int)(bits >> 23) - 126), -100.f);
-                    }
-                    const bool plain = k0 + kBlock <= start &&
-                                       (bs.valid[0] & bs.valid[1] & bs.valid[2] & bs.valid[3]) == 0xFFFFFFFFu;
-                    // what row k sees of keys 32 c .. 32 c + 31
-                    auto seen = [&](int k, int c) -> uint32_t {
-                        const int tok = (row_base + min(32 * quad + 8 * k + (lane >> 2), tile_rows - 1)) / a.group;
-                        const uint64_t word = a.mask != nullptr ? a.mask[t.s.first + tok] : 0;
-                        return bs.valid[c] & seen_bits(k0 + 32 * c - start, a.mask != nullptr, word, tok);
-                    };
-                    uint32_t p[2][32];  // weights: rows k = 2 hb (even places) and 2 hb + 1, pairs of keys
-                    float add[4], grow;
-                    auto weights = [&](auto masked) {  // p and its sums, against M
-                        constexpr bool MASKED = decltype(masked)::value;
-                        uint64_t sum[4] = {0, 0, 0, 0}, nm[4];
-                        grow = -INFINITY;
-                        #pragma unroll
-                        for (int k = 0; k < 4; ++k) nm[k] = pack2(-M[k], -M[k]);
-                        uint32_t sb[2][16];
-                        tmem_ld_frag32(ts, sb[0]);
-                        #pragma unroll
-                        for (int e = 0; e < 8; ++e) {  // 32 columns c of rows 2 hb, 2 hb + 1
-                            const int c = e >> 1, hb = e & 1;
-                            uint32_t see[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-                            if constexpr (MASKED) see[0] = seen(2 * hb, c), see[1] = seen(2 * hb + 1, c);
-                            tmem_ld_wait();
-                            if (e < 7) tmem_ld_frag32(ts + 32 * ((e + 1) >> 1) + ((e + 1) & 1) * kHalfLanes, sb[(e + 1) & 1]);
-                            const uint32_t* s = sb[e & 1];
-                            #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const int key = 8 * j + 2 * (lane & 3);
-                                const uint64_t kf = *reinterpret_cast<const uint64_t*>(bs.k + 32 * c + key);
-                                const uint64_t vf = *reinterpret_cast<const uint64_t*>(bs.v + 32 * c + key);
-                                #pragma unroll
-                                for (int rr = 0; rr < 2; ++rr) {
-                                    const int k = 2 * hb + rr;
-                                    float2 d = unpack2(fma2(pack2(__uint_as_float(s[4 * j + 2 * rr]), __uint_as_float(s[4 * j + 2 * rr + 1])), kf, nm[k]));
-                                    if constexpr (MASKED) {
-                                        if (!((see[rr] >> key) & 1)) d.x = -INFINITY;
-                                        if (!((see[rr] >> (key + 1)) & 1)) d.y = -INFINITY;
-                                    }
-                                    grow = fmaxf(grow, fmaxf(d.x, d.y));
-                                    const uint64_t x = pack2(exp2_fast(d.x), exp2_fast(d.y));
-                                    sum[k] = add2(sum[k], x);
-                                    float2 w = unpack2(mul2(x, vf));
-                                    if constexpr (MASKED) {  // an unseen key's scale may be anything
-                                        if (!((see[rr] >> key) & 1)) w.x = 0.f;
-                                        if (!((see[rr] >> (key + 1)) & 1)) w.y = 0.f;
-                                    }
-                                    p[hb][2 * (4 * c + j) + rr] = pack_half2(w.x, w.y);
-                                }
-                            }
-                        }
-                        #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 f = unpack2(sum[k]);
-                            add[k] = f.x + f.y;
-                        }
-                    };
-                    for (int pass = 0;; ++pass) {
-                        if (plain) weights(std::false_type());
-                        else weights(std::true_type());
-                        if (pass == 1 || !__any_sync(0xFFFFFFFFu, grow + ve > kTop + kSlack)) break;
-                        // raise the references that are too low: the rows' maxima
-                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, f[4];
+                    qk(0);
+                    commit();
+                    release(sh.kfree, 0);
+                    __syncwarp();
+                }
+            }
+            for (int i = 0; i < my_jobs; ++i) {
+                const int u = u0 + (two ? i : 2 * i + slot);
+                const int blk = block_of(i);
+                const BlockScales& bs = sh.sc[blk % kScaleRing];
+                ok = ok && wait(sh.scfull[blk % kScaleRing], blk / kScaleRing);
+                const int k0 = u * kBlock;
+                float ve = 0.f;  // 2^ve bounds the block's value scales
+                bool plain = true;
+                if (ok && !idle) {
+                    const float4 v = reinterpret_cast<const float4*>(bs.v)[lane];
+                    const unsigned bits = __reduce_max_sync(
+                        0xFFFFFFFFu, __float_as_uint(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)))));
+                    ve = fmaxf((float)((int)(bits >> 23) - 126), -100.f);
+                    plain = k0 + kBlock <= start && (bs.valid[0] & bs.valid[1] & bs.valid[2] & bs.valid[3]) == 0xFFFFFFFFu &&
+                            (bs.bad[0] | bs.bad[1] | bs.bad[2] | bs.bad[3]) == 0u;
+                }
+                ok = ok && wait(sh.sfull[slot], s_phase[slot] + i);
+                const bool work = ok && !idle;
+                const float* kf = bs.k + 64 * half + 2 * (lane & 3);  // scales of this thread's keys, 8 apart
+                const float* vf = bs.v + 64 * half + 2 * (lane & 3);
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                bool up = false;
+                if (work) {
+                    tc_fence_after_sync();
+                    if (!plain) {
+                        // S of an unseen key becomes what its factor takes to -inf, S of a seen
+                        // key with a scale that is not finite NaN
                         #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
+                        for (int e = 0; e < 4; ++e) {
+                            const int c = e >> 1, hb = e & 1;
+                            uint32_t s[16];
+                            tmem_ld_frag32(ts + 32 * c + hb * kHalfLanes, s);
+                            uint32_t see[2];
                             #pragma unroll
-                            for (int hb = 0; hb < 2; ++hb) {
-                                uint32_t s[16];
-                                tmem_ld_frag32(ts + 32 * c + hb * kHalfLanes, s);
-                                uint32_t see[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-                                if (!plain) see[0] = seen(2 * hb, c), see[1] = seen(2 * hb + 1, c);
-                                tmem_ld_wait();
-                                #pragma unroll
-                                for (int x = 0; x < 16; ++x) {
-                                    const int key = 8 * (x >> 2) + 2 * (lane & 3) + (x & 1), rr = (x >> 1) & 1;
-                                    if ((see[rr] >> key) & 1)
-                                        top[2 * hb + rr] = fmaxf(top[2 * hb + rr], __uint_as_float(s[x]) * bs.k[32 * c + key]);
-                                }
+                            for (int rr = 0; rr < 2; ++rr) {
+                                const int r = 32 * quad + 16 * hb + 8 * rr + (lane >> 2);
+                                see[rr] = bs.valid[2 * half + c] & seen_bits(k0 + 64 * half + 32 * c - start, a.mask != nullptr, sh.word[tl][r], sh.tok[tl][r]);
+                            }
+                            const uint32_t bad = bs.bad[2 * half + c];
+                            tmem_ld_wait();
+                            #pragma unroll
+                            for (int x = 0; x < 16; ++x) {
+                                const int key = 8 * (x >> 2) + 2 * (lane & 3) + (x & 1);
+                                if (!((see[(x >> 1) & 1] >> key) & 1))
+                                    s[x] = __float_as_uint(copysignf(INFINITY, -bs.k[64 * half + 32 * c + key]));
+                                else if ((bad >> key) & 1)
+                                    s[x] = 0x7FFFFFFFu;
+                            }
+                            tmem_st_frag32(ts + 32 * c + hb * kHalfLanes, s);
+                        }
+                        tmem_st_wait();
+                    }
+                    // the maxima of this thread's keys, rows k
+                    #pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int c = e >> 1, hb = e & 1;
+                        uint32_t s[16];
+                        tmem_ld_frag32(ts + 32 * c + hb * kHalfLanes, s);
+                        tmem_ld_wait();
+                        #pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint64_t kk = *reinterpret_cast<const uint64_t*>(kf + 32 * c + 8 * j);
+                            #pragma unroll
+                            for (int rr = 0; rr < 2; ++rr) {
+                                const float2 d = unpack2(mul2(pack2(__uint_as_float(s[4 * j + 2 * rr]), __uint_as_float(s[4 * j + 2 * rr + 1])), kk));
+                                top[2 * hb + rr] = fmaxf(top[2 * hb + rr], fmaxf(d.x, d.y));
                             }
                         }
+                    }
+                    #pragma unroll
+                    for (int k = 0; k < 4; ++k) up |= top[k] - M[k] + ve > kTop + kSlack;
+                }
+                // raise the references that are too low: both halves of the keys alike
+                if (named_bar_or(1 + slot, kSlotWarps * 32, up)) {
+                    #pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        top[k] = fmaxf(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], 1));
+                        top[k] = fmaxf(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], 2));
+                        if ((lane & 3) == 0) sh.top[slot][half][32 * quad + 8 * k + (lane >> 2)] = top[k];
+                    }
+                    named_bar_sync(1 + slot, kSlotWarps * 32);
+                    if (work) {
+                        float f[4];
                         #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            top[k] = fmaxf(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], 1));
-                            top[k] = fmaxf(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], 2));
-                            const bool up = top[k] - M[k] + ve > kTop + kSlack;
-                            const float Mn = up ? top[k] + ve - kTop : M[k];
-                            f[k] = !up ? 1.f : M[k] == -INFINITY ? 0.f : exp2_fast(M[k] - Mn);
+                            const float m = fmaxf(top[k], sh.top[slot][half ^ 1][32 * quad + 8 * k + (lane >> 2)]);
+                            const bool raise = m - M[k] + ve > kTop + kSlack;
+                            const float Mn = raise ? m + ve - kTop : M[k];
+                            f[k] = !raise ? 1.f : M[k] == -INFINITY ? 0.f : exp2_fast(M[k] - Mn);
                             M[k] = Mn;
                             l[k] *= f[k];
                         }
-                        if (i > 0) {
-                            ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.pvdone[slot]), (q - 1) & 1, &sh.abort));
-                            if (!ok) break;
-                            tc_fence_after_sync();
+                        if (i > 0) {  // O is settled: this S was issued after the last product into it
                             #pragma unroll 1
-                            for (int c = 0; c < DIM / 32; ++c) {
+                            for (int e = 0; e < DIM / 32; ++e) {
+                                const uint32_t at = to + 32 * (e >> 1) + (e & 1) * kHalfLanes;
+                                const float f0 = e & 1 ? f[2] : f[0], f1 = e & 1 ? f[3] : f[1];
+                                uint32_t o[16];
+                                tmem_ld_frag32(at, o);
+                                tmem_ld_wait();
                                 #pragma unroll
-                                for (int hb = 0; hb < 2; ++hb) {
-                                    uint32_t o[16];
-                                    tmem_ld_frag32(to + 32 * c + hb * kHalfLanes, o);
-                                    tmem_ld_wait();
-                                    #pragma unroll
-                                    for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f[2 * hb + ((x >> 1) & 1)]);
-                                    tmem_st_frag32(to + 32 * c + hb * kHalfLanes, o);
-                                }
+                                for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * (x & 2 ? f1 : f0));
+                                tmem_st_frag32(at, o);
                             }
                             tmem_st_wait();
                         }
                     }
-                    if (!ok) break;
+                }
+                if (work) {
+                    // weights: sums in fp32, W rounded to binary16 over S
+                    uint64_t sum[4] = {0, 0, 0, 0}, nm[4];
                     #pragma unroll
-                    for (int k = 0; k < 4; ++k) l[k] += add[k];
-                    tmem_st_pairs64(ts, p[0]);
-                    tmem_st_pairs64(ts + kHalfLanes, p[1]);
+                    for (int k = 0; k < 4; ++k) {
+                        const float x = M[k] == -INFINITY ? 0.f : -M[k];  // nothing seen yet: S is -inf throughout
+                        nm[k] = pack2(x, x);
+                    }
+                    #pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int c = e >> 1, hb = e & 1;
+                        uint32_t s[16], w[8];
+                        tmem_ld_frag32(ts + 32 * c + hb * kHalfLanes, s);
+                        tmem_ld_wait();
+                        #pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint64_t kk = *reinterpret_cast<const uint64_t*>(kf + 32 * c + 8 * j);
+                            const uint64_t vv = *reinterpret_cast<const uint64_t*>(vf + 32 * c + 8 * j);
+                            #pragma unroll
+                            for (int rr = 0; rr < 2; ++rr) {
+                                const int k = 2 * hb + rr;
+                                const float2 d = unpack2(fma2(pack2(__uint_as_float(s[4 * j + 2 * rr]), __uint_as_float(s[4 * j + 2 * rr + 1])), kk, nm[k]));
+                                const uint64_t x = pack2(exp2_fast(d.x), exp2_fast(d.y));
+                                sum[k] = add2(sum[k], x);
+                                const float2 y = unpack2(mul2(x, vv));
+                                w[2 * j + rr] = pack_half2(y.x, y.y);
+                            }
+                        }
+                        tmem_st_pairs16(ts + 16 * c + hb * kHalfLanes, w);
+                    }
+                    #pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 f = unpack2(sum[k]);
+                        l[k] += f.x + f.y;
+                    }
                     tmem_st_wait();
                     tc_fence_before_sync();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.pready[slot]));
-                if (quad == 0) ok = pv(i) && (i + 1 >= my_jobs || qk(i + 1));
+                if (first) {
+                    named_bar_sync(1 + slot, kSlotWarps * 32);
+                    ok = ok && wait(sh.vfull[blk & 1], blk >> 1);
+                    if (ok) {
+                        tc_fence_after_sync();
+                        pv(i);
+                        release(sh.vfree, i);
+                        if (i + 1 < my_jobs && (ok = wait_keys(i + 1))) {
+                            tc_fence_after_sync();
+                            qk(i + 1);
+                            release(sh.kfree, i + 1);
+                        }
+                        commit();
+                        __syncwarp();
+                    }
+                } else {
+                    named_bar_arrive(1 + slot, kSlotWarps * 32);
+                }
             }
             // settled: the slot's last product, and what its rows' sums are relative to
-            if (ok && !idle && my_jobs > 0)
-                ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.pvdone[slot]), (jobs_done[slot] + my_jobs - 1) & 1, &sh.abort));
+            if (my_jobs > 0) ok = ok && wait(sh.sfull[slot], s_phase[slot] + my_jobs);
             #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 l[k] += __shfl_xor_sync(0xFFFFFFFFu, l[k], 1);
                 l[k] += __shfl_xor_sync(0xFFFFFFFFu, l[k], 2);
                 if ((lane & 3) == 0) {
-                    sh.stat[0][slot][32 * quad + 8 * k + (lane >> 2)] = M[k];
-                    sh.stat[1][slot][32 * quad + 8 * k + (lane >> 2)] = l[k];
+                    sh.ref[slot][32 * quad + 8 * k + (lane >> 2)] = M[k];
+                    sh.sum[slot][half][32 * quad + 8 * k + (lane >> 2)] = l[k];
                 }
             }
         }
         blocks_done += nb;
-        jobs_done[0] += two ? nb : (nb + 1) / 2;
-        jobs_done[1] += two ? nb : nb / 2;
+        for (int i = 0; i < 2; ++i) {
+            const int n = two ? nb : (nb + 1 - i) / 2;
+            s_phase[i] += n > 0 ? n + 1 : 0;  // the first S, and one after each job
+        }
 
         tc_fence_before_sync();
         __syncthreads();  // roles done: operands, TMEM and statistics are settled
         tc_fence_after_sync();
         if (sh.abort) break;
         // the tile's sums go out, normalized, or to this CTA's piece: a thread per
-        // row (TMEM lane); of one tile's two slots each takes half of the
-        // dimensions of both
+        // row (TMEM lane); the warps that hold a row share its dimensions (of one
+        // tile's two slots each has a part of both)
         if (warp < kSoftWarps) {
-            const int slot = warp >> 2, r = 32 * (warp & 3) + lane;
+            const int slot = warp / kSlotWarps, half = (warp >> 2) & 1, r = 32 * (warp & 3) + lane;
             const int tile_rows = two ? min(kRowsTile, t.rows - slot * kRowsTile) : t.rows;
             if (32 * (warp & 3) < tile_rows) {
                 const int tl = two ? slot : 0;
                 const bool whole = t.u0 == 0 && t.u1 == t.units;
-                float m, sum, f0 = 1.f, f1 = 0.f;
-                if (two) {
-                    m = sh.stat[0][slot][r];
-                    sum = sh.stat[1][slot][r];
-                } else {
-                    const float m0 = sh.stat[0][0][r], m1 = sh.stat[0][1][r];
+                float m = sh.ref[tl][r], sum = sh.sum[tl][0][r] + sh.sum[tl][1][r], f0 = 1.f, f1 = 0.f;
+                if (!two) {
+                    const float m0 = m, m1 = sh.ref[1][r], l1 = sh.sum[1][0][r] + sh.sum[1][1][r];
                     m = fmaxf(m0, m1);
                     f0 = m0 == -INFINITY ? 0.f : exp2_fast(m0 - m);  // a slot of which nothing is seen: its sums are 0 or not written
                     f1 = m1 == -INFINITY ? 0.f : exp2_fast(m1 - m);
-                    sum = sh.stat[1][0][r] * (m0 == -INFINITY ? 1.f : f0) + sh.stat[1][1][r] * (m1 == -INFINITY ? 1.f : f1);
+                    sum = sum * (m0 == -INFINITY ? 1.f : f0) + l1 * (m1 == -INFINITY ? 1.f : f1);
                 }
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 const int row = t.row0 + tl * kRowsTile + min(r, tile_rows - 1);
                 __half* out = a.out + ((int64_t)(t.s.first + row / a.group) * a.heads_q + t.h * a.group + row % a.group) * DIM;
                 float* piece = a.parts + (((int64_t)blockIdx.x * 2 + (t.u0 == 0 ? 1 : 0)) * 2 + tl) * C::kPiece;
                 const uint32_t to = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + C::kO;
-                const int c0 = two ? 0 : slot * (DIM / 64), c1 = two ? DIM / 32 : c0 + DIM / 64;
+                const int share = two ? DIM / 32 : DIM / 64;  // columns, by 16
+                const int c0 = (two ? half : 2 * slot + half) * share;
                 #pragma unroll 1
-                for (int c = c0; c < c1; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32(to + (two ? DIM * slot : 0) + 32 * c, o);
-                    tmem_ld_wait();
-                    if (!two) {
-                        uint32_t x[32];
-                        if (nb > 1) {
-                            tmem_ld32(to + DIM + 32 * c, x);
-                            tmem_ld_wait();
-                        }
+                for (int c = c0; c < c0 + share; ++c) {
+                    uint32_t o[16];
+                    tmem_ld16(to + (two ? DIM * slot : 0) + 16 * c, o);
+                    if (!two && nb > 1) {
+                        uint32_t x[16];
+                        tmem_ld16(to + DIM + 16 * c, x);
+                        tmem_ld_wait();
                         #pragma unroll
-                        for (int y = 0; y < 32; ++y) {
-                            float z = __uint_as_float(o[y]) * f0;
-                            if (nb > 1) z = fmaf(__uint_as_float(x[y]), f1, z);
-                            o[y] = __float_as_uint(z);
-                        }
+                        for (int y = 0; y < 16; ++y)
+                            o[y] = __float_as_uint(fmaf(__uint_as_float(x[y]), f1, __uint_as_float(o[y]) * f0));
+                    } else {
+                        tmem_ld_wait();
+                        #pragma unroll
+                        for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f0);
                     }
                     if (whole) {
                         #pragma unroll
-                        for (int x = 0; x < 32; x += 8) {
+                        for (int x = 0; x < 16; x += 8) {
                             float f[8];
                             #pragma unroll
                             for (int y = 0; y < 8; ++y) f[y] = __uint_as_float(o[x + column_of<BITS>(y)]) * inv;
-                            if (r < tile_rows) store8(out + 32 * c + x, f);
+                            if (r < tile_rows) store8(out + 16 * c + x, f);
                         }
                     } else {
                         #pragma unroll
-                        for (int x = 0; x < 32; ++x) piece[(32 * c + x) * kRowsTile + r] = __uint_as_float(o[x]);
+                        for (int x = 0; x < 16; ++x) piece[(16 * c + x) * kRowsTile + r] = __uint_as_float(o[x]);
                     }
                 }
-                if (!whole && (two || slot == 0)) {
+                if (!whole && half == 0 && (two || slot == 0)) {
                     piece[DIM * kRowsTile + r] = m;
                     piece[(DIM + 1) * kRowsTile + r] = sum;
                 }
@@ -598,10 +662,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
         tc_fence_after_sync();
     }
     // the tensor core is idle before its memory is given back
-    if (warp == 0 || warp == 4) {
+    if (warp == 0 || warp == kSlotWarps) {
         if (leader) {
-            tc_commit(smem_u32(&sh.drain[warp >> 2]));
-            if (!mbar_wait(smem_u32(&sh.drain[warp >> 2]), 0)) atomicOr(&g_attn_error, kErrDrainWait);
+            tc_commit(smem_u32(&sh.drain[warp / kSlotWarps]));
+            if (!mbar_wait(smem_u32(&sh.drain[warp / kSlotWarps]), 0)) atomicOr(&g_attn_error, kErrDrainWait);
         }
         __syncwarp();
     }
