@@ -27,15 +27,6 @@ constexpr int kWarps = 4;
 constexpr int kStep = 32;                 // keys of a warp's step
 constexpr int kUnit = kStep * kWarps;     // keys of a CTA's unit of work
 
-__device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 template <int N>
 __device__ __forceinline__ void lds(uint32_t* v, uint32_t addr) {
     if constexpr (N == 4)

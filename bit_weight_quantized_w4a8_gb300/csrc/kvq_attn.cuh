@@ -3,11 +3,12 @@
 //
 // The rows of a (sequence, cache head), tokens x group of them, are taken in
 // tiles of R rows and row blocks of up to P tiles; a row block walks the
-// sequence's keys in units.  A unit of a block of p tiles counts p.  The batch's
-// units, ordered by sequence, head, row block and key, are cut into one run per
-// CTA on the device, from the lengths found there: long and short
-// sequences fill the GPU alike, a captured graph follows its lengths, and
-// which CTA does what depends on nothing else.
+// sequence's keys in units, each of which counts what it costs (for P = 2: 4 with
+// two tiles, 3 with one, as measured: the keys cost the same, the rows less).
+// The batch's work, ordered by sequence, head, row block and key, is cut into
+// one run per CTA on the device, from the lengths found there: long and
+// short sequences fill the GPU alike, a captured graph follows its lengths,
+// and which CTA does what depends on nothing else.
 #pragma once
 
 #include "layer.cuh"
@@ -78,14 +79,17 @@ struct AttnWalk {
     struct Shared {
         int64_t units[THREADS / 32], find[2];
     };
+    static constexpr int kCost1 = P == 1 ? 1 : 3, kCostP = P == 1 ? 1 : 4;  // of a unit
+    static_assert(P <= 2, "a row block has one tile or P");
     struct Work {
-        int64_t tiles, units;
+        int64_t tiles, units, per_head;
     };
     static __device__ __forceinline__ Work work(const AttnArgs& a, const KvqSeq& s) {
         Work w;
         w.tiles = ((int64_t)s.count * a.group + R - 1) / R;
         const int e = keys(a, s);
         w.units = e > 0 ? (e + UNIT - 1) / UNIT : 1;  // one at least: it writes the zeros
+        w.per_head = w.units * (w.tiles / P * kCostP + (w.tiles % P ? kCost1 : 0));
         return w;
     }
     static __device__ __forceinline__ bool too_wide(const AttnArgs& a, const KvqSeq& s) {
@@ -107,7 +111,7 @@ struct AttnWalk {
             const KvqSeq s = seq(a, i);
             if (!s.ok || too_wide(a, s)) atomicOr(&g_attn_error, kErrCacheRange);
             const Work w = work(a, s);
-            total += w.units * w.tiles * a.c.heads;
+            total += w.per_head * a.c.heads;
         }
         #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
@@ -115,9 +119,9 @@ struct AttnWalk {
         __syncthreads();
         total = 0;
         for (int w = 0; w < THREADS / 32; ++w) total += sh.units[w];
-        // no less than a unit of P tiles, so that every CTA from the first to the
+        // no less than a unit, so that every CTA from the first to the
         // last with a part of a row block has one
-        per = max((int64_t)P, (total + gridDim.x - 1) / gridDim.x);
+        per = max((int64_t)kCostP, (total + gridDim.x - 1) / gridDim.x);
         at = per * blockIdx.x;
         end = min(at + per, total);
         if (at >= end) return false;
@@ -128,7 +132,7 @@ struct AttnWalk {
                 int64_t n = 0;
                 if (b0 + lane < a.b.seqs) {
                     const Work w = work(a, seq(a, b0 + lane));
-                    n = w.units * w.tiles * a.c.heads;
+                    n = w.per_head * a.c.heads;
                 }
                 int64_t sum = n;
                 #pragma unroll
@@ -159,7 +163,7 @@ struct AttnWalk {
         while (at < end) {
             t.s = seq(a, b);
             const Work w = work(a, t.s);
-            const int64_t per_head = w.units * w.tiles;
+            const int64_t per_head = w.per_head;
             if (at >= seq_first + per_head * a.c.heads) {
                 seq_first += per_head * a.c.heads;
                 ++b;
@@ -168,16 +172,17 @@ struct AttnWalk {
             t.b = b;
             t.h = (int)((at - seq_first) / per_head);
             const int64_t in_head = at - seq_first - t.h * per_head;
-            const int64_t rb = in_head / (P * w.units);
+            const int64_t rb = in_head / (kCostP * w.units);
             t.tiles = (int)min((int64_t)P, w.tiles - rb * P);
-            t.first = seq_first + t.h * per_head + rb * P * w.units;
+            t.first = seq_first + t.h * per_head + rb * kCostP * w.units;
+            const int cost = t.tiles == P ? kCostP : kCost1;
             t.row0 = (int)(rb * P * R);
             t.rows = (int)min((int64_t)P * R, (int64_t)t.s.count * a.group - t.row0);
             t.units = (int)w.units;
             // a unit belongs to the run in which it begins
-            t.u0 = (int)((at - t.first + t.tiles - 1) / t.tiles);
-            t.u1 = (int)min(w.units, (end - t.first + t.tiles - 1) / t.tiles);
-            at = min(end, t.first + w.units * t.tiles);
+            t.u0 = (int)((at - t.first + cost - 1) / cost);
+            t.u1 = (int)min(w.units, (end - t.first + cost - 1) / cost);
+            at = min(end, t.first + w.units * cost);
             t.key_end = keys(a, t.s);
             if (a.mask == nullptr) {
                 const int64_t last = (int64_t)t.s.start + (t.row0 + t.rows - 1) / a.group + 1;
@@ -190,7 +195,7 @@ struct AttnWalk {
     // The first and last CTA with a part of the row block.
     __device__ __forceinline__ int64_t first_cta(const AttnTile& t) const { return t.first / per; }
     __device__ __forceinline__ int64_t last_cta(const AttnTile& t) const {
-        return (t.first + (int64_t)(t.units - 1) * t.tiles) / per;
+        return (t.first + (int64_t)(t.units - 1) * (t.tiles == P ? kCostP : kCost1)) / per;
     }
 };
 

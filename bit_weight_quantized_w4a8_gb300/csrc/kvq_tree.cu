@@ -5,7 +5,7 @@
 // With hundreds of rows on each key the work is the two products, which only
 // tcgen05 runs at full rate, so the codes are widened to binary16 once
 // per CTA, in shared memory, for up to 256 rows:
-//   warps 16-19 load the codes of 128 keys and values, widen them and store them
+//   warps 16-23 load the codes of 128 keys and values, widen them and store them
 //     in the tensor core's 128-byte swizzled layout (two stages each);
 //   warps 0-7 and 8-15 are two slots of softmax: S is read from TMEM, the
 //     weights go back over it as binary16;
@@ -31,13 +31,15 @@
 namespace w4a8 {
 namespace {
 
-// Two slots of eight softmax warps and four that load: five warps to a scheduler.
-// Everything here waits for something (loads, TMEM, barriers), and with half
-// the softmax warps, each with twice the keys, a block took half as long again.
-constexpr int kSlotWarps = 8, kSoftWarps = 2 * kSlotWarps, kLoadWarps = 4;
+// Two slots of eight softmax warps and eight that load: six warps to a scheduler,
+// 80 registers a thread.  Everything here waits for something (loads, TMEM,
+// barriers), so many warps with little each; a spilled register costs a trip to
+// L2, as the tiles leave no first-level cache.
+constexpr int kSlotWarps = 8, kSoftWarps = 2 * kSlotWarps, kLoadWarps = 8;
 constexpr int kTreeThreads = (kSoftWarps + kLoadWarps) * 32;
 constexpr int kRowsTile = 128;   // rows of a tile, TMEM lanes
 constexpr int kBlock = 128;      // keys of a unit
+constexpr int kRawStages = 2;    // blocks whose codes are held as they came
 constexpr int kScaleRing = 4;    // blocks whose scales are held
 constexpr float kTop = 10.f;     // log2 of the weight of a fresh maximum
 constexpr float kSlack = 4.f;    // log2 of what it may grow by before O is rescaled
@@ -45,15 +47,17 @@ constexpr float kSlack = 4.f;    // log2 of what it may grow by before O is resc
 struct alignas(16) BlockScales {  // read as 16-byte vectors
     float k[kBlock];        // ks * scale * log2(e), never 0
     float v[kBlock];        // vs, 0 where one of the two is not finite
-    uint32_t valid[4];      // bit i of word w: key 32 w + i is there
-    uint32_t bad[4];        // it has a scale that is not finite
+    float vmax[8];          // largest |v| of keys 16 w .. 16 w + 15
+    uint32_t odd[8];        // not 0: some of them is not there or bad
+    uint16_t valid[8];      // bit i of word w: key 16 w + i is there
+    uint16_t bad[8];        // it has a scale that is not finite
 };
 
 struct TreeShared {
-    uint64_t kfull[2], vfull[2];   // [stage]: a block's keys, values are in place
+    uint64_t kfull[2], vfull[2];   // [block % 2]: its keys, values are in place
     uint64_t scfull[kScaleRing];   // [block % 4]: its scales are
     uint64_t sfull[2];             // [slot]: S of a job is there, and the product before it done
-    uint64_t kfree[2], vfree[2];   // [stage]: both slots' products have used them
+    uint64_t kfree[2], vfree[2];   // [block % 2]: both slots' products have used them
     uint64_t drain[2];
     BlockScales sc[kScaleRing];
     AttnWalk<kTreeThreads, kRowsTile, 2, kBlock>::Shared find;
@@ -77,7 +81,9 @@ struct TreeCfg {
     static constexpr int W = DIM * BITS / 8;
     static constexpr int kHalf = kRowsTile * 128;            // 128 rows of 64 binary16 values
     static constexpr int kTileBytes = kHalf * (DIM / 64);
-    static constexpr int kOffQ = 0, kOffK = 2 * kTileBytes, kOffV = 4 * kTileBytes, kOffShared = 6 * kTileBytes;
+    static constexpr int kRawBytes = 16 * W;                 // codes of a loading warp's 16 keys or values
+    static constexpr int kOffQ = 0, kOffK = 2 * kTileBytes, kOffV = 3 * kTileBytes, kOffRaw = 4 * kTileBytes;
+    static constexpr int kOffShared = kOffRaw + kLoadWarps * 2 * kRawStages * kRawBytes;
     static constexpr int kSmem = kOffShared + (int)sizeof(TreeShared) + 1024;  // + alignment
     static constexpr int kPiece = kRowsTile * (DIM + 2);     // floats: O [DIM][128], M, sum
     static constexpr uint32_t kS = 0, kO = 256;              // TMEM columns: S of slot i at 128 i, O at 256 + DIM i
@@ -125,6 +131,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -232,106 +243,141 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
         __syncthreads();
 
         if (warp >= kSoftWarps) {
-            // codes of this warp's 32 keys of every block, widened
-            constexpr int CPR = C::W / 16;  // 16-byte chunks of codes per vector
+            // codes of this warp's 16 keys of every block: copied two blocks ahead as they
+            // are, then widened into the tiles; lanes 0-15 have a key each for the page
+            // table and the scales
+            constexpr int CPR = C::W / 16;             // 16-byte chunks of codes per vector
+            constexpr int N = CPR / 2;                 // of them per lane
             const int lw = warp - kSoftWarps;
             const int u0 = t.u0, u1 = t.u1, key_end = t.key_end, h = t.h;
             const int32_t* table = a.b.table + t.b * a.b.max_pages;
-            uint4 xk[CPR], xv[CPR];
-            float sk = 0.f, sv = 0.f;
-            uint32_t there = 0u;  // keys of the block being loaded that are in range
-            int64_t row_a = 0, row_b = 0;  // vectors of the first and second 16 keys (one page each)
+            const uint32_t raw = base + C::kOffRaw + lw * 2 * kRawStages * C::kRawBytes;
             const int pmask = (1 << a.c.shift) - 1;
-            // nothing here waits for what it has just loaded: page numbers are
-            // fetched two blocks ahead, codes and scales one
-            auto page_of = [&](int u) -> int {  // of this lane's key, as the table has it
-                const int k = u * kBlock + 32 * lw + lane;
+            const int key = 16 * lw + (lane & 15);
+            auto page_of = [&](int u) -> int {  // as the table has it
+                const int k = u * kBlock + key;
                 return u < u1 && k < key_end ? table[k >> a.c.shift] : -1;
             };
-            auto row_of = [&](int i) -> int {
-                return CPR >= 4 ? 8 * (i / (CPR / 4 > 0 ? CPR / 4 : 1)) + (lane & 7) : 16 * i + 8 * (lane >> 4) + (lane & 7);
+            // a block's place: the vector of the first of the 16 keys (one page holds all),
+            // this lane's, and which of them are in range
+            struct Place {
+                int64_t first, own;
+                uint32_t there;
             };
-            auto chunk_of = [&](int i) -> int {
-                return CPR >= 4 ? (lane >> 3) + 4 * (i % (CPR / 4 > 0 ? CPR / 4 : 1)) : (lane >> 3) & 1;
-            };
-            auto load = [&](const uint8_t* codes, uint4* x) {
-                #pragma unroll
-                for (int i = 0; i < CPR; ++i) {
-                    const int r = row_of(i);
-                    const int64_t v = (r < 16 ? row_a : row_b - 16) + r;
-                    x[i] = ld_global_nc_v4_if(codes + v * C::W + 16 * chunk_of(i), (there >> r) & 1);
-                }
-            };
-            auto load_k = [&](int u, int page) {
-                const int k = u * kBlock + 32 * lw + lane;
+            auto place = [&](int u, int page) -> Place {
+                const int k = u * kBlock + key;
                 const bool ok = page >= 0 && page < a.c.pages;
                 if (!ok && u < u1 && k < key_end) atomicOr(&g_attn_error, kErrCacheRange);
-                const int64_t vec = ok ? ((((int64_t)page * a.c.heads + h) << a.c.shift) + (k & pmask)) : 0;
-                there = __ballot_sync(0xFFFFFFFFu, ok);
-                row_a = __shfl_sync(0xFFFFFFFFu, vec, 0);
-                row_b = __shfl_sync(0xFFFFFFFFu, vec, 16);
-                load(a.c.k, xk);
-                sk = ok ? a.c.ks[vec] : 0.f;
-                sv = ok ? a.c.vs[vec] : 0.f;
+                Place p;
+                p.own = ok ? ((((int64_t)page * a.c.heads + h) << a.c.shift) + (k & pmask)) : 0;
+                p.there = __ballot_sync(0xFFFFFFFFu, ok) & 0xFFFFu;
+                p.first = __shfl_sync(0xFFFFFFFFu, p.own, 0);
+                return p;
             };
-            auto store = [&](uint32_t dst, const uint4* x) {
+            // chunk c of row r of a raw tile, permuted so that 8 rows' chunks c lie in
+            // different banks
+            auto raw_off = [&](int r, int c) -> uint32_t {
+                if (CPR >= 8) return r * C::W + (c >> 3) * 128 + (((c & 7) ^ (r & 7)) << 4);
+                if (CPR == 4) return (r >> 1) * 128 + ((((r & 1) << 2) + (c ^ ((r >> 1) & 3))) << 4);
+                return (r >> 2) * 128 + ((((r & 3) << 1) + (c ^ ((r >> 2) & 1))) << 4);
+            };
+            auto copy = [&](int u, const Place& p, const uint8_t* codes, int kv) {
+                if (u < u1) {
+                    const uint32_t dst = raw + (2 * ((u - u0) % kRawStages) + kv) * C::kRawBytes;
+                    #pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const int r = (32 * i + lane) / CPR, c = (32 * i + lane) % CPR;
+                        cp_async_16_zfill(dst + raw_off(r, c), codes + (p.first + r) * C::W + 16 * c, (p.there >> r) & 1 ? 16u : 0u);
+                    }
+                }
+                cp_async_commit();
+            };
+            // 8 lanes on 8 rows of one chunk meet each bank once, here and in the tile
+            auto widen = [&](uint32_t dst, int j, int kv) {
+                const uint32_t src = raw + (2 * (j % kRawStages) + kv) * C::kRawBytes;
                 #pragma unroll
-                for (int i = 0; i < CPR; ++i) {
-                    const int r = 32 * lw + row_of(i), c = chunk_of(i);
-                    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                for (int i = 0; i < N; ++i) {
+                    const int r = CPR >= 4 ? 8 * (i / (CPR / 4 > 0 ? CPR / 4 : 1)) + (lane & 7) : 8 * (lane >> 4) + (lane & 7);
+                    const int c = CPR >= 4 ? (lane >> 3) + 4 * (i % (CPR / 4 > 0 ? CPR / 4 : 1)) : (lane >> 3) & 1;
+                    uint32_t w[4];
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(src + raw_off(r, c)));
                     if constexpr (BITS == 8) {
-                        uint32_t h[8];
+                        uint32_t x[8];
                         #pragma unroll
-                        for (int j = 0; j < 4; ++j) widen8(w[j], h[2 * j], h[2 * j + 1]);
-                        sts16(dst + tile_off(r, 2 * c), h[0], h[1], h[2], h[3]);
-                        sts16(dst + tile_off(r, 2 * c + 1), h[4], h[5], h[6], h[7]);
+                        for (int y = 0; y < 4; ++y) widen8(w[y], x[2 * y], x[2 * y + 1]);
+                        sts16(dst + tile_off(16 * lw + r, 2 * c), x[0], x[1], x[2], x[3]);
+                        sts16(dst + tile_off(16 * lw + r, 2 * c + 1), x[4], x[5], x[6], x[7]);
                     } else {
                         #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t h[4];
-                            widen4(w[j], h[0], h[1]);
-                            widen4(w[j] >> 8, h[2], h[3]);
-                            sts16(dst + tile_off(r, 4 * c + j), h[0], h[1], h[2], h[3]);
+                        for (int y = 0; y < 4; ++y) {
+                            uint32_t x[4];
+                            widen4(w[y], x[0], x[1]);
+                            widen4(w[y] >> 8, x[2], x[3]);
+                            sts16(dst + tile_off(16 * lw + r, 4 * c + y), x[0], x[1], x[2], x[3]);
                         }
                     }
                 }
             };
-            load_k(u0, page_of(u0));
-            load(a.c.v, xv);
-            int page = page_of(u0 + 1);
+            auto freed = [&](uint64_t* bars, int blk) -> bool {  // of the block before blk
+                return blk == 0 || __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars[(blk - 1) & 1]), ((blk - 1) >> 1) & 1, &sh.abort));
+            };
+            auto arrive = [&](uint64_t& bar) {
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar));
+            };
+            auto scale_of = [&](const float* p, const Place& at) -> float { return at.there >> (lane & 15) & 1 ? p[at.own] : 0.f; };
+            Place p1 = place(u0, page_of(u0));
+            int page = page_of(u0 + 2);
+            float sk = scale_of(a.c.ks, p1), sv = scale_of(a.c.vs, p1);  // of the next block to be widened
+            uint32_t there = p1.there;
+            copy(u0, p1, a.c.k, 0);
+            copy(u0, p1, a.c.v, 1);
+            p1 = place(u0 + 1, page_of(u0 + 1));
+            copy(u0 + 1, p1, a.c.k, 0);
+            copy(u0 + 1, p1, a.c.v, 1);
             for (int j = 0; j < nb; ++j) {
-                const int blk = blocks_done + j, st = blk & 1;
-                if (blk >= 2 && !__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.kfree[st]), ((blk >> 1) - 1) & 1, &sh.abort))) break;
-                store(base + C::kOffK + st * C::kTileBytes, xk);
+                const int blk = blocks_done + j;
                 BlockScales& bs = sh.sc[blk % kScaleRing];
                 {
                     // a factor of 0 would make NaN of an unseen key's -inf; a key of zeros
                     // has logit 0 with any
                     const float kk = sk * a.scale_log2;
                     const bool fine = fabsf(kk) < INFINITY && fabsf(sv) < INFINITY;
-                    bs.k[32 * lw + lane] = fine && kk != 0.f ? kk : 1e-30f;
-                    bs.v[32 * lw + lane] = fine ? sv : 0.f;
-                    const unsigned bad = __ballot_sync(0xFFFFFFFFu, !fine);
+                    if (lane < 16) {
+                        bs.k[key] = fine && kk != 0.f ? kk : 1e-30f;
+                        bs.v[key] = fine ? sv : 0.f;
+                    }
+                    const unsigned bad = __ballot_sync(0xFFFFFFFFu, !fine) & 0xFFFFu;
+                    const unsigned vmax = __reduce_max_sync(0xFFFFFFFFu, fine ? __float_as_uint(fabsf(sv)) : 0u);
                     if (lane == 0) {
-                        bs.valid[lw] = there;
-                        bs.bad[lw] = bad;
+                        bs.vmax[lw] = __uint_as_float(vmax);
+                        bs.odd[lw] = (there ^ 0xFFFFu) | bad;
+                        bs.valid[lw] = (uint16_t)there;
+                        bs.bad[lw] = (uint16_t)bad;
                     }
                 }
-                fence_async_shared();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&sh.scfull[blk % kScaleRing]));
-                    mbar_arrive(smem_u32(&sh.kfull[st]));
-                }
-                if (j + 1 < nb) load_k(u0 + j + 1, page);
-                page = page_of(u0 + j + 2);
-                if (blk >= 2 && !__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.vfree[st]), ((blk >> 1) - 1) & 1, &sh.abort))) break;
-                store(base + C::kOffV + st * C::kTileBytes, xv);
-                fence_async_shared();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.scfull[blk % kScaleRing]));
+                sk = scale_of(a.c.ks, p1);
+                sv = scale_of(a.c.vs, p1);
+                there = p1.there;
+                p1 = place(u0 + j + 2, page);
+                page = page_of(u0 + j + 3);
+                cp_async_wait<3>();  // this block's keys are here; its values and the next block are on their way
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.vfull[st]));
-                if (j + 1 < nb) load(a.c.v, xv);
+                if (!freed(sh.kfree, blk)) break;
+                widen(base + C::kOffK, j, 0);
+                arrive(sh.kfull[blk & 1]);
+                copy(u0 + j + 2, p1, a.c.k, 0);
+                cp_async_wait<3>();
+                __syncwarp();
+                if (!freed(sh.vfree, blk)) break;
+                widen(base + C::kOffV, j, 1);
+                arrive(sh.vfull[blk & 1]);
+                copy(u0 + j + 2, p1, a.c.v, 1);
             }
+            cp_async_wait<0>();
         } else {
             // Softmax.  A slot's eight warps are its tile's four quarters of rows times
             // two halves of a block's keys.  S, W and O are held in fragments: rows 8 k +
@@ -357,10 +403,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
             auto block_of = [&](int i) -> int { return blocks_done + (two ? i : 2 * i + slot); };
             // products, issued by the slot's first warp (all of it in step, so that
             // descriptors live in uniform registers; one lane issues)
-            auto qk = [&](int i) {
-                const int st = __shfl_sync(0xFFFFFFFFu, block_of(i) & 1, 0);
+            auto qk = [&]() {
                 const uint64_t qd = sw128_desc(u_base + C::kOffQ) + u_q * (C::kTileBytes >> 4);
-                const uint64_t kd = sw128_desc(u_base + C::kOffK) + st * (C::kTileBytes >> 4);
+                const uint64_t kd = sw128_desc(u_base + C::kOffK);
                 if (leader) {
                     #pragma unroll
                     for (int k = 0; k < KSTEPS; ++k) {
@@ -370,8 +415,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                 }
             };
             auto pv = [&](int i) {
-                const int st = __shfl_sync(0xFFFFFFFFu, block_of(i) & 1, 0);
-                const uint64_t vd = sw128_desc_mn(u_base + C::kOffV, C::kHalf) + st * (C::kTileBytes >> 4);
+                const uint64_t vd = sw128_desc_mn(u_base + C::kOffV, C::kHalf);
                 if (leader) {
                     #pragma unroll
                     for (int k = 0; k < kBlock / 16; ++k)
@@ -404,7 +448,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                 ok = wait_keys(0);
                 if (ok) {
                     tc_fence_after_sync();
-                    qk(0);
+                    qk();
                     commit();
                     release(sh.kfree, 0);
                     __syncwarp();
@@ -419,12 +463,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                 float ve = 0.f;  // 2^ve bounds the block's value scales
                 bool plain = true;
                 if (ok && !idle) {
-                    const float4 v = reinterpret_cast<const float4*>(bs.v)[lane];
-                    const unsigned bits = __reduce_max_sync(
-                        0xFFFFFFFFu, __float_as_uint(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)))));
-                    ve = fmaxf((float)((int)(bits >> 23) - 126), -100.f);
-                    plain = k0 + kBlock <= start && (bs.valid[0] & bs.valid[1] & bs.valid[2] & bs.valid[3]) == 0xFFFFFFFFu &&
-                            (bs.bad[0] | bs.bad[1] | bs.bad[2] | bs.bad[3]) == 0u;
+                    const float4 v = reinterpret_cast<const float4*>(bs.vmax)[0], v2 = reinterpret_cast<const float4*>(bs.vmax)[1];
+                    const uint4 odd = reinterpret_cast<const uint4*>(bs.odd)[0], odd2 = reinterpret_cast<const uint4*>(bs.odd)[1];
+                    const float top = fmaxf(max3(v.x, v.y, max3(v.z, v.w, v2.x)), max3(v2.y, v2.z, v2.w));
+                    ve = fmaxf((float)((int)(__float_as_uint(top) >> 23) - 126), -100.f);
+                    plain = k0 + kBlock <= start && (odd.x | odd.y | odd.z | odd.w | odd2.x | odd2.y | odd2.z | odd2.w) == 0u;
                 }
                 ok = ok && wait(sh.sfull[slot], s_phase[slot] + i);
                 const bool work = ok && !idle;
@@ -446,9 +489,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                             #pragma unroll
                             for (int rr = 0; rr < 2; ++rr) {
                                 const int r = 32 * quad + 16 * hb + 8 * rr + (lane >> 2);
-                                see[rr] = bs.valid[2 * half + c] & seen_bits(k0 + 64 * half + 32 * c - start, a.mask != nullptr, sh.word[tl][r], sh.tok[tl][r]);
+                                see[rr] = reinterpret_cast<const uint32_t*>(bs.valid)[2 * half + c] & seen_bits(k0 + 64 * half + 32 * c - start, a.mask != nullptr, sh.word[tl][r], sh.tok[tl][r]);
                             }
-                            const uint32_t bad = bs.bad[2 * half + c];
+                            const uint32_t bad = reinterpret_cast<const uint32_t*>(bs.bad)[2 * half + c];
                             tmem_ld_wait();
                             #pragma unroll
                             for (int x = 0; x < 16; ++x) {
@@ -475,7 +518,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                             #pragma unroll
                             for (int rr = 0; rr < 2; ++rr) {
                                 const float2 d = unpack2(mul2(pack2(__uint_as_float(s[4 * j + 2 * rr]), __uint_as_float(s[4 * j + 2 * rr + 1])), kk));
-                                top[2 * hb + rr] = fmaxf(top[2 * hb + rr], fmaxf(d.x, d.y));
+                                top[2 * hb + rr] = max3(top[2 * hb + rr], d.x, d.y);
                             }
                         }
                     }
@@ -566,7 +609,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                         release(sh.vfree, i);
                         if (i + 1 < my_jobs && (ok = wait_keys(i + 1))) {
                             tc_fence_after_sync();
-                            qk(i + 1);
+                            qk();
                             release(sh.kfree, i + 1);
                         }
                         commit();
