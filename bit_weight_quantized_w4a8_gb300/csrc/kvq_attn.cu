@@ -503,31 +503,64 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(const AttnArgs a) {
             __syncthreads();
             if (s_last) {
                 __threadfence();
-                for (int e = tid; e < n_rows * DIM / 4; e += kAttnThreads) {
-                    const int r = e / (DIM / 4), d = (e % (DIM / 4)) * 4;
-                    float top = -INFINITY;
-                    for (int64_t c = c0; c <= c1; ++c) {
-                        const float* p = a.parts + (c * 2 + (c == c0 ? 1 : 0)) * C::kPart;
-                        top = fmaxf(top, __ldcg(p + ROWS * DIM + 2 * r));
-                    }
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    float sum = 0.f;
-                    #pragma unroll 4
-                    for (int64_t c = c0; c <= c1; ++c) {
-                        const float* p = a.parts + (c * 2 + (c == c0 ? 1 : 0)) * C::kPart;
-                        const float2 st = __ldcg(reinterpret_cast<const float2*>(p + ROWS * DIM + 2 * r));
-                        const float4 x = __ldcg(reinterpret_cast<const float4*>(p + r * DIM + d));
-                        const float f = st.x == -INFINITY ? 1.f : exp2_fast(st.x - top);  // no keys: zeros (or NaN)
-                        o.x = fmaf(x.x, f, o.x);
-                        o.y = fmaf(x.y, f, o.y);
-                        o.z = fmaf(x.z, f, o.z);
-                        o.w = fmaf(x.w, f, o.w);
-                        sum = fmaf(st.y, f, sum);
+                // a warp takes rows in turn, its lanes first a piece each (the statistics),
+                // then dimensions each, eight pieces under way
+                const int n = (int)(c1 - c0) + 1;
+                constexpr int V = DIM / 32;  // dimensions of a lane
+                auto piece = [&](int i) -> const float* {  // the first CTA's is its second
+                    return a.parts + ((c0 + i) * 2 + (i == 0 ? 1 : 0)) * C::kPart;
+                };
+                for (int r = warp; r < n_rows; r += kWarps) {
+                    float top = -INFINITY, sum = 0.f, o[V] = {};
+                    for (int i0 = 0; i0 < n; i0 += 32) {
+                        float2 st = make_float2(-INFINITY, 0.f);
+                        if (i0 + lane < n) st = __ldcg(reinterpret_cast<const float2*>(piece(i0 + lane) + ROWS * DIM + 2 * r));
+                        float most = st.x;
+                        #pragma unroll
+                        for (int x = 16; x >= 1; x >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, x));
+                        const float was = top;
+                        top = fmaxf(top, most);
+                        const float f = was == -INFINITY ? 1.f : exp2_fast(was - top);
+                        const float g = st.x == -INFINITY ? 1.f : exp2_fast(st.x - top);  // no keys: zeros (or NaN)
+                        float add = st.y * g;
+                        #pragma unroll
+                        for (int x = 16; x >= 1; x >>= 1) add += __shfl_xor_sync(0xFFFFFFFFu, add, x);
+                        sum = fmaf(sum, f, add);
+                        #pragma unroll
+                        for (int v = 0; v < V; ++v) o[v] *= f;
+                        const int m = min(32, n - i0);
+                        #pragma unroll 1
+                        for (int i = 0; i < m; i += 8) {
+                            float x[8][V];
+                            #pragma unroll
+                            for (int y = 0; y < 8; ++y) {
+                                const float* p = piece(i0 + min(i + y, m - 1)) + r * DIM + V * lane;
+                                if constexpr (V == 2) {
+                                    const float2 z = __ldcg(reinterpret_cast<const float2*>(p));
+                                    x[y][0] = z.x, x[y][1] = z.y;
+                                } else {
+                                    #pragma unroll
+                                    for (int v = 0; v < V; v += 4) {
+                                        const float4 z = __ldcg(reinterpret_cast<const float4*>(p + v));
+                                        x[y][v] = z.x, x[y][v + 1] = z.y, x[y][v + 2] = z.z, x[y][v + 3] = z.w;
+                                    }
+                                }
+                            }
+                            #pragma unroll
+                            for (int y = 0; y < 8; ++y) {
+                                const float w = __shfl_sync(0xFFFFFFFFu, g, (i + y) & 31);
+                                if (i + y < m) {
+                                    #pragma unroll
+                                    for (int v = 0; v < V; ++v) o[v] = fmaf(x[y][v], w, o[v]);
+                                }
+                            }
+                        }
                     }
                     const int row = t.row0 + r;
                     const float inv = top == -INFINITY && sum == 0.f ? 0.f : 1.f / sum;
-                    __half* out = a.out + ((int64_t)(s.first + row / a.group) * a.heads_q + h * a.group + row % a.group) * DIM + d;
-                    store4(out, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+                    __half* out = a.out + ((int64_t)(s.first + row / a.group) * a.heads_q + h * a.group + row % a.group) * DIM + V * lane;
+                    #pragma unroll
+                    for (int v = 0; v < V; v += 2) *reinterpret_cast<uint32_t*>(out + v) = pack_half2(o[v] * inv, o[v + 1] * inv);
                 }
             }
         }

@@ -219,29 +219,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
         const AttnTile& t = sh.tile;  // the roles take what they need of it into registers
         const int nb = t.u1 - t.u0;
         const bool two = t.tiles == 2;
-        // the queries of the block's rows, in the widened keys' order of dimensions, and
-        // what the rows see of the drafted tokens
-        #pragma unroll 4
-        for (int e = tid; e < t.tiles * kRowsTile * (DIM / 8); e += kTreeThreads) {
-            const int r = e / (DIM / 8), c = e % (DIM / 8);
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (r < t.rows) {
-                const int row = t.row0 + r, tok = row / a.group;
-                x = *reinterpret_cast<const uint4*>(a.Q + ((int64_t)(t.s.first + tok) * a.heads_q + t.h * a.group + row - tok * a.group) * DIM + 8 * c);
-            }
-            if constexpr (BITS == 4)
-                x = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
-                               __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
-            sts16(base + C::kOffQ + (r / kRowsTile) * C::kTileBytes + tile_off(r % kRowsTile, c), x.x, x.y, x.z, x.w);
-        }
-        if (tid < t.tiles * kRowsTile) {
-            const int tok = (t.row0 + min(tid, t.rows - 1)) / a.group;
-            sh.tok[tid / kRowsTile][tid % kRowsTile] = tok;
-            sh.word[tid / kRowsTile][tid % kRowsTile] = a.mask != nullptr ? a.mask[t.s.first + tok] : 0;
-        }
-        fence_async_shared();
-        __syncthreads();
-
         if (warp >= kSoftWarps) {
             // codes of this warp's 16 keys of every block: copied two blocks ahead as they
             // are, then widened into the tiles; lanes 0-15 have a key each for the page
@@ -379,6 +356,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
             }
             cp_async_wait<0>();
         } else {
+            // the queries of the block's rows, in the widened keys' order of dimensions, and
+            // what the rows see of the drafted tokens
+            #pragma unroll 8
+            for (int e = tid; e < t.tiles * kRowsTile * (DIM / 8); e += kSoftWarps * 32) {
+                const int r = e / (DIM / 8), c = e % (DIM / 8);
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (r < t.rows) {
+                    const int row = t.row0 + r, tok = row / a.group;
+                    x = *reinterpret_cast<const uint4*>(a.Q + ((int64_t)(t.s.first + tok) * a.heads_q + t.h * a.group + row - tok * a.group) * DIM + 8 * c);
+                }
+                if constexpr (BITS == 4)
+                    x = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
+                                   __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
+                sts16(base + C::kOffQ + (r / kRowsTile) * C::kTileBytes + tile_off(r % kRowsTile, c), x.x, x.y, x.z, x.w);
+            }
+            if (tid < t.tiles * kRowsTile) {
+                const int tok = (t.row0 + min(tid, t.rows - 1)) / a.group;
+                sh.tok[tid / kRowsTile][tid % kRowsTile] = tok;
+                sh.word[tid / kRowsTile][tid % kRowsTile] = a.mask != nullptr ? a.mask[t.s.first + tok] : 0;
+            }
+            fence_async_shared();
+            named_bar_sync(3, kSoftWarps * 32);
+
             // Softmax.  A slot's eight warps are its tile's four quarters of rows times
             // two halves of a block's keys.  S, W and O are held in fragments: rows 8 k +
             // lane / 4 of the warp's 32 (k < 4), columns 2 (lane % 4), + 1 of every 8.  A
@@ -721,13 +721,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
 }
 
 // Joins the pieces of the row block that began in the run of CTA blockIdx.x and
-// went on in the next ones, in their order: 8 dimensions of one tile a CTA,
-// a thread per row.  As its own launch it has the whole GPU for what the last
-// CTA to arrive would read alone (up to 2 MB).
+// went on in the next ones, in their order: 16 dimensions of one tile a CTA, a
+// thread has a row's eight and takes four pieces at a time (40 loads under
+// way; one after the other they took up to 100 us).  As its own launch it
+// has the whole GPU for what the last CTA to arrive would read alone.
+constexpr int kJoinThreads = 256;
 template <int DIM, int BITS>
-__global__ void __launch_bounds__(kRowsTile) tree_join_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const AttnArgs a) {
     using C = TreeCfg<DIM, BITS>;
-    using Walk = AttnWalk<kRowsTile, kRowsTile, 2, kBlock>;
+    using Walk = AttnWalk<kJoinThreads, kRowsTile, 2, kBlock>;
     __shared__ typename Walk::Shared find;
     griddep_launch_dependents();
     griddep_wait();
@@ -736,22 +738,41 @@ __global__ void __launch_bounds__(kRowsTile) tree_join_kernel(const AttnArgs a) 
     AttnTile t;
     const int64_t c0 = blockIdx.x;
     if (!walk.next(a, t, true) || walk.first_cta(t) != c0) return;
-    const int64_t c1 = walk.last_cta(t);
-    const int tl = blockIdx.y / (DIM / 8), c8 = blockIdx.y % (DIM / 8), r = threadIdx.x, rt = tl * kRowsTile + r;
-    if (c1 == c0 || rt >= t.rows) return;
-    auto piece = [&](int64_t c) { return a.parts + ((c * 2 + (c == c0 ? 1 : 0)) * 2 + tl) * C::kPiece; };
-    float top = -INFINITY;
-    #pragma unroll 4
-    for (int64_t c = c0; c <= c1; ++c) top = fmaxf(top, piece(c)[DIM * kRowsTile + r]);
-    float o[8] = {}, sum = 0.f;
-    #pragma unroll 2
-    for (int64_t c = c0; c <= c1; ++c) {
-        const float* p = piece(c);
-        const float m = p[DIM * kRowsTile + r];
-        const float f = m == -INFINITY ? 1.f : exp2_fast(m - top);  // nothing seen: zeros (or NaN)
-        sum = fmaf(p[(DIM + 1) * kRowsTile + r], f, sum);
+    const int n = (int)(walk.last_cta(t) - c0) + 1;  // pieces
+    const int tl = blockIdx.y / (DIM / 16), r = threadIdx.x % kRowsTile, rt = tl * kRowsTile + r;
+    const int c8 = blockIdx.y % (DIM / 16) * 2 + threadIdx.x / kRowsTile;
+    if (n == 1 || rt >= t.rows) return;
+    // the first CTA's piece is its second (of a block that it began), the others' their first
+    auto piece = [&](int i) -> const float* {
+        return a.parts + ((c0 + i) * 4 + (i == 0 ? 2 : 0) + tl) * C::kPiece + r;
+    };
+    float top = -INFINITY, sum = 0.f, o[8] = {};
+    for (int i0 = 0; i0 < n; i0 += 4) {
+        float m[4], l[4], x[4][8];
         #pragma unroll
-        for (int y = 0; y < 8; ++y) o[y] = fmaf(p[(8 * c8 + column_of<BITS>(y)) * kRowsTile + r], f, o[y]);
+        for (int i = 0; i < 4; ++i) {
+            const float* p = piece(min(i0 + i, n - 1));
+            m[i] = p[DIM * kRowsTile];
+            l[i] = p[(DIM + 1) * kRowsTile];
+            #pragma unroll
+            for (int y = 0; y < 8; ++y) x[i][y] = p[(8 * c8 + column_of<BITS>(y)) * kRowsTile];
+        }
+        const float was = top;
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, m[i]);
+        const float f = was == -INFINITY ? 0.f : exp2_fast(was - top);
+        // (nothing seen so far: sums of 0, or NaN, which stays)
+        sum = was == -INFINITY ? sum : sum * f;
+        #pragma unroll
+        for (int y = 0; y < 8; ++y) o[y] *= f;
+        #pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i0 + i < n) {
+                const float g = m[i] == -INFINITY ? 1.f : exp2_fast(m[i] - top);
+                sum = fmaf(l[i], g, sum);
+                #pragma unroll
+                for (int y = 0; y < 8; ++y) o[y] = fmaf(x[i][y], g, o[y]);
+            }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     #pragma unroll
@@ -770,11 +791,19 @@ auto by_config(const kvq_cache_t& c, F f) {
 
 int tree_ctas(int sms) { return sms < kAttnMaxCtas ? sms : kAttnMaxCtas; }
 
-// Rows that share a cache head, on average, from which this kernel serves a call.
-constexpr int64_t kTreeMinRows = 17;
-
+// Whether this kernel serves a call: it saves the difference of what a cached
+// token costs the two, times the tokens, against the 22 us that it takes longer
+// for a short cache.  Measured on GB300 (8 sequences of 4 heads of 128, 8 bits, ps per token and
+// cache head): the row-block kernel 38 for each 16 rows, this one 100 for one tile of 128
+// rows and 143 for two.  At 32001 tokens 56 rows take 135 us here and 164 there, 21
+// rows 132 and 96; at 64 tokens 448 rows 40 and 22.  The cache is taken to be as long
+// as the page table allows: its length is on the device.
 bool tree_serves(const kvq_cache_t& c, const kvq_batch_t& b, int heads_q) {
-    return c.dim <= 128 && (b.tokens * (heads_q / c.heads) + b.seqs - 1) / b.seqs >= kTreeMinRows;
+    if (c.dim > 128) return false;  // 256 dimensions of O for two tiles do not fit TMEM
+    const int64_t rows = (b.tokens * (heads_q / c.heads) + b.seqs - 1) / b.seqs, tiles = (rows + 127) / 128;
+    const double here = (double)(tiles / 2) * 143e-6 + (double)(tiles % 2) * 100e-6, there = (double)((rows + 15) / 16) * 38e-6;
+    const double keys = (double)b.seqs * c.heads * (double)(b.max_pages * c.page);
+    return keys * (there - here) > 22.0;
 }
 
 }  // namespace
@@ -803,7 +832,7 @@ cudaError_t launch_kvq_attention(const kvq_cache_t& c, const kvq_batch_t& b, con
         const unsigned ctas = (unsigned)tree_ctas(sms);
         e = layer_launch(tree_kernel<D, B>, dim3(ctas), kTreeThreads, TreeCfg<D, B>::kSmem, flags, stream, a);
         if (e != cudaSuccess) return e;
-        return layer_launch(tree_join_kernel<D, B>, dim3(ctas, 2 * D / 8), kRowsTile, 0, W4A8_LAUNCH_PDL, stream, a);
+        return layer_launch(tree_join_kernel<D, B>, dim3(ctas, 2 * D / 16), kJoinThreads, 0, W4A8_LAUNCH_PDL, stream, a);
     });
 }
 
