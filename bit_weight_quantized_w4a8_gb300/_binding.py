@@ -10,6 +10,7 @@ from __future__ import annotations
 import collections
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -704,31 +705,38 @@ def kvq_cache(pages: int, page: int, heads: int, dim: int, bits: int = 8, device
     return KVQCache(k, v, ks, vs)
 
 
+_pack_cache = struct.Struct("@4Pq4i").pack   # kvq_cache_t
+_pack_batch = struct.Struct("@3P3q").pack    # kvq_batch_t
+
+
 def _cache_arg(c):
+    """(kvq_cache_t as bytes, heads, dim)"""
     k, v, ks, vs = c
     if not isinstance(k, torch.Tensor) or k.dtype not in (torch.int8, torch.uint8):
         raise TypeError("the cache's codes must be int8 (8 bits) or uint8 (4 bits) tensors")
     if k.dim() != 4:
         raise ValueError("the cache's codes must be [pages][heads][page][dim]")
+    shape = k.shape
     _want(k, k.dtype, "k")
-    _want(v, k.dtype, "v", k.shape)
-    pages, heads, page, width = k.shape
-    _want(ks, torch.float32, "ks", (pages, heads, page))
-    _want(vs, torch.float32, "vs", (pages, heads, page))
-    bits = 8 if k.dtype == torch.int8 else 4
-    return _Cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, page, heads, width * 8 // bits,
-                  bits)
+    _want(v, k.dtype, "v", shape)
+    _want(ks, torch.float32, "ks", shape[:3])
+    _want(vs, torch.float32, "vs", shape[:3])
+    pages, heads, page, width = shape
+    bits = 8 if k.dtype is torch.int8 else 4
+    dim = width * 8 // bits
+    return _pack_cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, page, heads, dim, bits), heads, dim
 
 
 def _batch_arg(b, tokens):
+    """kvq_batch_t as bytes"""
     cu, start, table = b
     _want(cu, torch.int32, "cu")
     _want(start, torch.int32, "start")
     _want(table, torch.int32, "table")
-    if cu.dim() != 1 or start.dim() != 1 or table.dim() != 2 or cu.shape[0] != start.shape[0] + 1 or \
-            table.shape[0] != start.shape[0]:
+    cs, ss, ts = cu.shape, start.shape, table.shape
+    if len(cs) != 1 or len(ss) != 1 or len(ts) != 2 or cs[0] != ss[0] + 1 or ts[0] != ss[0]:
         raise ValueError("the batch must be cu [seqs + 1], start [seqs], table [seqs][max_pages]")
-    return _Batch(cu.data_ptr(), start.data_ptr(), table.data_ptr(), start.shape[0], tokens, table.shape[1])
+    return _pack_batch(cu.data_ptr(), start.data_ptr(), table.data_ptr(), ss[0], tokens, ts[1])
 
 
 def kvq_write(cache, batch, K, V, Q=None, pos=None, freqs=None, interleaved: bool = False, mscale: float = 1.0,
@@ -736,10 +744,10 @@ def kvq_write(cache, batch, K, V, Q=None, pos=None, freqs=None, interleaved: boo
     """Writes K, V [tokens][heads][dim] (fp32 or fp16, rows at any distance) into
     the cache, rotated first when freqs is given, and rotates Q
     [tokens][heads_q][dim] in the same launch; returns Q_out (fp16; None without Q)."""
-    ca = _cache_arg(cache)
+    ca, heads, dim = _cache_arg(cache)
     xt = _want_type(K, "K")
     n = K.shape[0]
-    shape = (n, ca.heads, ca.dim)
+    shape = (n, heads, dim)
     ld_k, ld_v = _want_heads(K, "K", shape), _want_heads(V, "V", shape)
     if V.dtype != K.dtype or (Q is not None and Q.dtype != K.dtype):
         raise TypeError("Q, K and V must have one type")
@@ -748,12 +756,12 @@ def kvq_write(cache, batch, K, V, Q=None, pos=None, freqs=None, interleaved: boo
     hq = ld_q = 0
     if Q is not None:
         hq = Q.shape[1]
-        ld_q = _want_heads(Q, "Q", (n, hq, ca.dim))
-        Q_out = torch.empty((n, hq, ca.dim), dtype=torch.float16, device=K.device) if Q_out is None else Q_out
-        _want(Q_out, torch.float16, "Q_out", (n, hq, ca.dim))
+        ld_q = _want_heads(Q, "Q", (n, hq, dim))
+        Q_out = torch.empty((n, hq, dim), dtype=torch.float16, device=K.device) if Q_out is None else Q_out
+        _want(Q_out, torch.float16, "Q_out", (n, hq, dim))
     elif Q_out is not None:
         raise ValueError("Q_out needs Q")
-    _check(lib().kvq_write(ctypes.byref(ca), ctypes.byref(ba), _ptr(K), ld_k, _ptr(V), ld_v, _ptr(Q), ld_q, hq, xt,
+    _check(lib().kvq_write(ca, ba, _ptr(K), ld_k, _ptr(V), ld_v, _ptr(Q), ld_q, hq, xt,
                            _ptr(pos), _ptr(freqs), rot, int(interleaved), mscale, _ptr(Q_out), flags, _stream(K)))
     return Q_out
 
@@ -761,32 +769,32 @@ def kvq_write(cache, batch, K, V, Q=None, pos=None, freqs=None, interleaved: boo
 def kvq_read(cache, batch, tokens: int, dtype=torch.float16, K=None, V=None, flags: int = 0):
     """The batch's keys and values (tokens = cu[-1]) as values:
     (K, V) [tokens][heads][dim], fp16 or fp32."""
-    ca = _cache_arg(cache)
+    ca, heads, dim = _cache_arg(cache)
     ba = _batch_arg(batch, tokens)
-    shape = (tokens, ca.heads, ca.dim)
+    shape = (tokens, heads, dim)
     K = torch.empty(shape, dtype=dtype, device=cache[0].device) if K is None else K
     V = torch.empty(shape, dtype=K.dtype, device=cache[0].device) if V is None else V
     yt = _want_type(K, "K")
     _want(K, K.dtype, "K", shape)
     _want(V, K.dtype, "V", shape)
-    _check(lib().kvq_read(ctypes.byref(ca), ctypes.byref(ba), _ptr(K), _ptr(V), yt, flags, _stream(K)))
+    _check(lib().kvq_read(ca, ba, _ptr(K), _ptr(V), yt, flags, _stream(K)))
     return K, V
 
 
 def kvq_keep(cache, batch, keep, flags: int = 0):
     """Moves a drafted tree's accepted tokens together: slot start[b] + i takes
     what slot start[b] + keep[cu[b] + i] held, until an entry is negative."""
-    ca = _cache_arg(cache)
+    ca, heads, dim = _cache_arg(cache)
     _want(keep, torch.int32, "keep")
     if keep.dim() != 1:
         raise ValueError("keep must have one dimension")
     ba = _batch_arg(batch, keep.shape[0])
-    _check(lib().kvq_keep(ctypes.byref(ca), ctypes.byref(ba), _ptr(keep), flags, _stream(keep)))
+    _check(lib().kvq_keep(ca, ba, _ptr(keep), flags, _stream(keep)))
 
 
 def kvq_attention_workspace_bytes(cache, batch, tokens: int, heads_q: int) -> int:
-    ca, ba = _cache_arg(cache), _batch_arg(batch, tokens)
-    return int(lib().kvq_attention_workspace_bytes(ctypes.byref(ca), ctypes.byref(ba), heads_q))
+    ca, ba = _cache_arg(cache)[0], _batch_arg(batch, tokens)
+    return int(lib().kvq_attention_workspace_bytes(ca, ba, heads_q))
 
 
 _attn_ws = {}
@@ -813,10 +821,10 @@ def kvq_attention(Q, cache, batch, mask=None, scale: float = None, out=None, ws=
     of the call's own tokens those whose bit is set in mask [tokens] (int64 as 64
     bits; a tree's ancestors and itself), or without mask those up to itself.
     scale: 1 / sqrt(dim) by default."""
-    ca = _cache_arg(cache)
+    ca, heads, dim = _cache_arg(cache)
     _want(Q, torch.float16, "Q")
-    if Q.dim() != 3 or Q.shape[2] != ca.dim:
-        raise ValueError("Q must be [tokens][heads_q][%d]" % ca.dim)
+    if Q.dim() != 3 or Q.shape[2] != dim:
+        raise ValueError("Q must be [tokens][heads_q][%d]" % dim)
     n, hq, d = Q.shape
     ba = _batch_arg(batch, n)
     if mask is not None:
@@ -827,18 +835,17 @@ def kvq_attention(Q, cache, batch, mask=None, scale: float = None, out=None, ws=
         _want(out, torch.float16, "out", Q.shape)
     L = lib()
     stream = _stream(Q)
-    ca_p, ba_p = ctypes.byref(ca), ctypes.byref(ba)
     mine = ws is None
     if mine:
         ws = _stream_workspace(Q.device, stream)
     mp = None if mask is None else mask.data_ptr()
     scale = d ** -0.5 if scale is None else scale
     while True:
-        st = L.kvq_attention(ca_p, ba_p, Q.data_ptr(), hq, mp, scale, out.data_ptr(), _ptr(ws),
+        st = L.kvq_attention(ca, ba, Q.data_ptr(), hq, mp, scale, out.data_ptr(), _ptr(ws),
                              0 if ws is None else ws.numel() * ws.element_size(), flags, stream)
         if st != ERR_WORKSPACE or not mine:
             break
-        ws, mine = _stream_workspace(Q.device, stream, int(L.kvq_attention_workspace_bytes(ca_p, ba_p, hq))), False
+        ws, mine = _stream_workspace(Q.device, stream, int(L.kvq_attention_workspace_bytes(ca, ba, hq))), False
     _check(st)
     return out
 

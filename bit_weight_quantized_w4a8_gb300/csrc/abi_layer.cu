@@ -210,8 +210,10 @@ int kvq_read(const kvq_cache_t* cache, const kvq_batch_t* batch, void* K, void* 
     if (!is_type(y_type)) return fail(W4A8_ERR_SHAPE, "kvq_read: unknown type");
     if (!aligned(K, 16) || !aligned(V, 16)) return fail(W4A8_ERR_ALIGN, "kvq_read: K and V need 16-byte alignment");
     if ((st = check_flags("kvq_read", flags)) != W4A8_OK) return st;
+    int sms = 0;
+    if ((st = w4a8::status_sm_count(&sms)) != W4A8_OK) return st;
     return w4a8::status_done(
-        w4a8::launch_kvq_read(*cache, *batch, K, V, y_type, flags, static_cast<cudaStream_t>(stream)),
+        w4a8::launch_kvq_read(*cache, *batch, K, V, y_type, sms, flags, static_cast<cudaStream_t>(stream)),
         "kvq_read launch");
 }
 

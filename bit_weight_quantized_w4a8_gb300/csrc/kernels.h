@@ -112,8 +112,8 @@ cudaError_t launch_kvq_write(const kvq_cache_t& c, const kvq_batch_t& b, const v
                              int64_t ld_v, const void* Q, int64_t ld_q, int heads_q, int x_f16, const int32_t* pos,
                              const double* freqs, int rot, int inter, float mscale, uint16_t* Q_out, int sms,
                              unsigned flags, cudaStream_t stream);
-cudaError_t launch_kvq_read(const kvq_cache_t& c, const kvq_batch_t& b, void* K, void* V, int y_f16, unsigned flags,
-                            cudaStream_t stream);
+cudaError_t launch_kvq_read(const kvq_cache_t& c, const kvq_batch_t& b, void* K, void* V, int y_f16, int sms,
+                            unsigned flags, cudaStream_t stream);
 cudaError_t launch_kvq_keep(const kvq_cache_t& c, const kvq_batch_t& b, const int32_t* keep, unsigned flags,
                             cudaStream_t stream);
 // Rows of a (sequence, cache head) in blocks of 8 or 16 (kvq_attn.cu); many of

@@ -9,6 +9,7 @@
 // through one rounding to fp32 into sincospi.
 #include <type_traits>
 
+#include "actq.cuh"
 #include "kernels.h"
 #include "layer.cuh"
 
@@ -46,6 +47,7 @@ struct WriteArgs {
     int heads_q, tokens_per_cta;
     void* Y;  // rotated queries
     int64_t ld_y;
+    int y_wide;  // binary16 rows on 16 bytes: runs of 8 go out in one store
 };
 
 // A head's vector is spread over DIM / 8 lanes of 8 values in two runs of 4
@@ -72,14 +74,58 @@ __device__ __forceinline__ void rotate8(float4& a, float4& b, const float2* cs, 
     }
 }
 
-__device__ __forceinline__ uint32_t codes4(float4 v, float s, float top) {
+// Codes of four values, a byte each: clamp(round_half_away(x / s), +-top).
+// Exact form: an IEEE division and roundf per value.
+__device__ __noinline__ uint32_t codes4_exact(float4 v, float s, float top) {
     return (uint32_t)(layer_code(v.x, s, top) & 0xFF) | (uint32_t)(layer_code(v.y, s, top) & 0xFF) << 8 |
            (uint32_t)(layer_code(v.z, s, top) & 0xFF) << 16 | (uint32_t)(layer_code(v.w, s, top) & 0xFF) << 24;
 }
+// Fast form, with 1 / s bracketed by lo and hi (quant_bracket; both 0 for s =
+// 0): the IEEE quotient lies strictly between x lo and x hi, so where both round to
+// one integer that is the code, no tie is involved, and |x| <= top s up to
+// two roundings of s needs no clamp; the few others take the exact form.
+__device__ __forceinline__ uint32_t codes4(float4 v, float s, float top, float lo, float hi) {
+    constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: the sum's low bits hold the rounded product
+    const float x[4] = {v.x, v.y, v.z, v.w};
+    uint32_t y[4], diff = 0u;
+    #pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        y[k] = __float_as_uint(__fmaf_rn(x[k], lo, kMagic));
+        diff |= y[k] ^ __float_as_uint(__fmaf_rn(x[k], hi, kMagic));
+    }
+    if (diff != 0u) return codes4_exact(v, s, top);
+    return __byte_perm(__byte_perm(y[0], y[1], 0x0040), __byte_perm(y[2], y[3], 0x0040), 0x5410);
+}
 
-// Queries [0, heads_q) rotated to Y, keys and values quantized into the cache
+// Walks the (token, vector) pairs of a CTA, one per group of LPV lanes and two
+// at a time, without a division: `vecs` vectors of each token, `part` of `parts`
+// CTAs that share them.  Whole warps iterate together.
+template <int LPV>
+struct PairWalk {
+    int t, v, vecs, step_t, step_v, left, stride;
+    __device__ __forceinline__ PairWalk(int nt, int vecs_, int part, int parts) : vecs(vecs_) {
+        constexpr int GROUPS = kLayerThreads / LPV;
+        const int e = part * GROUPS + threadIdx.x / LPV;
+        t = e / vecs;
+        v = e - t * vecs;
+        stride = parts * GROUPS;
+        step_t = stride / vecs;
+        step_v = stride % vecs;
+        left = nt * vecs - part * GROUPS;  // pairs from the CTA's first group on
+    }
+    __device__ __forceinline__ void next() {
+        t += step_t;
+        v += step_v;
+        if (v >= vecs) v -= vecs, ++t;
+    }
+};
+
+// Queries [0, heads_q) rotated to Y, then keys and values quantized into the cache
 // (HAS_KV).  A CTA takes tokens_per_cta tokens (gridDim.y CTAs share their
-// vectors) and computes their cos and sin once for all heads.
+// vectors) and computes their cos and sin once for all heads, with the first
+// queries under way.  Queries come first, on their own: with the keys' slots, a chain of
+// loads, in front of every load and both kinds in one loop, 8190 tokens of 32 +
+// 2 heads took 44 us instead of 36.5 (a floor of 33).
 template <typename TX, typename TYO, int DIM, int BITS, bool HAS_KV>
 __global__ void __launch_bounds__(kLayerThreads) rope_write_kernel(const WriteArgs a) {
     constexpr int LPV = DIM / 8;
@@ -90,14 +136,34 @@ __global__ void __launch_bounds__(kLayerThreads) rope_write_kernel(const WriteAr
     const int t0 = blockIdx.x * a.tokens_per_cta;
     const int nt = min(a.tokens_per_cta, a.b.tokens - t0);
     const int pairs = a.rope.freqs != nullptr ? a.rope.rot / 2 : 0;
-    for (int e = threadIdx.x; e < nt * pairs; e += kLayerThreads) {
-        const int t = e / pairs, i = e - t * pairs;
-        cs[e] = turn_cos_sin(turn_fraction(a.rope.freqs[i]), a.rope.pos[t0 + t], a.rope.mscale);
-    }
+    const int l = threadIdx.x % LPV;
+    const bool half = !a.rope.inter && 8 * l < 2 * pairs;
+    // a lane's two runs of a turned vector, and of one that stays in order
+    const int oa = half ? 4 * l : 8 * l, ob = half ? pairs + 4 * l : 8 * l + 4;
+
+    float4 va[2], vb[2];
+    int vt[2], vv[2];
+    bool live[2];
+    auto load_q = [&](PairWalk<LPV>& w) {
+        #pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            vt[i] = w.t;
+            vv[i] = w.v;
+            live[i] = w.t < nt;
+            if (live[i]) {
+                const TX* x = static_cast<const TX*>(a.Q) + (int64_t)(t0 + w.t) * a.ld_q + (int64_t)w.v * DIM;
+                va[i] = load4(x + oa);
+                vb[i] = load4(x + ob);
+            }
+            w.next();
+        }
+    };
+    PairWalk<LPV> wq(nt, max(a.heads_q, 1), blockIdx.y, gridDim.y);
+    if (a.heads_q > 0) load_q(wq);
+    int64_t row = -1;
     if constexpr (HAS_KV) {
         if ((int)threadIdx.x < nt) {
             const int i = t0 + threadIdx.x;
-            int64_t row = -1;
             const int b = kvq_find_seq(a.b.cu, a.b.seqs, i);
             if (b >= 0) {
                 const int64_t st = a.b.start[b];
@@ -108,62 +174,85 @@ __global__ void __launch_bounds__(kLayerThreads) rope_write_kernel(const WriteAr
             slot_row[threadIdx.x] = row;
         }
     }
+    // the last threads, whose warps have no look-up to make, first
+    for (int e = kLayerThreads - 1 - (int)threadIdx.x; e < nt * pairs; e += kLayerThreads) {
+        const int t = e / pairs, i = e - t * pairs;
+        cs[e] = turn_cos_sin(turn_fraction(a.rope.freqs[i]), a.rope.pos[t0 + t], a.rope.mscale);
+    }
     __syncthreads();
-    const int l = threadIdx.x % LPV;
-    const bool half = !a.rope.inter && 8 * l < 2 * pairs;
-    const int oa = half ? 4 * l : 8 * l, ob = half ? pairs + 4 * l : 8 * l + 4;
-    const int vecs = a.heads_q + (HAS_KV ? 2 * a.c.heads : 0);
-    // whole warps iterate together (the reductions below are warp-wide)
-    const int groups = kLayerThreads / LPV;
-    const int total = nt * vecs;
-    for (int base = blockIdx.y * groups; base < total; base += gridDim.y * groups) {
-        const int e = base + threadIdx.x / LPV;
-        const bool live = e < total;
-        const int t = live ? e / vecs : 0, h = live ? e - t * vecs : 0;
-        const int64_t tok = t0 + t;
-        const bool is_q = h < a.heads_q;
-        const int kv = is_q ? 0 : (h - a.heads_q) / a.c.heads;  // 0 key, 1 value
-        const int hk = is_q ? 0 : (h - a.heads_q) - kv * a.c.heads;
-        const TX* x = is_q ? static_cast<const TX*>(a.Q) + tok * a.ld_q + (int64_t)h * DIM
-                      : kv ? static_cast<const TX*>(a.V) + tok * a.ld_v + (int64_t)hk * DIM
-                           : static_cast<const TX*>(a.K) + tok * a.ld_k + (int64_t)hk * DIM;
-        float4 va = make_float4(0.f, 0.f, 0.f, 0.f), vb = va;
-        const bool turned = (is_q || kv == 0) && 8 * l < 2 * pairs;
-        // a value's vector has no pairs: its runs stay in order
-        const int pa = turned ? oa : 8 * l, pb = turned ? ob : 8 * l + 4;
-        if (live) {
-            va = load4(x + pa);
-            vb = load4(x + pb);
-        }
-        if (turned) rotate8(va, vb, cs + t * pairs + 4 * l, a.rope.inter);
-        if (is_q && live) {
-            TYO* y = static_cast<TYO*>(a.Y) + tok * a.ld_y + (int64_t)h * DIM;
-            store4(y + pa, va);
-            store4(y + pb, vb);
-        }
-        if constexpr (HAS_KV) {
-            float m = fmaxf(absmax4(va), absmax4(vb));
+    if (a.heads_q > 0) {
+        for (;;) {
             #pragma unroll
-            for (int o = LPV / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            if (!is_q && live && slot_row[t] >= 0) {
-                constexpr float top = BITS == 8 ? 127.f : 7.f;
-                const float s = __fmul_rn(m, 1.f / top);
-                const int64_t vec = kvq_vec(a.c, slot_row[t], hk);
-                const uint32_t qa = codes4(va, s, top), qb = codes4(vb, s, top);
-                uint8_t* codes = (kv ? a.c.v : a.c.k) + vec * (DIM * BITS / 8);
-                if constexpr (BITS == 8) {
-                    *reinterpret_cast<uint32_t*>(codes + pa) = qa;
-                    *reinterpret_cast<uint32_t*>(codes + pb) = qb;
+            for (int i = 0; i < 2; ++i) {
+                if (!live[i]) continue;
+                if (8 * l < 2 * pairs) rotate8(va[i], vb[i], cs + vt[i] * pairs + 4 * l, a.rope.inter);
+                TYO* y = static_cast<TYO*>(a.Y) + (int64_t)(t0 + vt[i]) * a.ld_y + (int64_t)vv[i] * DIM;
+                if (sizeof(TYO) == 2 && ob == oa + 4 && a.y_wide) {
+                    *reinterpret_cast<uint4*>(y + oa) = make_uint4(pack_half2(va[i].x, va[i].y), pack_half2(va[i].z, va[i].w),
+                                                                   pack_half2(vb[i].x, vb[i].y), pack_half2(vb[i].z, vb[i].w));
                 } else {
-                    auto pack = [](uint32_t q) {  // low nibbles of 4 bytes -> 16 bits
-                        q &= 0x0F0F0F0Fu;
-                        q |= q >> 4;
-                        return (uint16_t)((q & 0xFFu) | ((q >> 8) & 0xFF00u));
-                    };
-                    *reinterpret_cast<uint16_t*>(codes + pa / 2) = pack(qa);
-                    *reinterpret_cast<uint16_t*>(codes + pb / 2) = pack(qb);
+                    store4(y + oa, va[i]);
+                    store4(y + ob, vb[i]);
                 }
-                if (l == 0) (kv ? a.c.vs : a.c.ks)[vec] = s;
+            }
+            wq.left -= 2 * wq.stride;
+            if (wq.left <= 0) break;
+            load_q(wq);
+        }
+    }
+    if constexpr (HAS_KV) {
+        const int kv_heads = a.c.heads;
+        // the CTAs with the fewest queries first
+        PairWalk<LPV> w(nt, 2 * kv_heads, gridDim.y - 1 - blockIdx.y, gridDim.y);
+        for (; w.left > 0; w.left -= 2 * w.stride) {
+            int pa[2], pb[2];
+            #pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                vt[i] = w.t;
+                vv[i] = w.v;
+                live[i] = w.t < nt;
+                const bool turned = w.v < kv_heads && 8 * l < 2 * pairs;  // a value has no pairs
+                pa[i] = turned ? oa : 8 * l;
+                pb[i] = turned ? ob : 8 * l + 4;
+                va[i] = vb[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (live[i]) {
+                    const int64_t tok = t0 + w.t;
+                    const TX* x = w.v < kv_heads ? static_cast<const TX*>(a.K) + tok * a.ld_k + (int64_t)w.v * DIM
+                                                 : static_cast<const TX*>(a.V) + tok * a.ld_v + (int64_t)(w.v - kv_heads) * DIM;
+                    va[i] = load4(x + pa[i]);
+                    vb[i] = load4(x + pb[i]);
+                }
+                w.next();
+            }
+            #pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int kv = vv[i] >= kv_heads;  // 0 key, 1 value
+                if (live[i] && !kv && 8 * l < 2 * pairs) rotate8(va[i], vb[i], cs + vt[i] * pairs + 4 * l, a.rope.inter);
+                float m = fmaxf(absmax4(va[i]), absmax4(vb[i]));
+                #pragma unroll
+                for (int o = LPV / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                if (live[i] && slot_row[vt[i]] >= 0) {
+                    constexpr float top = BITS == 8 ? 127.f : 7.f;
+                    const float s = __fmul_rn(m, 1.f / top);
+                    float lo, hi;
+                    quant_bracket(s, &lo, &hi);
+                    const int64_t vec = kvq_vec(a.c, slot_row[vt[i]], vv[i] - kv * kv_heads);
+                    const uint32_t qa = codes4(va[i], s, top, lo, hi), qb = codes4(vb[i], s, top, lo, hi);
+                    uint8_t* codes = (kv ? a.c.v : a.c.k) + vec * (DIM * BITS / 8);
+                    if constexpr (BITS == 8) {
+                        *reinterpret_cast<uint32_t*>(codes + pa[i]) = qa;
+                        *reinterpret_cast<uint32_t*>(codes + pb[i]) = qb;
+                    } else {
+                        auto pack = [](uint32_t q) {  // low nibbles of 4 bytes -> 16 bits
+                            q &= 0x0F0F0F0Fu;
+                            q |= q >> 4;
+                            return (uint16_t)((q & 0xFFu) | ((q >> 8) & 0xFF00u));
+                        };
+                        *reinterpret_cast<uint16_t*>(codes + pa[i] / 2) = pack(qa);
+                        *reinterpret_cast<uint16_t*>(codes + pb[i] / 2) = pack(qb);
+                    }
+                    if (l == 0) (kv ? a.c.vs : a.c.ks)[vec] = s;
+                }
             }
         }
     }
@@ -172,6 +261,7 @@ __global__ void __launch_bounds__(kLayerThreads) rope_write_kernel(const WriteAr
 template <typename TX, typename TYO, int BITS, bool HAS_KV>
 cudaError_t launch_write(const WriteArgs& a0, int dim, int sms, unsigned flags, cudaStream_t stream) {
     WriteArgs a = a0;
+    a.y_wide = reinterpret_cast<uintptr_t>(a.Y) % 16 == 0 && a.ld_y % 8 == 0;
     const int vecs = a.heads_q + (HAS_KV ? 2 * a.c.heads : 0);
     a.tokens_per_cta = a.b.tokens >= 8 * sms ? 4 : 1;
     const int ctas = (a.b.tokens + a.tokens_per_cta - 1) / a.tokens_per_cta;
@@ -192,17 +282,22 @@ cudaError_t launch_write(const WriteArgs& a0, int dim, int sms, unsigned flags, 
 // read back
 // ---------------------------------------------------------------------------
 
-constexpr int kReadTokens = 16;
-
+// A CTA reads per_cta tokens; a thread takes 8 values of a key and of the value,
+// so that a warp's stores are whole lines (16 values in two stores each took
+// 104 us instead of 84 at 200,000 tokens of 4 heads and 4 bits, a floor of 76), of
+// two vectors at a time, and steps through (token, head) without a division.
+constexpr int kReadTokens = 32;
 template <typename TO, int DIM, int BITS>
-__global__ void __launch_bounds__(kLayerThreads) kvq_read_kernel(const KvqCacheArg c, const KvqBatchArg b, TO* K,
-                                                            TO* V) {
-    constexpr int UPV = DIM / 8;  // units of 8 values per vector
+__global__ void __launch_bounds__(kLayerThreads) kvq_read_kernel(const KvqCacheArg c, const KvqBatchArg b, int per_cta,
+                                                                 TO* K, TO* V) {
+    constexpr int UPV = DIM / 8;                   // units of 8 values per vector
+    constexpr int STEP = kLayerThreads / UPV;      // vectors that a pass of the CTA takes
+    constexpr int U = 2;
     __shared__ int64_t slot_row[kReadTokens];
     griddep_launch_dependents();
     griddep_wait();
-    const int t0 = blockIdx.x * kReadTokens;
-    const int nt = min(kReadTokens, b.tokens - t0);
+    const int t0 = blockIdx.x * per_cta;
+    const int nt = min(per_cta, b.tokens - t0);
     if ((int)threadIdx.x < nt) {
         const int i = t0 + threadIdx.x;
         int64_t row = -1;
@@ -213,27 +308,53 @@ __global__ void __launch_bounds__(kLayerThreads) kvq_read_kernel(const KvqCacheA
         slot_row[threadIdx.x] = row;
     }
     __syncthreads();
-    const int units = c.heads * UPV;
-    for (int e = threadIdx.x; e < 2 * nt * units; e += kLayerThreads) {
-        const int kv = e >= nt * units, r = e - kv * nt * units;
-        const int t = r / units, u = r - t * units;
-        if (slot_row[t] < 0) continue;
-        const int64_t vec = kvq_vec(c, slot_row[t], u / UPV);
-        const float s = (kv ? c.vs : c.ks)[vec];
-        const uint8_t* p = (kv ? c.v : c.k) + vec * (DIM * BITS / 8) + (u % UPV) * BITS;
-        float v[8];
-        if constexpr (BITS == 8) {
-            const uint2 w = *reinterpret_cast<const uint2*>(p);
+    const int u = threadIdx.x % UPV;
+    const int step_t = STEP / c.heads, step_h = STEP % c.heads;
+    int t = threadIdx.x / UPV / c.heads, h = threadIdx.x / UPV % c.heads;
+    while (t < nt) {
+        uint32_t w[U][2][BITS / 4];  // [vector][key, value]
+        float s[U][2];
+        int at[U];  // vector of the CTA's, -1: none
+        #pragma unroll
+        for (int x = 0; x < U; ++x) {
+            const int64_t row = t < nt ? slot_row[t] : -1;
+            at[x] = row >= 0 ? t * c.heads + h : -1;
+            const int64_t vec = row >= 0 ? kvq_vec(c, row, h) : 0;
             #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = (float)(int8_t)((k < 4 ? w.x : w.y) >> (8 * (k & 3))) * s;
-        } else {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-            #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = (float)((int32_t)(w << (28 - 4 * k)) >> 28) * s;
+            for (int kv = 0; kv < 2; ++kv) {
+                const uint8_t* p = (kv ? c.v : c.k) + vec * (DIM * BITS / 8) + u * BITS;
+                if constexpr (BITS == 8) {
+                    const uint2 q = *reinterpret_cast<const uint2*>(p);
+                    w[x][kv][0] = q.x, w[x][kv][1] = q.y;
+                } else {
+                    w[x][kv][0] = *reinterpret_cast<const uint32_t*>(p);
+                }
+                s[x][kv] = (kv ? c.vs : c.ks)[vec];
+            }
+            t += step_t;
+            h += step_h;
+            if (h >= c.heads) h -= c.heads, ++t;
         }
-        TO* o = (kv ? V : K) + ((int64_t)(t0 + t) * units + u) * 8;
-        store4(o, make_float4(v[0], v[1], v[2], v[3]));
-        store4(o + 4, make_float4(v[4], v[5], v[6], v[7]));
+        #pragma unroll
+        for (int x = 0; x < U; ++x)
+            #pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                if (at[x] < 0) continue;
+                float v[8];
+                #pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    constexpr int PER = 32 / BITS;  // codes of a word
+                    v[k] = (float)((int32_t)(w[x][kv][k / PER] << (32 - BITS - BITS * (k % PER))) >> (32 - BITS)) * s[x][kv];
+                }
+                TO* o = (kv ? V : K) + ((int64_t)t0 * c.heads + at[x]) * DIM + 8 * u;
+                if constexpr (sizeof(TO) == 2) {
+                    *reinterpret_cast<uint4*>(o) = make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]),
+                                                              pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
+                } else {
+                    store4(o, make_float4(v[0], v[1], v[2], v[3]));
+                    store4(o + 4, make_float4(v[4], v[5], v[6], v[7]));
+                }
+            }
     }
 }
 
@@ -333,15 +454,16 @@ cudaError_t launch_kvq_write(const kvq_cache_t& c, const kvq_batch_t& b, const v
                        : launch_write<float, __half, 4, true>(a, c.dim, sms, flags, stream);
 }
 
-cudaError_t launch_kvq_read(const kvq_cache_t& cc, const kvq_batch_t& bb, void* K, void* V, int y_f16,
+cudaError_t launch_kvq_read(const kvq_cache_t& cc, const kvq_batch_t& bb, void* K, void* V, int y_f16, int sms,
                             unsigned flags, cudaStream_t stream) {
     const KvqCacheArg c = cache_arg(cc);
     const KvqBatchArg b = batch_arg(bb);
-    const dim3 grid((unsigned)((b.tokens + kReadTokens - 1) / kReadTokens));
+    const int per_cta = b.tokens >= 64 * sms ? kReadTokens : 8;
+    const dim3 grid((unsigned)(((int64_t)b.tokens + per_cta - 1) / per_cta));
     auto go = [&](auto* out, auto dim, auto bits) {
         using T = std::remove_pointer_t<decltype(out)>;
         return layer_launch(kvq_read_kernel<T, decltype(dim)::value, decltype(bits)::value>, grid, kLayerThreads, 0, flags,
-                            stream, c, b, static_cast<T*>(K), static_cast<T*>(V));
+                            stream, c, b, per_cta, static_cast<T*>(K), static_cast<T*>(V));
     };
     auto by_bits = [&](auto* out, auto dim) {
         return cc.bits == 8 ? go(out, dim, std::integral_constant<int, 8>()) : go(out, dim, std::integral_constant<int, 4>());
