@@ -294,8 +294,17 @@ def check_attention(w4, rng, pg, q, c, host, hq, heads, dim, mask, scale, got, s
             assert off[i] <= 0, "sequence %d head %d row %s: got %r, want %r, bound %.3g" % (b, h, i, have[i], want[i], err[i])
 
 
-def run_attention(w4, rng, tok, ctx, page, hq, heads, dim, bits, tree, qstd=1.0, empty=(), spread=0.3):
-    pg = ref.Paged(rng, tok, ctx, page)
+# A table this wide (slots times heads) leaves a call of 49 rows or more of a cache
+# head to the kernel for many rows, whatever the lengths.
+WIDE = 500_000
+
+
+def wide_cols(seqs, heads, page):
+    return -(-WIDE // (seqs * heads * page))
+
+
+def run_attention(w4, rng, tok, ctx, page, hq, heads, dim, bits, tree, qstd=1.0, empty=(), spread=0.3, wide=False):
+    pg = ref.Paged(rng, tok, ctx, page, extra_cols=wide_cols(len(tok), heads, page) if wide else 1)
     c, gs, host = fill(w4, rng, pg, heads, dim, bits, spread)
     q = (qstd * rng.standard_normal((pg.tokens, hq, dim))).astype(F16)
     mask = ref.tree_masks(rng, tok, empty) if tree else None
@@ -340,6 +349,157 @@ def test_attention_head_groups(w4, hq, heads):
 def test_attention_flat_and_peaked(w4, qstd, spread):
     """All logits equal; logits that leave one key; scales over a wide range."""
     run_attention(w4, np.random.default_rng(3), (4, 1), (500, 90), 32, 14, 2, 128, 8, True, qstd=qstd, spread=spread)
+
+
+@pytest.mark.parametrize("dim,bits", [(128, 8), (128, 4), (64, 8), (64, 4)])
+@pytest.mark.parametrize("hq,heads,page", [(28, 4, 64), (32, 2, 16), (64, 1, 256), (48, 3, 32)])
+@pytest.mark.parametrize("tok,ctx,tree", [((8,), (0,), True), ((64,), (1,), True), ((17, 0, 20), (31, 9, 500), True),
+                                          ((33, 1, 40), (300, 128, 127), False), ((64, 50), (2000, 1023), True),
+                                          ((100,), (57,), False), ((9,), (9000,), True)])
+def test_attention_many_rows(w4, dim, bits, hq, heads, page, tok, ctx, tree):
+    """The kernel for many rows: one and two tiles a row block, whole and shared
+    by CTAs, blocks of keys that end inside."""
+    rng = np.random.default_rng(dim + bits + hq + sum(tok) + sum(ctx) + 1)
+    run_attention(w4, rng, tok, ctx, page, hq, heads, dim, bits, tree, wide=True)
+
+
+def test_attention_many_rows_routes(w4):
+    """Wide and narrow tables take the two kernels (their workspaces tell them apart)."""
+    rng = np.random.default_rng(0)
+    need = []
+    for cols in (1, wide_cols(1, 4, 64)):
+        pg = ref.Paged(rng, (64,), (10,), 64, extra_cols=cols)
+        c, _ = make_cache(w4, pg, 4, 128, 8)
+        need.append(w4.kvq_attention_workspace_bytes(c, make_batch(w4, pg), 64, 28))
+    assert need[0] < need[1]
+    pg = ref.Paged(rng, (64,), (10,), 64, extra_cols=wide_cols(1, 4, 64))
+    c, _ = make_cache(w4, pg, 4, 256, 8)  # 256 dimensions: row blocks always
+    assert w4.kvq_attention_workspace_bytes(c, make_batch(w4, pg), 64, 28) < need[1]
+
+
+@pytest.mark.parametrize("qstd,spread", [(0.0, 0.0), (30.0, 0.3), (1e-4, 2.0), (1000.0, 0.0), (3.0, 4.0)])
+@pytest.mark.parametrize("tok", [(5, 9), (30, 20)])
+def test_attention_many_rows_flat_and_peaked(w4, qstd, spread, tok):
+    run_attention(w4, np.random.default_rng(4), tok, (900, 90), 32, 32, 2, 128, 8, True, qstd=qstd, spread=spread, wide=True)
+
+
+def test_attention_many_rows_growing_logits(w4):
+    """Keys whose logits rise along the sequence: every block raises the
+    references and rescales what was summed before."""
+    rng = np.random.default_rng(5)
+    tok, ctx, hq, heads, dim = (6, 3), (1500, 700), 32, 2, 128
+    pg = ref.Paged(rng, tok, ctx, 64, extra_cols=wide_cols(2, heads, 64))
+    c, _, host = fill(w4, rng, pg, heads, dim, 8)
+    (kq, ks), (vq, vs) = host
+    for b in range(2):
+        p, o = pg.where(b, np.arange(tok[b] + ctx[b]))
+        ks[p, :, o] *= np.linspace(0.01, 12.0, len(p)).astype(F32)[:, None]
+        vs[p, :, o] *= np.exp2(np.linspace(-12, 6, len(p))).astype(F32)[:, None]
+    c.ks.copy_(dev(ks))
+    c.vs.copy_(dev(vs))
+    q = rng.standard_normal((9, hq, dim)).astype(F16)
+    mask = ref.tree_masks(rng, tok)
+    out = w4.kvq_attention(dev(q), c, make_batch(w4, pg), mask=dev(mask.view(np.int64)))
+    check_attention(w4, rng, pg, q, c, host, hq, heads, dim, mask, dim ** -0.5, out)
+
+
+def test_attention_many_rows_that_see_nothing(w4):
+    rng = np.random.default_rng(6)
+    out = run_attention(w4, rng, (6, 8), (0, 0), 16, 32, 2, 128, 8, True, empty=(2, 5, 6, 7, 8), wide=True)
+    assert not out[[2, 5, 6, 7, 8]].any() and bool(out[0].any())
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("which", ["k", "v", "both"])
+def test_attention_many_rows_bad_scales_in_masked_keys(w4, bits, bad, which):
+    rng = np.random.default_rng(7)
+    tok, ctx, hq, heads, dim = (5, 6), (170, 3), 32, 2, 128
+    pg = ref.Paged(rng, tok, ctx, 16, extra_cols=wide_cols(2, heads, 16))
+    c, _, host = fill(w4, rng, pg, heads, dim, bits)
+    mask = ref.tree_masks(rng, tok)
+    mask[:5] &= ~np.uint64(4)  # nobody but token 2 sees token 2
+    mask[2] |= np.uint64(4)
+    p, o = pg.where(0, [ctx[0] + 2])
+    q = rng.standard_normal((pg.tokens, hq, dim)).astype(F16)
+    if which != "v":
+        c.ks[int(p[0]), :, int(o[0])] = bad
+    if which != "k":
+        c.vs[int(p[0]), :, int(o[0])] = bad
+    out = w4.kvq_attention(dev(q), c, make_batch(w4, pg), mask=dev(mask.view(np.int64)))
+    assert bool(torch.isfinite(out[[0, 1, 3, 4, 5, 6, 7, 8, 9, 10]]).all())
+    assert not bool(torch.isfinite(out[2]).all())  # who sees it has it
+    check_attention(w4, rng, pg, q, c, host, hq, heads, dim, mask, dim ** -0.5, out, rows_off=(2,))
+
+
+def test_attention_many_rows_zero_scales(w4):
+    """Zero values weigh and add nothing; zero keys (scale 0) have logit 0."""
+    rng = np.random.default_rng(8)
+    tok, heads = (4, 5), 2
+    pg = ref.Paged(rng, tok, (150, 0), 32, extra_cols=wide_cols(2, heads, 32))
+    c, _, host = fill(w4, rng, pg, heads, 128, 8)
+    q = rng.standard_normal((9, 32, 128)).astype(F16)
+    host[0][1][:, :, 1::4] = 0
+    host[0][0][:, :, 1::4] = 0
+    c.ks[:, :, 1::4] = 0
+    c.k[:, :, 1::4] = 0
+    for zero in (slice(None, None, 3), slice(None)):
+        host[1][1][:, :, zero] = 0
+        c.vs[:, :, zero] = 0
+        out = w4.kvq_attention(dev(q), c, make_batch(w4, pg))
+        check_attention(w4, rng, pg, q, c, host, 32, heads, 128, None, 128 ** -0.5, out)
+    assert not out.any()
+
+
+def test_attention_scale_signs(w4):
+    """A negative, a zero and a large factor of the logits, both kernels."""
+    rng = np.random.default_rng(9)
+    for wide, hq in ((False, 8), (True, 64)):
+        pg = ref.Paged(rng, (3, 2), (140, 5), 32, extra_cols=wide_cols(2, 2, 32) if wide else 1)
+        c, _, host = fill(w4, rng, pg, 2, 128, 8)
+        q = rng.standard_normal((5, hq, 128)).astype(F16)
+        for scale in (-0.1, 0.0, 3.0):
+            out = w4.kvq_attention(dev(q), c, make_batch(w4, pg), scale=scale)
+            check_attention(w4, rng, pg, q, c, host, hq, 2, 128, None, scale, out)
+
+
+def test_attention_many_rows_bad_pages_and_graph(w4):
+    """A page out of range is seen by nobody and sets the error word; a captured
+    call follows lengths changed between replays."""
+    rng = np.random.default_rng(10)
+    tok, ctx, hq, heads, dim = (6, 7), (300, 500), 32, 2, 128
+    pg = ref.Paged(rng, tok, ctx, 32, extra_cols=wide_cols(2, heads, 32))
+    c, _, host = fill(w4, rng, pg, heads, dim, 8)
+    q = rng.standard_normal((13, hq, dim)).astype(F16)
+    qd = dev(q)
+    for entry in (-1, pg.pages, 2 ** 31 - 1, -2 ** 31):
+        table = pg.table.copy()
+        table[1, 3] = entry
+        out = w4.kvq_attention(qd, c, w4.KVQBatch(dev(pg.cu), dev(pg.start), dev(table)))
+        assert w4.w4a8_device_error() == 8
+        assert bool(torch.isfinite(out).all())
+        check_attention(w4, rng, pg, q, c, host, hq, heads, dim, None, dim ** -0.5, out, skip=(1,))
+        # sequence 1 as if the page's slots were not there
+        (kq, ks), (vq, vs) = host
+        slots = np.array([j for j in range(507) if not 96 <= j < 128])
+        p, o = pg.where(1, slots)
+        seen = np.repeat(ref.seen_of(pg, 1, None)[:, slots], hq // heads, 0)
+        for h in range(heads):
+            rows = q[6:, h * 16:(h + 1) * 16].reshape(-1, dim)
+            want, err = ref.attention(rows, kq[p, h, o], ks[p, h, o], vq[p, h, o], vs[p, h, o], seen, dim ** -0.5)
+            got = out[6:, h * 16:(h + 1) * 16].cpu().numpy().reshape(-1, dim)
+            assert np.all(np.abs(got - want) <= err)
+    b = make_batch(w4, pg)
+    w4.kvq_attention(qd, c, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = w4.kvq_attention(qd, c, b)
+    for new in ((300, 500), (2, 444), (0, 0), (127, 128)):
+        b.start.copy_(dev(np.array(new, np.int32)))
+        graph.replay()
+        assert torch.equal(out, w4.kvq_attention(qd, c, b))
+        pg.ctx, pg.start = list(new), np.array(new, np.int32)
+        check_attention(w4, rng, pg, q, c, host, hq, heads, dim, None, dim ** -0.5, out)
 
 
 def test_attention_rows_that_see_nothing(w4):
