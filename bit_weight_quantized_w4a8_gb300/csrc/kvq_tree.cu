@@ -45,12 +45,12 @@ constexpr float kTop = 10.f;     // log2 of the weight of a fresh maximum
 constexpr float kSlack = 4.f;    // log2 of what it may grow by before O is rescaled
 
 struct alignas(16) BlockScales {  // read as 16-byte vectors
-    float k[kBlock];        // ks * scale * log2(e), never 0
-    float v[kBlock];        // vs, 0 where one of the two is not finite
+    float k[kBlock];        // ks * scale * log2(e), never 0, of the scale's sign
+    float v[kBlock];        // vs, 0 where one of the two is bad: not finite, or ks below 0
     float vmax[8];          // largest |v| of keys 16 w .. 16 w + 15
     uint32_t odd[8];        // not 0: some of them is not there or bad
     uint16_t valid[8];      // bit i of word w: key 16 w + i is there
-    uint16_t bad[8];        // it has a scale that is not finite
+    uint16_t bad[8];        // it has a bad scale
 };
 
 struct TreeShared {
@@ -320,9 +320,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                     // a factor of 0 would make NaN of an unseen key's -inf; a key of zeros
                     // has logit 0 with any
                     const float kk = sk * a.scale_log2;
-                    const bool fine = fabsf(kk) < INFINITY && fabsf(sv) < INFINITY;
+                    const bool fine = fabsf(kk) < INFINITY && fabsf(sv) < INFINITY && sk >= 0.f;
                     if (lane < 16) {
-                        bs.k[key] = fine && kk != 0.f ? kk : 1e-30f;
+                        bs.k[key] = fine && kk != 0.f ? kk : a.scale_log2 < 0.f ? -1e-30f : 1e-30f;
                         bs.v[key] = fine ? sv : 0.f;
                     }
                     const unsigned bad = __ballot_sync(0xFFFFFFFFu, !fine) & 0xFFFFu;
@@ -358,18 +358,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
         } else {
             // the queries of the block's rows, in the widened keys' order of dimensions, and
             // what the rows see of the drafted tokens
-            #pragma unroll 8
-            for (int e = tid; e < t.tiles * kRowsTile * (DIM / 8); e += kSoftWarps * 32) {
-                const int r = e / (DIM / 8), c = e % (DIM / 8);
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (r < t.rows) {
-                    const int row = t.row0 + r, tok = row / a.group;
-                    x = *reinterpret_cast<const uint4*>(a.Q + ((int64_t)(t.s.first + tok) * a.heads_q + t.h * a.group + row - tok * a.group) * DIM + 8 * c);
+            {
+                constexpr int kRowsAt = kSoftWarps * 32 / (DIM / 8);  // rows of one pass
+                constexpr int kPasses = 2 * kRowsTile / kRowsAt;
+                const int c = tid % (DIM / 8), step_tok = kRowsAt / a.group, step_head = kRowsAt % a.group;
+                int r = tid / (DIM / 8), tok = (t.row0 + r) / a.group, head = (t.row0 + r) % a.group;
+                uint4 x[kPasses];
+                #pragma unroll
+                for (int i = 0; i < kPasses; ++i) {
+                    x[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r + kRowsAt * i < t.rows)
+                        x[i] = *reinterpret_cast<const uint4*>(a.Q + ((int64_t)(t.s.first + tok) * a.heads_q + t.h * a.group + head) * DIM + 8 * c);
+                    tok += step_tok;
+                    head += step_head;
+                    if (head >= a.group) head -= a.group, ++tok;
                 }
-                if constexpr (BITS == 4)
-                    x = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
-                                   __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
-                sts16(base + C::kOffQ + (r / kRowsTile) * C::kTileBytes + tile_off(r % kRowsTile, c), x.x, x.y, x.z, x.w);
+                #pragma unroll
+                for (int i = 0; i < kPasses; ++i, r += kRowsAt) {
+                    if (r >= t.tiles * kRowsTile) break;
+                    if constexpr (BITS == 4)
+                        x[i] = make_uint4(__byte_perm(x[i].x, x[i].z, 0x5410), __byte_perm(x[i].x, x[i].z, 0x7632),
+                                          __byte_perm(x[i].y, x[i].w, 0x5410), __byte_perm(x[i].y, x[i].w, 0x7632));
+                    sts16(base + C::kOffQ + (r / kRowsTile) * C::kTileBytes + tile_off(r % kRowsTile, c), x[i].x, x[i].y, x[i].z, x[i].w);
+                }
             }
             if (tid < t.tiles * kRowsTile) {
                 const int tok = (t.row0 + min(tid, t.rows - 1)) / a.group;
@@ -477,41 +488,36 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                 bool up = false;
                 if (work) {
                     tc_fence_after_sync();
-                    if (!plain) {
-                        // S of an unseen key becomes what its factor takes to -inf, S of a seen
-                        // key with a scale that is not finite NaN
-                        #pragma unroll 1
-                        for (int e = 0; e < 4; ++e) {
-                            const int c = e >> 1, hb = e & 1;
-                            uint32_t s[16];
-                            tmem_ld_frag32(ts + 32 * c + hb * kHalfLanes, s);
-                            uint32_t see[2];
-                            #pragma unroll
-                            for (int rr = 0; rr < 2; ++rr) {
-                                const int r = 32 * quad + 16 * hb + 8 * rr + (lane >> 2);
-                                see[rr] = reinterpret_cast<const uint32_t*>(bs.valid)[2 * half + c] & seen_bits(k0 + 64 * half + 32 * c - start, a.mask != nullptr, sh.word[tl][r], sh.tok[tl][r]);
-                            }
-                            const uint32_t bad = reinterpret_cast<const uint32_t*>(bs.bad)[2 * half + c];
-                            tmem_ld_wait();
-                            #pragma unroll
-                            for (int x = 0; x < 16; ++x) {
-                                const int key = 8 * (x >> 2) + 2 * (lane & 3) + (x & 1);
-                                if (!((see[(x >> 1) & 1] >> key) & 1))
-                                    s[x] = __float_as_uint(copysignf(INFINITY, -bs.k[64 * half + 32 * c + key]));
-                                else if ((bad >> key) & 1)
-                                    s[x] = 0x7FFFFFFFu;
-                            }
-                            tmem_st_frag32(ts + 32 * c + hb * kHalfLanes, s);
-                        }
-                        tmem_st_wait();
-                    }
-                    // the maxima of this thread's keys, rows k
+                    // the maxima of this thread's keys, rows k; first, in blocks that need it, S of
+                    // an unseen key becomes what its factor takes to -inf, and S of a seen key
+                    // with a bad scale NaN
+                    const float unseen = a.scale_log2 < 0.f ? INFINITY : -INFINITY;
                     #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int c = e >> 1, hb = e & 1;
                         uint32_t s[16];
                         tmem_ld_frag32(ts + 32 * c + hb * kHalfLanes, s);
-                        tmem_ld_wait();
+                        if (plain) {
+                            tmem_ld_wait();
+                        } else {
+                            const uint32_t bad = reinterpret_cast<const uint32_t*>(bs.bad)[2 * half + c] >> (2 * (lane & 3));
+                            uint32_t see[2];
+                            #pragma unroll
+                            for (int rr = 0; rr < 2; ++rr) {
+                                const int r = 32 * quad + 16 * hb + 8 * rr + (lane >> 2);
+                                see[rr] = (reinterpret_cast<const uint32_t*>(bs.valid)[2 * half + c] &
+                                           seen_bits(k0 + 64 * half + 32 * c - start, a.mask != nullptr, sh.word[tl][r], sh.tok[tl][r])) >> (2 * (lane & 3));
+                            }
+                            tmem_ld_wait();
+                            #pragma unroll
+                            for (int x = 0; x < 16; ++x) {
+                                constexpr uint32_t one = 1;
+                                const uint32_t bit = one << (8 * (x >> 2) + (x & 1));
+                                if (!(see[(x >> 1) & 1] & bit)) s[x] = __float_as_uint(unseen);
+                                else if (bad & bit) s[x] = 0x7FFFFFFFu;
+                            }
+                            tmem_st_frag32(ts + 32 * c + hb * kHalfLanes, s);
+                        }
                         #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const uint64_t kk = *reinterpret_cast<const uint64_t*>(kf + 32 * c + 8 * j);
@@ -522,6 +528,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                             }
                         }
                     }
+                    if (!plain) tmem_st_wait();
                     #pragma unroll
                     for (int k = 0; k < 4; ++k) up |= top[k] - M[k] + ve > kTop + kSlack;
                 }
@@ -601,13 +608,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                 }
                 __syncwarp();
                 if (first) {
+                    // of two tiles the next keys do not depend on this product (of one,
+                    // its other slot's values do, and they come in before those keys)
+                    const bool more = i + 1 < my_jobs;
+                    ok = ok && wait(sh.vfull[blk & 1], blk >> 1) && (!two || !more || wait_keys(i + 1));
                     named_bar_sync(1 + slot, kSlotWarps * 32);
-                    ok = ok && wait(sh.vfull[blk & 1], blk >> 1);
                     if (ok) {
                         tc_fence_after_sync();
                         pv(i);
                         release(sh.vfree, i);
-                        if (i + 1 < my_jobs && (ok = wait_keys(i + 1))) {
+                        if (more && (two || (ok = wait_keys(i + 1)))) {
                             tc_fence_after_sync();
                             qk();
                             release(sh.kfree, i + 1);
