@@ -79,7 +79,11 @@ template <int DIM, int BITS, int NR>
 struct Cfg {
     static constexpr int W = DIM * BITS / 8;                // bytes of a vector
     static constexpr int kStageBytes = 2 * kStep * W + 2 * kStep * 4;
-    static constexpr int kStages = W >= 256 ? 3 : W == 128 ? 3 : 4;
+    // three CTAs an SM where the registers of 8 rows allow it, with a stage less
+    // each: 24 sequences of 28 / 4 heads of 128 114.8 -> 113.6 us, 4 bits 112 -> 106, 8 / 8
+    // heads of 64 138 -> 122
+    static constexpr int kCtas = NR == 1 && DIM <= 128 ? 3 : W <= 128 ? 2 : 1;
+    static constexpr int kStages = W >= 256 ? 3 : W == 128 ? (kCtas == 3 ? 2 : 3) : (kCtas == 3 ? 3 : 4);
     static constexpr int kRing = kWarps * kStages * kStageBytes;
     static constexpr int kRows = 8 * NR;
     static constexpr int kPad = DIM + 4;
@@ -89,7 +93,7 @@ struct Cfg {
 };
 
 template <int DIM, int BITS, int NR>
-__global__ void __launch_bounds__(kAttnThreads) attn_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kAttnThreads, Cfg<DIM, BITS, NR>::kCtas) attn_kernel(const AttnArgs a) {
     using C = Cfg<DIM, BITS, NR>;
     constexpr int W = C::W, ROWS = C::kRows;
     constexpr int KC = W / 64 > 0 ? W / 64 : 1;  // 16-byte (W = 32: 8-byte) runs of a key per lane
@@ -504,7 +508,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(const AttnArgs a) {
             if (s_last) {
                 __threadfence();
                 // a warp takes rows in turn, its lanes first a piece each (the statistics),
-                // then dimensions each, eight pieces under way
+                // then dimensions each, 8 or 16 pieces under way
                 const int n = (int)(c1 - c0) + 1;
                 constexpr int V = DIM / 32;  // dimensions of a lane
                 auto piece = [&](int i) -> const float* {  // the first CTA's is its second
@@ -529,11 +533,12 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(const AttnArgs a) {
                         #pragma unroll
                         for (int v = 0; v < V; ++v) o[v] *= f;
                         const int m = min(32, n - i0);
+                        constexpr int Y = NR == 1 && V <= 4 ? 16 : 8;
                         #pragma unroll 1
-                        for (int i = 0; i < m; i += 8) {
-                            float x[8][V];
+                        for (int i = 0; i < m; i += Y) {
+                            float x[Y][V];
                             #pragma unroll
-                            for (int y = 0; y < 8; ++y) {
+                            for (int y = 0; y < Y; ++y) {
                                 const float* p = piece(i0 + min(i + y, m - 1)) + r * DIM + V * lane;
                                 if constexpr (V == 2) {
                                     const float2 z = __ldcg(reinterpret_cast<const float2*>(p));
@@ -547,7 +552,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(const AttnArgs a) {
                                 }
                             }
                             #pragma unroll
-                            for (int y = 0; y < 8; ++y) {
+                            for (int y = 0; y < Y; ++y) {
                                 const float w = __shfl_sync(0xFFFFFFFFu, g, (i + y) & 31);
                                 if (i + y < m) {
                                     #pragma unroll
@@ -570,9 +575,9 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(const AttnArgs a) {
 
 template <int DIM, int BITS, int NR>
 int attn_ctas(int sms) {
-    // two CTAs an SM where their rings fit
-    const int per_sm = 2 * (Cfg<DIM, BITS, NR>::kSmem + 2048) <= 227 * 1024 ? 2 : 1;
-    const int n = sms * per_sm;
+    using C = Cfg<DIM, BITS, NR>;
+    static_assert(C::kCtas * (C::kSmem + 2048) <= 227 * 1024, "the CTAs of an SM share its memory");
+    const int n = sms * C::kCtas;
     return n < kAttnMaxCtas ? n : kAttnMaxCtas;
 }
 

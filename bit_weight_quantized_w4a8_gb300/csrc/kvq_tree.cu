@@ -741,14 +741,18 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const AttnArgs 
     using C = TreeCfg<DIM, BITS>;
     using Walk = AttnWalk<kJoinThreads, kRowsTile, 2, kBlock>;
     __shared__ typename Walk::Shared find;
+    __shared__ AttnTile tile;
+    __shared__ int pieces;
     griddep_launch_dependents();
     griddep_wait();
     Walk walk;
     if (!walk.init(a, find, true)) return;
-    AttnTile t;
     const int64_t c0 = blockIdx.x;
-    if (!walk.next(a, t, true) || walk.first_cta(t) != c0) return;
-    const int n = (int)(walk.last_cta(t) - c0) + 1;  // pieces
+    if (threadIdx.x == 0)  // its divisions in every thread took most of this kernel's time
+        pieces = walk.next(a, tile, true) && walk.first_cta(tile) == c0 ? (int)(walk.last_cta(tile) - c0) + 1 : 1;
+    __syncthreads();
+    const AttnTile& t = tile;
+    const int n = pieces;
     const int tl = blockIdx.y / (DIM / 16), r = threadIdx.x % kRowsTile, rt = tl * kRowsTile + r;
     const int c8 = blockIdx.y % (DIM / 16) * 2 + threadIdx.x / kRowsTile;
     if (n == 1 || rt >= t.rows) return;
