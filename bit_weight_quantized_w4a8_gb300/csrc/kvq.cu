@@ -7,6 +7,13 @@
 // (mod 2^64), the turns of position p are p F mod 2^64, exact in integers
 // whatever p; its top 32 bits, read as a signed number of 2^-32 turns, go
 // through one rounding to fp32 into sincospi.
+//
+// Measured in graphs: 8191 x 32 x 128 fp32 rotated into binary16 31.1 us, 95% of the copy
+// rate (cos and sin once per token for all heads; the first loads issued before them, 33.6
+// without); 8190 tokens written with 32 query heads 36.4 us (41.3 with the
+// queries in the keys' loop and a division per code); 200000 x 4 x 128 4-bit codes
+// read back in 83 us, 92% (8 values a thread, whole-line stores; 104 with 16 in two
+// stores); one row 1.9, 7 tokens written 3.1.
 #include <type_traits>
 
 #include "actq.cuh"

@@ -13,6 +13,11 @@
 // W^T being S^T's weights transposed by movmatrix.  Codes are integers of
 // at most 7 bits and sign, exact in binary16, and the scales stay outside the products:
 // ks_j multiplies the fp32 logit, vs_j the fp32 weight before its rounding.
+//
+// Bound by the cache's bytes at 8 bits: 24 sequences of up to 32768 keys (28 heads on 4,
+// dim 128) 114.5 us in a graph, 89% of the copy rate, with three CTAs an SM (two: 120).
+// At 4 bits by the widening of the codes, about half of that rate.  One token over 2048
+// keys: 10 us, its loads' latency and the join.
 #include <atomic>
 #include <type_traits>
 

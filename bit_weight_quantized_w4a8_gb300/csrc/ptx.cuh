@@ -182,18 +182,5 @@ __device__ __forceinline__ uint4 ld_global_nc_v4(const void* p) {
                  : "l"(p));
     return v;
 }
-// The same where `there`, zeros where not: the load itself is predicated, so
-// that several stay in flight (a branch around it would wait for each).
-__device__ __forceinline__ uint4 ld_global_nc_v4_if(const void* p, bool there) {
-    uint4 v;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-        "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-        : "l"(p), "r"((uint32_t)there));
-    return v;
-}
 
 }  // namespace w4a8

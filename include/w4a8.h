@@ -604,10 +604,17 @@ int kvq_keep(const kvq_cache_t* cache, const kvq_batch_t* batch, const int32_t* 
  * infinite harms only the rows that see it.
  * Arithmetic: the products of binary16 queries and integer codes are summed in
  * fp32; softmax statistics, their merge over the pieces of a long cache and the
- * output sums are fp32; p_j vs_j is rounded to binary16 for the second product
- * (2^-11 relative at most above 2^-27 of the row's largest).  The pieces
- * depend on cu and start alone and are merged in their order: the same
- * call gives the same bits.
+ * output sums are fp32; p_j vs_j is rounded to binary16 for the second product:
+ * within 2^-11 of itself, or, where it is below 2^-21 of the row's largest p
+ * times the largest |vs|, within 2^-32 of that (value scales below 2^-100, less).
+ * The pieces depend on cu, start and the sizes alone and are merged in their
+ * order: the same call gives the same bits.
+ * Two kernels: rows of a (sequence, cache head), tokens x heads_q / heads of
+ * them, in blocks of 8 or 16 on warp-level products (kvq_attn.cu), or, where the rows
+ * and the length that the page table allows make it worth its longer start, in tiles of 128
+ * on tcgen05 (kvq_tree.cu; dim 64 or 128).  Results of the two differ in rounding.
+ * The second one's waits are bounded; one that runs out sets bit 0 of the device
+ * error word.
  *   Q, out [tokens][heads_q][dim] binary16; mask [tokens] uint64 or NULL.
  *   ws, ws_bytes: kvq_attention_workspace_bytes, rules of
  *   w4a8_workspace_bytes (zeroed once, left ready, one call at a time).
