@@ -79,7 +79,7 @@ struct AttnWalk {
     struct Shared {
         int64_t units[THREADS / 32], find[2];
     };
-    static constexpr int kCost1 = P == 1 ? 1 : 3, kCostP = P == 1 ? 1 : 4;  // of a unit
+    static constexpr int kCost1 = P == 1 ? 1 : 3, kCostP = P == 1 ? 1 : 5;  // of a unit: 86 to 146 ps a key measured
     static_assert(P <= 2, "a row block has one tile or P");
     struct Work {
         int64_t tiles, units, per_head;

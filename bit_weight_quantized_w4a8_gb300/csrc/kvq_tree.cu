@@ -5,8 +5,8 @@
 // With hundreds of rows on each key the work is the two products, which only
 // tcgen05 runs at full rate, so the codes are widened to binary16 once
 // per CTA, in shared memory, for up to 256 rows:
-//   warps 16-23 copy the codes of 128 keys and values into shared memory, two blocks
-//     ahead, widen them and store them in the tensor core's 128-byte swizzled
+//   warps 16-23 copy the codes of 128 keys and values into shared memory, one or
+//     two blocks ahead, widen them and store them in the tensor core's 128-byte swizzled
 //     layout (codes held in registers came at 12.6 bytes a cycle and SM: 260 us
 //     instead of 204 in the second case below);
 //   warps 0-7 and 8-15 are two slots of softmax: S is read from TMEM, the
@@ -23,11 +23,12 @@
 // 2^e being a bound of the value scales, and is raised (and O and the sum
 // rescaled) only when a weight would pass 2^14: so seldom that O stays in TMEM.
 //
-// Measured (a call with its join): 6 trees of 9, 32 heads on 2, 30001 keys of 4 bits 79 us;
-// 4 trees of 64, 28 heads on 4, 32001 keys of 8 bits 196 us, 27% of the tensor
+// Measured in graphs, with the join: 6 trees of 9, 32 heads on 2, 30001 keys of 4 bits 77 us;
+// 4 trees of 64, 28 heads on 4, 32001 keys of 8 bits 186 us, 28% of the tensor
 // cores' measured rate (kvq_attn.cu: 534).  A block of 128 keys and 256 rows takes
-// 3.0 us, its products 1.07: bound by the chain S, weights, product within a
-// slot and the softmax warps' issue.
+// 2.9 us, its products 1.07, the softmax without products and loads 2.1: bound by the chain S,
+// weights, product within a slot.  (Keys of the next block widened while this one is
+// at work: 84.5 -> 74.4 us for 4 trees of 16 on one tile, 194 -> 186 for those of 64.)
 #include <atomic>
 #include <cstddef>
 #include <type_traits>
@@ -47,7 +48,6 @@ constexpr int kSlotWarps = 8, kSoftWarps = 2 * kSlotWarps, kLoadWarps = 8;
 constexpr int kTreeThreads = (kSoftWarps + kLoadWarps) * 32;
 constexpr int kRowsTile = 128;   // rows of a tile, TMEM lanes
 constexpr int kBlock = 128;      // keys of a unit
-constexpr int kRawStages = 2;    // blocks whose codes are held as they came
 constexpr int kScaleRing = 4;    // blocks whose scales are held
 constexpr float kTop = 10.f;     // log2 of the weight of a fresh maximum
 constexpr float kSlack = 4.f;    // log2 of what it may grow by before O is rescaled
@@ -90,9 +90,15 @@ struct TreeCfg {
     static constexpr int kHalf = kRowsTile * 128;            // 128 rows of 64 binary16 values
     static constexpr int kTileBytes = kHalf * (DIM / 64);
     static constexpr int kRawBytes = 16 * W;                 // codes of a loading warp's 16 keys or values
-    static constexpr int kOffQ = 0, kOffK = 2 * kTileBytes, kOffV = 3 * kTileBytes, kOffRaw = 4 * kTileBytes;
-    static constexpr int kOffShared = kOffRaw + kLoadWarps * 2 * kRawStages * kRawBytes;
-    static constexpr int kSmem = kOffShared + (int)sizeof(TreeShared) + 1024;  // + alignment
+    // two tiles of Q and of K, then what fits: the raw codes of two blocks, two tiles of V
+    static constexpr int kRaw = kLoadWarps * 2 * kRawBytes;  // of a block
+    static constexpr int kRoom = 227 * 1024 - (int)sizeof(TreeShared) - 1024;  // - alignment
+    static constexpr int kRawStages = 5 * kTileBytes + 2 * kRaw <= kRoom ? 2 : 1;
+    static constexpr int kValueTiles = 6 * kTileBytes + kRawStages * kRaw <= kRoom ? 2 : 1;
+    static constexpr int kOffQ = 0, kOffK = 2 * kTileBytes, kOffV = 4 * kTileBytes, kOffRaw = (4 + kValueTiles) * kTileBytes;
+    static constexpr int kOffShared = kOffRaw + kRawStages * kRaw;
+    static constexpr int kSmem = kOffShared + (int)sizeof(TreeShared) + 1024;
+    static_assert(kSmem <= 227 * 1024, "one CTA's shared memory");
     static constexpr int kPiece = kRowsTile * (DIM + 2);     // floats: O [DIM][128], M, sum
     static constexpr uint32_t kS = 0, kO = 256;              // TMEM columns: S of slot i at 128 i, O at 256 + DIM i
     static constexpr uint32_t kCols = 512;
@@ -228,15 +234,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
         const int nb = t.u1 - t.u0;
         const bool two = t.tiles == 2;
         if (warp >= kSoftWarps) {
-            // codes of this warp's 16 keys of every block: copied two blocks ahead as they
+            // codes of this warp's 16 keys of every block: copied one or two ahead as they
             // are, then widened into the tiles; lanes 0-15 have a key each for the page
             // table and the scales
             constexpr int CPR = C::W / 16;             // 16-byte chunks of codes per vector
             constexpr int N = CPR / 2;                 // of them per lane
+            constexpr int R = C::kRawStages;
             const int lw = warp - kSoftWarps;
             const int u0 = t.u0, u1 = t.u1, key_end = t.key_end, h = t.h;
             const int32_t* table = a.b.table + t.b * a.b.max_pages;
-            const uint32_t raw = base + C::kOffRaw + lw * 2 * kRawStages * C::kRawBytes;
+            const uint32_t raw = base + C::kOffRaw + lw * 2 * R * C::kRawBytes;
             const int pmask = (1 << a.c.shift) - 1;
             const int key = 16 * lw + (lane & 15);
             auto page_of = [&](int u) -> int {  // as the table has it
@@ -268,7 +275,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
             };
             auto copy = [&](int u, const Place& p, const uint8_t* codes, int kv) {
                 if (u < u1) {
-                    const uint32_t dst = raw + (2 * ((u - u0) % kRawStages) + kv) * C::kRawBytes;
+                    const uint32_t dst = raw + (2 * ((u - u0) % R) + kv) * C::kRawBytes;
                     #pragma unroll
                     for (int i = 0; i < N; ++i) {
                         const int r = (32 * i + lane) / CPR, c = (32 * i + lane) % CPR;
@@ -279,7 +286,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
             };
             // 8 lanes on 8 rows of one chunk meet each bank once, here and in the tile
             auto widen = [&](uint32_t dst, int j, int kv) {
-                const uint32_t src = raw + (2 * (j % kRawStages) + kv) * C::kRawBytes;
+                const uint32_t src = raw + (2 * (j % R) + kv) * C::kRawBytes;
                 #pragma unroll
                 for (int i = 0; i < N; ++i) {
                     const int r = CPR >= 4 ? 8 * (i / (CPR / 4 > 0 ? CPR / 4 : 1)) + (lane & 7) : 8 * (lane >> 4) + (lane & 7);
@@ -303,8 +310,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                     }
                 }
             };
-            auto freed = [&](uint64_t* bars, int blk) -> bool {  // of the block before blk
-                return blk == 0 || __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars[(blk - 1) & 1]), ((blk - 1) >> 1) & 1, &sh.abort));
+            auto freed = [&](uint64_t* bars, int blk, int tiles) -> bool {  // of the block whose tile blk takes
+                const int was = blk - tiles;
+                return was < 0 || __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&bars[was & 1]), (was >> 1) & 1, &sh.abort));
             };
             auto arrive = [&](uint64_t& bar) {
                 fence_async_shared();
@@ -312,55 +320,67 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                 if (lane == 0) mbar_arrive(smem_u32(&bar));
             };
             auto scale_of = [&](const float* p, const Place& at) -> float { return at.there >> (lane & 15) & 1 ? p[at.own] : 0.f; };
-            Place p1 = place(u0, page_of(u0));
-            int page = page_of(u0 + 2);
-            float sk = scale_of(a.c.ks, p1), sv = scale_of(a.c.vs, p1);  // of the next block to be widened
-            uint32_t there = p1.there;
-            copy(u0, p1, a.c.k, 0);
-            copy(u0, p1, a.c.v, 1);
-            p1 = place(u0 + 1, page_of(u0 + 1));
-            copy(u0 + 1, p1, a.c.k, 0);
-            copy(u0 + 1, p1, a.c.v, 1);
-            for (int j = 0; j < nb; ++j) {
-                const int blk = blocks_done + j;
-                BlockScales& bs = sh.sc[blk % kScaleRing];
-                {
-                    // a factor of 0 would make NaN of an unseen key's -inf; a key of zeros
-                    // has logit 0 with any
-                    const float kk = sk * a.scale_log2;
-                    const bool fine = fabsf(kk) < INFINITY && fabsf(sv) < INFINITY && sk >= 0.f;
-                    if (lane < 16) {
-                        bs.k[key] = fine && kk != 0.f ? kk : a.scale_log2 < 0.f ? -1e-30f : 1e-30f;
-                        bs.v[key] = fine ? sv : 0.f;
+            Place at[R + 1];  // of blocks t .. t + R
+            #pragma unroll
+            for (int r = 0; r < R; ++r) {
+                at[r] = place(u0 + r, page_of(u0 + r));
+                copy(u0 + r, at[r], a.c.k, 0);
+                copy(u0 + r, at[r], a.c.v, 1);
+            }
+            int page = page_of(u0 + R);
+            float sk = scale_of(a.c.ks, at[0]), sv = scale_of(a.c.vs, at[0]);
+            // Keys of block t, then the values of the block before: the keys go into the
+            // tile that block t - 2 has left while block t - 1 is at work, the values, where
+            // they have one tile, follow its products.  A block's codes are copied when
+            // those R before it have been widened.
+            for (int t = 0; t <= nb; ++t) {
+                const int blk = blocks_done + t;
+                at[R] = place(u0 + t + R, page);
+                page = page_of(u0 + t + R + 1);
+                if (t < nb) {
+                    BlockScales& bs = sh.sc[blk % kScaleRing];
+                    {
+                        // a factor of 0 would make NaN of an unseen key's -inf; a key of zeros
+                        // has logit 0 with any
+                        const float kk = sk * a.scale_log2;
+                        const bool fine = fabsf(kk) < INFINITY && fabsf(sv) < INFINITY && sk >= 0.f;
+                        if (lane < 16) {
+                            bs.k[key] = fine && kk != 0.f ? kk : a.scale_log2 < 0.f ? -1e-30f : 1e-30f;
+                            bs.v[key] = fine ? sv : 0.f;
+                        }
+                        const unsigned bad = __ballot_sync(0xFFFFFFFFu, !fine) & 0xFFFFu;
+                        const unsigned vmax = __reduce_max_sync(0xFFFFFFFFu, fine ? __float_as_uint(fabsf(sv)) : 0u);
+                        if (lane == 0) {
+                            bs.vmax[lw] = __uint_as_float(vmax);
+                            bs.odd[lw] = (at[0].there ^ 0xFFFFu) | bad;
+                            bs.valid[lw] = (uint16_t)at[0].there;
+                            bs.bad[lw] = (uint16_t)bad;
+                        }
                     }
-                    const unsigned bad = __ballot_sync(0xFFFFFFFFu, !fine) & 0xFFFFu;
-                    const unsigned vmax = __reduce_max_sync(0xFFFFFFFFu, fine ? __float_as_uint(fabsf(sv)) : 0u);
-                    if (lane == 0) {
-                        bs.vmax[lw] = __uint_as_float(vmax);
-                        bs.odd[lw] = (there ^ 0xFFFFu) | bad;
-                        bs.valid[lw] = (uint16_t)there;
-                        bs.bad[lw] = (uint16_t)bad;
-                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.scfull[blk % kScaleRing]));
+                    sk = scale_of(a.c.ks, at[1]);
+                    sv = scale_of(a.c.vs, at[1]);
+                    if (t >= 1 && t <= R) cp_async_wait<2 * R - 2>();  // the first values went out before these keys
+                    else cp_async_wait<2 * R - 1>();
+                    __syncwarp();
+                    if (!freed(sh.kfree, blk, 2)) break;
+                    widen(base + C::kOffK + (blk & 1) * C::kTileBytes, t, 0);
+                    arrive(sh.kfull[blk & 1]);
+                    copy(u0 + t + R, at[R], a.c.k, 0);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.scfull[blk % kScaleRing]));
-                sk = scale_of(a.c.ks, p1);
-                sv = scale_of(a.c.vs, p1);
-                there = p1.there;
-                p1 = place(u0 + j + 2, page);
-                page = page_of(u0 + j + 3);
-                cp_async_wait<3>();  // this block's keys are here; its values and the next block are on their way
-                __syncwarp();
-                if (!freed(sh.kfree, blk)) break;
-                widen(base + C::kOffK, j, 0);
-                arrive(sh.kfull[blk & 1]);
-                copy(u0 + j + 2, p1, a.c.k, 0);
-                cp_async_wait<3>();
-                __syncwarp();
-                if (!freed(sh.vfree, blk)) break;
-                widen(base + C::kOffV, j, 1);
-                arrive(sh.vfull[blk & 1]);
-                copy(u0 + j + 2, p1, a.c.v, 1);
+                if (t > 0) {
+                    const int prev = blk - 1;
+                    if (t < nb) cp_async_wait<2 * R - 1>();
+                    else cp_async_wait<2 * R - 2>();
+                    __syncwarp();
+                    if (!freed(sh.vfree, prev, C::kValueTiles)) break;
+                    widen(base + C::kOffV + prev % C::kValueTiles * C::kTileBytes, t - 1, 1);
+                    arrive(sh.vfull[prev & 1]);
+                    copy(u0 + t - 1 + R, at[R - 1], a.c.v, 1);
+                }
+                #pragma unroll
+                for (int r = 0; r < R; ++r) at[r] = at[r + 1];
             }
             cp_async_wait<0>();
         } else {
@@ -422,9 +442,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
             auto block_of = [&](int i) -> int { return blocks_done + (two ? i : 2 * i + slot); };
             // products, issued by the slot's first warp (all of it in step, so that
             // descriptors live in uniform registers; one lane issues)
-            auto qk = [&]() {
+            auto qk = [&](int i) {
                 const uint64_t qd = sw128_desc(u_base + C::kOffQ) + u_q * (C::kTileBytes >> 4);
-                const uint64_t kd = sw128_desc(u_base + C::kOffK);
+                const uint64_t kd = sw128_desc(u_base + C::kOffK) + (block_of(i) & 1) * (C::kTileBytes >> 4);
                 if (leader) {
                     #pragma unroll
                     for (int k = 0; k < KSTEPS; ++k) {
@@ -434,7 +454,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                 }
             };
             auto pv = [&](int i) {
-                const uint64_t vd = sw128_desc_mn(u_base + C::kOffV, C::kHalf);
+                const uint64_t vd = sw128_desc_mn(u_base + C::kOffV, C::kHalf) + block_of(i) % C::kValueTiles * (C::kTileBytes >> 4);
                 if (leader) {
                     #pragma unroll
                     for (int k = 0; k < kBlock / 16; ++k)
@@ -467,7 +487,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                 ok = wait_keys(0);
                 if (ok) {
                     tc_fence_after_sync();
-                    qk();
+                    qk(0);
                     commit();
                     release(sh.kfree, 0);
                     __syncwarp();
@@ -627,7 +647,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                         release(sh.vfree, i);
                         if (more && (two || (ok = wait_keys(i + 1)))) {
                             tc_fence_after_sync();
-                            qk();
+                            qk(i + 1);
                             release(sh.kfree, i + 1);
                         }
                         commit();
@@ -816,14 +836,14 @@ int tree_ctas(int sms) { return sms < kAttnMaxCtas ? sms : kAttnMaxCtas; }
 // Whether this kernel serves a call: it saves the difference of what a cached
 // token costs the two, times the tokens, against the 22 us that it takes longer
 // for a short cache.  Measured on GB300 (8 sequences of 4 heads of 128, 8 bits, ps per token and
-// cache head): the row-block kernel 38 for each 16 rows, this one 100 for one tile of 128
-// rows and 143 for two.  At 32001 tokens 56 rows take 135 us here and 164 there, 21
-// rows 132 and 96; at 64 tokens 448 rows 40 and 22.  The cache is taken to be as long
+// cache head): the row-block kernel 38 for each 16 rows, this one 86 for one tile of 128
+// rows and 146 for two.  At 32001 tokens 56 rows take 108 us here and 164 there; at 64
+// tokens 448 rows 40 and 22.  The cache is taken to be as long
 // as the page table allows: its length is on the device.
 bool tree_serves(const kvq_cache_t& c, const kvq_batch_t& b, int heads_q) {
     if (c.dim > 128) return false;  // 256 dimensions of O for two tiles do not fit TMEM
     const int64_t rows = (b.tokens * (heads_q / c.heads) + b.seqs - 1) / b.seqs, tiles = (rows + 127) / 128;
-    const double here = (double)(tiles / 2) * 143e-6 + (double)(tiles % 2) * 100e-6, there = (double)((rows + 15) / 16) * 38e-6;
+    const double here = (double)(tiles / 2) * 146e-6 + (double)(tiles % 2) * 86e-6, there = (double)((rows + 15) / 16) * 38e-6;
     const double keys = (double)b.seqs * c.heads * (double)(b.max_pages * c.page);
     return keys * (there - here) > 22.0;
 }
