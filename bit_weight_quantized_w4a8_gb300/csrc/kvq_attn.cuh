@@ -102,9 +102,8 @@ struct AttnWalk {
         return kvq_seq(a.b.cu, a.b.start, i, a.b.tokens, a.b.max_pages, a.c.shift);
     }
 
-    // The run of this CTA; false when it has none.  Every thread calls it.  last:
-    // start at the run's last unit instead of its first.
-    __device__ bool init(const AttnArgs& a, Shared& sh, bool last = false) {
+    // The run of this CTA; false when it has none.  Every thread calls it.
+    __device__ bool init(const AttnArgs& a, Shared& sh) {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         int64_t total = 0;
         for (int i = tid; i < a.b.seqs; i += THREADS) {
@@ -125,7 +124,6 @@ struct AttnWalk {
         at = per * blockIdx.x;
         end = min(at + per, total);
         if (at >= end) return false;
-        if (last) at = end - 1;
         if (warp == 0) {  // the sequence that holds unit `at`, 32 sequences a time
             int64_t before = 0;
             for (int b0 = 0; b0 < a.b.seqs; b0 += 32) {
@@ -157,9 +155,8 @@ struct AttnWalk {
         return true;
     }
 
-    // The next row block that this CTA has a part of (any: that `at` lies in,
-    // part or not); false at the run's end.
-    __device__ bool next(const AttnArgs& a, AttnTile& t, bool any = false) {
+    // The next row block that this CTA has a part of; false at the run's end.
+    __device__ bool next(const AttnArgs& a, AttnTile& t) {
         while (at < end) {
             t.s = seq(a, b);
             const Work w = work(a, t.s);
@@ -188,7 +185,7 @@ struct AttnWalk {
                 const int64_t last = (int64_t)t.s.start + (t.row0 + t.rows - 1) / a.group + 1;
                 if (last < t.key_end) t.key_end = (int)last;
             }
-            if (t.u0 < t.u1 || any) return true;
+            if (t.u0 < t.u1) return true;
         }
         return false;
     }

@@ -23,8 +23,8 @@
 // 2^e being a bound of the value scales, and is raised (and O and the sum
 // rescaled) only when a weight would pass 2^14: so seldom that O stays in TMEM.
 //
-// Measured in graphs, with the join: 6 trees of 9, 32 heads on 2, 30001 keys of 4 bits 77 us;
-// 4 trees of 64, 28 heads on 4, 32001 keys of 8 bits 186 us, 28% of the tensor
+// Measured in graphs, with the join: 6 trees of 9, 32 heads on 2, 30001 keys of 4 bits 65 us;
+// 4 trees of 64, 28 heads on 4, 32001 keys of 8 bits 178 us, 30% of the tensor
 // cores' measured rate (kvq_attn.cu: 534).  A block of 128 keys and 256 rows takes
 // 2.9 us, its products 1.07, the softmax without products and loads 2.1: bound by the chain S,
 // weights, product within a slot.  (Keys of the next block widened while this one is
@@ -103,6 +103,17 @@ struct TreeCfg {
     static constexpr uint32_t kS = 0, kO = 256;              // TMEM columns: S of slot i at 128 i, O at 256 + DIM i
     static constexpr uint32_t kCols = 512;
 };
+
+// What a CTA leaves behind its piece for the join: the row block that it began and
+// that others went on with.
+struct alignas(16) JoinRecord {
+    int pieces;  // 1: there is none
+    int rows, row0, first, h;
+};
+template <int DIM, int BITS>
+__device__ __forceinline__ JoinRecord* join_record(const AttnArgs& a, int cta) {
+    return reinterpret_cast<JoinRecord*>(a.parts + (int64_t)gridDim.x * 4 * TreeCfg<DIM, BITS>::kPiece) + cta;
+}
 
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
     #pragma unroll 1
@@ -198,6 +209,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // one value for the warp, known to the compiler as such
 
+    if (tid == 0) join_record<DIM, BITS>(a, blockIdx.x)->pieces = 1;
     {
         AttnWalk<kTreeThreads, kRowsTile, 2, kBlock> walk;
         if (!walk.init(a, sh.find)) return;
@@ -679,6 +691,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
         __syncthreads();  // roles done: operands, TMEM and statistics are settled
         tc_fence_after_sync();
         if (sh.abort) break;
+        if (warp == kSoftWarps && lane == 0 && t.u0 == 0 && t.u1 < t.units)
+            *join_record<DIM, BITS>(a, blockIdx.x) = {(int)(sh.walk.last_cta(t) - blockIdx.x) + 1, t.rows, t.row0, t.s.first, t.h};
         // the tile's sums go out, normalized, or to this CTA's piece: a thread per
         // row (TMEM lane); the warps that hold a row share its dimensions (of one
         // tile's two slots each has a part of both)
@@ -762,25 +776,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
 // went on in the next ones, in their order: 16 dimensions of one tile a CTA, a
 // thread has a row's eight and takes four pieces at a time (40 loads under
 // way; one after the other they took up to 100 us).  As its own launch it
-// has the whole GPU for what the last CTA to arrive would read alone.
+// has the whole GPU for what the last CTA to arrive would read alone.  (Its CTAs read
+// what to join from a record: finding it again in the batch
+// took most of their time: a call of 4 trees of 64 185.4 -> 178.5 us, 6 of 9 69.5 -> 65.1.)
 constexpr int kJoinThreads = 256;
 template <int DIM, int BITS>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const AttnArgs a) {
     using C = TreeCfg<DIM, BITS>;
-    using Walk = AttnWalk<kJoinThreads, kRowsTile, 2, kBlock>;
-    __shared__ typename Walk::Shared find;
-    __shared__ AttnTile tile;
-    __shared__ int pieces;
     griddep_launch_dependents();
     griddep_wait();
-    Walk walk;
-    if (!walk.init(a, find, true)) return;
     const int64_t c0 = blockIdx.x;
-    if (threadIdx.x == 0)  // its divisions in every thread took most of this kernel's time
-        pieces = walk.next(a, tile, true) && walk.first_cta(tile) == c0 ? (int)(walk.last_cta(tile) - c0) + 1 : 1;
-    __syncthreads();
-    const AttnTile& t = tile;
-    const int n = pieces;
+    const JoinRecord t = *join_record<DIM, BITS>(a, blockIdx.x);
+    const int n = t.pieces;
     const int tl = blockIdx.y / (DIM / 16), r = threadIdx.x % kRowsTile, rt = tl * kRowsTile + r;
     const int c8 = blockIdx.y % (DIM / 16) * 2 + threadIdx.x / kRowsTile;
     if (n == 1 || rt >= t.rows) return;
@@ -820,7 +827,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const AttnArgs 
     #pragma unroll
     for (int y = 0; y < 8; ++y) o[y] *= inv;
     const int row = t.row0 + rt;
-    store8(a.out + ((int64_t)(t.s.first + row / a.group) * a.heads_q + t.h * a.group + row % a.group) * DIM + 8 * c8, o);
+    store8(a.out + ((int64_t)(t.first + row / a.group) * a.heads_q + t.h * a.group + row % a.group) * DIM + 8 * c8, o);
 }
 
 template <typename F>
@@ -854,7 +861,7 @@ size_t kvq_attn_workspace(const kvq_cache_t& c, const kvq_batch_t& b, int heads_
     if (!tree_serves(c, b, heads_q)) return attn_rows_workspace(c, b, heads_q, sms);
     return by_config(c, [&](auto dim, auto bits) -> size_t {
         return kAttnTicketBytes +
-               (size_t)tree_ctas(sms) * 4 * TreeCfg<decltype(dim)::value, decltype(bits)::value>::kPiece * sizeof(float);
+               tree_ctas(sms) * (4 * TreeCfg<decltype(dim)::value, decltype(bits)::value>::kPiece * sizeof(float) + sizeof(JoinRecord));
     });
 }
 
