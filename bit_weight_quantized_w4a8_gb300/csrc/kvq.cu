@@ -87,11 +87,14 @@ __device__ __noinline__ uint32_t codes4_exact(float4 v, float s, float top) {
     return (uint32_t)(layer_code(v.x, s, top) & 0xFF) | (uint32_t)(layer_code(v.y, s, top) & 0xFF) << 8 |
            (uint32_t)(layer_code(v.z, s, top) & 0xFF) << 16 | (uint32_t)(layer_code(v.w, s, top) & 0xFF) << 24;
 }
-// Fast form, with 1 / s bracketed by lo and hi (quant_bracket; both 0 for s =
-// 0): the IEEE quotient lies strictly between x lo and x hi, so where both round to
-// one integer that is the code, no tie is involved, and |x| <= top s up to
-// two roundings of s needs no clamp; the few others take the exact form.
+// Fast form, with 1 / s bracketed by lo and hi (quant_bracket): the IEEE quotient
+// lies strictly between x lo and x hi, so where both round to one integer that is
+// the code, no tie is involved, and |x| <= top s up to two roundings of s needs
+// no clamp; the few others take the exact form.  All of this needs a normal s: below 2^-126
+// its own rounding is no longer relative (the largest code may need the clamp), below
+// 2^-128 the bracket is infinite; such vectors take the exact form too.
 __device__ __forceinline__ uint32_t codes4(float4 v, float s, float top, float lo, float hi) {
+    if (s < 0x1p-126f) return codes4_exact(v, s, top);
     constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: the sum's low bits hold the rounded product
     const float x[4] = {v.x, v.y, v.z, v.w};
     uint32_t y[4], diff = 0u;
