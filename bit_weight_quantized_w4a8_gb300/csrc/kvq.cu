@@ -81,20 +81,22 @@ __device__ __forceinline__ void rotate8(float4& a, float4& b, const float2* cs, 
     }
 }
 
-// Codes of four values, a byte each: clamp(round_half_away(x / s), +-top).
+// Codes of four values, a byte each: clamp(round_half_away(x / s), +-top), or 0
+// where s is 0, infinite or NaN (the scale then tells what the vector holds).
 // Exact form: an IEEE division and roundf per value.
 __device__ __noinline__ uint32_t codes4_exact(float4 v, float s, float top) {
+    if (!(s < INFINITY)) return 0u;
     return (uint32_t)(layer_code(v.x, s, top) & 0xFF) | (uint32_t)(layer_code(v.y, s, top) & 0xFF) << 8 |
            (uint32_t)(layer_code(v.z, s, top) & 0xFF) << 16 | (uint32_t)(layer_code(v.w, s, top) & 0xFF) << 24;
 }
 // Fast form, with 1 / s bracketed by lo and hi (quant_bracket): the IEEE quotient
 // lies strictly between x lo and x hi, so where both round to one integer that is
 // the code, no tie is involved, and |x| <= top s up to two roundings of s needs
-// no clamp; the few others take the exact form.  All of this needs a normal s: below 2^-126
-// its own rounding is no longer relative (the largest code may need the clamp), below
-// 2^-128 the bracket is infinite; such vectors take the exact form too.
+// no clamp; the few others take the exact form.  All of this needs a normal, finite s: below
+// 2^-126 its own rounding is no longer relative (the largest code may need the clamp),
+// below 2^-128 the bracket is infinite; such vectors take the exact form too.
 __device__ __forceinline__ uint32_t codes4(float4 v, float s, float top, float lo, float hi) {
-    if (s < 0x1p-126f) return codes4_exact(v, s, top);
+    if (!(s >= 0x1p-126f && s < INFINITY)) return codes4_exact(v, s, top);
     constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: the sum's low bits hold the rounded product
     const float x[4] = {v.x, v.y, v.z, v.w};
     uint32_t y[4], diff = 0u;
@@ -238,9 +240,9 @@ __global__ void __launch_bounds__(kLayerThreads) rope_write_kernel(const WriteAr
             for (int i = 0; i < 2; ++i) {
                 const int kv = vv[i] >= kv_heads;  // 0 key, 1 value
                 if (live[i] && !kv && 8 * l < 2 * pairs) rotate8(va[i], vb[i], cs + vt[i] * pairs + 4 * l, a.rope.inter);
-                float m = fmaxf(absmax4(va[i]), absmax4(vb[i]));
+                float m = max_nan(absmax4_nan(va[i]), absmax4_nan(vb[i]));
                 #pragma unroll
-                for (int o = LPV / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                for (int o = LPV / 2; o >= 1; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
                 if (live[i] && slot_row[vt[i]] >= 0) {
                     constexpr float top = BITS == 8 ? 127.f : 7.f;
                     const float s = __fmul_rn(m, 1.f / top);

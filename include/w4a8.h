@@ -533,7 +533,9 @@ int rope_rotate(const void* X, int x_type, int64_t ld_x, int64_t tokens, int hea
  * of max|x| / top); code = clamp(round_half_away(x / scale), -top, top) with
  * the IEEE quotient by that stored scale, so code * scale is within half a step of x
  * (where the scale is a normal number; below 2^-126 it is rounded to a multiple of
- * 2^-149 and the clamp may cut more).  A zero vector gets scale 0 and codes 0.
+ * 2^-149 and the clamp may cut more).  A zero vector gets scale 0 and codes 0,
+ * one that holds a NaN scale NaN, one that holds an infinity and no NaN scale infinity,
+ * both codes 0: every value of such a vector reads back NaN.
  * A page of one head is contiguous: the attention streams it.  Requires page 16, 32, 64, 128 or 256, dim 64, 128 or 256, 1 <=
  * heads <= 1024, 1 <= pages <= 2^31 - 1; k, v 16-byte, ks, vs 4-byte aligned. */
 typedef struct {

@@ -48,3 +48,55 @@ def test_write_of_tiny_vectors_is_exact(w4, dim, bits):  # noqa: F811
         q, s = ref.quantize(t, bits)
         assert np.array_equal(scales.cpu().numpy()[p, :, o], s)
         assert np.array_equal(codes.cpu().numpy()[p, :, o], ref.pack(q, bits))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dim,bits,rot,inter", [(128, 8, 0, False), (64, 4, 0, False), (128, 8, 128, False), (128, 4, 64, True)])
+def test_write_keeps_what_is_not_finite_in_the_scale(w4, bad, dim, bits, rot, inter):  # noqa: F811
+    """A vector with a NaN or an infinity: a scale that is neither finite nor 0,
+    codes 0, so that every value reads back NaN; its neighbours as ever."""
+    rng = np.random.default_rng(dim + bits + rot)
+    n, heads = 6, 2
+    k, v = (rng.standard_normal((n, heads, dim)).astype(F32) for _ in range(2))
+    clean = [t.copy() for t in (k, v)]
+    k[1, 0, 3] = k[4, 1, dim - 1] = v[2, 1, 0] = v[5, 0, 40] = bad
+    k[3, 0, 7], k[3, 0, 8] = float("nan"), bad   # with a NaN beside it: NaN
+    pg = ref.Paged(rng, (n,), (10,), 16)
+    pos = dev(rng.integers(0, 5000, n).astype(np.int32))
+    freqs = w4.rope_frequencies(rot, 1e4)[0].cuda() if rot else None
+    got = []
+    for a, b in ((k, v), clean):
+        c, gs = make_cache(w4, pg, heads, dim, bits)
+        w4.kvq_write(c, make_batch(w4, pg), dev(a), dev(b), pos=pos if rot else None, freqs=freqs, interleaved=inter)
+        guards.check_all(*gs)
+        got.append(c)
+    c, sound = got
+    p, o = pg.own()
+    at = lambda t: t.cpu().numpy()[p, :, o]  # noqa: E731
+    kb, vb = np.zeros((n, heads), bool), np.zeros((n, heads), bool)
+    kb[[1, 4, 3], [0, 1, 0]] = True
+    vb[[2, 5], [1, 0]] = True
+    for codes, scales, s_codes, s_scales, b in ((c.k, c.ks, sound.k, sound.ks, kb), (c.v, c.vs, sound.v, sound.vs, vb)):
+        assert not np.isfinite(at(scales)[b]).any() and not at(codes)[b].any()
+        assert np.array_equal(at(scales)[~b], at(s_scales)[~b]) and np.array_equal(at(codes)[~b], at(s_codes)[~b])
+    assert np.isnan(at(c.ks)[3, 0])
+    rk, rv = w4.kvq_read(c, make_batch(w4, pg), n, dtype=torch.float32)
+    assert np.isnan(rk.cpu().numpy()[kb]).all() and np.isnan(rv.cpu().numpy()[vb]).all()
+    assert torch.isfinite(rk[dev(~kb)]).all() and torch.isfinite(rv[dev(~vb)]).all()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_a_nan_that_is_written_reaches_the_rows_that_see_it(w4, wide, which):  # noqa: F811
+    rng = np.random.default_rng(21)
+    tok, ctx, hq, heads, dim = (5,), (150,), 32, 2, 128
+    pg = ref.Paged(rng, tok, ctx, 32, extra_cols=wide_cols(1, heads, 32) if wide else 1)
+    c, _, _ = fill(w4, rng, pg, heads, dim, 8)
+    mask = np.array([1, 3, 4, 9, 17], np.uint64)  # token 2 is seen by itself alone
+    x = {t: rng.standard_normal((5, heads, dim)).astype(F32) for t in "kv"}
+    x[which][2, :, 11] = float("nan")
+    q = rng.standard_normal((5, hq, dim)).astype(F16)
+    b = make_batch(w4, pg)
+    w4.kvq_write(c, b, dev(x["k"]), dev(x["v"]))
+    out = w4.kvq_attention(dev(q), c, b, mask=dev(mask.view(np.int64)))
+    assert bool(torch.isfinite(out[[0, 1, 3, 4]]).all()) and not bool(torch.isfinite(out[2]).any())
