@@ -35,6 +35,7 @@
 
 #include "kernels.h"
 #include "kvq_attn.cuh"
+#include "kvq_roles.h"
 #include "tc.cuh"
 
 namespace w4a8 {
@@ -428,7 +429,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                 sh.word[tid / kRowsTile][tid % kRowsTile] = a.mask != nullptr ? a.mask[t.s.first + tok] : 0;
             }
             fence_async_shared();
-            named_bar_sync(3, kSoftWarps * 32);
+            named_bar_sync(kBarQueries, kSoftWarps * 32);
 
             // Softmax.  A slot's eight warps are its tile's four quarters of rows times
             // two halves of a block's keys.  S, W and O are held in fragments: rows 8 k +
@@ -493,7 +494,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                 return wait(sh.kfull[blk & 1], blk >> 1);
             };
             // a wait that gave up (ok false) skips the work of what follows, but each
-            // warp still meets the slot's barrier once a job
+            // warp still votes and hands over once a job (kvq_roles.h)
             bool ok = true;
             if (first && my_jobs > 0) {
                 ok = wait_keys(0);
@@ -573,14 +574,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                     for (int k = 0; k < 4; ++k) up |= top[k] - M[k] + ve > kTop + kSlack;
                 }
                 // raise the references that are too low: both halves of the keys alike
-                if (named_bar_or(1 + slot, kSlotWarps * 32, up)) {
+                if (named_bar_or(bar_vote(slot), kSlotWarps * 32, up)) {
                     #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         top[k] = fmaxf(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], 1));
                         top[k] = fmaxf(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], 2));
                         if ((lane & 3) == 0) sh.top[slot][half][32 * quad + 8 * k + (lane >> 2)] = top[k];
                     }
-                    named_bar_sync(1 + slot, kSlotWarps * 32);
+                    named_bar_sync(bar_vote(slot), kSlotWarps * 32);
                     if (work) {
                         float f[4];
                         #pragma unroll
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                     // its other slot's values do, and they come in before those keys)
                     const bool more = i + 1 < my_jobs;
                     ok = ok && wait(sh.vfull[blk & 1], blk >> 1) && (!two || !more || wait_keys(i + 1));
-                    named_bar_sync(1 + slot, kSlotWarps * 32);
+                    named_bar_sync(bar_hand(slot), kSlotWarps * 32);
                     if (ok) {
                         tc_fence_after_sync();
                         pv(i);
@@ -666,7 +667,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                         __syncwarp();
                     }
                 } else {
-                    named_bar_arrive(1 + slot, kSlotWarps * 32);
+                    named_bar_arrive(bar_hand(slot), kSlotWarps * 32);
                 }
             }
             // settled: the slot's last product, and what its rows' sums are relative to
