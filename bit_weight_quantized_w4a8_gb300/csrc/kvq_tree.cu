@@ -52,6 +52,10 @@ constexpr int kBlock = 128;      // keys of a unit
 constexpr int kScaleRing = 4;    // blocks whose scales are held
 constexpr float kTop = 10.f;     // log2 of the weight of a fresh maximum
 constexpr float kSlack = 4.f;    // log2 of what it may grow by before O is rescaled
+// log2 of the least bound of a block's value scales.  Smaller values (zeros above all)
+// give at most 2^-17, and a reference taken that low would make the weights' sum, in units of
+// 2^reference, overflow: at -100, 2^18 keys of zero values did (outputs of 0).
+constexpr float kLeastValue = -24.f;
 
 struct alignas(16) BlockScales {  // read as 16-byte vectors
     float k[kBlock];        // ks * scale * log2(e), never 0, of the scale's sign
@@ -518,7 +522,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                     const float4 v = reinterpret_cast<const float4*>(bs.vmax)[0], v2 = reinterpret_cast<const float4*>(bs.vmax)[1];
                     const uint4 odd = reinterpret_cast<const uint4*>(bs.odd)[0], odd2 = reinterpret_cast<const uint4*>(bs.odd)[1];
                     const float top = fmaxf(max3(v.x, v.y, max3(v.z, v.w, v2.x)), max3(v2.y, v2.z, v2.w));
-                    ve = fmaxf((float)((int)(__float_as_uint(top) >> 23) - 126), -100.f);
+                    ve = fmaxf((float)((int)(__float_as_uint(top) >> 23) - 126), kLeastValue);
                     plain = k0 + kBlock <= start && (odd.x | odd.y | odd.z | odd.w | odd2.x | odd2.y | odd2.z | odd2.w) == 0u;
                 }
                 ok = ok && wait(sh.sfull[slot], s_phase[slot] + i);

@@ -609,7 +609,8 @@ int kvq_keep(const kvq_cache_t* cache, const kvq_batch_t* batch, const int32_t* 
  * fp32; softmax statistics, their merge over the pieces of a long cache and the
  * output sums are fp32; p_j vs_j is rounded to binary16 for the second product:
  * within 2^-11 of itself, or, where it is below 2^-21 of the row's largest p
- * times the largest |vs|, within 2^-32 of that (value scales below 2^-100, less).
+ * times the largest |vs|, within 2^-32 of that (|vs| below 2^-24 taken as 2^-24, whose
+ * values a binary16 output holds as subnormals).
  * The pieces depend on cu, start and the sizes alone and are merged in their
  * order: the same call gives the same bits.
  * Two kernels: rows of a (sequence, cache head), tokens x heads_q / heads of

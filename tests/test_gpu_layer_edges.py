@@ -100,3 +100,29 @@ def test_a_nan_that_is_written_reaches_the_rows_that_see_it(w4, wide, which):  #
     w4.kvq_write(c, b, dev(x["k"]), dev(x["v"]))
     out = w4.kvq_attention(dev(q), c, b, mask=dev(mask.view(np.int64)))
     assert bool(torch.isfinite(out[[0, 1, 3, 4]]).all()) and not bool(torch.isfinite(out[2]).any())
+
+
+# -- attention ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("hq,dim", [(8, 64), (64, 64), (64, 128)])
+@pytest.mark.parametrize("order", ["zeros first", "zeros last"])
+def test_attention_many_zero_values(w4, hq, dim, order):  # noqa: F811
+    """2^19 keys whose values are zero beside 2^15 ordinary ones, all with one
+    logit: the zeros weigh as much as the others.  (8 rows and 64 take the two kernels.)"""
+    rng = np.random.default_rng(24)
+    zeros, rest, page = 1 << 19, 1 << 15, 256
+    pg = ref.Paged(rng, (1,), (zeros + rest - 1,), page)
+    c, _, host = fill(w4, rng, pg, 1, dim, 8)
+    p, o = pg.where(0, np.arange(zeros) + (0 if order == "zeros first" else rest))
+    vq, vs = host[1]
+    vs[p, :, o] = 0
+    vq[...] = np.abs(vq)  # a mean that is not 0
+    c.vs.copy_(dev(vs))
+    c.v.copy_(dev(vq))
+    q = np.zeros((1, hq, dim), F16)
+    out = w4.kvq_attention(dev(q), c, make_batch(w4, pg)).cpu().numpy().astype(np.float64)
+    p, o = pg.where(0, np.arange(zeros + rest))
+    (kq, ks), (vq, vs) = host
+    want, err = ref.attention(q[0, :1], kq[p, 0, o], ks[p, 0, o], vq[p, 0, o], vs[p, 0, o], np.ones((1, zeros + rest), bool),
+                              dim ** -0.5)
+    assert np.all(np.abs(out[0] - want) <= err) and np.all(want > 0.01)
