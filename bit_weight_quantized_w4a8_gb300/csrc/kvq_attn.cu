@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<DIM, BITS, NR>::kCtas) attn_
         }
 
         float acc[NR][MT][4];
-        float m[NR][2], l[NR][2];
+        float m[NR][2], l[NR][2];  // references (kTop, kSlack) and sums of 2^(t - m)
         #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
             m[nr][0] = m[nr][1] = -INFINITY;
@@ -172,11 +172,6 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<DIM, BITS, NR>::kCtas) attn_
                 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[nr][i][k] = 0.f;
         }
-        // value scales are taken relative to v_unit, a power of two above all met
-        // so far, times 2^-8: weights below 2^-6 of the largest keep 11 bits
-        // down to 2^-22 of it
-        float v_unit = 0x1p-100f;
-
         // page of this lane's key (lane = key of the step) for step u
         auto page_of = [&](int u) -> int {
             const int k = u * kUnit + warp * kStep + lane;
@@ -312,38 +307,47 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<DIM, BITS, NR>::kCtas) attn_
                     }
             }
 
-            // running maximum per row
-            float mn[NR][2];
-            bool grew = false;
+            // references: log2 of a bound of the value scales, the step's, or, where some
+            // row does not see all of it, of the keys that the row and lane see (a large
+            // value must cost only who sees it)
+            float ve = 0.f;
+            if (plain) {
+                const float v = fabsf(lds_f(sv + 4 * lane));
+                ve = log2_bound(__reduce_max_sync(0xFFFFFFFFu, v < INFINITY ? __float_as_uint(v) : 0u));
+            }
+            float top[NR][2];
+            bool up = false;
             #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
                 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float x = fmaxf(fmaxf(sc[0][nr][e], sc[0][nr][2 + e]), fmaxf(sc[1][nr][e], sc[1][nr][2 + e]));
-                    #pragma unroll
-                    for (int o = 4; o <= 16; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
-                    mn[nr][e] = fmaxf(m[nr][e], x);
-                    grew |= mn[nr][e] > m[nr][e];
+                    float x = fmaxf(fmaxf(sc[0][nr][e], sc[0][nr][2 + e]), fmaxf(sc[1][nr][e], sc[1][nr][2 + e])) + ve;
+                    if (!plain) {
+                        float v = 0.f;
+                        #pragma unroll
+                        for (int mt = 0; mt < 2; ++mt)
+                            #pragma unroll
+                            for (int hf = 0; hf < 2; ++hf)
+                                if ((seen >> ((mt * NR + nr) * 4 + 2 * hf + e)) & 1 && fabsf(vf[mt][hf]) < INFINITY)
+                                    v = fmaxf(v, fabsf(vf[mt][hf]));
+                        x += log2_bound(__float_as_uint(v));
+                    }
+                    top[nr][e] = x;
+                    up |= x - m[nr][e] > kTop + kSlack;
                 }
-            // largest finite value scale of the step
-            float v_old = v_unit;
-            {
-                const float v = fabsf(lds_f(sv + 4 * lane));
-                const unsigned top = __reduce_max_sync(0xFFFFFFFFu, v < INFINITY ? __float_as_uint(v) : 0u);
-                if (__uint_as_float(top) > v_unit)
-                    v_unit = __uint_as_float(min((top & 0x7F800000u) + 0x00800000u, 0x7E800000u));
-            }
-            if (__any_sync(0xFFFFFFFFu, grew) || v_unit != v_old) {
-                const float vr = v_old / v_unit;
+            if (__any_sync(0xFFFFFFFFu, up)) {
                 #pragma unroll
                 for (int nr = 0; nr < NR; ++nr) {
                     float f[2];
                     #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        f[e] = mn[nr][e] == -INFINITY ? 1.f : exp2_fast(m[nr][e] - mn[nr][e]);
+                        float x = top[nr][e];
+                        #pragma unroll
+                        for (int o = 4; o <= 16; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+                        const bool raise = x - m[nr][e] > kTop + kSlack;
+                        f[e] = raise ? exp2_fast(m[nr][e] - (x - kTop)) : 1.f;
+                        if (raise) m[nr][e] = x - kTop;
                         l[nr][e] *= f[e];
-                        f[e] *= vr;
-                        m[nr][e] = mn[nr][e];
                     }
                     #pragma unroll
                     for (int i = 0; i < MT; ++i) {
@@ -354,7 +358,6 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<DIM, BITS, NR>::kCtas) attn_
                     }
                 }
             }
-            const float v_inv = 256.f / v_unit;
             uint32_t wf[2][NR][2];
             #pragma unroll
             for (int nr = 0; nr < NR; ++nr) {
@@ -368,8 +371,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<DIM, BITS, NR>::kCtas) attn_
                         const float p1 = exp2_fast(sc[mt][nr][2 * hf + 1] - m1);
                         l[nr][0] += p0;
                         l[nr][1] += p1;
-                        const float vv = vf[mt][hf] * v_inv;
-                        float w0 = p0 * vv, w1 = p1 * vv;
+                        float w0 = p0 * vf[mt][hf], w1 = p1 * vf[mt][hf];
                         if (!plain) {  // an unseen key's scale may be anything
                             if (!((seen >> ((mt * NR + nr) * 4 + 2 * hf)) & 1)) w0 = 0.f;
                             if (!((seen >> ((mt * NR + nr) * 4 + 2 * hf + 1)) & 1)) w1 = 0.f;
@@ -457,7 +459,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<DIM, BITS, NR>::kCtas) attn_
                 float top = -INFINITY;
                 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_stat[0][w][r]);
-                const float f = m[nr][e] == -INFINITY ? 0.f : exp2_fast(m[nr][e] - top) * (v_unit * 0x1p-8f);
+                const float f = m[nr][e] == -INFINITY ? 0.f : exp2_fast(m[nr][e] - top);
                 float* dst = join + (warp * ROWS + r) * C::kPad;
                 constexpr int RUN = DIM >= 256 && W >= 256 ? 16 : DIM / 8;  // dimensions of a lane's run
                 #pragma unroll

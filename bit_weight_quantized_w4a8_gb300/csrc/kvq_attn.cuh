@@ -36,6 +36,18 @@ __device__ __forceinline__ float exp2_fast(float x) {  // within 2^-22 relative
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// A row's reference M: its weights are 2^(t - M) vs.  A bound of log2 of the largest one is
+// kTop when M is set and may grow by kSlack before M is raised and the sums rescaled;
+// weights down to 2^-23 of the largest 2^(t - M) times the largest vs keep 11 bits.
+constexpr float kTop = 10.f, kSlack = 4.f;
+// e with v < 2^e for the finite value scale v >= 0 whose bits are given, kLeastValue at least:
+// smaller values (zeros above all) give outputs of at most 2^-17, and a reference taken
+// that low would make the sum of 2^(t - reference) overflow: at -100, 2^18
+// keys of zero values did (outputs of 0).
+constexpr float kLeastValue = -24.f;
+__device__ __forceinline__ float log2_bound(uint32_t bits) {
+    return fmaxf((float)((int)(bits >> 23) - 126), kLeastValue);
+}
 __device__ __forceinline__ uint32_t hsub2_u(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));

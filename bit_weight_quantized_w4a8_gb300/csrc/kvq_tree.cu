@@ -19,8 +19,8 @@
 // one slot computes weights the tensor core works for the other.
 //
 // Softmax: row r keeps a reference M; p_j = 2^(t_j - M) is summed in fp32 and w_j
-// = p_j vs_j rounded to binary16.  M is the row's maximum so far plus e - 10,
-// 2^e being a bound of the value scales, and is raised (and O and the sum
+// = p_j vs_j rounded to binary16.  M is the maximum of t_j + e - 10 so far, 2^e being a bound
+// of the value scales that the row sees near j, and is raised (and O and the sum
 // rescaled) only when a weight would pass 2^14: so seldom that O stays in TMEM.
 //
 // Measured in graphs, with the join: 6 trees of 9, 32 heads on 2, 30001 keys of 4 bits 65 us;
@@ -50,12 +50,6 @@ constexpr int kTreeThreads = (kSoftWarps + kLoadWarps) * 32;
 constexpr int kRowsTile = 128;   // rows of a tile, TMEM lanes
 constexpr int kBlock = 128;      // keys of a unit
 constexpr int kScaleRing = 4;    // blocks whose scales are held
-constexpr float kTop = 10.f;     // log2 of the weight of a fresh maximum
-constexpr float kSlack = 4.f;    // log2 of what it may grow by before O is rescaled
-// log2 of the least bound of a block's value scales.  Smaller values (zeros above all)
-// give at most 2^-17, and a reference taken that low would make the weights' sum, in units of
-// 2^reference, overflow: at -100, 2^18 keys of zero values did (outputs of 0).
-constexpr float kLeastValue = -24.f;
 
 struct alignas(16) BlockScales {  // read as 16-byte vectors
     float k[kBlock];        // ks * scale * log2(e), never 0, of the scale's sign
@@ -187,6 +181,53 @@ __device__ __forceinline__ uint32_t seen_bits(int d0, bool tree, uint64_t word, 
     }
     if (d0 >= 0) return d0 < 64 ? (uint32_t)(word >> d0) : 0u;
     return (uint32_t)(word << -d0) | ((1u << -d0) - 1u);
+}
+
+// Maxima of t plus log2 of a bound of the value's scale over the keys that four rows of
+// this thread see, for a block that some rows do not see all of.  S of an
+// unseen key first becomes what its factor takes to -inf, S of a seen key with a bad scale NaN.
+// Each logit counts with its own value's scale: a large value must cost only the rows that
+// see it.  (A call, so that the registers it takes are not taken from the blocks that all see.)
+__device__ __noinline__ float4 score_masked(uint32_t ts, const BlockScales* bs, const uint64_t* word, const int* tok, int d0, int half, bool tree, float unseen) {
+    const int c2 = 2 * (threadIdx.x & 3);
+    const float* kf = bs->k + 64 * half + c2;
+    const float* vf = bs->v + 64 * half + c2;
+    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    #pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const uint32_t valid = reinterpret_cast<const uint32_t*>(bs->valid)[2 * half + c];
+        const uint32_t bad = reinterpret_cast<const uint32_t*>(bs->bad)[2 * half + c] >> c2;
+        #pragma unroll
+        for (int hb = 0; hb < 2; ++hb) {
+            uint32_t s[16], see[2];
+            tmem_ld_frag32(ts + 32 * c + hb * (16u << 16), s);
+            #pragma unroll
+            for (int rr = 0; rr < 2; ++rr)
+                see[rr] = (valid & seen_bits(d0 + 32 * c, tree, word[16 * hb + 8 * rr], tok[16 * hb + 8 * rr])) >> c2;
+            tmem_ld_wait();
+            #pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                constexpr uint32_t one = 1;
+                const uint32_t bit = one << (8 * (x >> 2) + (x & 1));
+                if (!(see[(x >> 1) & 1] & bit)) s[x] = __float_as_uint(unseen);
+                else if (bad & bit) s[x] = 0x7FFFFFFFu;
+            }
+            tmem_st_frag32(ts + 32 * c + hb * (16u << 16), s);
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint64_t kk = *reinterpret_cast<const uint64_t*>(kf + 32 * c + 8 * j);
+                const uint2 v = *reinterpret_cast<const uint2*>(vf + 32 * c + 8 * j);
+                const uint64_t vl = pack2(log2_bound(v.x & 0x7FFFFFFFu), log2_bound(v.y & 0x7FFFFFFFu));
+                #pragma unroll
+                for (int rr = 0; rr < 2; ++rr) {
+                    const float2 d = unpack2(fma2(pack2(__uint_as_float(s[4 * j + 2 * rr]), __uint_as_float(s[4 * j + 2 * rr + 1])), kk, vl));
+                    top[2 * hb + rr] = max3(top[2 * hb + rr], d.x, d.y);
+                }
+            }
+        }
+    }
+    tmem_st_wait();
+    return make_float4(top[0], top[1], top[2], top[3]);
 }
 
 // Column of dimension y in a group of eight: the widened 4-bit codes come in the
@@ -516,13 +557,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                 const BlockScales& bs = sh.sc[blk % kScaleRing];
                 ok = ok && wait(sh.scfull[blk % kScaleRing], blk / kScaleRing);
                 const int k0 = u * kBlock;
-                float ve = 0.f;  // 2^ve bounds the block's value scales
+                float ve = 0.f;  // 2^ve bounds the value scales of a plain block
                 bool plain = true;
                 if (ok && !idle) {
                     const float4 v = reinterpret_cast<const float4*>(bs.vmax)[0], v2 = reinterpret_cast<const float4*>(bs.vmax)[1];
                     const uint4 odd = reinterpret_cast<const uint4*>(bs.odd)[0], odd2 = reinterpret_cast<const uint4*>(bs.odd)[1];
-                    const float top = fmaxf(max3(v.x, v.y, max3(v.z, v.w, v2.x)), max3(v2.y, v2.z, v2.w));
-                    ve = fmaxf((float)((int)(__float_as_uint(top) >> 23) - 126), kLeastValue);
+                    ve = log2_bound(__float_as_uint(fmaxf(max3(v.x, v.y, max3(v.z, v.w, v2.x)), max3(v2.y, v2.z, v2.w))));
                     plain = k0 + kBlock <= start && (odd.x | odd.y | odd.z | odd.w | odd2.x | odd2.y | odd2.z | odd2.w) == 0u;
                 }
                 ok = ok && wait(sh.sfull[slot], s_phase[slot] + i);
@@ -533,49 +573,34 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                 bool up = false;
                 if (work) {
                     tc_fence_after_sync();
-                    // the maxima of this thread's keys, rows k; first, in blocks that need it, S of
-                    // an unseen key becomes what its factor takes to -inf, and S of a seen key
-                    // with a bad scale NaN
-                    const float unseen = a.scale_log2 < 0.f ? INFINITY : -INFINITY;
-                    #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int c = e >> 1, hb = e & 1;
-                        uint32_t s[16];
-                        tmem_ld_frag32(ts + 32 * c + hb * kHalfLanes, s);
-                        if (plain) {
-                            tmem_ld_wait();
-                        } else {
-                            const uint32_t bad = reinterpret_cast<const uint32_t*>(bs.bad)[2 * half + c] >> (2 * (lane & 3));
-                            uint32_t see[2];
-                            #pragma unroll
-                            for (int rr = 0; rr < 2; ++rr) {
-                                const int r = 32 * quad + 16 * hb + 8 * rr + (lane >> 2);
-                                see[rr] = (reinterpret_cast<const uint32_t*>(bs.valid)[2 * half + c] &
-                                           seen_bits(k0 + 64 * half + 32 * c - start, a.mask != nullptr, sh.word[tl][r], sh.tok[tl][r])) >> (2 * (lane & 3));
-                            }
+                    // the maxima of this thread's keys, rows k
+                    if (plain) {
+                        #pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int c = e >> 1, hb = e & 1;
+                            uint32_t s[16];
+                            tmem_ld_frag32(ts + 32 * c + hb * kHalfLanes, s);
                             tmem_ld_wait();
                             #pragma unroll
-                            for (int x = 0; x < 16; ++x) {
-                                constexpr uint32_t one = 1;
-                                const uint32_t bit = one << (8 * (x >> 2) + (x & 1));
-                                if (!(see[(x >> 1) & 1] & bit)) s[x] = __float_as_uint(unseen);
-                                else if (bad & bit) s[x] = 0x7FFFFFFFu;
+                            for (int j = 0; j < 4; ++j) {
+                                const uint64_t kk = *reinterpret_cast<const uint64_t*>(kf + 32 * c + 8 * j);
+                                #pragma unroll
+                                for (int rr = 0; rr < 2; ++rr) {
+                                    const float2 d = unpack2(mul2(pack2(__uint_as_float(s[4 * j + 2 * rr]), __uint_as_float(s[4 * j + 2 * rr + 1])), kk));
+                                    top[2 * hb + rr] = max3(top[2 * hb + rr], d.x, d.y);
+                                }
                             }
-                            tmem_st_frag32(ts + 32 * c + hb * kHalfLanes, s);
                         }
                         #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint64_t kk = *reinterpret_cast<const uint64_t*>(kf + 32 * c + 8 * j);
-                            #pragma unroll
-                            for (int rr = 0; rr < 2; ++rr) {
-                                const float2 d = unpack2(mul2(pack2(__uint_as_float(s[4 * j + 2 * rr]), __uint_as_float(s[4 * j + 2 * rr + 1])), kk));
-                                top[2 * hb + rr] = max3(top[2 * hb + rr], d.x, d.y);
-                            }
-                        }
+                        for (int k = 0; k < 4; ++k) top[k] += ve;
+                    } else {
+                        const int r = 32 * quad + (lane >> 2);
+                        const float4 m = score_masked(ts, &bs, sh.word[tl] + r, sh.tok[tl] + r, k0 + 64 * half - start, half, a.mask != nullptr,
+                                                      a.scale_log2 < 0.f ? INFINITY : -INFINITY);
+                        top[0] = m.x, top[1] = m.y, top[2] = m.z, top[3] = m.w;
                     }
-                    if (!plain) tmem_st_wait();
                     #pragma unroll
-                    for (int k = 0; k < 4; ++k) up |= top[k] - M[k] + ve > kTop + kSlack;
+                    for (int k = 0; k < 4; ++k) up |= top[k] - M[k] > kTop + kSlack;
                 }
                 // raise the references that are too low: both halves of the keys alike
                 if (named_bar_or(bar_vote(slot), kSlotWarps * 32, up)) {
@@ -591,8 +616,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                         #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const float m = fmaxf(top[k], sh.top[slot][half ^ 1][32 * quad + 8 * k + (lane >> 2)]);
-                            const bool raise = m - M[k] + ve > kTop + kSlack;
-                            const float Mn = raise ? m + ve - kTop : M[k];
+                            const bool raise = m - M[k] > kTop + kSlack;
+                            const float Mn = raise ? m - kTop : M[k];
                             f[k] = !raise ? 1.f : M[k] == -INFINITY ? 0.f : exp2_fast(M[k] - Mn);
                             M[k] = Mn;
                             l[k] *= f[k];

@@ -603,14 +603,14 @@ int kvq_keep(const kvq_cache_t* cache, const kvq_batch_t* batch, const int32_t* 
  * over the slots j that token t = cu[b] + i sees: every j < start[b], and of the
  * drafted tokens those whose bit j - start[b] is set in mask[t] (the
  * token's ancestors and itself, for a tree), or, with mask NULL, j <= start[b]
- * + i.  A token that sees nothing gets zeros.  A key whose scale is NaN or
- * infinite harms only the rows that see it.
+ * + i.  A token that sees nothing gets zeros.  A key whose scale, or whose value's,
+ * is NaN, infinite or large harms only the rows that see it.
  * Arithmetic: the products of binary16 queries and integer codes are summed in
  * fp32; softmax statistics, their merge over the pieces of a long cache and the
  * output sums are fp32; p_j vs_j is rounded to binary16 for the second product:
- * within 2^-11 of itself, or, where it is below 2^-21 of the row's largest p
- * times the largest |vs|, within 2^-32 of that (|vs| below 2^-24 taken as 2^-24, whose
- * values a binary16 output holds as subnormals).
+ * within 2^-11 of itself, or, where it is below 2^-23 of the row's largest p
+ * times the largest |vs| that the row sees, within 2^-34 of that (|vs| below 2^-24 taken as
+ * 2^-24, whose values a binary16 output holds as subnormals).
  * The pieces depend on cu, start and the sizes alone and are merged in their
  * order: the same call gives the same bits.
  * Two kernels: rows of a (sequence, cache head), tokens x heads_q / heads of

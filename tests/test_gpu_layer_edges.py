@@ -104,6 +104,26 @@ def test_a_nan_that_is_written_reaches_the_rows_that_see_it(w4, wide, which):  #
 
 # -- attention ------------------------------------------------------------------------
 
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("big", [1e6, -1e6, 1e30, -1e30])
+@pytest.mark.parametrize("tok,ctx", [((5, 6), (170, 3)), ((40, 9), (900, 90))])
+def test_attention_large_values_in_masked_keys(w4, wide, bits, big, tok, ctx):  # noqa: F811
+    """A drafted token with a large value vector changes only the rows that see it."""
+    rng = np.random.default_rng(22)
+    hq, heads, dim = 32, 2, 128
+    pg = ref.Paged(rng, tok, ctx, 16, extra_cols=wide_cols(2, heads, 16) if wide else 1)
+    c, _, host = fill(w4, rng, pg, heads, dim, bits)
+    mask = ref.tree_masks(rng, tok)
+    mask[:tok[0]] &= ~np.uint64(4)  # nobody but token 2 sees token 2
+    mask[2] |= np.uint64(4)
+    p, o = pg.where(0, [ctx[0] + 2])
+    c.vs[int(p[0]), :, int(o[0])] = big
+    q = rng.standard_normal((pg.tokens, hq, dim)).astype(F16)
+    out = w4.kvq_attention(dev(q), c, make_batch(w4, pg), mask=dev(mask.view(np.int64)))
+    check_attention(w4, rng, pg, q, c, host, hq, heads, dim, mask, dim ** -0.5, out, rows_off=(2,))
+
+
 @pytest.mark.parametrize("hq,dim", [(8, 64), (64, 64), (64, 128)])
 @pytest.mark.parametrize("order", ["zeros first", "zeros last"])
 def test_attention_many_zero_values(w4, hq, dim, order):  # noqa: F811
