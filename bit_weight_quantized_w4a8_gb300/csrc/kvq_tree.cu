@@ -52,8 +52,8 @@ constexpr int kBlock = 128;      // keys of a unit
 constexpr int kScaleRing = 4;    // blocks whose scales are held
 
 struct alignas(16) BlockScales {  // read as 16-byte vectors
-    float k[kBlock];        // ks * scale * log2(e), never 0, of the scale's sign
-    float v[kBlock];        // vs, 0 where one of the two is bad: not finite, or ks below 0
+    float k[kBlock];        // ks * scale * log2(e), never 0
+    float v[kBlock];        // vs, 0 where one of the two is bad: not finite
     float vmax[8];          // largest |v| of keys 16 w .. 16 w + 15
     uint32_t odd[8];        // not 0: some of them is not there or bad
     uint16_t valid[8];      // bit i of word w: key 16 w + i is there
@@ -185,10 +185,11 @@ __device__ __forceinline__ uint32_t seen_bits(int d0, bool tree, uint64_t word, 
 
 // Maxima of t plus log2 of a bound of the value's scale over the keys that four rows of
 // this thread see, for a block that some rows do not see all of.  S of an
-// unseen key first becomes what its factor takes to -inf, S of a seen key with a bad scale NaN.
+// unseen key first becomes what its factor, of either sign, takes to -inf, S of a seen key
+// with a bad scale NaN.
 // Each logit counts with its own value's scale: a large value must cost only the rows that
 // see it.  (A call, so that the registers it takes are not taken from the blocks that all see.)
-__device__ __noinline__ float4 score_masked(uint32_t ts, const BlockScales* bs, const uint64_t* word, const int* tok, int d0, int half, bool tree, float unseen) {
+__device__ __noinline__ float4 score_masked(uint32_t ts, const BlockScales* bs, const uint64_t* word, const int* tok, int d0, int half, bool tree) {
     const int c2 = 2 * (threadIdx.x & 3);
     const float* kf = bs->k + 64 * half + c2;
     const float* vf = bs->v + 64 * half + c2;
@@ -209,7 +210,8 @@ __device__ __noinline__ float4 score_masked(uint32_t ts, const BlockScales* bs, 
             for (int x = 0; x < 16; ++x) {
                 constexpr uint32_t one = 1;
                 const uint32_t bit = one << (8 * (x >> 2) + (x & 1));
-                if (!(see[(x >> 1) & 1] & bit)) s[x] = __float_as_uint(unseen);
+                const uint32_t k = __float_as_uint(kf[32 * c + 8 * (x >> 2) + (x & 1)]);
+                if (!(see[(x >> 1) & 1] & bit)) s[x] = 0xFF800000u ^ (k & 0x80000000u);
                 else if (bad & bit) s[x] = 0x7FFFFFFFu;
             }
             tmem_st_frag32(ts + 32 * c + hb * (16u << 16), s);
@@ -401,9 +403,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                         // a factor of 0 would make NaN of an unseen key's -inf; a key of zeros
                         // has logit 0 with any
                         const float kk = sk * a.scale_log2;
-                        const bool fine = fabsf(kk) < INFINITY && fabsf(sv) < INFINITY && sk >= 0.f;
+                        const bool fine = fabsf(kk) < INFINITY && fabsf(sv) < INFINITY;
                         if (lane < 16) {
-                            bs.k[key] = fine && kk != 0.f ? kk : a.scale_log2 < 0.f ? -1e-30f : 1e-30f;
+                            bs.k[key] = fine && kk != 0.f ? kk : 1e-30f;
                             bs.v[key] = fine ? sv : 0.f;
                         }
                         const unsigned bad = __ballot_sync(0xFFFFFFFFu, !fine) & 0xFFFFu;
@@ -595,8 +597,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
                         for (int k = 0; k < 4; ++k) top[k] += ve;
                     } else {
                         const int r = 32 * quad + (lane >> 2);
-                        const float4 m = score_masked(ts, &bs, sh.word[tl] + r, sh.tok[tl] + r, k0 + 64 * half - start, half, a.mask != nullptr,
-                                                      a.scale_log2 < 0.f ? INFINITY : -INFINITY);
+                        const float4 m = score_masked(ts, &bs, sh.word[tl] + r, sh.tok[tl] + r, k0 + 64 * half - start, half, a.mask != nullptr);
                         top[0] = m.x, top[1] = m.y, top[2] = m.z, top[3] = m.w;
                     }
                     #pragma unroll

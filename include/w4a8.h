@@ -603,8 +603,8 @@ int kvq_keep(const kvq_cache_t* cache, const kvq_batch_t* batch, const int32_t* 
  * over the slots j that token t = cu[b] + i sees: every j < start[b], and of the
  * drafted tokens those whose bit j - start[b] is set in mask[t] (the
  * token's ancestors and itself, for a tree), or, with mask NULL, j <= start[b]
- * + i.  A token that sees nothing gets zeros.  A key whose scale, or whose value's,
- * is NaN, infinite or large harms only the rows that see it.
+ * + i.  A token that sees nothing gets zeros.  Scales may have either sign; one (a key's
+ * or a value's) that is NaN, infinite or large harms only the rows that see it.
  * Arithmetic: the products of binary16 queries and integer codes are summed in
  * fp32; softmax statistics, their merge over the pieces of a long cache and the
  * output sums are fp32; p_j vs_j is rounded to binary16 for the second product:

@@ -124,6 +124,24 @@ def test_attention_large_values_in_masked_keys(w4, wide, bits, big, tok, ctx):  
     check_attention(w4, rng, pg, q, c, host, hq, heads, dim, mask, dim ** -0.5, out, rows_off=(2,))
 
 
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("scale", [0.1, -0.1])
+def test_attention_negative_scales(w4, wide, bits, scale):  # noqa: F811
+    """Scales of either sign are factors like any other, in both kernels."""
+    rng = np.random.default_rng(23)
+    tok, ctx, hq, heads, dim = (5, 3), (300, 20), 32, 2, 128
+    pg = ref.Paged(rng, tok, ctx, 32, extra_cols=wide_cols(2, heads, 32) if wide else 1)
+    c, _, host = fill(w4, rng, pg, heads, dim, bits)
+    for (_, s), t in zip(host, (c.ks, c.vs)):
+        s *= np.where(rng.random(s.shape) < 0.5, -1, 1).astype(F32)
+        t.copy_(dev(s))
+    q = rng.standard_normal((pg.tokens, hq, dim)).astype(F16)
+    mask = ref.tree_masks(rng, tok)
+    out = w4.kvq_attention(dev(q), c, make_batch(w4, pg), mask=dev(mask.view(np.int64)), scale=scale)
+    check_attention(w4, rng, pg, q, c, host, hq, heads, dim, mask, scale, out)
+
+
 @pytest.mark.parametrize("hq,dim", [(8, 64), (64, 64), (64, 128)])
 @pytest.mark.parametrize("order", ["zeros first", "zeros last"])
 def test_attention_many_zero_values(w4, hq, dim, order):  # noqa: F811
