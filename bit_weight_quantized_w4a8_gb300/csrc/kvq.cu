@@ -178,9 +178,8 @@ __global__ void __launch_bounds__(kLayerThreads) rope_write_kernel(const WriteAr
             const int i = t0 + threadIdx.x;
             const int b = kvq_find_seq(a.b.cu, a.b.seqs, i);
             if (b >= 0) {
-                const int64_t st = a.b.start[b];
-                if (st >= 0)
-                    row = kvq_slot_row(a.b.table, a.b.max_pages, a.c.pages, a.c.shift, b, st + (i - a.b.cu[b]));
+                const int64_t slot = kvq_token_slot(a.b.cu, a.b.start, b, i);
+                if (slot >= 0) row = kvq_slot_row(a.b.table, a.b.max_pages, a.c.pages, a.c.shift, b, slot);
             }
             if (row < 0) atomicOr(&g_kvq_error, kErrCacheRange);
             slot_row[threadIdx.x] = row;
@@ -314,8 +313,7 @@ __global__ void __launch_bounds__(kLayerThreads) kvq_read_kernel(const KvqCacheA
         const int i = t0 + threadIdx.x;
         int64_t row = -1;
         const int s = kvq_find_seq(b.cu, b.seqs, i);
-        if (s >= 0 && b.start[s] >= 0)
-            row = kvq_slot_row(b.table, b.max_pages, c.pages, c.shift, s, (int64_t)b.start[s] + (i - b.cu[s]));
+        if (s >= 0) row = kvq_slot_row(b.table, b.max_pages, c.pages, c.shift, s, kvq_token_slot(b.cu, b.start, s, i));
         if (row < 0) atomicOr(&g_kvq_error, kErrCacheRange);
         slot_row[threadIdx.x] = row;
     }

@@ -14,7 +14,7 @@
 namespace w4a8 {
 
 // Sequence of token i: the b with cu[b] <= i < cu[b + 1], or -1 when the
-// offsets hold none (they do not cover i, or are not in order).
+// offsets hold none (they do not cover i, are negative or not in order).
 KVQ_HD int kvq_find_seq(const int32_t* cu, int seqs, int i) {
     int lo = 0, hi = seqs;  // cu[lo] <= i would hold, cu[hi] > i
     while (hi - lo > 1) {
@@ -24,7 +24,13 @@ KVQ_HD int kvq_find_seq(const int32_t* cu, int seqs, int i) {
         else
             hi = mid;
     }
-    return cu[lo] <= i && i < cu[lo + 1] ? lo : -1;
+    return cu[lo] >= 0 && cu[lo] <= i && i < cu[lo + 1] ? lo : -1;
+}
+
+// Slot of token i of the sequence b that kvq_find_seq gives, or -1 where its start is negative.
+KVQ_HD int64_t kvq_token_slot(const int32_t* cu, const int32_t* start, int b, int i) {
+    const int64_t s = start[b];
+    return s < 0 ? -1 : s + (i - cu[b]);
 }
 
 // Row of the pool (page * page_size + offset) of slot s of sequence b, or -1
