@@ -275,7 +275,7 @@ cudaError_t launch_write(const WriteArgs& a0, int dim, int sms, unsigned flags, 
     a.y_wide = reinterpret_cast<uintptr_t>(a.Y) % 16 == 0 && a.ld_y % 8 == 0;
     const int vecs = a.heads_q + (HAS_KV ? 2 * a.c.heads : 0);
     a.tokens_per_cta = a.b.tokens >= 8 * sms ? 4 : 1;
-    const int ctas = (a.b.tokens + a.tokens_per_cta - 1) / a.tokens_per_cta;
+    const int ctas = kvq_ctas(a.b.tokens, a.tokens_per_cta);
     const int groups = kLayerThreads / (dim / 8);
     int gy = 1;
     while (ctas * gy < 2 * sms && gy * groups < vecs * a.tokens_per_cta) gy *= 2;
@@ -469,7 +469,7 @@ cudaError_t launch_kvq_read(const kvq_cache_t& cc, const kvq_batch_t& bb, void* 
     const KvqCacheArg c = cache_arg(cc);
     const KvqBatchArg b = batch_arg(bb);
     const int per_cta = b.tokens >= 64 * sms ? kReadTokens : 8;
-    const dim3 grid((unsigned)(((int64_t)b.tokens + per_cta - 1) / per_cta));
+    const dim3 grid((unsigned)kvq_ctas(b.tokens, per_cta));
     auto go = [&](auto* out, auto dim, auto bits) {
         using T = std::remove_pointer_t<decltype(out)>;
         return layer_launch(kvq_read_kernel<T, decltype(dim)::value, decltype(bits)::value>, grid, kLayerThreads, 0, flags,

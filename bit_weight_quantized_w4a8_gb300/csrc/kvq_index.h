@@ -13,6 +13,9 @@
 
 namespace w4a8 {
 
+// CTAs of `per` tokens each for `tokens` of them, up to 2^31 - 1.
+KVQ_HD int kvq_ctas(int tokens, int per) { return tokens / per + (tokens % per != 0); }
+
 // Sequence of token i: the b with cu[b] <= i < cu[b + 1], or -1 when the
 // offsets hold none (they do not cover i, are negative or not in order).
 KVQ_HD int kvq_find_seq(const int32_t* cu, int seqs, int i) {

@@ -17,6 +17,7 @@ def index(tmp_path_factory):
 extern "C" int64_t slot(const int32_t* cu, const int32_t* st, int seqs, int i) {
     const int b = w4a8::kvq_find_seq(cu, seqs, i);
     return b < 0 ? -1 : w4a8::kvq_token_slot(cu, st, b, i); }
+extern "C" int ctas(int tokens, int per) { return w4a8::kvq_ctas(tokens, per); }
 """)
     subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover=undefined", "-shared", "-fPIC",
                     "-o", str(d / "index.so"), str(d / "index.cpp")], check=True)
@@ -41,3 +42,10 @@ def test_token_slots(index):
 def test_negative_offsets_and_starts_have_no_slot(index, cu, start):
     """A negative offset once moved tokens to slots further on, and far ones wrapped around."""
     assert all(slot(index, cu, start, i) == -1 for i in range(5))
+
+
+def test_ctas_of_any_token_count(index):
+    """Rounding up by adding first passed 2^31 at the largest counts that the entry points take."""
+    for per in (1, 4, 8, 32):
+        for tokens in (1, 3, 4, 5, 8191, 2 ** 31 - 4, 2 ** 31 - 2, 2 ** 31 - 1):
+            assert index.ctas(tokens, per) == -(-tokens // per)
