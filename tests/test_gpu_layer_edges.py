@@ -164,3 +164,46 @@ def test_attention_many_zero_values(w4, hq, dim, order):  # noqa: F811
     want, err = ref.attention(q[0, :1], kq[p, 0, o], ks[p, 0, o], vq[p, 0, o], vs[p, 0, o], np.ones((1, zeros + rest), bool),
                               dim ** -0.5)
     assert np.all(np.abs(out[0] - want) <= err) and np.all(want > 0.01)
+
+
+# -- dependent launches ---------------------------------------------------------------
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_dependent_launches_give_the_same_bits(w4, wide):  # noqa: F811
+    """A chain of all entry points, each reading what the one before wrote, with and
+    without W4A8_LAUNCH_PDL: the kernels start early and wait before they read."""
+    rng = np.random.default_rng(25)
+    tok, ctx, hq, heads, dim, page = (9, 30), (700, 45), 32, 2, 128, 32
+    pg = ref.Paged(rng, tok, ctx, page, extra_cols=wide_cols(2, heads, page) if wide else 1)
+    c, gs, _ = fill(w4, rng, pg, heads, dim, 8)
+    n = pg.tokens
+    b = make_batch(w4, pg)
+    normal = lambda *shape: dev(rng.standard_normal(shape).astype(F32))  # noqa: E731
+    q, k, v, r, w = normal(n, hq, dim), normal(n, heads, dim), normal(n, heads, dim), normal(n, hq * dim), normal(hq * dim)
+    pos = dev(rng.integers(0, 5000, n).astype(np.int32))
+    freqs = w4.rope_frequencies(dim, 1e4)[0].cuda()
+    mask = dev(ref.tree_masks(rng, tok).view(np.int64))
+    keep = np.full(n, -1, np.int32)
+    keep[:3], keep[9:11] = [2, 5, 8], [1, 29]
+    keep = dev(keep)
+    before = [t.clone() for t in c]
+    ws = torch.zeros(w4.kvq_attention_workspace_bytes(c, b, n, hq), dtype=torch.uint8, device="cuda")
+
+    def chain(flags):
+        for t, u in zip(c, before):
+            t.copy_(u)
+        out, x = [], q
+        for _ in range(3):
+            x = w4.rope_rotate(x, pos, freqs, flags=flags)
+            qo = w4.kvq_write(c, b, k, v, Q=x, pos=pos, freqs=freqs, flags=flags)
+            a = w4.kvq_attention(qo, c, b, mask=mask, ws=ws, flags=flags)
+            r2, x2 = w4.add_norm(r, w, y=a.view(n, -1), flags=flags)
+            w4.kvq_keep(c, b, keep, flags=flags)
+            out += [qo, a, r2, x2, *w4.kvq_read(c, b, n, flags=flags)]
+            x = r2.view(n, hq, dim)
+        return [t.clone() for t in out + list(c)]
+
+    plain = chain(0)
+    for _ in range(5):
+        assert all(torch.equal(x, y) for x, y in zip(plain, chain(1)))
+    guards.check_all(*gs)

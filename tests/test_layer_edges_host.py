@@ -49,3 +49,23 @@ def test_ctas_of_any_token_count(index):
     for per in (1, 4, 8, 32):
         for tokens in (1, 3, 4, 5, 8191, 2 ** 31 - 4, 2 ** 31 - 2, 2 ** 31 - 1):
             assert index.ctas(tokens, per) == -(-tokens // per)
+
+
+@pytest.mark.parametrize("rot,base,factor,old_ctx,low,high", [(128, 1e6, 4.0, 32768, 1.0, 32.0), (64, 1e4, 16.0, 4096, 1.0, 32.0),
+                                                              (256, 5e5, 2.0, 8192, 2.0, 20.0)])
+def test_yarn_between_its_ends(rot, base, factor, old_ctx, low, high):
+    """The ramp over the pair index, from the pair that turns `high` times within old_ctx
+    positions (rounded down) to the one that turns `low` times (rounded up)."""
+    import math
+
+    import bit_weight_quantized_w4a8_gb300 as w4
+    w4.build()
+    got, mscale = w4.rope_frequencies(rot, base, "yarn", factor, old_ctx=old_ctx, low=low, high=high)
+    # freq(i) * old_ctx / (2 pi) = turns  <=>  i = rot / 2 * log_base(old_ctx / (2 pi turns))
+    pair = lambda turns: rot / 2 * math.log(old_ctx / (2 * math.pi * turns)) / math.log(base)  # noqa: E731
+    a, z = max(math.floor(pair(high)), 0), min(math.ceil(pair(low)), rot - 1)
+    i = np.arange(rot // 2)
+    f = base ** (-2.0 * i / rot)
+    part = np.clip((i - a) / (z - a), 0, 1)
+    assert np.allclose(got.numpy(), f * (1 - part) + f / factor * part, rtol=1e-13, atol=0)
+    assert ((part > 0) & (part < 1)).sum() > 3 and mscale == np.float32(0.1 * math.log(factor) + 1)
