@@ -12,12 +12,16 @@
 // that 8 rows are enough to fill an instruction: S^T = K Q^T, then O^T = V^T W^T,
 // W^T being S^T's weights transposed by movmatrix.  Codes are integers of
 // at most 7 bits and sign, exact in binary16, and the scales stay outside the products:
-// ks_j multiplies the fp32 logit, vs_j the fp32 weight before its rounding.
+// ks_j multiplies the fp32 logit, vs_j the fp32 weight before its rounding to binary16, the
+// operand type of the second product (the error against 64 bits is 2.9e-4 with it, 2.1e-4
+// with fp32 weights, which is the output's own rounding; fp32 weights would need a second
+// product of their low halves).
 //
 // Bound by the cache's bytes at 8 bits: 24 sequences of up to 32768 keys (28 heads on 4,
-// dim 128) 114.5 us in a graph, 89% of the copy rate, with three CTAs an SM (two: 120).
-// At 4 bits by the widening of the codes, about half of that rate.  One token over 2048
-// keys: 10 us, its loads' latency and the join.
+// dim 128) 115 us in a graph, 89% of the copy rate, with three CTAs an SM (two: 120); 32 heads
+// on 2 (16 rows, two CTAs an SM), up to 16384 keys: 49 us, 52% of it.
+// At 4 bits by the widening of the codes: 52% of the copy rate (102 us) and
+// 30% (44.5).  One token over 2048 keys: 10 us, its loads' latency and the join.
 #include <atomic>
 #include <type_traits>
 

@@ -3,8 +3,11 @@
 //
 // The rows of a (sequence, cache head), tokens x group of them, are taken in
 // tiles of R rows and row blocks of up to P tiles; a row block walks the
-// sequence's keys in units, each of which counts what it costs (for P = 2: 4 with
+// sequence's keys in units, each of which counts what it costs (for P = 2: 5 with
 // two tiles, 3 with one, as measured: the keys cost the same, the rows less).
+// Every row block has the units of its sequence's whole length: without a mask, an early
+// block's last ones, which none of its rows sees, are counted too (and the tile kernel computes
+// them), nothing up to 64 tokens, half of the work for a long prompt from an empty cache.
 // The batch's work, ordered by sequence, head, row block and key, is cut into
 // one run per CTA on the device, from the lengths found there: long and
 // short sequences fill the GPU alike, a captured graph follows its lengths,
@@ -91,7 +94,7 @@ struct AttnWalk {
     struct Shared {
         int64_t units[THREADS / 32], find[2];
     };
-    static constexpr int kCost1 = P == 1 ? 1 : 3, kCostP = P == 1 ? 1 : 5;  // of a unit: 86 to 146 ps a key measured
+    static constexpr int kCost1 = P == 1 ? 1 : 3, kCostP = P == 1 ? 1 : 5;  // of a unit: 92 to 157 ps a key measured
     static_assert(P <= 2, "a row block has one tile or P");
     struct Work {
         int64_t tiles, units, per_head;

@@ -23,9 +23,9 @@
 // of the value scales that the row sees near j, and is raised (and O and the sum
 // rescaled) only when a weight would pass 2^14: so seldom that O stays in TMEM.
 //
-// Measured in graphs, with the join: 6 trees of 9, 32 heads on 2, 30001 keys of 4 bits 65 us;
+// Measured in graphs, with the join: 6 trees of 9, 32 heads on 2, 30001 keys of 4 bits 66 us;
 // 4 trees of 64, 28 heads on 4, 32001 keys of 8 bits 178 us, 30% of the tensor
-// cores' measured rate (kvq_attn.cu: 534).  A block of 128 keys and 256 rows takes
+// cores' measured rate (kvq_attn.cu: 534), heads of 64 148.  A block of 128 keys and 256 rows takes
 // 2.9 us, its products 1.07, the softmax without products and loads 2.1: bound by the chain S,
 // weights, product within a slot.  (Keys of the next block widened while this one is
 // at work: 84.5 -> 74.4 us for 4 trees of 16 on one tile, 194 -> 186 for those of 64.)
@@ -43,8 +43,9 @@ namespace {
 
 // Two slots of eight softmax warps and eight that load: six warps to a scheduler,
 // 80 registers a thread.  Everything here waits for something (loads, TMEM,
-// barriers), so many warps with little each; a spilled register costs a trip to
-// L2, as the tiles leave no first-level cache.
+// barriers), so many warps with little each.  All four forms spill (32 to 56 bytes a thread,
+// -Xptxas -v), and a spilled register costs a trip to L2, as the tiles leave no
+// first-level cache: what only some blocks need is kept out of the others' way (score_masked).
 constexpr int kSlotWarps = 8, kSoftWarps = 2 * kSlotWarps, kLoadWarps = 8;
 constexpr int kTreeThreads = (kSoftWarps + kLoadWarps) * 32;
 constexpr int kRowsTile = 128;   // rows of a tile, TMEM lanes
@@ -183,13 +184,13 @@ __device__ __forceinline__ uint32_t seen_bits(int d0, bool tree, uint64_t word, 
     return (uint32_t)(word << -d0) | ((1u << -d0) - 1u);
 }
 
-// Maxima of t plus log2 of a bound of the value's scale over the keys that four rows of
-// this thread see, for a block that some rows do not see all of.  S of an
-// unseen key first becomes what its factor, of either sign, takes to -inf, S of a seen key
-// with a bad scale NaN.
-// Each logit counts with its own value's scale: a large value must cost only the rows that
-// see it.  (A call, so that the registers it takes are not taken from the blocks that all see.)
-__device__ __noinline__ float4 score_masked(uint32_t ts, const BlockScales* bs, const uint64_t* word, const int* tok, int d0, int half, bool tree) {
+// Maxima of t + e over this thread's keys that its four rows see, 2^e a bound of the key's own
+// value scale, for a block that some rows do not see all of: a large value must cost
+// only the rows that see it.  S of an unseen key first becomes what its factor, of either
+// sign, takes to -inf, S of a seen key with a bad scale NaN.  (A call of its own: written
+// out, it made the other blocks slower, trees of 64 176 -> 182 us, 4 of 16 72 -> 74.)
+__device__ __noinline__ float4 score_masked(uint32_t ts, const BlockScales* bs, const uint64_t* word, const int* tok, int d0,
+                                            int half, bool tree) {
     const int c2 = 2 * (threadIdx.x & 3);
     const float* kf = bs->k + 64 * half + c2;
     const float* vf = bs->v + 64 * half + c2;
@@ -252,6 +253,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const AttnArgs a)
     uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
     const uint32_t base = smem_u32(smem);
     TreeShared& sh = *reinterpret_cast<TreeShared*>(smem + C::kOffShared);
+    // (The join's CTAs do not fit beside this one, so that nothing after them, which might
+    // hold TMEM while it waits for this kernel, starts before the allocation below.)
     griddep_launch_dependents();
     griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31;
@@ -871,15 +874,18 @@ auto by_config(const kvq_cache_t& c, F f) {
 
 int tree_ctas(int sms) { return sms < kAttnMaxCtas ? sms : kAttnMaxCtas; }
 
-// Whether this kernel serves a call: it saves the difference of what a cached
-// token costs the two, times the tokens, against the 22 us that it takes longer
-// for a short cache.  Measured on GB300 (8 sequences of 4 heads of 128, 8 bits, ps per token and
-// cache head): the row-block kernel 38 for each 16 rows, this one 86 for one tile of 128
-// rows and 146 for two.  At 32001 tokens 56 rows take 108 us here and 164 there; at 64
-// tokens 448 rows 40 and 22.  The cache is taken to be as long
-// as the page table allows: its length is on the device.
+// Whether this kernel serves a call: where it saves more than 22 us by the difference of
+// what a cached token costs the two.  Measured on GB300 (8 sequences of 4 heads,
+// 8192 to 32000 tokens, ps per token and cache head), at 128 dimensions: the row-block
+// kernel 40 to 43 for each 16 rows, this one 88 to 94 for one tile of 128 rows and 152 to 161 for
+// two, 4 and 8 bits alike; at 64 dimensions 26 to 28, and 70 to 78 and 133 to 139: nearly the same
+// ratios.  At 64 tokens and up to 128 rows this one takes 10 to 19 us longer (20 to 29 us against
+// 6 to 15).  22 us is high for a table as long as the sequences (over 672 calls of 8 to 448 rows and 64 to 32000
+// tokens the rule takes 1.03 of the better kernel's time on average, at most 1.83;
+// with 5 us 1.02, at most 1.46), but the cache is taken to be as long as the page table
+// allows, as its length is on the device, and a captured step has a table for the longest.
 bool tree_serves(const kvq_cache_t& c, const kvq_batch_t& b, int heads_q) {
-    if (c.dim > 128) return false;  // 256 dimensions of O for two tiles do not fit TMEM
+    if (c.dim > 128) return false;  // two tiles' O of 256 dimensions do not fit TMEM; there is no form for one
     const int64_t rows = (b.tokens * (heads_q / c.heads) + b.seqs - 1) / b.seqs, tiles = (rows + 127) / 128;
     const double here = (double)(tiles / 2) * 146e-6 + (double)(tiles % 2) * 86e-6, there = (double)((rows + 15) / 16) * 38e-6;
     const double keys = (double)b.seqs * c.heads * (double)(b.max_pages * c.page);

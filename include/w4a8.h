@@ -613,6 +613,9 @@ int kvq_keep(const kvq_cache_t* cache, const kvq_batch_t* batch, const int32_t* 
  * 2^-24, whose values a binary16 output holds as subnormals).
  * The pieces depend on cu, start and the sizes alone and are merged in their
  * order: the same call gives the same bits.
+ * Without a mask every block of a sequence's rows is charged the sequence's whole length:
+ * nothing more for a few tokens on a long cache, twice the work for a long
+ * prompt on an empty one.  Rows of tokens that no sequence holds are left as they are.
  * Two kernels: rows of a (sequence, cache head), tokens x heads_q / heads of
  * them, in blocks of 8 or 16 on warp-level products (kvq_attn.cu), or, where the rows
  * and the length that the page table allows make it worth its longer start, in tiles of 128
