@@ -23,8 +23,8 @@
 // of the value scales that the row sees near j, and is raised (and O and the sum
 // rescaled) only when a weight would pass 2^14: so seldom that O stays in TMEM.
 //
-// Measured in graphs, with the join: 6 trees of 9, 32 heads on 2, 30001 keys of 4 bits 66 us;
-// 4 trees of 64, 28 heads on 4, 32001 keys of 8 bits 178 us, 30% of the tensor
+// Measured in graphs, with the join: 6 trees of 9, 32 heads on 2, 30001 keys of 4 bits 65 us;
+// 4 trees of 64, 28 heads on 4, 32001 keys of 8 bits 177 us, 30% of the tensor
 // cores' measured rate (kvq_attn.cu: 534), heads of 64 148.  A block of 128 keys and 256 rows takes
 // 2.9 us, its products 1.07, the softmax without products and loads 2.1: bound by the chain S,
 // weights, product within a slot.  (Keys of the next block widened while this one is
@@ -43,7 +43,7 @@ namespace {
 
 // Two slots of eight softmax warps and eight that load: six warps to a scheduler,
 // 80 registers a thread.  Everything here waits for something (loads, TMEM,
-// barriers), so many warps with little each.  All four forms spill (32 to 56 bytes a thread,
+// barriers), so many warps with little each.  All four forms spill (60 to 88 bytes a thread,
 // -Xptxas -v), and a spilled register costs a trip to L2, as the tiles leave no
 // first-level cache: what only some blocks need is kept out of the others' way (score_masked).
 constexpr int kSlotWarps = 8, kSoftWarps = 2 * kSlotWarps, kLoadWarps = 8;
@@ -188,7 +188,7 @@ __device__ __forceinline__ uint32_t seen_bits(int d0, bool tree, uint64_t word, 
 // value scale, for a block that some rows do not see all of: a large value must cost
 // only the rows that see it.  S of an unseen key first becomes what its factor, of either
 // sign, takes to -inf, S of a seen key with a bad scale NaN.  (A call of its own: written
-// out, it made the other blocks slower, trees of 64 176 -> 182 us, 4 of 16 72 -> 74.)
+// out, it made the other blocks slower, trees of 64 177 -> 182 us, 4 of 16 72 -> 74.)
 __device__ __noinline__ float4 score_masked(uint32_t ts, const BlockScales* bs, const uint64_t* word, const int* tok, int d0,
                                             int half, bool tree) {
     const int c2 = 2 * (threadIdx.x & 3);
@@ -199,6 +199,16 @@ __device__ __noinline__ float4 score_masked(uint32_t ts, const BlockScales* bs, 
     for (int c = 0; c < 2; ++c) {
         const uint32_t valid = reinterpret_cast<const uint32_t*>(bs->valid)[2 * half + c];
         const uint32_t bad = reinterpret_cast<const uint32_t*>(bs->bad)[2 * half + c] >> c2;
+        uint64_t kk[4], ve[4];
+        uint32_t none[8];  // what an unseen key's S becomes
+        #pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint2 k = *reinterpret_cast<const uint2*>(kf + 32 * c + 8 * j), v = *reinterpret_cast<const uint2*>(vf + 32 * c + 8 * j);
+            kk[j] = pack2(__uint_as_float(k.x), __uint_as_float(k.y));
+            ve[j] = pack2(log2_bound(v.x & 0x7FFFFFFFu), log2_bound(v.y & 0x7FFFFFFFu));
+            none[2 * j] = 0xFF800000u ^ (k.x & 0x80000000u);
+            none[2 * j + 1] = 0xFF800000u ^ (k.y & 0x80000000u);
+        }
         #pragma unroll
         for (int hb = 0; hb < 2; ++hb) {
             uint32_t s[16], see[2];
@@ -211,19 +221,15 @@ __device__ __noinline__ float4 score_masked(uint32_t ts, const BlockScales* bs, 
             for (int x = 0; x < 16; ++x) {
                 constexpr uint32_t one = 1;
                 const uint32_t bit = one << (8 * (x >> 2) + (x & 1));
-                const uint32_t k = __float_as_uint(kf[32 * c + 8 * (x >> 2) + (x & 1)]);
-                if (!(see[(x >> 1) & 1] & bit)) s[x] = 0xFF800000u ^ (k & 0x80000000u);
+                if (!(see[(x >> 1) & 1] & bit)) s[x] = none[2 * (x >> 2) + (x & 1)];
                 else if (bad & bit) s[x] = 0x7FFFFFFFu;
             }
             tmem_st_frag32(ts + 32 * c + hb * (16u << 16), s);
             #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint64_t kk = *reinterpret_cast<const uint64_t*>(kf + 32 * c + 8 * j);
-                const uint2 v = *reinterpret_cast<const uint2*>(vf + 32 * c + 8 * j);
-                const uint64_t vl = pack2(log2_bound(v.x & 0x7FFFFFFFu), log2_bound(v.y & 0x7FFFFFFFu));
                 #pragma unroll
                 for (int rr = 0; rr < 2; ++rr) {
-                    const float2 d = unpack2(fma2(pack2(__uint_as_float(s[4 * j + 2 * rr]), __uint_as_float(s[4 * j + 2 * rr + 1])), kk, vl));
+                    const float2 d = unpack2(fma2(pack2(__uint_as_float(s[4 * j + 2 * rr]), __uint_as_float(s[4 * j + 2 * rr + 1])), kk[j], ve[j]));
                     top[2 * hb + rr] = max3(top[2 * hb + rr], d.x, d.y);
                 }
             }
