@@ -265,7 +265,7 @@ def _pages(c, g):
 def _prep_axes(c, g):
     i = np.arange(c["rot"] // 2, dtype=np.float64)
     s = {"freqs": torch.from_numpy(c["base"] ** (-2.0 * i / c["rot"])).to(DEV),
-         "axis": torch.tensor(_axis_of(c), dtype=torch.uint8, device=DEV)}
+         "axis": torch.tensor(_axis_of(c), device=DEV), "axis_host": bytes(_axis_of(c))}
     if c["op"] == "axes":
         n = c["rows"]
         s["x"] = _normal(g, (n, c["heads"], c["dim"]), c["x"])
@@ -400,7 +400,6 @@ def _plan_call(s, add):
     stack_w[torch.where(gone, place, stack.numel())] = table
     stack.copy_(stack_w[:-1])
     top = top + back.sum()
-    table.masked_fill_(gone, -1)
     held, lens = torch.where(end, 0, held), torch.where(end, 0, lens)
     # pages go out, rows in order, as far as they and the tokens reach
     n = add.clamp_min(0).long()
@@ -436,7 +435,7 @@ def _plan(s):
 def _turn(x, s):
     """x [tokens][heads][dim] in 32 bits; angles of far positions in 64."""
     rot = 2 * s["freqs"].numel()
-    a = s["pos"][s["axis"].long()].t().double() * s["freqs"]
+    a = s["pos"][s["axis"]].t().double() * s["freqs"]
     cos, sin = torch.cos(a).float()[:, None, :], torch.sin(a).float()[:, None, :]
     x = x.float()
     if s["case"]["inter"]:
@@ -489,10 +488,10 @@ def run(state):
         return [batch.cu, pos, slot, seq] + [s[k] for k in ("lens", "held", "table", "stack", "top")]
     if c["op"] == "axes":
         return m.rope_rotate(s["x"], s["pos"], s["freqs"], interleaved=c["inter"], dtype=getattr(torch, c["out"]),
-                             axis=s["axis"])
+                             axis=s["axis_host"])
     cache, batch = m.KVQCache(s["k"], s["v"], s["ks"], s["vs"]), m.KVQBatch(s["cu"], s["start"], s["table"])
     q = m.kvq_write(cache, batch, s["K"], s["V"], Q=s["Q"], pos=s["pos"], freqs=s["freqs"], interleaved=c["inter"],
-                    axis=s["axis"])
+                    axis=s["axis_host"])
     return [q] + list(m.kvq_read(cache, batch, s["tokens"]))
 
 
@@ -613,7 +612,6 @@ def _exact_plan(c, s):
             if add[b] < 0:
                 for j in reversed(range(held[b])):
                     stack[top] = table[b, j]
-                    table[b, j] = -1
                     top += 1
                 held[b] = lens[b] = 0
         asked_pages = asked_tokens = 0
