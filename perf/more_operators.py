@@ -224,8 +224,10 @@ def _prep_plan(c, seed):
     ctx = ctx + rng.integers(0, 200, seqs)
     held = -(-ctx // page)
     ends = (np.arange(seqs) % 2 == 0) & c["swap"]
-    if c["swap"]:  # not only in the rows' order
+    if c["swap"]:  # not only in the rows' order; the others' next token fits their last page
         ends = ends[rng.permutation(seqs)]
+        ctx = ctx | 1
+        held = -(-ctx // page)
     after = -(-(np.where(ends, 0, ctx) + tok) // page)
     if c["swap"]:
         after = np.where(ends, after, -(-(ctx + 1) // page))
@@ -413,7 +415,6 @@ def _plan_call(s, add):
     k = col - held[:, None]
     new = (k >= 0) & (k < need[:, None])
     table.copy_(torch.where(new, stack[torch.where(new, top - 1 - before[:, None] - k, 0)], table))
-    stack.masked_fill_(torch.arange(stack.numel(), device=DEV) >= top - need.sum(), -1)
     s["held"].copy_(held + need)
     s["top"].copy_(top - need.sum())
     s["lens"].copy_(lens)
@@ -629,7 +630,7 @@ def _exact_plan(c, s):
             if ok:
                 for _ in range(need):
                     top -= 1
-                    table[b, held[b]], stack[top] = stack[top], -1
+                    table[b, held[b]] = stack[top]
                     held[b] += 1
                 for i in range(n):
                     x = int(lens[b]) + i
