@@ -35,6 +35,10 @@ EXPORTS = [
     "w4_interleave_rows", "w4a8_gate_up_silu_workspace_bytes", "w4a8_gate_up_silu", "w4a8_silu_mul",
     "add_norm", "rope_frequencies", "rope_rotate", "kvq_write", "kvq_read", "kvq_keep",
     "kvq_attention_workspace_bytes", "kvq_attention",
+    "rope_rotate_axes", "kvq_write_axes",
+    "kvq_plan_workspace_bytes", "kvq_plan", "draft_verify_workspace_bytes", "draft_verify",
+    "f8_quantize_weights", "f8_quantize_rows", "f8_gemm_workspace_bytes", "f8_gemm", "f8_linear_workspace_bytes",
+    "f8_linear",
 ]
 
 
@@ -62,6 +66,12 @@ class _Cache(ctypes.Structure):
 class _Batch(ctypes.Structure):
     _fields_ = [("cu", ctypes.c_void_p), ("start", ctypes.c_void_p), ("table", ctypes.c_void_p),
                 ("seqs", ctypes.c_int64), ("tokens", ctypes.c_int64), ("max_pages", ctypes.c_int64)]
+
+
+class _Pool(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("held", ctypes.c_void_p), ("stack", ctypes.c_void_p),
+                ("top", ctypes.c_void_p), ("seqs", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("pages", ctypes.c_int64), ("page", ctypes.c_int)]
 
 
 _i64, _p, _u = ctypes.c_int64, ctypes.c_void_p, ctypes.c_uint
@@ -113,6 +123,21 @@ _SIGS = {
     "kvq_keep": (ctypes.c_int, [_p, _p, _p, _u, _p]),
     "kvq_attention_workspace_bytes": (ctypes.c_size_t, [_p, _p, _int]),
     "kvq_attention": (ctypes.c_int, [_p, _p, _p, _int, _p, _f, _p, _p, ctypes.c_size_t, _u, _p]),
+    "rope_rotate_axes": (ctypes.c_int, [_p, _int, _i64, _i64, _int, _int, _p, _int, _p, _p, _int, _int, _f, _p, _int,
+                                        _i64, _u, _p]),
+    "kvq_write_axes": (ctypes.c_int, [_p, _p, _p, _i64, _p, _i64, _p, _i64, _int, _int, _p, _int, _p, _p, _int, _int, _f,
+                                      _p, _u, _p]),
+    "kvq_plan_workspace_bytes": (ctypes.c_size_t, [_p]),
+    "kvq_plan": (ctypes.c_int, [_p, _p, _p, _p, _p, _i64, _p, _p, _p, _p, _p, ctypes.c_size_t, _u, _p]),
+    "draft_verify_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
+    "draft_verify": (ctypes.c_int, [_p, _int, _i64, _i64, _p, _i64, _i64, _p, _p, _p, _int, _i64, _p, _p, _p, _p, _p, _p,
+                                    ctypes.c_size_t, _u, _p]),
+    "f8_quantize_weights": (ctypes.c_int, [_p, _i64, _i64, _p, _p, _p]),
+    "f8_quantize_rows": (ctypes.c_int, [_p, _int, _i64, _i64, _p, _p, _u, _p]),
+    "f8_gemm_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "f8_gemm": (ctypes.c_int, [_p, _p, _i64, _i64, _p, _p, _i64, _p, _int, _p, ctypes.c_size_t, _u, _p]),
+    "f8_linear_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "f8_linear": (ctypes.c_int, [_p, _int, _i64, _i64, _p, _p, _i64, _p, _int, _p, ctypes.c_size_t, _u, _p]),
 }
 
 _lib = None
@@ -661,26 +686,56 @@ def _want_heads(t, name, shape=None):
     return st[0] if n > 1 else max(st[0], h * d)
 
 
-def _want_rope(pos, freqs, tokens):
-    _want(pos, torch.int32, "pos", (tokens,))
+def _want_rope(pos, freqs, tokens, axis=None):
+    """rot and, with `axis` (the axis of each pair), (axes, axis as bytes)"""
     _want(freqs, torch.float64, "freqs")
     if freqs.dim() != 1:
         raise ValueError("freqs must have one dimension")
-    return 2 * freqs.shape[0]
+    pairs = freqs.shape[0]
+    if axis is None:
+        _want(pos, torch.int32, "pos", (tokens,))
+        return 2 * pairs, None
+    if not isinstance(axis, bytes):
+        axis = bytes(axis)
+    if len(axis) != pairs:
+        raise ValueError("axis must have one entry for each of the %d pairs, got %d" % (pairs, len(axis)))
+    _want(pos, torch.int32, "pos")
+    if pos.dim() != 2 or pos.shape[1] != tokens:
+        raise ValueError("pos must be [axes][%d]" % tokens)
+    return 2 * pairs, (pos.shape[0], axis)
 
 
-def rope_rotate(X, pos, freqs, interleaved: bool = False, mscale: float = 1.0, Y=None, dtype=None, flags: int = 0):
+def rope_axes(sections, cycled: bool = False) -> bytes:
+    """The axis of each pair for rotary positions with several axes: `sections`
+    gives the pairs of each axis (time, height, width), in blocks one after the
+    other, or, cycled, the axes in turn for as long as each has pairs left."""
+    sections = [int(n) for n in sections]
+    if not 1 <= len(sections) <= 4 or min(sections) < 0:
+        raise ValueError("sections must be 1 to 4 counts of pairs")
+    if not cycled:
+        return bytes(a for a, n in enumerate(sections) for _ in range(n))
+    return bytes(a for i in range(max(sections)) for a, n in enumerate(sections) if i < n)
+
+
+def rope_rotate(X, pos, freqs, interleaved: bool = False, mscale: float = 1.0, Y=None, dtype=None, flags: int = 0,
+                axis=None):
     """Rotary positions on X [tokens][heads][dim] (fp32 or fp16, rows at any
     distance): pairs (i, i + rot/2), or (2i, 2i + 1) when interleaved, turned by
-    pos * freqs[i]; rot = 2 * len(freqs).  Returns Y (Y may be X)."""
+    pos * freqs[i]; rot = 2 * len(freqs).  With axis (rope_axes, or any sequence
+    of len(freqs) numbers) pos is [axes][tokens] and pair i turns by
+    pos[axis[i]] * freqs[i].  Returns Y (Y may be X)."""
     xt = _want_type(X, "X")
     ld = _want_heads(X, "X")
     n, h, d = X.shape
-    rot = _want_rope(pos, freqs, n)
+    rot, axes = _want_rope(pos, freqs, n, axis)
     if Y is None:
         Y = torch.empty((n, h, d), dtype=dtype or X.dtype, device=X.device)
     yt = _want_type(Y, "Y")
     ld_y = _want_heads(Y, "Y", X.shape)
+    if axes is not None:
+        _check(lib().rope_rotate_axes(_ptr(X), xt, ld, n, h, d, _ptr(pos), *axes, _ptr(freqs), rot, int(interleaved),
+                                      mscale, _ptr(Y), yt, ld_y, flags, _stream(X)))
+        return Y
     _check(lib().rope_rotate(_ptr(X), xt, ld, n, h, d, _ptr(pos), _ptr(freqs), rot, int(interleaved), mscale,
                              _ptr(Y), yt, ld_y, flags, _stream(X)))
     return Y
@@ -740,10 +795,11 @@ def _batch_arg(b, tokens):
 
 
 def kvq_write(cache, batch, K, V, Q=None, pos=None, freqs=None, interleaved: bool = False, mscale: float = 1.0,
-              Q_out=None, flags: int = 0):
+              Q_out=None, flags: int = 0, axis=None):
     """Writes K, V [tokens][heads][dim] (fp32 or fp16, rows at any distance) into
     the cache, rotated first when freqs is given, and rotates Q
-    [tokens][heads_q][dim] in the same launch; returns Q_out (fp16; None without Q)."""
+    [tokens][heads_q][dim] in the same launch; returns Q_out (fp16; None without Q).
+    axis: positions with several axes, as in rope_rotate."""
     ca, heads, dim = _cache_arg(cache)
     xt = _want_type(K, "K")
     n = K.shape[0]
@@ -752,7 +808,9 @@ def kvq_write(cache, batch, K, V, Q=None, pos=None, freqs=None, interleaved: boo
     if V.dtype != K.dtype or (Q is not None and Q.dtype != K.dtype):
         raise TypeError("Q, K and V must have one type")
     ba = _batch_arg(batch, n)
-    rot = _want_rope(pos, freqs, n) if freqs is not None else 0
+    if axis is not None and freqs is None:
+        raise ValueError("axis needs freqs")
+    rot, axes = _want_rope(pos, freqs, n, axis) if freqs is not None else (0, None)
     hq = ld_q = 0
     if Q is not None:
         hq = Q.shape[1]
@@ -761,6 +819,10 @@ def kvq_write(cache, batch, K, V, Q=None, pos=None, freqs=None, interleaved: boo
         _want(Q_out, torch.float16, "Q_out", (n, hq, dim))
     elif Q_out is not None:
         raise ValueError("Q_out needs Q")
+    if axes is not None:
+        _check(lib().kvq_write_axes(ca, ba, _ptr(K), ld_k, _ptr(V), ld_v, _ptr(Q), ld_q, hq, xt, _ptr(pos), *axes,
+                                    _ptr(freqs), rot, int(interleaved), mscale, _ptr(Q_out), flags, _stream(K)))
+        return Q_out
     _check(lib().kvq_write(ca, ba, _ptr(K), ld_k, _ptr(V), ld_v, _ptr(Q), ld_q, hq, xt,
                            _ptr(pos), _ptr(freqs), rot, int(interleaved), mscale, _ptr(Q_out), flags, _stream(K)))
     return Q_out
@@ -848,6 +910,261 @@ def kvq_attention(Q, cache, batch, mask=None, scale: float = None, out=None, ws=
         ws, mine = _stream_workspace(Q.device, stream, int(L.kvq_attention_workspace_bytes(ca, ba, hq))), False
     _check(st)
     return out
+
+
+# --------------------------------------------------------------------------
+# a serving step around the layers
+# --------------------------------------------------------------------------
+
+def _one_device(first, *others):
+    """The tensors' device; raises where they lie on different ones or it is not
+    the current one, on whose stream the call would run."""
+    d = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != d:
+            raise ValueError("all tensors must be on one device")
+    if d != torch.cuda.current_device():
+        raise ValueError("the tensors are on cuda:%d, the current device is cuda:%d" % (d, torch.cuda.current_device()))
+    return first.device
+
+
+def _scratch(ws, nbytes, device):
+    """The caller's workspace, or one of this call's own: the allocator hands it on in
+    the stream's order (in a captured graph: within the graph)."""
+    if ws is None:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return ws, ws.numel() * ws.element_size()
+
+
+# The pages of a pool and who holds them: table int32 [seqs][max_pages], held
+# int32 [seqs], stack int32 [pages], top int32 [1] (kvq_pool_t in the C header).
+KVQPool = collections.namedtuple("KVQPool", "table held stack top")
+
+_pack_pool = struct.Struct("@4P3qi").pack   # kvq_pool_t
+
+
+def kvq_pool(seqs: int, max_pages: int, pages: int, device="cuda") -> KVQPool:
+    """A pool whose pages are all free, for up to `seqs` requests of up to max_pages pages."""
+    table = torch.full((seqs, max_pages), -1, dtype=torch.int32, device=device)
+    held = torch.zeros((seqs,), dtype=torch.int32, device=device)
+    stack = torch.arange(pages, dtype=torch.int32, device=device)
+    return KVQPool(table, held, stack, torch.full((1,), pages, dtype=torch.int32, device=device))
+
+
+def _pool_arg(p, page):
+    """(kvq_pool_t as bytes, seqs)"""
+    table, held, stack, top = p
+    for t, name in ((table, "table"), (held, "held"), (stack, "stack"), (top, "top")):
+        _want(t, torch.int32, name)
+    if table.dim() != 2 or held.shape != table.shape[:1] or stack.dim() != 1 or top.shape != (1,):
+        raise ValueError("the pool must be table [seqs][max_pages], held [seqs], stack [pages], top [1]")
+    seqs, width = table.shape
+    return _pack_pool(table.data_ptr(), held.data_ptr(), stack.data_ptr(), top.data_ptr(), seqs, width, stack.shape[0],
+                      page), seqs
+
+
+def kvq_plan_workspace_bytes(pool, page: int) -> int:
+    return int(lib().kvq_plan_workspace_bytes(_pool_arg(pool, page)[0]))
+
+
+def kvq_plan(pool, page: int, lens, add, tokens: int, grow=None, mask=None, cu=None, pos=None, slot=None, seq=None,
+             ws=None, flags: int = 0):
+    """Plans a step of up to `tokens` tokens: lens [seqs] int32 += grow, requests
+    with add[b] < 0 end and give their pages back, those with add[b] > 0 take the
+    pages they lack (or wait, if these or the tokens do not reach).  Returns
+    (KVQBatch(cu, lens, pool.table), pos, slot, seq): positions int32 (with mask
+    [tokens] int64: by depth in the drafted tree), rows of the pool int64 and
+    rows of the batch int32 of the step's tokens."""
+    pa, seqs = _pool_arg(pool, page)
+    _want(lens, torch.int32, "lens", (seqs,))
+    _want(add, torch.int32, "add", (seqs,))
+    if grow is not None:
+        _want(grow, torch.int32, "grow", (seqs,))
+    if mask is not None:
+        _want(mask, torch.int64, "mask", (tokens,))
+    dev = _one_device(lens, *pool, add, grow, mask, cu, pos, slot, seq, ws)
+    cu = torch.empty((seqs + 1,), dtype=torch.int32, device=dev) if cu is None else cu
+    pos = torch.empty((tokens,), dtype=torch.int32, device=dev) if pos is None else pos
+    slot = torch.empty((tokens,), dtype=torch.int64, device=dev) if slot is None else slot
+    seq = torch.empty((tokens,), dtype=torch.int32, device=dev) if seq is None else seq
+    _want(cu, torch.int32, "cu", (seqs + 1,))
+    _want(pos, torch.int32, "pos", (tokens,))
+    _want(slot, torch.int64, "slot", (tokens,))
+    _want(seq, torch.int32, "seq", (tokens,))
+    L = lib()
+    ws, wsb = _scratch(ws, L.kvq_plan_workspace_bytes(pa), dev)
+    _check(L.kvq_plan(pa, lens.data_ptr(), _ptr(grow), add.data_ptr(), _ptr(mask), tokens, cu.data_ptr(), pos.data_ptr(),
+                      slot.data_ptr(), seq.data_ptr(), ws.data_ptr(), wsb, flags, _stream(lens)))
+    return KVQBatch(cu, lens, pool[0]), pos, slot, seq
+
+
+def _want_rows(t, name, shape):
+    """[rows][cols] with contiguous columns, rows at any distance; returns the distance."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    n, v = shape
+    if (v > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < v):
+        raise ValueError("%s: the values of a row must be contiguous, its rows apart" % name)
+    return t.stride(0) if n > 1 else v
+
+
+def draft_verify_workspace_bytes(tokens: int, vocab: int) -> int:
+    return int(lib().draft_verify_workspace_bytes(tokens, vocab))
+
+
+def draft_verify(logits, cu, ids, u, mask=None, q=None, temp=None, keep=None, out=None, count=None, ws=None,
+                 flags: int = 0):
+    """Which drafted tokens stay, and the next token of each sequence.
+
+    logits [tokens][vocab] fp32 or fp16 (rows at any distance): the target's
+    answers after each token of the batch, cu [seqs + 1] int32 its offsets; the
+    first token of a sequence is certain, the others are drafts ids [tokens]
+    int32, in a chain or, with mask [tokens] int64, a tree of ancestors' bits.
+    q [tokens][vocab]: the probabilities that the children of each token were
+    drawn from (None: the drafts are given).  u [tokens] fp32 in [0, 1): the
+    random numbers of the tests, the root's that of the draw.  temp [seqs] fp32
+    (None: 1; 0: greedy).  Returns (keep, out, count) int32: places kept (for
+    kvq_keep), tokens said, how many of each (for kvq_plan's grow)."""
+    lt = _want_type(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [tokens][vocab]")
+    n, v = logits.shape
+    ld = _want_rows(logits, "logits", (n, v))
+    _want(cu, torch.int32, "cu")
+    if cu.dim() != 1 or cu.shape[0] < 2:
+        raise ValueError("cu must be [seqs + 1]")
+    seqs = cu.shape[0] - 1
+    _want(ids, torch.int32, "ids", (n,))
+    _want(u, torch.float32, "u", (n,))
+    if mask is not None:
+        _want(mask, torch.int64, "mask", (n,))
+    if temp is not None:
+        _want(temp, torch.float32, "temp", (seqs,))
+    qt = ld_q = 0
+    if q is not None:
+        qt = _want_type(q, "q")
+        ld_q = _want_rows(q, "q", (n, v))
+    dev = _one_device(logits, cu, ids, u, mask, q, temp, keep, out, count, ws)
+    keep = torch.empty((n,), dtype=torch.int32, device=dev) if keep is None else keep
+    out = torch.empty((n,), dtype=torch.int32, device=dev) if out is None else out
+    count = torch.empty((seqs,), dtype=torch.int32, device=dev) if count is None else count
+    _want(keep, torch.int32, "keep", (n,))
+    _want(out, torch.int32, "out", (n,))
+    _want(count, torch.int32, "count", (seqs,))
+    L = lib()
+    ws, wsb = _scratch(ws, L.draft_verify_workspace_bytes(n, v), dev)
+    _check(L.draft_verify(logits.data_ptr(), lt, ld, v, cu.data_ptr(), seqs, n, ids.data_ptr(), _ptr(mask), _ptr(q), qt,
+                          ld_q, _ptr(temp), u.data_ptr(), keep.data_ptr(), out.data_ptr(), count.data_ptr(),
+                          ws.data_ptr(), wsb, flags, _stream(logits)))
+    return keep, out, count
+
+
+# --------------------------------------------------------------------------
+# linear with 8-bit floating-point blocks of 128
+# --------------------------------------------------------------------------
+
+F8_BLOCK = 128
+
+
+def _f8_blocks(n: int) -> int:
+    return -(-n // F8_BLOCK)
+
+
+def f8_quantize_weights(W, Wf=None, sw=None):
+    """W [N][K] fp32 -> (Wf [N][K] uint8 (e4m3), sw [ceil(N/128)][ceil(K/128)] fp32)."""
+    _want(W, torch.float32, "W")
+    if W.dim() != 2:
+        raise ValueError("W must have two dimensions")
+    N, K = W.shape
+    dev = _one_device(W, Wf, sw)
+    Wf = torch.empty((N, K), dtype=torch.uint8, device=dev) if Wf is None else Wf
+    sw = torch.empty((_f8_blocks(N), _f8_blocks(K)), dtype=torch.float32, device=dev) if sw is None else sw
+    _want(Wf, torch.uint8, "Wf", (N, K))
+    _want(sw, torch.float32, "sw", (_f8_blocks(N), _f8_blocks(K)))
+    _check(lib().f8_quantize_weights(W.data_ptr(), N, K, Wf.data_ptr(), sw.data_ptr(), _stream(W)))
+    return Wf, sw
+
+
+def f8_quantize_rows(X, Xf=None, sa=None, flags: int = 0):
+    """X [M][K] fp32 or fp16 -> (Xf [M][K] uint8 (e4m3), sa [ceil(K/128)][M] fp32)."""
+    xt = _want_type(X, "X")
+    _want(X, X.dtype, "X")
+    if X.dim() != 2:
+        raise ValueError("X must have two dimensions")
+    M, K = X.shape
+    dev = _one_device(X, Xf, sa)
+    Xf = torch.empty((M, K), dtype=torch.uint8, device=dev) if Xf is None else Xf
+    sa = torch.empty((_f8_blocks(K), M), dtype=torch.float32, device=dev) if sa is None else sa
+    _want(Xf, torch.uint8, "Xf", (M, K))
+    _want(sa, torch.float32, "sa", (_f8_blocks(K), M))
+    _check(lib().f8_quantize_rows(X.data_ptr(), xt, M, K, Xf.data_ptr(), sa.data_ptr(), flags, _stream(X)))
+    return Xf, sa
+
+
+def _f8_weights(Wf, sw, K):
+    _want(Wf, torch.uint8, "Wf")
+    if Wf.dim() != 2 or Wf.shape[1] != K:
+        raise ValueError("Wf must be [N][%d]" % K)
+    N = Wf.shape[0]
+    _want(sw, torch.float32, "sw", (_f8_blocks(N), _f8_blocks(K)))
+    return N
+
+
+def _f8_out(Y, shape, dtype, device):
+    if Y is None:
+        Y = torch.empty(shape, dtype=dtype, device=device)
+    yt = _want_type(Y, "Y")
+    _want(Y, Y.dtype, "Y", shape)
+    return Y, yt
+
+
+def f8_gemm_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(lib().f8_gemm_workspace_bytes(M, K, N))
+
+
+def f8_linear_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(lib().f8_linear_workspace_bytes(M, K, N))
+
+
+def f8_gemm(Xf, sa, Wf, sw, dtype=torch.float32, Y=None, ws=None, flags: int = 0):
+    """Y [M][N] (fp32 or fp16): the product of e4m3 codes with a scale for each row
+    and 128 values of X and each 128 x 128 block of W."""
+    _want(Xf, torch.uint8, "Xf")
+    if Xf.dim() != 2:
+        raise ValueError("Xf must have two dimensions")
+    M, K = Xf.shape
+    _want(sa, torch.float32, "sa", (_f8_blocks(K), M))
+    N = _f8_weights(Wf, sw, K)
+    dev = _one_device(Xf, sa, Wf, sw, Y, ws)
+    Y, yt = _f8_out(Y, (M, N), dtype, dev)
+    L = lib()
+    nbytes = L.f8_gemm_workspace_bytes(M, K, N)
+    ws, wsb = _scratch(ws, nbytes, dev) if nbytes or ws is not None else (None, 0)
+    _check(L.f8_gemm(Xf.data_ptr(), sa.data_ptr(), M, K, Wf.data_ptr(), sw.data_ptr(), N, Y.data_ptr(), yt, _ptr(ws), wsb,
+                     flags, _stream(Xf)))
+    return Y
+
+
+def f8_linear(X, Wf, sw, dtype=torch.float32, Y=None, ws=None, flags: int = 0):
+    """f8_quantize_rows and f8_gemm in one call: X [M][K] fp32 or fp16, any number
+    of rows; Y [M][N] fp32 or fp16."""
+    xt = _want_type(X, "X")
+    _want(X, X.dtype, "X")
+    if X.dim() != 2:
+        raise ValueError("X must have two dimensions")
+    M, K = X.shape
+    N = _f8_weights(Wf, sw, K)
+    dev = _one_device(X, Wf, sw, Y, ws)
+    Y, yt = _f8_out(Y, (M, N), dtype, dev)
+    L = lib()
+    ws, wsb = _scratch(ws, L.f8_linear_workspace_bytes(M, K, N), dev)
+    _check(L.f8_linear(X.data_ptr(), xt, M, K, Wf.data_ptr(), sw.data_ptr(), N, Y.data_ptr(), yt, ws.data_ptr(), wsb,
+                       flags, _stream(X)))
+    return Y
 
 
 def w4a8_last_error() -> str:

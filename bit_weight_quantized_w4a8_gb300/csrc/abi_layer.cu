@@ -68,6 +68,17 @@ int check_rope(const char* who, const int32_t* pos, const double* freqs, int rot
     return W4A8_OK;
 }
 
+// Axis of each pair: a host array of rot / 2 entries.
+int check_axis(const char* who, int axes, const uint8_t* axis, int rot) {
+    if (!axis) return fail(W4A8_ERR_NULL, "%s: NULL axis", who);
+    if (axes < 1 || axes > ROPE_MAX_AXES)
+        return fail(W4A8_ERR_SHAPE, "%s: axes=%d outside [1, %d]", who, axes, ROPE_MAX_AXES);
+    for (int i = 0; i < rot / 2; ++i)
+        if (axis[i] >= axes)
+            return fail(W4A8_ERR_SHAPE, "%s: pair %d is on axis %d of %d", who, i, (int)axis[i], axes);
+    return W4A8_OK;
+}
+
 // Rows of `heads` vectors of dim values, ld elements apart.
 int check_rows(const char* who, const char* name, const void* p, int type, int64_t ld, int64_t heads, int dim) {
     if (!p) return fail(W4A8_ERR_NULL, "%s: NULL %s", who, name);
@@ -151,54 +162,90 @@ int rope_frequencies(int rot, double base, int scaling, double factor, double ol
     return w4a8::status_done(cudaSuccess, "");
 }
 
+// axes 0: one axis, no map.
+static int rotate_rows(const char* who, const void* X, int x_type, int64_t ld_x, int64_t tokens, int heads, int dim,
+                       const int32_t* pos, int axes, const uint8_t* axis, const double* freqs, int rot, int interleaved,
+                       float mscale, void* Y, int y_type, int64_t ld_y, unsigned flags, void* stream) {
+    if (!is_type(x_type) || !is_type(y_type)) return fail(W4A8_ERR_SHAPE, "%s: unknown type", who);
+    if (dim != 64 && dim != 128 && dim != 256)
+        return fail(W4A8_ERR_SHAPE, "%s: dim=%d must be 64, 128 or 256", who, dim);
+    if (tokens < 1 || tokens > 0x7FFFFFFF || heads < 1 || heads > 16384)
+        return fail(W4A8_ERR_SHAPE, "%s: tokens=%lld or heads=%d out of range", who, (long long)tokens, heads);
+    int st;
+    if ((st = check_rows(who, "X", X, x_type, ld_x, heads, dim)) != W4A8_OK) return st;
+    if ((st = check_rows(who, "Y", Y, y_type, ld_y, heads, dim)) != W4A8_OK) return st;
+    if (X == Y && (x_type != y_type || ld_x != ld_y))
+        return fail(W4A8_ERR_SHAPE, "%s: in place needs one type and one row distance", who);
+    if ((st = check_rope(who, pos, freqs, rot, dim, mscale)) != W4A8_OK) return st;
+    if (axes != 0 && (st = check_axis(who, axes, axis, rot)) != W4A8_OK) return st;
+    if ((st = check_flags(who, flags)) != W4A8_OK) return st;
+    int sms = 0;
+    if ((st = w4a8::status_sm_count(&sms)) != W4A8_OK) return st;
+    return w4a8::status_done(w4a8::launch_rope_rotate(X, x_type, ld_x, tokens, heads, dim, pos, axis, freqs, rot,
+                                                      interleaved != 0, mscale, Y, y_type, ld_y, sms, flags,
+                                                      static_cast<cudaStream_t>(stream)),
+                             who);
+}
+
 int rope_rotate(const void* X, int x_type, int64_t ld_x, int64_t tokens, int heads, int dim, const int32_t* pos,
                 const double* freqs, int rot, int interleaved, float mscale, void* Y, int y_type, int64_t ld_y,
                 unsigned flags, void* stream) {
-    if (!is_type(x_type) || !is_type(y_type)) return fail(W4A8_ERR_SHAPE, "rope_rotate: unknown type");
-    if (dim != 64 && dim != 128 && dim != 256)
-        return fail(W4A8_ERR_SHAPE, "rope_rotate: dim=%d must be 64, 128 or 256", dim);
-    if (tokens < 1 || tokens > 0x7FFFFFFF || heads < 1 || heads > 16384)
-        return fail(W4A8_ERR_SHAPE, "rope_rotate: tokens=%lld or heads=%d out of range", (long long)tokens, heads);
+    return rotate_rows("rope_rotate", X, x_type, ld_x, tokens, heads, dim, pos, 0, nullptr, freqs, rot, interleaved, mscale,
+                  Y, y_type, ld_y, flags, stream);
+}
+
+int rope_rotate_axes(const void* X, int x_type, int64_t ld_x, int64_t tokens, int heads, int dim, const int32_t* pos,
+                     int axes, const uint8_t* axis, const double* freqs, int rot, int interleaved, float mscale,
+                     void* Y, int y_type, int64_t ld_y, unsigned flags, void* stream) {
+    if (axes == 0) return fail(W4A8_ERR_SHAPE, "rope_rotate_axes: axes=0 outside [1, %d]", ROPE_MAX_AXES);
+    return rotate_rows("rope_rotate_axes", X, x_type, ld_x, tokens, heads, dim, pos, axes, axis, freqs, rot, interleaved,
+                  mscale, Y, y_type, ld_y, flags, stream);
+}
+
+static int write_tokens(const char* who, const kvq_cache_t* cache, const kvq_batch_t* batch, const void* K, int64_t ld_k,
+                        const void* V, int64_t ld_v, const void* Q, int64_t ld_q, int heads_q, int x_type, const int32_t* pos,
+                        int axes, const uint8_t* axis, const double* freqs, int rot, int interleaved, float mscale,
+                        uint16_t* Q_out, unsigned flags, void* stream) {
     int st;
-    if ((st = check_rows("rope_rotate", "X", X, x_type, ld_x, heads, dim)) != W4A8_OK) return st;
-    if ((st = check_rows("rope_rotate", "Y", Y, y_type, ld_y, heads, dim)) != W4A8_OK) return st;
-    if (X == Y && (x_type != y_type || ld_x != ld_y))
-        return fail(W4A8_ERR_SHAPE, "rope_rotate: in place needs one type and one row distance");
-    if ((st = check_rope("rope_rotate", pos, freqs, rot, dim, mscale)) != W4A8_OK) return st;
-    if ((st = check_flags("rope_rotate", flags)) != W4A8_OK) return st;
+    if ((st = check_cache(who, cache)) != W4A8_OK) return st;
+    if ((st = check_batch(who, batch)) != W4A8_OK) return st;
+    if (!is_type(x_type)) return fail(W4A8_ERR_SHAPE, "%s: unknown type", who);
+    if ((st = check_rows(who, "K", K, x_type, ld_k, cache->heads, cache->dim)) != W4A8_OK) return st;
+    if ((st = check_rows(who, "V", V, x_type, ld_v, cache->heads, cache->dim)) != W4A8_OK) return st;
+    if ((!Q) != (!Q_out)) return fail(W4A8_ERR_NULL, "%s: Q and Q_out come together", who);
+    if (Q) {
+        if (heads_q < 1 || heads_q > 16384)
+            return fail(W4A8_ERR_SHAPE, "%s: heads_q=%d outside [1, 16384]", who, heads_q);
+        if ((st = check_rows(who, "Q", Q, x_type, ld_q, heads_q, cache->dim)) != W4A8_OK) return st;
+        if (!aligned(Q_out, 8)) return fail(W4A8_ERR_ALIGN, "%s: Q_out needs 8-byte alignment", who);
+    }
+    if (freqs && (st = check_rope(who, pos, freqs, rot, cache->dim, mscale)) != W4A8_OK) return st;
+    if (axes != 0 && (st = check_axis(who, axes, axis, rot)) != W4A8_OK) return st;
+    if ((st = check_flags(who, flags)) != W4A8_OK) return st;
     int sms = 0;
     if ((st = w4a8::status_sm_count(&sms)) != W4A8_OK) return st;
-    return w4a8::status_done(w4a8::launch_rope_rotate(X, x_type, ld_x, tokens, heads, dim, pos, freqs, rot,
-                                                      interleaved != 0, mscale, Y, y_type, ld_y, sms, flags,
-                                                      static_cast<cudaStream_t>(stream)),
-                             "rope_rotate launch");
+    return w4a8::status_done(w4a8::launch_kvq_write(*cache, *batch, K, ld_k, V, ld_v, Q, ld_q, heads_q, x_type, pos,
+                                                    axis, freqs, rot, interleaved != 0, mscale, Q_out, sms, flags,
+                                                    static_cast<cudaStream_t>(stream)),
+                             who);
 }
 
 int kvq_write(const kvq_cache_t* cache, const kvq_batch_t* batch, const void* K, int64_t ld_k, const void* V,
               int64_t ld_v, const void* Q, int64_t ld_q, int heads_q, int x_type, const int32_t* pos,
               const double* freqs, int rot, int interleaved, float mscale, uint16_t* Q_out, unsigned flags,
               void* stream) {
-    int st;
-    if ((st = check_cache("kvq_write", cache)) != W4A8_OK) return st;
-    if ((st = check_batch("kvq_write", batch)) != W4A8_OK) return st;
-    if (!is_type(x_type)) return fail(W4A8_ERR_SHAPE, "kvq_write: unknown type");
-    if ((st = check_rows("kvq_write", "K", K, x_type, ld_k, cache->heads, cache->dim)) != W4A8_OK) return st;
-    if ((st = check_rows("kvq_write", "V", V, x_type, ld_v, cache->heads, cache->dim)) != W4A8_OK) return st;
-    if ((!Q) != (!Q_out)) return fail(W4A8_ERR_NULL, "kvq_write: Q and Q_out come together");
-    if (Q) {
-        if (heads_q < 1 || heads_q > 16384)
-            return fail(W4A8_ERR_SHAPE, "kvq_write: heads_q=%d outside [1, 16384]", heads_q);
-        if ((st = check_rows("kvq_write", "Q", Q, x_type, ld_q, heads_q, cache->dim)) != W4A8_OK) return st;
-        if (!aligned(Q_out, 8)) return fail(W4A8_ERR_ALIGN, "kvq_write: Q_out needs 8-byte alignment");
-    }
-    if (freqs && (st = check_rope("kvq_write", pos, freqs, rot, cache->dim, mscale)) != W4A8_OK) return st;
-    if ((st = check_flags("kvq_write", flags)) != W4A8_OK) return st;
-    int sms = 0;
-    if ((st = w4a8::status_sm_count(&sms)) != W4A8_OK) return st;
-    return w4a8::status_done(w4a8::launch_kvq_write(*cache, *batch, K, ld_k, V, ld_v, Q, ld_q, heads_q, x_type, pos,
-                                                    freqs, rot, interleaved != 0, mscale, Q_out, sms, flags,
-                                                    static_cast<cudaStream_t>(stream)),
-                             "kvq_write launch");
+    return write_tokens("kvq_write", cache, batch, K, ld_k, V, ld_v, Q, ld_q, heads_q, x_type, pos, 0, nullptr, freqs, rot,
+                 interleaved, mscale, Q_out, flags, stream);
+}
+
+int kvq_write_axes(const kvq_cache_t* cache, const kvq_batch_t* batch, const void* K, int64_t ld_k, const void* V,
+                   int64_t ld_v, const void* Q, int64_t ld_q, int heads_q, int x_type, const int32_t* pos, int axes,
+                   const uint8_t* axis, const double* freqs, int rot, int interleaved, float mscale, uint16_t* Q_out,
+                   unsigned flags, void* stream) {
+    if (axes == 0) return fail(W4A8_ERR_SHAPE, "kvq_write_axes: axes=0 outside [1, %d]", ROPE_MAX_AXES);
+    if (!freqs) return fail(W4A8_ERR_NULL, "kvq_write_axes: NULL positions or frequencies");
+    return write_tokens("kvq_write_axes", cache, batch, K, ld_k, V, ld_v, Q, ld_q, heads_q, x_type, pos, axes, axis, freqs, rot,
+                 interleaved, mscale, Q_out, flags, stream);
 }
 
 int kvq_read(const kvq_cache_t* cache, const kvq_batch_t* batch, void* K, void* V, int y_type, unsigned flags,

@@ -106,12 +106,13 @@ cudaError_t launch_add_norm(const void* r, int r_f16, const void* y, int y_f16, 
                             float beta, float eps, void* r_out, uint16_t* X, int8_t* Xq, float* sa, bool vec,
                             unsigned flags, cudaStream_t stream);
 cudaError_t launch_rope_rotate(const void* X, int x_f16, int64_t ld_x, int64_t tokens, int heads, int dim,
-                               const int32_t* pos, const double* freqs, int rot, int inter, float mscale, void* Y,
-                               int y_f16, int64_t ld_y, int sms, unsigned flags, cudaStream_t stream);
+                               const int32_t* pos, const uint8_t* axis, const double* freqs, int rot, int inter,
+                               float mscale, void* Y, int y_f16, int64_t ld_y, int sms, unsigned flags,
+                               cudaStream_t stream);
 cudaError_t launch_kvq_write(const kvq_cache_t& c, const kvq_batch_t& b, const void* K, int64_t ld_k, const void* V,
                              int64_t ld_v, const void* Q, int64_t ld_q, int heads_q, int x_f16, const int32_t* pos,
-                             const double* freqs, int rot, int inter, float mscale, uint16_t* Q_out, int sms,
-                             unsigned flags, cudaStream_t stream);
+                             const uint8_t* axis, const double* freqs, int rot, int inter, float mscale,
+                             uint16_t* Q_out, int sms, unsigned flags, cudaStream_t stream);
 cudaError_t launch_kvq_read(const kvq_cache_t& c, const kvq_batch_t& b, void* K, void* V, int y_f16, int sms,
                             unsigned flags, cudaStream_t stream);
 cudaError_t launch_kvq_keep(const kvq_cache_t& c, const kvq_batch_t& b, const int32_t* keep, unsigned flags,
@@ -129,5 +130,28 @@ cudaError_t launch_kvq_attention(const kvq_cache_t& c, const kvq_batch_t& b, con
                                  cudaStream_t stream);
 cudaError_t read_and_clear_kvq_error(unsigned* flags, cudaStream_t stream);
 cudaError_t read_and_clear_attn_error(unsigned* flags, cudaStream_t stream);
+
+// The step around the layer: pages and positions (kvq_pool.cu), the drafts'
+// verification (verify.cu).
+size_t kvq_plan_workspace(const kvq_pool_t& p);
+cudaError_t launch_kvq_plan(const kvq_pool_t& p, int32_t* lens, const int32_t* grow, const int32_t* add,
+                            const uint64_t* mask, int64_t tokens, int32_t* cu, int32_t* pos, int64_t* slot,
+                            int32_t* seq, void* ws, int sms, unsigned flags, cudaStream_t stream);
+cudaError_t read_and_clear_pool_error(unsigned* flags, cudaStream_t stream);
+size_t draft_verify_workspace(int64_t tokens, int64_t vocab, int sms);
+cudaError_t launch_draft_verify(const void* L, int l_f16, int64_t ld_l, int64_t vocab, const int32_t* cu, int64_t seqs,
+                                int64_t tokens, const int32_t* ids, const uint64_t* mask, const void* Q, int q_f16,
+                                int64_t ld_q, const float* temp, const float* u, int32_t* keep, int32_t* out,
+                                int32_t* count, void* ws, int sms, unsigned flags, cudaStream_t stream);
+cudaError_t read_and_clear_verify_error(unsigned* flags, cudaStream_t stream);
+
+// The linear with e4m3 blocks of 128 (f8.cu).
+cudaError_t launch_f8_quantize_weights(const float* W, int64_t N, int64_t K, uint8_t* Wf, float* sw,
+                                       cudaStream_t stream);
+cudaError_t launch_f8_quantize_rows(const void* X, int x_f16, int64_t M, int64_t K, uint8_t* Xf, float* sa,
+                                    unsigned flags, cudaStream_t stream);
+size_t f8_gemm_workspace(int64_t M, int64_t K, int64_t N, int sms);
+cudaError_t launch_f8_gemm(const uint8_t* Xf, const float* sa, int64_t M, int64_t K, const uint8_t* Wf, const float* sw,
+                           int64_t N, void* Y, int y_f16, void* ws, int sms, unsigned flags, cudaStream_t stream);
 
 }  // namespace w4a8

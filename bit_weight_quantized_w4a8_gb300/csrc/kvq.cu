@@ -39,10 +39,13 @@ __device__ __forceinline__ float2 turn_cos_sin(uint64_t f, int pos, float mscale
 }
 
 struct RopeArg {
-    const int32_t* pos;
+    const int32_t* pos;   // [axes][tokens]
     const double* freqs;  // NULL: no rotation
     int rot, inter;
     float mscale;
+    int64_t ld_pos;
+    uint32_t axis[8];  // of each pair, two bits: in the launch's constants, so that no load stands in front of
+                       // the position's (with one axis all are 0)
 };
 
 struct WriteArgs {
@@ -188,7 +191,8 @@ __global__ void __launch_bounds__(kLayerThreads) rope_write_kernel(const WriteAr
     // the last threads, whose warps have no look-up to make, first
     for (int e = kLayerThreads - 1 - (int)threadIdx.x; e < nt * pairs; e += kLayerThreads) {
         const int t = e / pairs, i = e - t * pairs;
-        cs[e] = turn_cos_sin(turn_fraction(a.rope.freqs[i]), a.rope.pos[t0 + t], a.rope.mscale);
+        const int64_t axis = a.rope.axis[i >> 4] >> (2 * (i & 15)) & 3;
+        cs[e] = turn_cos_sin(turn_fraction(a.rope.freqs[i]), a.rope.pos[axis * a.rope.ld_pos + t0 + t], a.rope.mscale);
     }
     __syncthreads();
     if (a.heads_q > 0) {
@@ -267,6 +271,14 @@ __global__ void __launch_bounds__(kLayerThreads) rope_write_kernel(const WriteAr
             }
         }
     }
+}
+
+// axis: host array of rot / 2 entries below 4, or NULL (one axis).
+RopeArg rope_arg(const int32_t* pos, int64_t tokens, const uint8_t* axis, const double* freqs, int rot, int inter,
+                 float mscale) {
+    RopeArg r = {pos, freqs, rot, inter, mscale, tokens, {}};
+    for (int i = 0; axis != nullptr && i < rot / 2; ++i) r.axis[i / 16] |= (uint32_t)axis[i] << (2 * (i % 16));
+    return r;
 }
 
 template <typename TX, typename TYO, int BITS, bool HAS_KV>
@@ -423,11 +435,11 @@ __global__ void __launch_bounds__(kLayerThreads) kvq_keep_kernel(const KvqCacheA
 }  // namespace
 
 cudaError_t launch_rope_rotate(const void* X, int x_f16, int64_t ld_x, int64_t tokens, int heads, int dim,
-                               const int32_t* pos, const double* freqs, int rot, int inter, float mscale, void* Y,
-                               int y_f16, int64_t ld_y, int sms, unsigned flags, cudaStream_t stream) {
+                               const int32_t* pos, const uint8_t* axis, const double* freqs, int rot, int inter,
+                               float mscale, void* Y, int y_f16, int64_t ld_y, int sms, unsigned flags, cudaStream_t stream) {
     WriteArgs a = {};
     a.b.tokens = (int)tokens;
-    a.rope = {pos, freqs, rot, inter, mscale};
+    a.rope = rope_arg(pos, tokens, axis, freqs, rot, inter, mscale);
     a.Q = X;
     a.ld_q = ld_x;
     a.heads_q = heads;
@@ -442,12 +454,12 @@ cudaError_t launch_rope_rotate(const void* X, int x_f16, int64_t ld_x, int64_t t
 
 cudaError_t launch_kvq_write(const kvq_cache_t& c, const kvq_batch_t& b, const void* K, int64_t ld_k, const void* V,
                              int64_t ld_v, const void* Q, int64_t ld_q, int heads_q, int x_f16, const int32_t* pos,
-                             const double* freqs, int rot, int inter, float mscale, uint16_t* Q_out, int sms,
-                             unsigned flags, cudaStream_t stream) {
+                             const uint8_t* axis, const double* freqs, int rot, int inter, float mscale,
+                             uint16_t* Q_out, int sms, unsigned flags, cudaStream_t stream) {
     WriteArgs a = {};
     a.c = cache_arg(c);
     a.b = batch_arg(b);
-    a.rope = {pos, freqs, freqs ? rot : 0, inter, mscale};
+    a.rope = rope_arg(pos, b.tokens, axis, freqs, freqs ? rot : 0, inter, mscale);
     a.Q = Q;
     a.K = K;
     a.V = V;

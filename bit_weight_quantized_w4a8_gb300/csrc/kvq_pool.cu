@@ -1,0 +1,327 @@
+// kvq_pool.cu -- the cache's pages handed out and taken back on the device,
+// and a step's offsets, positions and slots from request lengths.
+//
+// Everything is a prefix sum over the rows (requests) and a look-up per token
+// or page:
+//   back[b]  = pages row b gives back;  mid = top + sum back
+//   need[b]  = max(ceil((lens[b] + n[b]) / page) - held[b], 0)
+//   row b goes in when the rows up to it ask for no more than mid pages (or it
+//   needs none) and no more tokens than there is room for
+//   page k of all pages handed out (rows in order) is place mid - 1 - k of the
+//   stack, page k of all pages given back goes to place mid - 1 - k: a call
+//   that hands out and one that takes all of it back leave the stack as it was.
+// A place from top on that a page of this same call came back to is read from
+// that page's row instead of the stack, so that both directions run side by
+// side: no barrier stands between them and nothing is written that is read.
+//
+// One cluster of CTAs scans (a thread has up to 8 rows, so 65536 rows take one
+// pass) and, for short steps, writes all; for long ones a second launch writes
+// with the whole GPU.
+#include <cooperative_groups.h>
+
+#include "kernels.h"
+#include "layer.cuh"
+
+namespace w4a8 {
+namespace {
+
+namespace cg = cooperative_groups;
+
+__device__ unsigned g_pool_error;
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanItems = 8;     // rows of a thread, at most
+constexpr int kPlanCluster = 8;   // 8 x 1024 x 8 = 65536 rows
+constexpr int kFillThreads = 256;
+
+// What the scan leaves for the look-ups.
+struct PlanTotals {
+    int64_t back, need;  // pages given back, handed out
+    int top, mid;        // of the stack before and after the former
+    int tokens;
+};
+
+struct PlanArgs {
+    int32_t *table, *held, *stack, *top;
+    int64_t max_pages, pages;
+    int seqs, shift, room;
+    int32_t* lens;
+    const int32_t *grow, *add;
+    const uint64_t* mask;
+    int32_t *cu, *pos, *seq;
+    int64_t* slot;
+    // workspace: first page of each row among those given back and handed out,
+    // pages held before, totals
+    int32_t *back_at, *need_at, *old_held;
+    PlanTotals* totals;
+};
+
+struct Pair {
+    int64_t a, b;
+    __device__ __forceinline__ Pair operator+(Pair o) const { return {a + o.a, b + o.b}; }
+};
+
+// Exclusive prefix of v over the threads of the cluster; *total over all.
+__device__ Pair cluster_scan(Pair v, Pair* warp_sum, Pair* cta_sum, Pair* total) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    Pair x = v;
+    #pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const Pair y = {__shfl_up_sync(0xFFFFFFFFu, x.a, o), __shfl_up_sync(0xFFFFFFFFu, x.b, o)};
+        if (lane >= o) x = x + y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        Pair w = warp_sum[lane], s = w;
+        #pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const Pair y = {__shfl_up_sync(0xFFFFFFFFu, s.a, o), __shfl_up_sync(0xFFFFFFFFu, s.b, o)};
+            if (lane >= o) s = s + y;
+        }
+        warp_sum[lane] = {s.a - w.a, s.b - w.b};
+        if (lane == 31) *cta_sum = s;
+    }
+    cg::cluster_group cl = cg::this_cluster();
+    Pair before = {0, 0};
+    *total = {0, 0};
+    if (cl.num_blocks() > 1) {
+        cl.sync();
+        for (unsigned r = 0; r < cl.num_blocks(); ++r) {
+            const Pair s = *cl.map_shared_rank(cta_sum, r);
+            if (r < cl.block_rank()) before = before + s;
+            *total = *total + s;
+        }
+        cl.sync();  // the sums are free for the next scan, and no CTA leaves while they are read
+    } else {
+        __syncthreads();
+        *total = *cta_sum;
+    }
+    const Pair base = warp_sum[warp];
+    __syncthreads();
+    return {before.a + base.a + x.a - v.a, before.b + base.b + x.b - v.b};
+}
+
+// The last row b with at[b] <= k.
+__device__ __forceinline__ int row_of(const int32_t* at, int rows, int64_t k) {
+    int lo = 0, hi = rows;
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (at[mid] <= k)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// Page k of those given back.
+__device__ __forceinline__ int32_t page_back(const PlanArgs& a, int64_t k) {
+    const int b = row_of(a.back_at, a.seqs, k);
+    return a.table[b * a.max_pages + (k - a.back_at[b])];
+}
+// Page k of those handed out.
+__device__ __forceinline__ int32_t page_out(const PlanArgs& a, const PlanTotals& t, int64_t k) {
+    const int64_t p = t.mid - 1 - k;
+    return p < t.top ? a.stack[p] : page_back(a, (int64_t)t.top + t.back - 1 - p);
+}
+
+// Tokens, pages handed out and pages given back, by thread i of n.
+__device__ void plan_fill(const PlanArgs& a, const PlanTotals& t, int64_t i, int64_t n) {
+    for (int64_t k = i; k < t.need; k += n) {
+        const int b = row_of(a.need_at, a.seqs, k);
+        a.table[b * a.max_pages + a.old_held[b] + (k - a.need_at[b])] = page_out(a, t, k);
+    }
+    for (int64_t k = i; k < t.back; k += n) {
+        const int64_t p = (int64_t)t.top + t.back - 1 - k;
+        if (p < a.pages) a.stack[p] = page_back(a, k);
+    }
+    if (a.pos == nullptr && a.slot == nullptr && a.seq == nullptr) return;
+    for (int64_t k = i; k < a.room; k += n) {
+        int pos = 0, row = -1;
+        int64_t slot = -1;
+        if (k < t.tokens) {
+            row = row_of(a.cu, a.seqs, k);
+            const int x = a.lens[row] + (int)(k - a.cu[row]);
+            pos = a.mask != nullptr ? a.lens[row] + __popcll(a.mask[k]) - 1 : x;
+            if (a.slot != nullptr) {
+                const int64_t j = x >> a.shift, old = a.old_held[row];
+                const int32_t page = j < old ? a.table[row * a.max_pages + j] : page_out(a, t, a.need_at[row] + j - old);
+                if (page >= 0 && page < a.pages) slot = ((int64_t)page << a.shift) + (x & ((1 << a.shift) - 1));
+            }
+        }
+        if (a.pos != nullptr) a.pos[k] = pos;
+        if (a.slot != nullptr) a.slot[k] = slot;
+        if (a.seq != nullptr) a.seq[k] = row;
+    }
+}
+
+template <bool FILL>
+__global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const PlanArgs a) {
+    __shared__ Pair warp_sum[32], cta_sum;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int ctas = gridDim.x, per = (a.seqs + ctas * kPlanThreads - 1) / (ctas * kPlanThreads);
+    const int r0 = (blockIdx.x * kPlanThreads + threadIdx.x) * per;
+    const int rows = max(0, min(per, a.seqs - r0));
+    bool bad = false;
+    int64_t len[kPlanItems], n[kPlanItems];
+    int held[kPlanItems], back[kPlanItems], back_sum = 0;
+    int64_t back_total = 0;
+    #pragma unroll
+    for (int i = 0; i < kPlanItems; ++i) {
+        len[i] = n[i] = 0;
+        held[i] = back[i] = 0;
+        if (i < rows) {
+            const int r = r0 + i;
+            const int add = a.add[r], h = a.held[r];
+            len[i] = (int64_t)a.lens[r] + (a.grow != nullptr ? a.grow[r] : 0);
+            held[i] = (int)min((int64_t)max(h, 0), a.max_pages);
+            bad |= held[i] != h || len[i] < 0 || len[i] > kKvqMaxSlots;
+            len[i] = min(max(len[i], (int64_t)0), (int64_t)kKvqMaxSlots);
+            n[i] = max(add, 0);
+            if (add < 0) {
+                back[i] = held[i];
+                held[i] = 0;
+                len[i] = 0;
+            }
+            back_total += back[i];
+        }
+    }
+    int top = *a.top;
+    const int top_in = (int)min((int64_t)max(top, 0), a.pages);
+    bad |= top_in != top;
+    top = top_in;
+    Pair total;
+    const Pair bp = cluster_scan({back_total, 0}, warp_sum, &cta_sum, &total);
+    PlanTotals t;
+    t.top = top;
+    t.back = total.a;
+    t.mid = (int)min(top + total.a, a.pages);
+    bad |= top + total.a > a.pages;
+
+    int64_t need[kPlanItems], ask_p = 0, ask_n = 0;
+    #pragma unroll
+    for (int i = 0; i < kPlanItems; ++i) {
+        need[i] = 0;
+        if (n[i] > 0) {
+            const int64_t end = len[i] + n[i], want = (end + (1 << a.shift) - 1) >> a.shift;
+            if (want > a.max_pages || end > kKvqMaxSlots)
+                n[i] = 0;
+            else
+                need[i] = max(want - held[i], (int64_t)0);
+        }
+        ask_p += need[i];
+        ask_n += n[i];
+    }
+    Pair up = cluster_scan({ask_p, ask_n}, warp_sum, &cta_sum, &total);
+    int64_t got_p = 0, got_n = 0;
+    #pragma unroll
+    for (int i = 0; i < kPlanItems; ++i) {
+        up = up + Pair{need[i], n[i]};
+        if ((need[i] > 0 && up.a > t.mid) || up.b > a.room) need[i] = n[i] = 0;
+        got_p += need[i];
+        got_n += n[i];
+    }
+    const Pair at = cluster_scan({got_p, got_n}, warp_sum, &cta_sum, &total);
+    t.need = total.a;
+    t.tokens = (int)total.b;
+    int64_t b_at = bp.a, p_at = at.a, n_at = at.b;
+    #pragma unroll
+    for (int i = 0; i < kPlanItems; ++i) {
+        if (i < rows) {
+            const int r = r0 + i;
+            a.lens[r] = (int)len[i];
+            a.held[r] = held[i] + (int)need[i];
+            a.cu[r] = (int)n_at;
+            // a count of at most 65536 x 2^31 pages given back says nothing past 2^31: clamped, marked
+            a.back_at[r] = (int)min(b_at, (int64_t)0x7FFFFFFF);
+            a.need_at[r] = (int)p_at;
+            a.old_held[r] = held[i];
+            b_at += back[i];
+            p_at += need[i];
+            n_at += n[i];
+        }
+    }
+    if (t.back > 0x7FFFFFFF) t.back = 0x7FFFFFFF, bad = true;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        a.cu[a.seqs] = t.tokens;
+        *a.top = t.mid - (int)t.need;
+        *a.totals = t;
+    }
+    if (bad) atomicOr(&g_pool_error, kErrCacheRange);
+    if constexpr (FILL) {
+        if (ctas > 1)
+            cg::this_cluster().sync();
+        else
+            __syncthreads();
+        plan_fill(a, t, blockIdx.x * kPlanThreads + threadIdx.x, (int64_t)ctas * kPlanThreads);
+    }
+}
+
+__global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(const PlanArgs a) {
+    griddep_launch_dependents();
+    griddep_wait();
+    plan_fill(a, *a.totals, (int64_t)blockIdx.x * kFillThreads + threadIdx.x, (int64_t)gridDim.x * kFillThreads);
+}
+
+}  // namespace
+
+size_t kvq_plan_workspace(const kvq_pool_t& p) { return 256 + 3 * (size_t)((p.seqs + 63) / 64 * 64) * 4; }
+
+cudaError_t launch_kvq_plan(const kvq_pool_t& p, int32_t* lens, const int32_t* grow, const int32_t* add,
+                            const uint64_t* mask, int64_t tokens, int32_t* cu, int32_t* pos, int64_t* slot,
+                            int32_t* seq, void* ws, int sms, unsigned flags, cudaStream_t stream) {
+    PlanArgs a = {};
+    a.table = p.table;
+    a.held = p.held;
+    a.stack = p.stack;
+    a.top = p.top;
+    a.max_pages = p.max_pages;
+    a.pages = p.pages;
+    a.seqs = (int)p.seqs;
+    while ((1 << a.shift) < p.page) ++a.shift;
+    a.room = (int)tokens;
+    a.lens = lens;
+    a.grow = grow;
+    a.add = add;
+    a.mask = mask;
+    a.cu = cu;
+    a.pos = pos;
+    a.slot = slot;
+    a.seq = seq;
+    const int64_t pad = (p.seqs + 63) / 64 * 64;
+    a.totals = static_cast<PlanTotals*>(ws);
+    a.back_at = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + 256);
+    a.need_at = a.back_at + pad;
+    a.old_held = a.need_at + pad;
+    const int ctas = p.seqs <= kPlanThreads && tokens <= 4096 && p.seqs * p.max_pages <= 1 << 17 ? 1 : kPlanCluster;
+    const bool two = tokens > 16384;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)ctas, 1, 1};
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = flags & 1u ? 2 : 1;
+    cudaError_t e = two ? cudaLaunchKernelEx(&cfg, plan_scan_kernel<false>, a) : cudaLaunchKernelEx(&cfg, plan_scan_kernel<true>, a);
+    if (e != cudaSuccess || !two) return e;
+    return layer_launch(plan_fill_kernel, dim3((unsigned)(4 * sms)), kFillThreads, 0, 1u, stream, a);
+}
+
+cudaError_t read_and_clear_pool_error(unsigned* flags, cudaStream_t stream) {
+    unsigned v = 0, z = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_pool_error, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
+    if (e != cudaSuccess) return e;
+    e = cudaMemcpyToSymbolAsync(g_pool_error, &z, sizeof(z), 0, cudaMemcpyHostToDevice, stream);
+    if (e != cudaSuccess) return e;
+    e = cudaStreamSynchronize(stream);
+    *flags |= v;
+    return e;
+}
+
+}  // namespace w4a8

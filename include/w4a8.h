@@ -521,6 +521,17 @@ int rope_rotate(const void* X, int x_type, int64_t ld_x, int64_t tokens, int hea
                 const int32_t* pos, const double* freqs, int rot, int interleaved, float mscale, void* Y,
                 int y_type, int64_t ld_y, unsigned flags, void* stream);
 
+/* The same with positions of several axes (time, height and width of an image's
+ * or a video's tokens; text has one number on all of them): pair i turns by
+ * pos[axis[i]][token] * freqs[i].
+ *   pos [axes][tokens] int32, device; axis: HOST array of rot / 2 entries below
+ *   axes, copied into the launch (any order: blocks of pairs, axes in turn).
+ * Requires 1 <= axes <= ROPE_MAX_AXES and what rope_rotate does. */
+#define ROPE_MAX_AXES 4
+int rope_rotate_axes(const void* X, int x_type, int64_t ld_x, int64_t tokens, int heads, int dim,
+                     const int32_t* pos, int axes, const uint8_t* axis, const double* freqs, int rot,
+                     int interleaved, float mscale, void* Y, int y_type, int64_t ld_y, unsigned flags, void* stream);
+
 /* The quantized paged key/value cache.  A pool of `pages` pages of `page`
  * slots; one slot holds the key and the value of one token for `heads` heads,
  * each head's vector of `dim` values as codes with one fp32 scale:
@@ -581,6 +592,12 @@ int kvq_write(const kvq_cache_t* cache, const kvq_batch_t* batch, const void* K,
               const double* freqs, int rot, int interleaved, float mscale, uint16_t* Q_out, unsigned flags,
               void* stream);
 
+/* kvq_write with positions of several axes (rope_rotate_axes); freqs is required. */
+int kvq_write_axes(const kvq_cache_t* cache, const kvq_batch_t* batch, const void* K, int64_t ld_k, const void* V,
+                   int64_t ld_v, const void* Q, int64_t ld_q, int heads_q, int x_type, const int32_t* pos, int axes,
+                   const uint8_t* axis, const double* freqs, int rot, int interleaved, float mscale,
+                   uint16_t* Q_out, unsigned flags, void* stream);
+
 /* Reads the batch's keys and values back: code * scale in fp32, rounded once
  * to the output type.  K, V [tokens][heads][dim], y_type, 16-byte aligned.  Rows of
  * tokens out of range are left as they are. */
@@ -634,6 +651,142 @@ int kvq_attention(const kvq_cache_t* cache, const kvq_batch_t* batch, const uint
                   unsigned flags, void* stream);
 
 /* ---------------------------------------------------------------------- */
+/* A serving step around the layers: pages and positions, verification      */
+/* ---------------------------------------------------------------------- */
+
+/* The pages of a cache's pool and who holds them (all device arrays of int32,
+ * so that a captured graph plans its own steps):
+ *   table [seqs][max_pages], held [seqs]: row b holds the first held[b] pages of
+ *     its table row (what lies behind them means nothing);
+ *   stack [pages], top [1]: the free pages are stack[0] .. stack[top - 1].
+ * To begin with: held 0, stack 0 .. pages - 1, top = pages. */
+typedef struct {
+    int32_t* table;
+    int32_t* held;
+    int32_t* stack;
+    int32_t* top;
+    int64_t seqs, max_pages, pages;
+    int page;
+} kvq_pool_t;
+
+/* Plans a step from the requests' lengths: hands out and takes back pages and
+ * writes what a kvq_batch_t and the rotary positions of the step need.  Per row
+ * b, in this order:
+ *   lens[b] += grow[b] (grow NULL: 0), the tokens that the step before left cached;
+ *   add[b] < 0: the request ended; its pages go back onto the stack and
+ *     lens[b] = held[b] = 0 (rows in order, each row's pages in order, the
+ *     first of all on top);
+ *   add[b] = n > 0: n tokens go in and the row takes the pages it lacks for slots up to
+ *     lens[b] + n, off the stack's top, rows in order -- if the rows up to b ask for no
+ *     more than the free pages (those that came back among them; a row that
+ *     needs none is not held up) and for no more than `tokens` tokens.  Else the row waits: no
+ *     tokens, no pages (cu tells), and is asked about again when add says so.
+ *     A row that would need more than max_pages waits and counts for nothing.
+ *   add[b] = 0: no tokens, nothing changes.
+ * Outputs: cu [seqs + 1]; lens is the batch's start; for token t of row b,
+ * slot s = lens[b] + t - cu[b]: pos [tokens] = s (with mask: lens[b] + the number
+ * of bits of mask[t] - 1, the depth in a drafted tree whose words hold ancestors and self),
+ * slot [tokens] int64 = page * (the row's page of s) + s % page, the row of
+ * the pool in kvq_cache_t, -1 where that page is outside the pool, seq [tokens] = b;
+ * from cu[seqs] on pos 0, slot -1, seq -1.  pos, slot, seq: NULL to skip.
+ * Counters out of range (held, lens, top, pages coming back onto a full stack)
+ * are cut to it and set bit 3 of the device error word; no address outside the arrays is
+ * touched as long as page numbers are only moved, which is all this call does.
+ *   lens, add, grow [seqs] int32; mask [tokens] uint64 or NULL;
+ *   ws, ws_bytes: kvq_plan_workspace_bytes, 256-byte aligned (need not be
+ *   zeroed; one call at a time).
+ * Requires 1 <= seqs <= 65536, 1 <= tokens <= 2^31 - 1, 1 <= pages, max_pages
+ * <= 2^31 - 1, page 16, 32, 64, 128 or 256; int32 arrays 4-byte, mask and slot
+ * 8-byte aligned. */
+size_t kvq_plan_workspace_bytes(const kvq_pool_t* pool);
+int kvq_plan(const kvq_pool_t* pool, int32_t* lens, const int32_t* grow, const int32_t* add, const uint64_t* mask,
+             int64_t tokens, int32_t* cu, int32_t* pos, int64_t* slot, int32_t* seq, void* ws, size_t ws_bytes,
+             unsigned flags, void* stream);
+
+/* Verifies drafted tokens against the target's logits.  The tokens of sequence
+ * b are cu[b] .. cu[b + 1] - 1 (kvq_batch_t); the first, the root, is the last
+ * token that is certain, the others are drafts: children of the token that
+ * mask[t] names (its ancestors' bits; the highest one below its own is
+ * the parent), or, with mask NULL, each of the one before.  Row t of the logits is the
+ * target's answer after token t.
+ * From the root on, the children of the current token are tested in order.
+ * With p = softmax(L / temp) of the current token's row, u = the child's random number:
+ *   Q NULL: the drafts are given; a child x is taken when u < p(x), else p(x) = 0 and p is
+ *     scaled to sum 1 again (a token drafted twice is refused the second time);
+ *   Q: the children of a token were drawn from row Q of it, each on its own; x is taken when
+ *     u Q(x) < p(x), else p = max(p - Q, 0), scaled to sum 1.
+ * A child taken becomes the current token.  At the end one token is drawn from what p is
+ * then: the first whose cumulative sum passes u of the root times the whole.  The tokens
+ * said follow the target's distribution in both cases.  temp 0 (below 2^-20): p is 1 at the
+ * first of the largest logits; the tests and the draw are a comparison of tokens.
+ * Outputs per sequence, in its places from cu[b] on, the rest -1:
+ *   keep [tokens]: 0 (the root), then the tokens taken, as places in the
+ *     sequence: what kvq_keep takes;
+ *   out [tokens]: the tokens taken, then the one drawn (its place in the next
+ *     step is the root's);
+ *   count [seqs]: how many are kept (1 + taken), which is how many are said and what the
+ *     sequence's cache grows by (kvq_plan's grow); 0 for a sequence without tokens.
+ * Rows of tokens that no sequence holds are left as they are.
+ * Arithmetic: tests in fp32 (sums of fp32 weights over the vocabulary, relative error below
+ * 2^-18); the draw on integer weights in units of 2^-40 of the largest weight's power of two, each within 4
+ * units, whose sums are exact: the same call gives the same tokens.
+ * -infinity takes a token out; a row that holds a NaN, +infinity or nothing but -infinity has
+ * no distribution: its children are refused, the token drawn is -1.  A draft outside the vocabulary
+ * is refused.  If refusals left nothing but roundings, the draw takes the whole row.  u outside [0, 1) counts
+ * as the nearest number inside, temp that is negative or NaN as 0.
+ *   L [tokens][vocab] l_type, rows ld_l elements apart; Q [tokens][vocab] q_type, ld_q, or NULL;
+ *   ids [tokens] int32 (the root's is not read); temp [seqs] fp32 or NULL (1); u [tokens] fp32.
+ *   ws, ws_bytes: draft_verify_workspace_bytes, 256-byte aligned (need not be
+ *   zeroed; one call at a time).
+ * A sequence of more than KVQ_MAX_TREE tokens sets bit 3 of the device error word: count 0, keep and out -1.
+ * Requires 1 <= seqs <= 65536, 1 <= tokens <= 2^31 - 1, 1 <= vocab <= 2^22, ld >= vocab;
+ * mask 8-byte aligned, the others to their element. */
+size_t draft_verify_workspace_bytes(int64_t tokens, int64_t vocab);
+int draft_verify(const void* L, int l_type, int64_t ld_l, int64_t vocab, const int32_t* cu, int64_t seqs,
+                 int64_t tokens, const int32_t* ids, const uint64_t* mask, const void* Q, int q_type, int64_t ld_q,
+                 const float* temp, const float* u, int32_t* keep, int32_t* out, int32_t* count, void* ws,
+                 size_t ws_bytes, unsigned flags, void* stream);
+
+/* ---------------------------------------------------------------------- */
+/* Linear with 8-bit floating-point blocks of 128                          */
+/* ---------------------------------------------------------------------- */
+
+/* Weights and activations in e4m3 (4 exponent, 3 mantissa bits, up to 448) with one fp32
+ * scale for each block: of the weights 128 rows x 128 values of K, of the
+ * activation one row x 128 values; the last blocks may be smaller.  For any number of rows:
+ * a prompt's as well as a decode step's.
+ *   scale = max|block| * fl(1 / 448); code = the e4m3 number nearest to x / scale (the
+ *   quotient itself, ties to even, at most 448).  A zero block gets scale 0 and codes 0. */
+#define F8_BLOCK 128
+
+/* W [N][K] fp32 in; Wf [N][K] e4m3 out; sw [ceil(N/128)][ceil(K/128)] fp32 out.
+ * Requires 1 <= N <= 2^31 - 1, 16 <= K <= 131072, K % 16 == 0; W and Wf 16-byte aligned. */
+int f8_quantize_weights(const float* W, int64_t N, int64_t K, uint8_t* Wf, float* sw, void* stream);
+
+/* X [M][K] x_type in; Xf [M][K] e4m3 out; sa [ceil(K/128)][M] fp32 out (a block's
+ * scales of all rows side by side).  Requires 1 <= M <= 2^24, the limits of K
+ * above; X and Xf 16-byte aligned. */
+int f8_quantize_rows(const void* X, int x_type, int64_t M, int64_t K, uint8_t* Xf, float* sa, unsigned flags,
+                     void* stream);
+
+/* Y[m][n] = sum_kb (sa[kb][m] * sw[n / 128][kb]) * sum_{k in block kb} Xf[m][k] Wf[n][k]:
+ * products and sums of a block in fp32 on the tensor cores, the blocks' sums scaled and added in
+ * fp32 in order (of pieces of K, then the pieces in order), one rounding to y_type.
+ * The same call gives the same bits.
+ *   Y [M][N] y_type out; ws, ws_bytes: f8_gemm_workspace_bytes, 256-byte aligned
+ *   (need not be zeroed; one call at a time).
+ * Requires the limits above; Xf and Wf 16-byte aligned, the others to their element. */
+size_t f8_gemm_workspace_bytes(int64_t M, int64_t K, int64_t N);
+int f8_gemm(const uint8_t* Xf, const float* sa, int64_t M, int64_t K, const uint8_t* Wf, const float* sw, int64_t N,
+            void* Y, int y_type, void* ws, size_t ws_bytes, unsigned flags, void* stream);
+
+/* f8_quantize_rows and f8_gemm in one call, the codes in the workspace
+ * (f8_linear_workspace_bytes): the same Y. */
+size_t f8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N);
+int f8_linear(const void* X, int x_type, int64_t M, int64_t K, const uint8_t* Wf, const float* sw, int64_t N, void* Y,
+              int y_type, void* ws, size_t ws_bytes, unsigned flags, void* stream);
+
+/* ---------------------------------------------------------------------- */
 /* Diagnostics                                                             */
 /* ---------------------------------------------------------------------- */
 
@@ -645,7 +798,7 @@ const char* w4a8_last_error(void);
 /* Copies the current device's error word into *flags and clears it.  Bit 0:
  * a wait for weight data ran out; bit 1: unused; bit 2: a wait for
  * in-flight copies at exit ran out; bit 3: a cache call met a slot or page out
- * of range (kvq_batch_t), which touches no workspace.  A non-zero word means that some call's
+ * of range (kvq_batch_t, kvq_pool_t) or a tree of too many tokens, which touches no workspace.  A non-zero word means that some call's
  * outputs are unspecified and that the split-K arrival counters of the
  * workspace it used may be left non-zero: zero-fill that workspace again
  * before reusing it.  (The static scratch of w4a8_linear_noalloc is cleared
