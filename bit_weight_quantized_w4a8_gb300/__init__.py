@@ -18,7 +18,7 @@ from ._binding import (  # noqa: F401
     KVQBatch, KVQCache, add_norm, kvq_attention, kvq_attention_workspace_bytes, kvq_cache, kvq_keep, kvq_read,
     kvq_write, rope_frequencies, rope_rotate,
     KVQPool, draft_verify, draft_verify_workspace_bytes, kvq_plan, kvq_plan_workspace_bytes, kvq_pool, rope_axes,
-    F8_BLOCK, f8_gemm, f8_gemm_workspace_bytes, f8_linear, f8_linear_workspace_bytes, f8_quantize_rows,
+    F8_BLOCK, f8_gemm, f8_linear, f8_linear_workspace_bytes, f8_quantize_rows,
     f8_quantize_weights,
     w4_interleave_rows, w4a8_gate_up_silu, w4a8_gate_up_silu_workspace_bytes, w4a8_silu_mul,
 )

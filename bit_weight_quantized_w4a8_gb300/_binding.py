@@ -37,8 +37,7 @@ EXPORTS = [
     "kvq_attention_workspace_bytes", "kvq_attention",
     "rope_rotate_axes", "kvq_write_axes",
     "kvq_plan_workspace_bytes", "kvq_plan", "draft_verify_workspace_bytes", "draft_verify",
-    "f8_quantize_weights", "f8_quantize_rows", "f8_gemm_workspace_bytes", "f8_gemm", "f8_linear_workspace_bytes",
-    "f8_linear",
+    "f8_quantize_weights", "f8_quantize_rows", "f8_gemm", "f8_linear_workspace_bytes", "f8_linear",
 ]
 
 
@@ -134,8 +133,7 @@ _SIGS = {
                                     ctypes.c_size_t, _u, _p]),
     "f8_quantize_weights": (ctypes.c_int, [_p, _i64, _i64, _p, _p, _p]),
     "f8_quantize_rows": (ctypes.c_int, [_p, _int, _i64, _i64, _p, _p, _u, _p]),
-    "f8_gemm_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
-    "f8_gemm": (ctypes.c_int, [_p, _p, _i64, _i64, _p, _p, _i64, _p, _int, _p, ctypes.c_size_t, _u, _p]),
+    "f8_gemm": (ctypes.c_int, [_p, _p, _i64, _i64, _p, _p, _i64, _p, _int, _u, _p]),
     "f8_linear_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
     "f8_linear": (ctypes.c_int, [_p, _int, _i64, _i64, _p, _p, _i64, _p, _int, _p, ctypes.c_size_t, _u, _p]),
 }
@@ -1122,15 +1120,11 @@ def _f8_out(Y, shape, dtype, device):
     return Y, yt
 
 
-def f8_gemm_workspace_bytes(M: int, K: int, N: int) -> int:
-    return int(lib().f8_gemm_workspace_bytes(M, K, N))
-
-
 def f8_linear_workspace_bytes(M: int, K: int, N: int) -> int:
     return int(lib().f8_linear_workspace_bytes(M, K, N))
 
 
-def f8_gemm(Xf, sa, Wf, sw, dtype=torch.float32, Y=None, ws=None, flags: int = 0):
+def f8_gemm(Xf, sa, Wf, sw, dtype=torch.float32, Y=None, flags: int = 0):
     """Y [M][N] (fp32 or fp16): the product of e4m3 codes with a scale for each row
     and 128 values of X and each 128 x 128 block of W."""
     _want(Xf, torch.uint8, "Xf")
@@ -1139,13 +1133,10 @@ def f8_gemm(Xf, sa, Wf, sw, dtype=torch.float32, Y=None, ws=None, flags: int = 0
     M, K = Xf.shape
     _want(sa, torch.float32, "sa", (_f8_blocks(K), M))
     N = _f8_weights(Wf, sw, K)
-    dev = _one_device(Xf, sa, Wf, sw, Y, ws)
+    dev = _one_device(Xf, sa, Wf, sw, Y)
     Y, yt = _f8_out(Y, (M, N), dtype, dev)
-    L = lib()
-    nbytes = L.f8_gemm_workspace_bytes(M, K, N)
-    ws, wsb = _scratch(ws, nbytes, dev) if nbytes or ws is not None else (None, 0)
-    _check(L.f8_gemm(Xf.data_ptr(), sa.data_ptr(), M, K, Wf.data_ptr(), sw.data_ptr(), N, Y.data_ptr(), yt, _ptr(ws), wsb,
-                     flags, _stream(Xf)))
+    _check(lib().f8_gemm(Xf.data_ptr(), sa.data_ptr(), M, K, Wf.data_ptr(), sw.data_ptr(), N, Y.data_ptr(), yt, flags,
+                         _stream(Xf)))
     return Y
 
 

@@ -735,6 +735,7 @@ int w4a8_device_error(unsigned* flags, void* stream) {
     if (e == cudaSuccess) e = w4a8::read_and_clear_attn_error(flags, static_cast<cudaStream_t>(stream));
     if (e == cudaSuccess) e = w4a8::read_and_clear_pool_error(flags, static_cast<cudaStream_t>(stream));
     if (e == cudaSuccess) e = w4a8::read_and_clear_verify_error(flags, static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) e = w4a8::read_and_clear_f8_error(flags, static_cast<cudaStream_t>(stream));
     // a wait that gave up may leave split-K arrival counters non-zero; the
     // static scratch of w4a8_linear_noalloc is cleared here (caller-owned
     // workspaces must be re-zeroed by the caller)

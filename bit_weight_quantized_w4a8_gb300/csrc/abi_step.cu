@@ -57,6 +57,7 @@ int check_linear(const char* who, int64_t M, int64_t K, int64_t N) {
     if (K < 16 || K > 131072 || K % 16)
         return fail(W4A8_ERR_SHAPE, "%s: K=%lld must be a multiple of 16 in [16, 131072]", who, (long long)K);
     if (N < 1 || N > kIntMax) return fail(W4A8_ERR_SHAPE, "%s: N=%lld outside [1, 2^31-1]", who, (long long)N);
+    if (M * N > (int64_t)1 << 43) return fail(W4A8_ERR_SHAPE, "%s: M * N above 2^43", who);
     return W4A8_OK;
 }
 
@@ -68,9 +69,9 @@ int check_vocab(const char* who, int64_t tokens, int64_t vocab) {
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 int64_t blocks(int64_t k) { return (k + F8_BLOCK - 1) / F8_BLOCK; }
-// f8_linear's workspace: codes, scales, the product's own.
+// f8_linear's workspace: codes, scales.
 size_t linear_scales_at(int64_t M, int64_t K) { return round256((size_t)M * K); }
-size_t linear_gemm_at(int64_t M, int64_t K) { return linear_scales_at(M, K) + round256((size_t)M * blocks(K) * 4); }
+size_t linear_bytes(int64_t M, int64_t K) { return linear_scales_at(M, K) + round256((size_t)M * blocks(K) * 4); }
 
 cudaStream_t st_of(void* stream) { return static_cast<cudaStream_t>(stream); }
 
@@ -155,14 +156,8 @@ int f8_quantize_rows(const void* X, int x_type, int64_t M, int64_t K, uint8_t* X
                              "f8_quantize_rows launch");
 }
 
-size_t f8_gemm_workspace_bytes(int64_t M, int64_t K, int64_t N) {
-    int sms = 0;
-    if (check_linear("f8_gemm", M, K, N) != W4A8_OK || w4a8::status_sm_count(&sms) != W4A8_OK) return 0;
-    return w4a8::f8_gemm_workspace(M, K, N, sms);
-}
-
 int f8_gemm(const uint8_t* Xf, const float* sa, int64_t M, int64_t K, const uint8_t* Wf, const float* sw, int64_t N,
-            void* Y, int y_type, void* ws, size_t ws_bytes, unsigned flags, void* stream) {
+            void* Y, int y_type, unsigned flags, void* stream) {
     if (!Xf || !sa || !Wf || !sw || !Y) return fail(W4A8_ERR_NULL, "f8_gemm: NULL pointer");
     if (!is_type(y_type)) return fail(W4A8_ERR_SHAPE, "f8_gemm: unknown type");
     int st;
@@ -172,15 +167,12 @@ int f8_gemm(const uint8_t* Xf, const float* sa, int64_t M, int64_t K, const uint
     if ((st = check_flags("f8_gemm", flags)) != W4A8_OK) return st;
     int sms = 0;
     if ((st = w4a8::status_sm_count(&sms)) != W4A8_OK) return st;
-    if ((st = check_workspace("f8_gemm", ws, ws_bytes, w4a8::f8_gemm_workspace(M, K, N, sms))) != W4A8_OK) return st;
-    return w4a8::status_done(
-        w4a8::launch_f8_gemm(Xf, sa, M, K, Wf, sw, N, Y, y_type, ws, sms, flags, st_of(stream)), "f8_gemm launch");
+    return w4a8::status_done(w4a8::launch_f8_gemm(Xf, sa, M, K, Wf, sw, N, Y, y_type, sms, flags, st_of(stream)),
+                             "f8_gemm launch");
 }
 
 size_t f8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N) {
-    int sms = 0;
-    if (check_linear("f8_linear", M, K, N) != W4A8_OK || w4a8::status_sm_count(&sms) != W4A8_OK) return 0;
-    return linear_gemm_at(M, K) + w4a8::f8_gemm_workspace(M, K, N, sms);
+    return check_linear("f8_linear", M, K, N) == W4A8_OK ? linear_bytes(M, K) : 0;
 }
 
 int f8_linear(const void* X, int x_type, int64_t M, int64_t K, const uint8_t* Wf, const float* sw, int64_t N, void* Y,
@@ -194,13 +186,12 @@ int f8_linear(const void* X, int x_type, int64_t M, int64_t K, const uint8_t* Wf
     if ((st = check_flags("f8_linear", flags)) != W4A8_OK) return st;
     int sms = 0;
     if ((st = w4a8::status_sm_count(&sms)) != W4A8_OK) return st;
-    const size_t at = linear_gemm_at(M, K);
-    if ((st = check_workspace("f8_linear", ws, ws_bytes, at + w4a8::f8_gemm_workspace(M, K, N, sms))) != W4A8_OK) return st;
+    if ((st = check_workspace("f8_linear", ws, ws_bytes, linear_bytes(M, K))) != W4A8_OK) return st;
     uint8_t* Xf = static_cast<uint8_t*>(ws);
     float* sa = reinterpret_cast<float*>(Xf + linear_scales_at(M, K));
     cudaError_t e = w4a8::launch_f8_quantize_rows(X, x_type, M, K, Xf, sa, flags, st_of(stream));
     if (e == cudaSuccess)
-        e = w4a8::launch_f8_gemm(Xf, sa, M, K, Wf, sw, N, Y, y_type, Xf + at, sms, W4A8_LAUNCH_PDL, st_of(stream));
+        e = w4a8::launch_f8_gemm(Xf, sa, M, K, Wf, sw, N, Y, y_type, sms, W4A8_LAUNCH_PDL, st_of(stream));
     return w4a8::status_done(e, "f8_linear launch");
 }
 

@@ -1,8 +1,5 @@
 // f8.cu -- the linear with e4m3 weights and activations and a scale for each
-// block of 128: quantizers and the product.
-//
-//   Y[m][n] = sum over the blocks kb of 128 values of K of
-//             (sa[kb][m] * sw[n / 128][kb]) * sum_{k in kb} xq[m][k] wq[n][k]
+// block of 128: the quantizers (the product: f8_mma.cu).
 #include <cuda_fp16.h>
 
 #include "f8.cuh"
@@ -67,59 +64,6 @@ __global__ void __launch_bounds__(kF8Threads) f8_weights_kernel(const float* W, 
     if (threadIdx.x == 0) sw[blockIdx.x] = s;
 }
 
-__device__ __forceinline__ float e4m3_value(uint8_t c) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
-}
-
-// 64 x 64 outputs a CTA, 4 x 4 a thread; fp32 products.
-template <typename TY>
-__global__ void __launch_bounds__(kF8Threads) f8_gemm_kernel(const uint8_t* Xf, const float* sa, int M, int K, int kbs,
-                                                             const uint8_t* Wf, const float* sw, int64_t N, TY* Y) {
-    __shared__ float xs[32][65], ws[32][65];
-    griddep_launch_dependents();
-    griddep_wait();
-    const int64_t n0 = (int64_t)blockIdx.x * 64;
-    const int m0 = blockIdx.y * 64;
-    const int tn = threadIdx.x % 16, tm = threadIdx.x / 16;
-    float sum[4][4] = {};
-    for (int kb = 0; kb < kbs; ++kb) {
-        float part[4][4] = {};
-        for (int k0 = kb * kF8Block; k0 < min(K, (kb + 1) * kF8Block); k0 += 32) {
-            __syncthreads();
-            for (int e = threadIdx.x; e < 64 * 32; e += kF8Threads) {
-                const int r = e / 32, k = e % 32;
-                xs[k][r] = m0 + r < M && k0 + k < K ? e4m3_value(Xf[(int64_t)(m0 + r) * K + k0 + k]) : 0.f;
-                ws[k][r] = n0 + r < N && k0 + k < K ? e4m3_value(Wf[(n0 + r) * K + k0 + k]) : 0.f;
-            }
-            __syncthreads();
-            #pragma unroll 4
-            for (int k = 0; k < 32; ++k)
-                #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    #pragma unroll
-                    for (int j = 0; j < 4; ++j) part[i][j] = fmaf(xs[k][tm + 16 * i], ws[k][tn + 16 * j], part[i][j]);
-        }
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = min(m0 + tm + 16 * i, M - 1);
-            const float a = sa[(int64_t)kb * M + m];
-            #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t n = min(n0 + tn + 16 * j, N - 1);
-                sum[i][j] = fmaf(a * sw[n / kF8Block * kbs + kb], part[i][j], sum[i][j]);
-            }
-        }
-    }
-    #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + tm + 16 * i;
-            const int64_t n = n0 + tn + 16 * j;
-            if (m < M && n < N) Y[(int64_t)m * N + n] = (TY)sum[i][j];
-        }
-}
-
 int f8_blocks(int64_t k) { return (int)((k + kF8Block - 1) / kF8Block); }
 
 }  // namespace
@@ -138,17 +82,6 @@ cudaError_t launch_f8_quantize_rows(const void* X, int x_f16, int64_t M, int64_t
                                 (int)M, (int)K, kbs, Xf, sa)
                  : layer_launch(f8_rows_kernel<float>, grid, kF8Threads, 0, flags, stream, static_cast<const float*>(X),
                                 (int)M, (int)K, kbs, Xf, sa);
-}
-
-size_t f8_gemm_workspace(int64_t, int64_t, int64_t, int) { return 0; }
-
-cudaError_t launch_f8_gemm(const uint8_t* Xf, const float* sa, int64_t M, int64_t K, const uint8_t* Wf, const float* sw,
-                           int64_t N, void* Y, int y_f16, void*, int, unsigned flags, cudaStream_t stream) {
-    const dim3 grid((unsigned)((N + 63) / 64), (unsigned)((M + 63) / 64));
-    return y_f16 ? layer_launch(f8_gemm_kernel<__half>, grid, kF8Threads, 0, flags, stream, Xf, sa, (int)M, (int)K,
-                                f8_blocks(K), Wf, sw, N, static_cast<__half*>(Y))
-                 : layer_launch(f8_gemm_kernel<float>, grid, kF8Threads, 0, flags, stream, Xf, sa, (int)M, (int)K,
-                                f8_blocks(K), Wf, sw, N, static_cast<float*>(Y));
 }
 
 }  // namespace w4a8

@@ -1,0 +1,604 @@
+// f8_mma.cu -- the product of e4m3 codes with a scale for each block of 128
+// values of K, on tcgen05.
+//
+//   Y[m][n] = sum_kb (sa[kb][m] * sw[n / 128][kb]) * sum_{k in kb} xq[m][k] wq[n][k]
+//
+// One block of K is one 128-byte row of both operands: a TMA box in the 128-byte
+// swizzle, four MMAs of K = 32.  The sums of a block are complete in TMEM; the
+// consumer warps read them, scale them and add them to fp32 sums in registers while
+// the tensor core fills the other half of TMEM with the next block.  The
+// registers hold a tile's sums until its last block, so TMEM belongs to the next tile
+// while a tile is written.
+//
+// Two kernels:
+//  wide    128 rows of X x 256 of W a CTA: a thread has one row of X and 128
+//          columns, so one scale a block.  For many rows.
+//  narrow  128 rows of W x 16 .. 128 of X: the weights fill the tensor core's 128 rows
+//          whatever the batch, K is cut over a cluster whose sums are joined through
+//          distributed shared memory in the order of the pieces.  For few rows.
+#include <cooperative_groups.h>
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "f8.cuh"
+#include "kernels.h"
+#include "tc.cuh"
+
+namespace w4a8 {
+namespace {
+
+namespace cg = cooperative_groups;
+
+__device__ unsigned g_f8_error;
+
+constexpr int kProducerThreads = 128;  // warp 0 copies, warp 1 issues the MMAs
+constexpr int kRows = 128;             // TMEM lanes: rows of operand A
+constexpr int kKBytes = 128;           // a block of K
+constexpr int kABytes = kRows * kKBytes;
+
+struct F8Args {
+    CUtensorMap tm_a, tm_b;
+    const float *sa, *sw;
+    void* Y;
+    int64_t N;
+    int M, kbs, tiles_a, tiles;
+};
+
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    #pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    for (;;) {
+        #pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            *abort_flag = 1;
+            atomicOr(&g_f8_error, kErrFullWait);
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
+    if (!mbar_wait(bar, parity)) atomicOr(&g_f8_error, kErrDrainWait);
+}
+
+// 32 columns of the warp's 32 lanes; the values are there after tmem_ld32_wait,
+// which names them so that nothing that uses them moves in front of it.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                   "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
+}
+// Two fp32 multiply-adds in one instruction.
+__device__ __forceinline__ void fma2(uint64_t& c, uint32_t a0, uint32_t a1, uint64_t s2) {
+    asm("{\n\t.reg .b64 a;\n\tmov.b64 a, {%1, %2};\n\tfma.rn.f32x2 %0, a, %3, %0;\n\t}" : "+l"(c) : "r"(a0), "r"(a1), "l"(s2));
+}
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 halves_of(uint64_t c) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(c));
+    return r;
+}
+
+// What a CTA's warps share besides the operands.
+template <int S>
+struct Bars {
+    uint64_t full[S], empty[S], d_full[2], d_empty[2];
+    uint32_t tmem;
+    int abort;
+};
+
+// One block of K: four MMAs of 32 bytes.
+__device__ __forceinline__ void issue_block(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+    const uint64_t ad = sw128_desc(a), bd = sw128_desc(b);
+    #pragma unroll
+    for (int k = 0; k < kKBytes / 32; ++k) tc_mma_e4m3(d, ad + 2 * k, bd + 2 * k, idesc, k > 0);
+}
+
+// ---------------------------------------------------------------------------
+// wide
+// ---------------------------------------------------------------------------
+
+constexpr int kWideCols = 256;
+constexpr int kWideStages = 4;
+constexpr int kWideWarps = 8;  // consumers: warp w has lanes 32 (w % 4) .., columns 128 (w / 4) ..
+constexpr int kWideThreads = kProducerThreads + 32 * kWideWarps;
+constexpr int kWideStage = kABytes + kWideCols * kKBytes;
+constexpr int kWideOut = 32 * 128;  // a warp's outputs on their way: 32 rows of 128 bytes
+constexpr int kWideSmem = kWideStages * kWideStage + kWideWarps * kWideOut + 1024;
+
+// 32 rows of 128 bytes in a warp's buffer, 16-byte chunk c of row r at c ^ (r % 8).
+__device__ __forceinline__ uint4* out_chunk(uint8_t* buf, int r, int c) {
+    return reinterpret_cast<uint4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
+}
+
+// The warp's rows m0 + 0..31, columns n0 + 0.. of 128 / sizeof(TY), from the buffer.
+template <typename TY>
+__device__ __forceinline__ void store_rows(uint8_t* buf, TY* Y, int m0, int M, int64_t n0, int64_t N, bool vec) {
+    constexpr int PER = 16 / sizeof(TY);
+    const int lane = threadIdx.x % 32, c = lane % 8;
+    const int64_t n = n0 + c * PER;
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + lane / 8;
+        const uint4 v = *out_chunk(buf, r, c);
+        if (m0 + r >= M || n >= N) continue;
+        TY* y = Y + (int64_t)(m0 + r) * N + n;
+        if (vec && n + PER <= N) {
+            *reinterpret_cast<uint4*>(y) = v;
+        } else {
+            const TY* e = reinterpret_cast<const TY*>(&v);
+            #pragma unroll
+            for (int k = 0; k < PER; ++k)
+                if (n + k < N) y[k] = e[k];
+        }
+    }
+}
+
+template <typename TY>
+__global__ void __launch_bounds__(kWideThreads, 1) f8_wide_kernel(const __grid_constant__ F8Args a) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Bars<kWideStages> sh;
+    uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+    const uint32_t sbase = smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    if (tid == 0) {
+        for (int i = 0; i < kWideStages; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 1);
+            mbar_init(smem_u32(&sh.empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.d_full[i]), 1);
+            mbar_init(smem_u32(&sh.d_empty[i]), kWideWarps);
+        }
+        sh.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), 512);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    griddep_launch_dependents();
+    griddep_wait();
+    const uint32_t tmem = sh.tmem;
+    const int mine = a.tiles > (int)blockIdx.x ? (a.tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+    const int steps = mine * a.kbs;  // blocks of all tiles
+    int issued = 0;
+
+    if (warp == 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (lane == 0) {
+            const uint64_t keep = l2_evict_last_policy();
+            int kb = 0, tile = blockIdx.x;
+            for (int i = 0; i < steps; ++i) {
+                const int s = i % kWideStages;
+                if (i >= kWideStages && !wait_bounded(smem_u32(&sh.empty[s]), (i / kWideStages - 1) & 1, &sh.abort)) break;
+                const uint32_t at = sbase + s * kWideStage, bar = smem_u32(&sh.full[s]);
+                mbar_arrive_expect_tx(bar, kWideStage);
+                tma_load_2d_hint(at, &a.tm_a, kb * kKBytes, tile % a.tiles_a * kRows, bar, keep);
+                tma_load_2d_hint(at + kABytes, &a.tm_b, kb * kKBytes, tile / a.tiles_a * kWideCols, bar, keep);
+                issued = i + 1;
+                if (++kb == a.kbs) kb = 0, tile += gridDim.x;
+            }
+            for (int i = max(0, issued - kWideStages); i < issued; ++i)
+                drain(smem_u32(&sh.full[i % kWideStages]), (i / kWideStages) & 1);
+        }
+    } else if (warp == 1) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (lane == 0) {
+            const uint32_t idesc = e4m3_idesc(kRows, kWideCols);
+            for (int i = 0; i < steps; ++i) {
+                const int s = i % kWideStages, b = i & 1;
+                if (i >= 2 && !wait_bounded(smem_u32(&sh.d_empty[b]), (i / 2 - 1) & 1, &sh.abort)) break;
+                if (!wait_bounded(smem_u32(&sh.full[s]), (i / kWideStages) & 1, &sh.abort)) break;
+                tc_fence_after_sync();
+                const uint32_t at = sbase + s * kWideStage;
+                issue_block(tmem + kWideCols * b, at, at + kABytes, idesc);
+                tc_commit(smem_u32(&sh.empty[s]));
+                tc_commit(smem_u32(&sh.d_full[b]));
+                issued = i + 1;
+            }
+            // every MMA is done before TMEM is given back
+            if (issued > 0) drain(smem_u32(&sh.d_full[(issued - 1) & 1]), ((issued - 1) / 2) & 1);
+        }
+    } else if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        const int cw = warp - 4, q = warp % 4, g = cw / 4;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + 128 * g;
+        uint8_t* buf = smem + kWideStages * kWideStage + cw * kWideOut;
+        const bool vec = a.N % (16 / sizeof(TY)) == 0 && reinterpret_cast<uintptr_t>(a.Y) % 16 == 0;
+        const int64_t nbs = (a.N + kF8Block - 1) / kF8Block;
+        int i = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; ok && tile < a.tiles; tile += gridDim.x) {
+            const int m0 = tile % a.tiles_a * kRows + 32 * q;
+            const int64_t nb = min((int64_t)(tile / a.tiles_a) * 2 + g, nbs - 1);
+            const float* sa = a.sa + min(m0 + lane, a.M - 1);
+            const float* sw = a.sw + nb * a.kbs;
+            uint64_t acc[64];
+            #pragma unroll
+            for (int j = 0; j < 64; ++j) acc[j] = 0;
+            float sa_next = *sa, sw_next = *sw;
+            for (int kb = 0; kb < a.kbs; ++kb, ++i) {
+                const float s = sa_next * sw_next;
+                const uint64_t s2 = pair_of(s, s);
+                if (kb + 1 < a.kbs) {
+                    sa_next = sa[(int64_t)(kb + 1) * a.M];
+                    sw_next = sw[kb + 1];
+                }
+                const int b = i & 1;
+                ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.d_full[b]), (i / 2) & 1, &sh.abort));
+                if (!ok) break;
+                tc_fence_after_sync();
+                uint32_t v[2][32];
+                tmem_ld32(lanes + kWideCols * b, v[0]);
+                tmem_ld32_wait(v[0]);
+                #pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c < 3) tmem_ld32(lanes + kWideCols * b + 32 * (c + 1), v[(c + 1) & 1]);
+                    #pragma unroll
+                    for (int j = 0; j < 16; ++j) fma2(acc[16 * c + j], v[c & 1][2 * j], v[c & 1][2 * j + 1], s2);
+                    if (c < 3) tmem_ld32_wait(v[(c + 1) & 1]);
+                    if (c == 2) {  // all of it is in registers
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&sh.d_empty[b]));
+                    }
+                }
+            }
+            if (!ok) break;
+            constexpr int PER = 128 / sizeof(TY);  // columns of a trip through the buffer
+            #pragma unroll
+            for (int c = 0; c < 128 / PER; ++c) {
+                #pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    uint4 w;
+                    if constexpr (sizeof(TY) == 4) {
+                        const float2 x = halves_of(acc[PER / 2 * c + 2 * u]), y = halves_of(acc[PER / 2 * c + 2 * u + 1]);
+                        w = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
+                    } else {
+                        uint32_t h[4];
+                        #pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 x = halves_of(acc[PER / 2 * c + 4 * u + k]);
+                            h[k] = pack_half2(x.x, x.y);
+                        }
+                        w = make_uint4(h[0], h[1], h[2], h[3]);
+                    }
+                    *out_chunk(buf, lane, u) = w;
+                }
+                __syncwarp();
+                store_rows(buf, static_cast<TY*>(a.Y), m0, a.M, (int64_t)(tile / a.tiles_a) * kWideCols + 128 * g + c * PER, a.N, vec);
+                __syncwarp();
+            }
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// narrow
+// ---------------------------------------------------------------------------
+
+constexpr int kNarrowThreads = kProducerThreads + 128;
+constexpr int kNarrowCluster = 8;  // pieces of K, at most
+
+template <int BN>
+struct Narrow {
+    static constexpr int kStage = kABytes + BN * kKBytes;
+    static constexpr int kCtas = BN <= 64 ? 2 : 1;  // per SM
+    static constexpr int kStages = BN <= 64 ? (110 * 1024) / kStage : 6;
+    static constexpr int kCols = BN < 32 ? 32 : 2 * BN;  // TMEM
+    static constexpr int kSmem = kStages * kStage + 1024;
+    static_assert(kStages * kStage >= BN * kRows * 4, "the sums have to fit");
+};
+
+template <int BN, typename TY>
+__global__ void __launch_bounds__(kNarrowThreads, Narrow<BN>::kCtas) f8_narrow_kernel(const __grid_constant__ F8Args a) {
+    using C = Narrow<BN>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Bars<C::kStages> sh;
+    __shared__ __align__(16) float scale[2][BN];
+    cg::cluster_group cl = cg::this_cluster();
+    uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+    const uint32_t sbase = smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    if (tid == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 1);
+            mbar_init(smem_u32(&sh.empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.d_full[i]), 1);
+            mbar_init(smem_u32(&sh.d_empty[i]), 4);
+        }
+        sh.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), C::kCols);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    griddep_launch_dependents();
+    const uint32_t tmem = sh.tmem;
+    const int pieces = gridDim.x, p = blockIdx.x;  // cluster (pieces, 1, 1)
+    const int kb0 = (int)((int64_t)a.kbs * p / pieces), steps = (int)((int64_t)a.kbs * (p + 1) / pieces) - kb0;
+    const int64_t n0 = (int64_t)blockIdx.y * kRows;
+    const int m0 = blockIdx.z * BN;
+    int issued = 0;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t once = l2_evict_first_policy(), keep = l2_evict_last_policy();
+            auto load_w = [&](int i) {
+                const uint32_t bar = smem_u32(&sh.full[i % C::kStages]);
+                mbar_arrive_expect_tx(bar, C::kStage);
+                tma_load_2d_hint(sbase + i % C::kStages * C::kStage, &a.tm_a, (kb0 + i) * kKBytes, (int)n0, bar, once);
+            };
+            auto load_x = [&](int i) {
+                tma_load_2d_hint(sbase + i % C::kStages * C::kStage + kABytes, &a.tm_b, (kb0 + i) * kKBytes, m0,
+                                 smem_u32(&sh.full[i % C::kStages]), keep);
+            };
+            // the weights do not come from the kernel before
+            const int ahead = min(steps, C::kStages);
+            for (int i = 0; i < ahead; ++i) load_w(i);
+            griddep_wait();
+            for (int i = 0; i < ahead; ++i) load_x(i);
+            issued = ahead;
+            for (int i = ahead; i < steps; ++i) {
+                if (!wait_bounded(smem_u32(&sh.empty[i % C::kStages]), (i / C::kStages - 1) & 1, &sh.abort)) break;
+                load_w(i);
+                load_x(i);
+                issued = i + 1;
+            }
+            for (int i = max(0, issued - C::kStages); i < issued; ++i)
+                drain(smem_u32(&sh.full[i % C::kStages]), (i / C::kStages) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = e4m3_idesc(kRows, BN);
+            for (int i = 0; i < steps; ++i) {
+                const int s = i % C::kStages, b = i & 1;
+                if (i >= 2 && !wait_bounded(smem_u32(&sh.d_empty[b]), (i / 2 - 1) & 1, &sh.abort)) break;
+                if (!wait_bounded(smem_u32(&sh.full[s]), (i / C::kStages) & 1, &sh.abort)) break;
+                tc_fence_after_sync();
+                const uint32_t at = sbase + s * C::kStage;
+                issue_block(tmem + BN * b, at, at + kABytes, idesc);
+                tc_commit(smem_u32(&sh.empty[s]));
+                tc_commit(smem_u32(&sh.d_full[b]));
+                issued = i + 1;
+            }
+            if (issued > 0) drain(smem_u32(&sh.d_full[(issued - 1) & 1]), ((issued - 1) / 2) & 1);
+        }
+    } else if (warp >= 4) {
+        griddep_wait();
+        const int q = warp % 4, t = tid - kProducerThreads;  // t: the thread's column for scales, its lane for sums
+        const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
+        const float* sa = a.sa + (int64_t)kb0 * a.M + min(m0 + t, a.M - 1);
+        const float* sw = a.sw + blockIdx.y * (int64_t)a.kbs + kb0;
+        auto scale_at = [&](int i) { return i < steps && t < BN ? sa[(int64_t)i * a.M] * sw[i] : 0.f; };
+        uint64_t acc[BN / 2];
+        #pragma unroll
+        for (int j = 0; j < BN / 2; ++j) acc[j] = 0;
+        float s1 = scale_at(0), s2 = scale_at(1);
+        bool ok = true;
+        for (int i = 0; i < steps; ++i) {
+            if (t < BN) scale[i & 1][t] = s1;
+            s1 = s2;
+            s2 = scale_at(i + 2);
+            named_bar_sync(1, 128);  // also: the block before the last has been read by all
+            const int b = i & 1;
+            if (ok) ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.d_full[b]), (i / 2) & 1, &sh.abort));
+            if (!ok) continue;  // (the others still meet at the barrier)
+            tc_fence_after_sync();
+            #pragma unroll
+            for (int c = 0; c < BN / 16; ++c) {
+                uint32_t v[16];
+                tmem_ld16(lanes + BN * b + 16 * c, v);
+                tmem_ld16_wait(v);
+                #pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 s = *reinterpret_cast<const float4*>(&scale[b][16 * c + 4 * j]);
+                    fma2(acc[8 * c + 2 * j], v[4 * j], v[4 * j + 1], pair_of(s.x, s.y));
+                    fma2(acc[8 * c + 2 * j + 1], v[4 * j + 2], v[4 * j + 3], pair_of(s.z, s.w));
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.d_empty[b]));
+        }
+        const int64_t n = n0 + t;
+        if (pieces == 1) {
+            if (ok && n < a.N)
+                #pragma unroll
+                for (int j = 0; j < BN; ++j) {
+                    const float2 x = halves_of(acc[j / 2]);
+                    if (m0 + j < a.M) static_cast<TY*>(a.Y)[(int64_t)(m0 + j) * a.N + n] = (TY)(j % 2 ? x.y : x.x);
+                }
+        } else {
+            // all copies have landed and all MMAs have read them (the last block's are done)
+            float* sums = reinterpret_cast<float*>(smem);
+            #pragma unroll
+            for (int j = 0; j < BN; ++j) {
+                const float2 x = halves_of(acc[j / 2]);
+                if (m0 + j < a.M) sums[j * kRows + t] = ok ? (j % 2 ? x.y : x.x) : 0.f;
+            }
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, C::kCols);
+    }
+    if (pieces > 1) {
+        cl.sync();
+        // rows p, p + pieces, ... of the batch: the pieces' sums in order
+        const int r = tid % kRows, rows = min(BN, a.M - m0);
+        const int64_t n = n0 + r;
+        for (int j = p + pieces * (tid / kRows); j < rows; j += pieces * (kNarrowThreads / kRows)) {
+            float y[kNarrowCluster];
+            #pragma unroll
+            for (int k = 0; k < kNarrowCluster; ++k)
+                if (k < pieces) y[k] = cl.map_shared_rank(reinterpret_cast<float*>(smem), k)[j * kRows + r];
+            float sum = y[0];
+            #pragma unroll
+            for (int k = 1; k < kNarrowCluster; ++k)
+                if (k < pieces) sum += y[k];
+            if (n < a.N) static_cast<TY*>(a.Y)[(int64_t)(m0 + j) * a.N + n] = (TY)sum;
+        }
+        cl.sync();  // no CTA leaves while its sums may be read
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// Codes [rows][K] in boxes of one block of K and `box` rows; zeros past the ends.
+bool code_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, int box) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)K};
+    const cuuint32_t boxes[2] = {kKBytes, (cuuint32_t)box}, steps[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, boxes, steps,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename TY>
+cudaError_t launch_wide(F8Args& a, int sms, unsigned flags, cudaStream_t stream) {
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = layer_smem(f8_wide_kernel<TY>, kWideSmem, ready);
+    if (e != cudaSuccess) return e;
+    const int grid = a.tiles < sms ? a.tiles : sms;
+    return layer_launch(f8_wide_kernel<TY>, dim3((unsigned)grid), kWideThreads, kWideSmem, flags, stream, a);
+}
+
+template <int BN, typename TY>
+cudaError_t launch_narrow(F8Args& a, int pieces, unsigned flags, cudaStream_t stream) {
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = layer_smem(f8_narrow_kernel<BN, TY>, Narrow<BN>::kSmem, ready);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)pieces, (unsigned)a.tiles_a, (unsigned)((a.M + BN - 1) / BN));
+    cfg.blockDim = dim3(kNarrowThreads);
+    cfg.dynamicSmemBytes = Narrow<BN>::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)pieces, 1, 1};
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = flags & 1u ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, f8_narrow_kernel<BN, TY>, a);
+}
+
+template <typename TY>
+cudaError_t launch_gemm(const uint8_t* Xf, const float* sa, int64_t M, int64_t K, const uint8_t* Wf, const float* sw,
+                        int64_t N, void* Y, int sms, unsigned flags, cudaStream_t stream) {
+    F8Args a = {};
+    a.sa = sa;
+    a.sw = sw;
+    a.Y = Y;
+    a.N = N;
+    a.M = (int)M;
+    a.kbs = (int)((K + kF8Block - 1) / kF8Block);
+    const int64_t wide = (M + kRows - 1) / kRows * ((N + kWideCols - 1) / kWideCols);
+    // narrow tiles take half as long: wide from two thirds of the SMs on
+    const int64_t n_tiles = (N + kRows - 1) / kRows;
+    if ((M > 128 && 3 * wide >= 2 * sms) || n_tiles > 65535) {
+        a.tiles_a = (int)((M + kRows - 1) / kRows);
+        a.tiles = (int)wide;
+        if (!code_map(&a.tm_a, Xf, M, K, kRows) || !code_map(&a.tm_b, Wf, N, K, kWideCols)) return cudaErrorNotSupported;
+        return launch_wide<TY>(a, sms, flags, stream);
+    }
+    const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    a.tiles_a = (int)n_tiles;
+    const int64_t ctas = n_tiles * ((M + bn - 1) / bn);
+    const int64_t slots = (bn <= 64 ? 2 : 1) * (int64_t)sms;
+    int pieces = 1;
+    // pieces of at least 4 blocks, as many as leave one wave
+    while (pieces < kNarrowCluster && (pieces + 1) * ctas <= slots && a.kbs / (pieces + 1) >= 4) ++pieces;
+    if (!code_map(&a.tm_a, Wf, N, K, kRows) || !code_map(&a.tm_b, Xf, M, K, bn)) return cudaErrorNotSupported;
+    switch (bn) {
+        case 16: return launch_narrow<16, TY>(a, pieces, flags, stream);
+        case 32: return launch_narrow<32, TY>(a, pieces, flags, stream);
+        case 64: return launch_narrow<64, TY>(a, pieces, flags, stream);
+        default: return launch_narrow<128, TY>(a, pieces, flags, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_f8_gemm(const uint8_t* Xf, const float* sa, int64_t M, int64_t K, const uint8_t* Wf, const float* sw,
+                           int64_t N, void* Y, int y_f16, int sms, unsigned flags, cudaStream_t stream) {
+    return y_f16 ? launch_gemm<__half>(Xf, sa, M, K, Wf, sw, N, Y, sms, flags, stream)
+                 : launch_gemm<float>(Xf, sa, M, K, Wf, sw, N, Y, sms, flags, stream);
+}
+
+cudaError_t read_and_clear_f8_error(unsigned* flags, cudaStream_t stream) {
+    unsigned v = 0, z = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_f8_error, sizeof(v), 0, cudaMemcpyDeviceToHost, stream);
+    if (e != cudaSuccess) return e;
+    e = cudaMemcpyToSymbolAsync(g_f8_error, &z, sizeof(z), 0, cudaMemcpyHostToDevice, stream);
+    if (e != cudaSuccess) return e;
+    e = cudaStreamSynchronize(stream);
+    *flags |= v;
+    return e;
+}
+
+}  // namespace w4a8

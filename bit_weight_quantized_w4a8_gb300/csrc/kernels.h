@@ -145,13 +145,13 @@ cudaError_t launch_draft_verify(const void* L, int l_f16, int64_t ld_l, int64_t 
                                 int32_t* count, void* ws, int sms, unsigned flags, cudaStream_t stream);
 cudaError_t read_and_clear_verify_error(unsigned* flags, cudaStream_t stream);
 
-// The linear with e4m3 blocks of 128 (f8.cu).
+// The linear with e4m3 blocks of 128: quantizers (f8.cu), product (f8_mma.cu).
 cudaError_t launch_f8_quantize_weights(const float* W, int64_t N, int64_t K, uint8_t* Wf, float* sw,
                                        cudaStream_t stream);
 cudaError_t launch_f8_quantize_rows(const void* X, int x_f16, int64_t M, int64_t K, uint8_t* Xf, float* sa,
                                     unsigned flags, cudaStream_t stream);
-size_t f8_gemm_workspace(int64_t M, int64_t K, int64_t N, int sms);
 cudaError_t launch_f8_gemm(const uint8_t* Xf, const float* sa, int64_t M, int64_t K, const uint8_t* Wf, const float* sw,
-                           int64_t N, void* Y, int y_f16, void* ws, int sms, unsigned flags, cudaStream_t stream);
+                           int64_t N, void* Y, int y_f16, int sms, unsigned flags, cudaStream_t stream);
+cudaError_t read_and_clear_f8_error(unsigned* flags, cudaStream_t stream);
 
 }  // namespace w4a8

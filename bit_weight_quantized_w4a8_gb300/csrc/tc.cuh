@@ -79,6 +79,17 @@ __device__ __forceinline__ void tc_mma_e4m3_tmem_a(uint32_t d_tmem, uint32_t a_t
         : "memory");
 }
 
+// Both in shared memory (128-byte rows of K, sw128_desc).
+__device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
 // Warp-collective store of 32 consecutive 32-bit columns into this warp's
 // 32 TMEM lanes (thread t writes lane base + t), then wait for it.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {

@@ -773,15 +773,15 @@ int f8_quantize_rows(const void* X, int x_type, int64_t M, int64_t K, uint8_t* X
  * products and sums of a block in fp32 on the tensor cores, the blocks' sums scaled and added in
  * fp32 in order (of pieces of K, then the pieces in order), one rounding to y_type.
  * The same call gives the same bits.
- *   Y [M][N] y_type out; ws, ws_bytes: f8_gemm_workspace_bytes, 256-byte aligned
- *   (need not be zeroed; one call at a time).
- * Requires the limits above; Xf and Wf 16-byte aligned, the others to their element. */
-size_t f8_gemm_workspace_bytes(int64_t M, int64_t K, int64_t N);
+ *   Y [M][N] y_type out.
+ * Requires the limits above and M * N <= 2^43; Xf and Wf 16-byte aligned, the others to their element.
+ * Waits are bounded; one that runs out sets bit 0 of the device error word. */
 int f8_gemm(const uint8_t* Xf, const float* sa, int64_t M, int64_t K, const uint8_t* Wf, const float* sw, int64_t N,
-            void* Y, int y_type, void* ws, size_t ws_bytes, unsigned flags, void* stream);
+            void* Y, int y_type, unsigned flags, void* stream);
 
 /* f8_quantize_rows and f8_gemm in one call, the codes in the workspace
- * (f8_linear_workspace_bytes): the same Y. */
+ * (f8_linear_workspace_bytes, 256-byte aligned, need not be zeroed, one call at a
+ * time): the same Y. */
 size_t f8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N);
 int f8_linear(const void* X, int x_type, int64_t M, int64_t K, const uint8_t* Wf, const float* sw, int64_t N, void* Y,
               int y_type, void* ws, size_t ws_bytes, unsigned flags, void* stream);
