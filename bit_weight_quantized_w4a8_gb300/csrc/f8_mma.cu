@@ -11,8 +11,9 @@
 // while a tile is written.
 //
 // Two kernels:
-//  wide    128 rows of X x 256 of W a CTA: a thread has one row of X and 128
-//          columns, so one scale a block.  For many rows.
+//  wide    256 rows of X x 256 of W by a pair of CTAs, 128 rows of X and half of W's in the
+//          shared memory of each: a thread has one row of X and 128 columns, so one
+//          scale a block.  For many rows.
 //  narrow  128 rows of W x 16 .. 128 of X: the weights fill the tensor core's 128 rows
 //          whatever the batch, K is cut over a cluster whose sums are joined through
 //          distributed shared memory in the order of the pieces.  For few rows.
@@ -113,11 +114,21 @@ __device__ __forceinline__ float2 halves_of(uint64_t c) {
 }
 
 // What a CTA's warps share besides the operands.
-template <int S>
+template <int S, int D>
 struct Bars {
-    uint64_t full[S], empty[S], d_full[2], d_empty[2];
+    uint64_t full[S], empty[S], d_full[D], d_empty[D];
     uint32_t tmem;
     int abort;
+};
+
+// A place in a ring of N and the parity of the pass over it.
+template <int N>
+struct Ring {
+    int at = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == N) at = 0, phase ^= 1;
+    }
 };
 
 // One block of K: four MMAs of 32 bytes.
@@ -132,28 +143,49 @@ __device__ __forceinline__ void issue_block(uint32_t d, uint32_t a, uint32_t b, 
 // ---------------------------------------------------------------------------
 
 constexpr int kWideCols = 256;
-constexpr int kWideStages = 4;
+constexpr int kWideBufs = 2;  // of 256 columns in TMEM
+constexpr int kWideStages = 5;
 constexpr int kWideWarps = 8;  // consumers: warp w has lanes 32 (w % 4) .., columns 128 (w / 4) ..
+constexpr int kWarpCols = kWideCols / 2;
 constexpr int kWideThreads = kProducerThreads + 32 * kWideWarps;
-constexpr int kWideStage = kABytes + kWideCols * kKBytes;
-constexpr int kWideOut = 32 * 128;  // a warp's outputs on their way: 32 rows of 128 bytes
-constexpr int kWideSmem = kWideStages * kWideStage + kWideWarps * kWideOut + 1024;
+constexpr int kWideStage = kABytes + kWideCols / 2 * kKBytes;  // of one CTA
+constexpr int kWideOut = 32 * 64;  // a warp's outputs on their way: 32 rows of 16 columns
+constexpr int kWideAhead = 4;      // blocks whose scales of X a warp has or has asked for
+constexpr int kWideSa = kWideAhead * 32 * 4;
+constexpr int kWideSmem = kWideStages * kWideStage + kWideWarps * (kWideOut + kWideSa) + 1024;
+static_assert(kWideBufs * kWideCols <= 512 && kWideStage % 1024 == 0, "TMEM columns, operands on 1024 bytes");
 
-// 32 rows of 128 bytes in a warp's buffer, 16-byte chunk c of row r at c ^ (r % 8).
+// A warp's buffer of 32 rows of 16 outputs in 16-byte chunks, swapped about so that
+// 8 lanes with 8 rows, or with all chunks of a few, meet all banks.
+template <typename TY>
 __device__ __forceinline__ uint4* out_chunk(uint8_t* buf, int r, int c) {
-    return reinterpret_cast<uint4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
+    constexpr int CH = sizeof(TY);  // chunks a row
+    return reinterpret_cast<uint4*>(buf + (r * CH + (c ^ (r / (8 / CH) & (CH - 1)))) * 16);
 }
 
-// The warp's rows m0 + 0..31, columns n0 + 0.. of 128 / sizeof(TY), from the buffer.
+// The warp's rows m0 + 0..31, columns n0 + 0..15, through the buffer.
 template <typename TY>
-__device__ __forceinline__ void store_rows(uint8_t* buf, TY* Y, int m0, int M, int64_t n0, int64_t N, bool vec) {
-    constexpr int PER = 16 / sizeof(TY);
-    const int lane = threadIdx.x % 32, c = lane % 8;
+__device__ __forceinline__ void store_cols16(uint8_t* buf, const float* x, TY* Y, int m0, int M, int64_t n0, int64_t N,
+                                             bool vec) {
+    constexpr int CH = sizeof(TY), PER = 16 / sizeof(TY);
+    const int lane = threadIdx.x % 32;
+    #pragma unroll
+    for (int u = 0; u < CH; ++u) {
+        if constexpr (sizeof(TY) == 4) {
+            *out_chunk<TY>(buf, lane, u) = make_uint4(__float_as_uint(x[4 * u]), __float_as_uint(x[4 * u + 1]),
+                                                      __float_as_uint(x[4 * u + 2]), __float_as_uint(x[4 * u + 3]));
+        } else {
+            *out_chunk<TY>(buf, lane, u) = make_uint4(pack_half2(x[8 * u], x[8 * u + 1]), pack_half2(x[8 * u + 2], x[8 * u + 3]),
+                                                      pack_half2(x[8 * u + 4], x[8 * u + 5]), pack_half2(x[8 * u + 6], x[8 * u + 7]));
+        }
+    }
+    __syncwarp();
+    const int c = lane % CH;
     const int64_t n = n0 + c * PER;
     #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + lane / 8;
-        const uint4 v = *out_chunk(buf, r, c);
+    for (int i = 0; i < CH; ++i) {
+        const int r = 32 / CH * i + lane / CH;
+        const uint4 v = *out_chunk<TY>(buf, r, c);
         if (m0 + r >= M || n >= N) continue;
         TY* y = Y + (int64_t)(m0 + r) * N + n;
         if (vec && n + PER <= N) {
@@ -165,12 +197,17 @@ __device__ __forceinline__ void store_rows(uint8_t* buf, TY* Y, int m0, int M, i
                 if (n + k < N) y[k] = e[k];
         }
     }
+    __syncwarp();
 }
 
 template <typename TY>
 __global__ void __launch_bounds__(kWideThreads, 1) f8_wide_kernel(const __grid_constant__ F8Args a) {
+    // of the pair's barriers, full and d_empty count in the even CTA, which issues
+    // the MMAs; empty and d_full are told to both
     extern __shared__ uint8_t smem_raw[];
-    __shared__ Bars<kWideStages> sh;
+    __shared__ Bars<kWideStages, kWideBufs> sh;
+    cg::cluster_group cl = cg::this_cluster();
+    const int rank = (int)cl.block_rank();
     uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -179,139 +216,161 @@ __global__ void __launch_bounds__(kWideThreads, 1) f8_wide_kernel(const __grid_c
             mbar_init(smem_u32(&sh.full[i]), 1);
             mbar_init(smem_u32(&sh.empty[i]), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kWideBufs; ++i) {
             mbar_init(smem_u32(&sh.d_full[i]), 1);
-            mbar_init(smem_u32(&sh.d_empty[i]), kWideWarps);
+            mbar_init(smem_u32(&sh.d_empty[i]), 2 * kWideWarps);
         }
         sh.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), 512);
+    if (warp == 1) tmem_alloc_pair(smem_u32(&sh.tmem), 512);
     tc_fence_before_sync();
-    __syncthreads();
+    cl.sync();
     tc_fence_after_sync();
     griddep_launch_dependents();
     griddep_wait();
     const uint32_t tmem = sh.tmem;
-    const int mine = a.tiles > (int)blockIdx.x ? (a.tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
-    const int steps = mine * a.kbs;  // blocks of all tiles
+    const int first = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const int steps = ((a.tiles - 1 - first) / pairs + 1) * a.kbs;  // blocks of all tiles
     int issued = 0;
 
     if (warp == 0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (lane == 0) {
-            const uint64_t keep = l2_evict_last_policy();
-            int kb = 0, tile = blockIdx.x;
-            for (int i = 0; i < steps; ++i) {
-                const int s = i % kWideStages;
-                if (i >= kWideStages && !wait_bounded(smem_u32(&sh.empty[s]), (i / kWideStages - 1) & 1, &sh.abort)) break;
-                const uint32_t at = sbase + s * kWideStage, bar = smem_u32(&sh.full[s]);
-                mbar_arrive_expect_tx(bar, kWideStage);
-                tma_load_2d_hint(at, &a.tm_a, kb * kKBytes, tile % a.tiles_a * kRows, bar, keep);
-                tma_load_2d_hint(at + kABytes, &a.tm_b, kb * kKBytes, tile / a.tiles_a * kWideCols, bar, keep);
-                issued = i + 1;
-                if (++kb == a.kbs) kb = 0, tile += gridDim.x;
+        // (whole warps go along in both loops, so that descriptors and addresses are
+        // uniform: one lane on its own took 100 cycles for each MMA or copy)
+        const uint64_t keep = l2_evict_last_policy();
+        const uint32_t full0 = cluster_addr(smem_u32(&sh.full[0]), 0);
+        int kb = 0, tile = first;
+        Ring<kWideStages> st;
+        for (int i = 0; i < steps; ++i, st.next()) {
+            if (i >= kWideStages &&
+                !__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.empty[st.at]), st.phase ^ 1, &sh.abort)))
+                break;
+            if (elect_one()) {
+                const uint32_t at = sbase + st.at * kWideStage, bar = full0 + 8 * st.at;
+                if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh.full[st.at]), 2 * kWideStage);
+                tma_load_2d_pair(at, &a.tm_a, kb * kKBytes, (tile % a.tiles_a * 2 + rank) * kRows, bar, keep);
+                tma_load_2d_pair(at + kABytes, &a.tm_b, kb * kKBytes, (tile / a.tiles_a * 2 + rank) * (kWideCols / 2), bar, keep);
             }
-            for (int i = max(0, issued - kWideStages); i < issued; ++i)
+            issued = i + 1;
+            if (++kb == a.kbs) kb = 0, tile += pairs;
+        }
+        // nothing may come to this CTA after it has gone: copies (all have landed when
+        // their stage is told to be empty; both CTAs' count in the even one) and what is told to it
+        for (int i = max(0, issued - kWideStages); lane == 0 && i < issued; ++i) {
+            if (!*(volatile int*)&sh.abort)
+                drain(smem_u32(&sh.empty[i % kWideStages]), (i / kWideStages) & 1);
+            else if (rank == 0)
                 drain(smem_u32(&sh.full[i % kWideStages]), (i / kWideStages) & 1);
         }
+        __syncwarp();
     } else if (warp == 1) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (lane == 0) {
-            const uint32_t idesc = e4m3_idesc(kRows, kWideCols);
-            for (int i = 0; i < steps; ++i) {
-                const int s = i % kWideStages, b = i & 1;
-                if (i >= 2 && !wait_bounded(smem_u32(&sh.d_empty[b]), (i / 2 - 1) & 1, &sh.abort)) break;
-                if (!wait_bounded(smem_u32(&sh.full[s]), (i / kWideStages) & 1, &sh.abort)) break;
+        if (rank == 0) {
+            const uint32_t idesc = e4m3_idesc(2 * kRows, kWideCols);
+            Ring<kWideStages> st;
+            Ring<kWideBufs> d;
+            for (int i = 0; i < steps; ++i, st.next(), d.next()) {
+                if (i >= kWideBufs &&
+                    !__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.d_empty[d.at]), d.phase ^ 1, &sh.abort)))
+                    break;
+                if (!__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.full[st.at]), st.phase, &sh.abort))) break;
                 tc_fence_after_sync();
-                const uint32_t at = sbase + s * kWideStage;
-                issue_block(tmem + kWideCols * b, at, at + kABytes, idesc);
-                tc_commit(smem_u32(&sh.empty[s]));
-                tc_commit(smem_u32(&sh.d_full[b]));
+                if (elect_one()) {
+                    const uint32_t at = sbase + st.at * kWideStage;
+                    const uint64_t ad = sw128_desc(at), bd = sw128_desc(at + kABytes);
+                    #pragma unroll
+                    for (int k = 0; k < kKBytes / 32; ++k)
+                        tc_mma_e4m3_pair(tmem + kWideCols * d.at, ad + 2 * k, bd + 2 * k, idesc, k > 0);
+                    tc_commit_pair(smem_u32(&sh.d_full[d.at]));
+                    tc_commit_pair(smem_u32(&sh.empty[st.at]));
+                }
                 issued = i + 1;
             }
             // every MMA is done before TMEM is given back
-            if (issued > 0) drain(smem_u32(&sh.d_full[(issued - 1) & 1]), ((issued - 1) / 2) & 1);
+            if (issued > 0 && lane == 0)
+                drain(smem_u32(&sh.d_full[(issued - 1) % kWideBufs]), ((issued - 1) / kWideBufs) & 1);
+            __syncwarp();
         }
     } else if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int cw = warp - 4, q = warp % 4, g = cw / 4;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + 128 * g;
         uint8_t* buf = smem + kWideStages * kWideStage + cw * kWideOut;
         const bool vec = a.N % (16 / sizeof(TY)) == 0 && reinterpret_cast<uintptr_t>(a.Y) % 16 == 0;
         const int64_t nbs = (a.N + kF8Block - 1) / kF8Block;
+        const uint32_t d_empty = cluster_addr(smem_u32(&sh.d_empty[0]), 0);
+        // The row's scales come by asynchronous copies, each lane's for itself, those of W
+        // 32 blocks at a time, one a lane: loads into registers that far ahead all had to be
+        // waited for with the nearest one.
+        float* sa_ring = reinterpret_cast<float*>(smem + kWideStages * kWideStage + kWideWarps * kWideOut + cw * kWideSa) + lane;
+        const float* ask_at = nullptr;
+        int ask_tile = first, ask_left = 0, ask_i = 0;
+        auto ask = [&]() {
+            if (ask_left == 0 && ask_tile < a.tiles) {
+                ask_at = a.sa + min((ask_tile % a.tiles_a * 2 + rank) * kRows + 32 * q + lane, a.M - 1);
+                ask_left = a.kbs;
+                ask_tile += pairs;
+            }
+            if (ask_left > 0) {
+                cp_async_4(smem_u32(sa_ring + (ask_i & (kWideAhead - 1)) * 32), ask_at);
+                ask_at += a.M;
+                --ask_left;
+            }
+            cp_async_commit();
+            ++ask_i;
+        };
+        for (int k = 0; k < kWideAhead - 1; ++k) ask();
         int i = 0;
         bool ok = true;
-        for (int tile = blockIdx.x; ok && tile < a.tiles; tile += gridDim.x) {
-            const int m0 = tile % a.tiles_a * kRows + 32 * q;
-            const int64_t nb = min((int64_t)(tile / a.tiles_a) * 2 + g, nbs - 1);
-            const float* sa = a.sa + min(m0 + lane, a.M - 1);
-            const float* sw = a.sw + nb * a.kbs;
-            uint64_t acc[64];
+        Ring<kWideBufs> d;
+        for (int tile = first; ok && tile < a.tiles; tile += pairs) {
+            const int m0 = (tile % a.tiles_a * 2 + rank) * kRows + 32 * q;
+            const int64_t n0 = (int64_t)(tile / a.tiles_a) * kWideCols + kWarpCols * g;
+            const float* sw = a.sw + min(n0 / kF8Block, nbs - 1) * a.kbs;
+            float acc[kWarpCols];
             #pragma unroll
-            for (int j = 0; j < 64; ++j) acc[j] = 0;
-            float sa_next = *sa, sw_next = *sw;
-            for (int kb = 0; kb < a.kbs; ++kb, ++i) {
-                const float s = sa_next * sw_next;
-                const uint64_t s2 = pair_of(s, s);
-                if (kb + 1 < a.kbs) {
-                    sa_next = sa[(int64_t)(kb + 1) * a.M];
-                    sw_next = sw[kb + 1];
-                }
-                const int b = i & 1;
-                ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.d_full[b]), (i / 2) & 1, &sh.abort));
+            for (int j = 0; j < kWarpCols; ++j) acc[j] = 0.f;
+            float sw32 = 0.f;
+            for (int kb = 0; kb < a.kbs; ++kb, ++i, d.next()) {
+                // (the scales belong in front of the wait: behind the loads from TMEM they
+                // cost 10%, on the way from a block's sums to the release of their columns)
+                if (kb % 32 == 0) sw32 = sw[min(kb + lane, a.kbs - 1)];
+                cp_async_wait<kWideAhead - 2>();
+                const float s = sa_ring[(i & (kWideAhead - 1)) * 32] * __shfl_sync(0xFFFFFFFFu, sw32, kb % 32);
+                ask();
+                ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.d_full[d.at]), d.phase, &sh.abort));
                 if (!ok) break;
                 tc_fence_after_sync();
+                const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + kWideCols * d.at + kWarpCols * g;
                 uint32_t v[2][32];
-                tmem_ld32(lanes + kWideCols * b, v[0]);
-                tmem_ld32_wait(v[0]);
+                tmem_ld32(lanes, v[0]);
                 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (c < 3) tmem_ld32(lanes + kWideCols * b + 32 * (c + 1), v[(c + 1) & 1]);
-                    #pragma unroll
-                    for (int j = 0; j < 16; ++j) fma2(acc[16 * c + j], v[c & 1][2 * j], v[c & 1][2 * j + 1], s2);
-                    if (c < 3) tmem_ld32_wait(v[(c + 1) & 1]);
-                    if (c == 2) {  // all of it is in registers
+                for (int c = 0; c < kWarpCols / 32; ++c) {
+                    tmem_ld32_wait(v[c & 1]);
+                    if (c + 1 < kWarpCols / 32) {
+                        tmem_ld32(lanes + 32 * (c + 1), v[(c + 1) & 1]);
+                    } else {  // all of it is in registers
                         tc_fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&sh.d_empty[b]));
+                        if (lane == 0) mbar_arrive_cluster(d_empty + 8 * d.at);
                     }
+                    #pragma unroll
+                    for (int j = 0; j < 32; ++j) acc[32 * c + j] = fmaf(__uint_as_float(v[c & 1][j]), s, acc[32 * c + j]);
                 }
             }
             if (!ok) break;
-            constexpr int PER = 128 / sizeof(TY);  // columns of a trip through the buffer
             #pragma unroll
-            for (int c = 0; c < 128 / PER; ++c) {
-                #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    uint4 w;
-                    if constexpr (sizeof(TY) == 4) {
-                        const float2 x = halves_of(acc[PER / 2 * c + 2 * u]), y = halves_of(acc[PER / 2 * c + 2 * u + 1]);
-                        w = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
-                    } else {
-                        uint32_t h[4];
-                        #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 x = halves_of(acc[PER / 2 * c + 4 * u + k]);
-                            h[k] = pack_half2(x.x, x.y);
-                        }
-                        w = make_uint4(h[0], h[1], h[2], h[3]);
-                    }
-                    *out_chunk(buf, lane, u) = w;
-                }
-                __syncwarp();
-                store_rows(buf, static_cast<TY*>(a.Y), m0, a.M, (int64_t)(tile / a.tiles_a) * kWideCols + 128 * g + c * PER, a.N, vec);
-                __syncwarp();
-            }
+            for (int c = 0; c < kWarpCols / 16; ++c)
+                store_cols16(buf, acc + 16 * c, static_cast<TY*>(a.Y), m0, a.M, n0 + 16 * c, a.N, vec);
         }
     }
     tc_fence_before_sync();
-    __syncthreads();
+    cl.sync();  // neither CTA's shared memory or barriers are needed any more
     if (warp == 1) {
         tc_fence_after_sync();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc_pair(tmem, 512);
     }
 }
 
@@ -336,7 +395,7 @@ template <int BN, typename TY>
 __global__ void __launch_bounds__(kNarrowThreads, Narrow<BN>::kCtas) f8_narrow_kernel(const __grid_constant__ F8Args a) {
     using C = Narrow<BN>;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ Bars<C::kStages> sh;
+    __shared__ Bars<C::kStages, 2> sh;
     __shared__ __align__(16) float scale[2][BN];
     cg::cluster_group cl = cg::this_cluster();
     uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
@@ -518,13 +577,31 @@ bool code_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, i
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <typename F>
+cudaError_t cluster_launch(F* f, dim3 grid, int cluster, int threads, int smem, unsigned flags, cudaStream_t stream,
+                           const F8Args& a) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)cluster, 1, 1};
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = flags & 1u ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, f, a);
+}
+
 template <typename TY>
 cudaError_t launch_wide(F8Args& a, int sms, unsigned flags, cudaStream_t stream) {
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = layer_smem(f8_wide_kernel<TY>, kWideSmem, ready);
     if (e != cudaSuccess) return e;
-    const int grid = a.tiles < sms ? a.tiles : sms;
-    return layer_launch(f8_wide_kernel<TY>, dim3((unsigned)grid), kWideThreads, kWideSmem, flags, stream, a);
+    const int pairs = a.tiles < sms / 2 ? a.tiles : sms / 2;
+    return cluster_launch(f8_wide_kernel<TY>, dim3((unsigned)(2 * pairs)), 2, kWideThreads, kWideSmem, flags, stream, a);
 }
 
 template <int BN, typename TY>
@@ -532,19 +609,8 @@ cudaError_t launch_narrow(F8Args& a, int pieces, unsigned flags, cudaStream_t st
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = layer_smem(f8_narrow_kernel<BN, TY>, Narrow<BN>::kSmem, ready);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)pieces, (unsigned)a.tiles_a, (unsigned)((a.M + BN - 1) / BN));
-    cfg.blockDim = dim3(kNarrowThreads);
-    cfg.dynamicSmemBytes = Narrow<BN>::kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {(unsigned)pieces, 1, 1};
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = flags & 1u ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, f8_narrow_kernel<BN, TY>, a);
+    const dim3 grid((unsigned)pieces, (unsigned)a.tiles_a, (unsigned)((a.M + BN - 1) / BN));
+    return cluster_launch(f8_narrow_kernel<BN, TY>, grid, pieces, kNarrowThreads, Narrow<BN>::kSmem, flags, stream, a);
 }
 
 template <typename TY>
@@ -557,13 +623,12 @@ cudaError_t launch_gemm(const uint8_t* Xf, const float* sa, int64_t M, int64_t K
     a.N = N;
     a.M = (int)M;
     a.kbs = (int)((K + kF8Block - 1) / kF8Block);
-    const int64_t wide = (M + kRows - 1) / kRows * ((N + kWideCols - 1) / kWideCols);
-    // narrow tiles take half as long: wide from two thirds of the SMs on
+    const int64_t m_tiles = (M + 2 * kRows - 1) / (2 * kRows), wide = m_tiles * ((N + kWideCols - 1) / kWideCols);
     const int64_t n_tiles = (N + kRows - 1) / kRows;
-    if ((M > 128 && 3 * wide >= 2 * sms) || n_tiles > 65535) {
-        a.tiles_a = (int)((M + kRows - 1) / kRows);
+    if ((M > 128 && 3 * wide >= sms) || n_tiles > 65535) {
+        a.tiles_a = (int)m_tiles;
         a.tiles = (int)wide;
-        if (!code_map(&a.tm_a, Xf, M, K, kRows) || !code_map(&a.tm_b, Wf, N, K, kWideCols)) return cudaErrorNotSupported;
+        if (!code_map(&a.tm_a, Xf, M, K, kRows) || !code_map(&a.tm_b, Wf, N, K, kWideCols / 2)) return cudaErrorNotSupported;
         return launch_wide<TY>(a, sms, flags, stream);
     }
     const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
