@@ -98,21 +98,6 @@ __device__ __forceinline__ void tmem_ld16_wait(uint32_t (&v)[16]) {
                  :
                  : "memory");
 }
-// Two fp32 multiply-adds in one instruction.
-__device__ __forceinline__ void fma2(uint64_t& c, uint32_t a0, uint32_t a1, uint64_t s2) {
-    asm("{\n\t.reg .b64 a;\n\tmov.b64 a, {%1, %2};\n\tfma.rn.f32x2 %0, a, %3, %0;\n\t}" : "+l"(c) : "r"(a0), "r"(a1), "l"(s2));
-}
-__device__ __forceinline__ uint64_t pair_of(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 halves_of(uint64_t c) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(c));
-    return r;
-}
-
 // What a CTA's warps share besides the operands.
 template <int S, int D>
 struct Bars {
@@ -380,12 +365,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) f8_wide_kernel(const __grid_c
 
 constexpr int kNarrowThreads = kProducerThreads + 128;
 constexpr int kNarrowCluster = 8;  // pieces of K, at most
+constexpr int kNarrowAhead = 8;    // blocks whose scales have been asked for
 
 template <int BN>
 struct Narrow {
     static constexpr int kStage = kABytes + BN * kKBytes;
     static constexpr int kCtas = BN <= 64 ? 2 : 1;  // per SM
-    static constexpr int kStages = BN <= 64 ? (110 * 1024) / kStage : 6;
+    static constexpr int kStages = BN <= 64 ? (107 * 1024) / kStage : 6;
     static constexpr int kCols = BN < 32 ? 32 : 2 * BN;  // TMEM
     static constexpr int kSmem = kStages * kStage + 1024;
     static_assert(kStages * kStage >= BN * kRows * 4, "the sums have to fit");
@@ -397,6 +383,7 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<BN>::kCtas) f8_narrow_k
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars<C::kStages, 2> sh;
     __shared__ __align__(16) float scale[2][BN];
+    __shared__ float2 scale_ring[kNarrowAhead][BN];  // of X's rows and of W on their way
     cg::cluster_group cl = cg::this_cluster();
     uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     const uint32_t sbase = smem_u32(smem);
@@ -426,101 +413,135 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<BN>::kCtas) f8_narrow_k
     int issued = 0;
 
     if (warp == 0) {
-        if (lane == 0) {
-            const uint64_t once = l2_evict_first_policy(), keep = l2_evict_last_policy();
-            auto load_w = [&](int i) {
-                const uint32_t bar = smem_u32(&sh.full[i % C::kStages]);
-                mbar_arrive_expect_tx(bar, C::kStage);
-                tma_load_2d_hint(sbase + i % C::kStages * C::kStage, &a.tm_a, (kb0 + i) * kKBytes, (int)n0, bar, once);
-            };
-            auto load_x = [&](int i) {
-                tma_load_2d_hint(sbase + i % C::kStages * C::kStage + kABytes, &a.tm_b, (kb0 + i) * kKBytes, m0,
-                                 smem_u32(&sh.full[i % C::kStages]), keep);
-            };
-            // the weights do not come from the kernel before
-            const int ahead = min(steps, C::kStages);
-            for (int i = 0; i < ahead; ++i) load_w(i);
-            griddep_wait();
-            for (int i = 0; i < ahead; ++i) load_x(i);
-            issued = ahead;
-            for (int i = ahead; i < steps; ++i) {
-                if (!wait_bounded(smem_u32(&sh.empty[i % C::kStages]), (i / C::kStages - 1) & 1, &sh.abort)) break;
-                load_w(i);
-                load_x(i);
-                issued = i + 1;
-            }
-            for (int i = max(0, issued - C::kStages); i < issued; ++i)
-                drain(smem_u32(&sh.full[i % C::kStages]), (i / C::kStages) & 1);
+        const uint64_t once = l2_evict_first_policy(), keep = l2_evict_last_policy();
+        auto load_w = [&](int i, int s) {
+            if (!elect_one()) return;
+            mbar_arrive_expect_tx(smem_u32(&sh.full[s]), C::kStage);
+            tma_load_2d_hint(sbase + s * C::kStage, &a.tm_a, (kb0 + i) * kKBytes, (int)n0, smem_u32(&sh.full[s]), once);
+        };
+        auto load_x = [&](int i, int s) {
+            if (elect_one())
+                tma_load_2d_hint(sbase + s * C::kStage + kABytes, &a.tm_b, (kb0 + i) * kKBytes, m0, smem_u32(&sh.full[s]), keep);
+        };
+        // the weights do not come from the kernel before
+        const int ahead = min(steps, C::kStages);
+        for (int i = 0; i < ahead; ++i) load_w(i, i);
+        griddep_wait();
+        for (int i = 0; i < ahead; ++i) load_x(i, i);
+        issued = ahead;
+        int s = 0;
+        uint32_t phase = 0;
+        for (int i = ahead; i < steps; ++i) {
+            if (!__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.empty[s]), phase, &sh.abort))) break;
+            load_w(i, s);
+            load_x(i, s);
+            issued = i + 1;
+            if (++s == C::kStages) s = 0, phase ^= 1;
         }
+        for (int i = max(0, issued - C::kStages); lane == 0 && i < issued; ++i)
+            drain(smem_u32(&sh.full[i % C::kStages]), (i / C::kStages) & 1);
+        __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = e4m3_idesc(kRows, BN);
-            for (int i = 0; i < steps; ++i) {
-                const int s = i % C::kStages, b = i & 1;
-                if (i >= 2 && !wait_bounded(smem_u32(&sh.d_empty[b]), (i / 2 - 1) & 1, &sh.abort)) break;
-                if (!wait_bounded(smem_u32(&sh.full[s]), (i / C::kStages) & 1, &sh.abort)) break;
-                tc_fence_after_sync();
+        const uint32_t idesc = e4m3_idesc(kRows, BN);
+        int s = 0;
+        uint32_t phase = 0;
+        Ring<2> d;
+        for (int i = 0; i < steps; ++i, d.next()) {
+            if (i >= 2 && !__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.d_empty[d.at]), d.phase ^ 1, &sh.abort))) break;
+            if (!__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.full[s]), phase, &sh.abort))) break;
+            tc_fence_after_sync();
+            if (elect_one()) {
                 const uint32_t at = sbase + s * C::kStage;
-                issue_block(tmem + BN * b, at, at + kABytes, idesc);
+                issue_block(tmem + BN * d.at, at, at + kABytes, idesc);
+                tc_commit(smem_u32(&sh.d_full[d.at]));
                 tc_commit(smem_u32(&sh.empty[s]));
-                tc_commit(smem_u32(&sh.d_full[b]));
-                issued = i + 1;
             }
-            if (issued > 0) drain(smem_u32(&sh.d_full[(issued - 1) & 1]), ((issued - 1) / 2) & 1);
+            issued = i + 1;
+            if (++s == C::kStages) s = 0, phase ^= 1;
         }
+        if (issued > 0 && lane == 0) drain(smem_u32(&sh.d_full[(issued - 1) & 1]), ((issued - 1) / 2) & 1);
+        __syncwarp();
     } else if (warp >= 4) {
         griddep_wait();
         const int q = warp % 4, t = tid - kProducerThreads;  // t: the thread's column for scales, its lane for sums
         const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
+        // Scales by asynchronous copies, each thread's of its column for itself, several
+        // blocks ahead: loads into registers stalled every block for their latency.
         const float* sa = a.sa + (int64_t)kb0 * a.M + min(m0 + t, a.M - 1);
         const float* sw = a.sw + blockIdx.y * (int64_t)a.kbs + kb0;
-        auto scale_at = [&](int i) { return i < steps && t < BN ? sa[(int64_t)i * a.M] * sw[i] : 0.f; };
-        uint64_t acc[BN / 2];
+        auto ask = [&](int i) {
+            if (i < steps && t < BN) {
+                const uint32_t at = smem_u32(&scale_ring[i % kNarrowAhead][t]);
+                cp_async_4(at, sa + (int64_t)i * a.M);
+                cp_async_4(at + 4, sw + i);
+            }
+            cp_async_commit();
+        };
+        for (int i = 0; i < kNarrowAhead - 1; ++i) ask(i);
+        float acc[BN];
         #pragma unroll
-        for (int j = 0; j < BN / 2; ++j) acc[j] = 0;
-        float s1 = scale_at(0), s2 = scale_at(1);
+        for (int j = 0; j < BN; ++j) acc[j] = 0.f;
         bool ok = true;
-        for (int i = 0; i < steps; ++i) {
-            if (t < BN) scale[i & 1][t] = s1;
-            s1 = s2;
-            s2 = scale_at(i + 2);
+        Ring<2> d;
+        for (int i = 0; i < steps; ++i, d.next()) {
+            cp_async_wait<kNarrowAhead - 2>();
+            if (t < BN) {
+                const float2 s = scale_ring[i % kNarrowAhead][t];
+                scale[d.at][t] = s.x * s.y;
+            }
+            ask(i + kNarrowAhead - 1);
             named_bar_sync(1, 128);  // also: the block before the last has been read by all
-            const int b = i & 1;
-            if (ok) ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.d_full[b]), (i / 2) & 1, &sh.abort));
+            if (ok) ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.d_full[d.at]), d.phase, &sh.abort));
             if (!ok) continue;  // (the others still meet at the barrier)
             tc_fence_after_sync();
-            #pragma unroll
-            for (int c = 0; c < BN / 16; ++c) {
-                uint32_t v[16];
-                tmem_ld16(lanes + BN * b + 16 * c, v);
-                tmem_ld16_wait(v);
+            const uint32_t from = lanes + BN * d.at;
+            auto add = [&](int j, const uint32_t* v, int n) {
                 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 s = *reinterpret_cast<const float4*>(&scale[b][16 * c + 4 * j]);
-                    fma2(acc[8 * c + 2 * j], v[4 * j], v[4 * j + 1], pair_of(s.x, s.y));
-                    fma2(acc[8 * c + 2 * j + 1], v[4 * j + 2], v[4 * j + 3], pair_of(s.z, s.w));
+                for (int k = 0; k < n; k += 4) {
+                    const float4 s = *reinterpret_cast<const float4*>(&scale[d.at][j + k]);
+                    acc[j + k] = fmaf(__uint_as_float(v[k]), s.x, acc[j + k]);
+                    acc[j + k + 1] = fmaf(__uint_as_float(v[k + 1]), s.y, acc[j + k + 1]);
+                    acc[j + k + 2] = fmaf(__uint_as_float(v[k + 2]), s.z, acc[j + k + 2]);
+                    acc[j + k + 3] = fmaf(__uint_as_float(v[k + 3]), s.w, acc[j + k + 3]);
+                }
+            };
+            auto release = [&]() {
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.d_empty[d.at]));
+            };
+            if constexpr (BN == 16) {
+                uint32_t v[16];
+                tmem_ld16(from, v);
+                tmem_ld16_wait(v);
+                release();
+                add(0, v, 16);
+            } else {
+                uint32_t v[BN > 32 ? 2 : 1][32];
+                tmem_ld32(from, v[0]);
+                #pragma unroll
+                for (int c = 0; c < BN / 32; ++c) {
+                    tmem_ld32_wait(v[c & (BN > 32)]);
+                    if (c + 1 < BN / 32)
+                        tmem_ld32(from + 32 * (c + 1), v[(c + 1) & (BN > 32)]);
+                    else
+                        release();
+                    add(32 * c, v[c & (BN > 32)], 32);
                 }
             }
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh.d_empty[b]));
         }
         const int64_t n = n0 + t;
         if (pieces == 1) {
             if (ok && n < a.N)
                 #pragma unroll
-                for (int j = 0; j < BN; ++j) {
-                    const float2 x = halves_of(acc[j / 2]);
-                    if (m0 + j < a.M) static_cast<TY*>(a.Y)[(int64_t)(m0 + j) * a.N + n] = (TY)(j % 2 ? x.y : x.x);
-                }
+                for (int j = 0; j < BN; ++j)
+                    if (m0 + j < a.M) static_cast<TY*>(a.Y)[(int64_t)(m0 + j) * a.N + n] = (TY)acc[j];
         } else {
             // all copies have landed and all MMAs have read them (the last block's are done)
             float* sums = reinterpret_cast<float*>(smem);
             #pragma unroll
-            for (int j = 0; j < BN; ++j) {
-                const float2 x = halves_of(acc[j / 2]);
-                if (m0 + j < a.M) sums[j * kRows + t] = ok ? (j % 2 ? x.y : x.x) : 0.f;
-            }
+            for (int j = 0; j < BN; ++j)
+                if (m0 + j < a.M) sums[j * kRows + t] = ok ? acc[j] : 0.f;
         }
     }
     tc_fence_before_sync();
@@ -531,19 +552,29 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<BN>::kCtas) f8_narrow_k
     }
     if (pieces > 1) {
         cl.sync();
-        // rows p, p + pieces, ... of the batch: the pieces' sums in order
-        const int r = tid % kRows, rows = min(BN, a.M - m0);
-        const int64_t n = n0 + r;
-        for (int j = p + pieces * (tid / kRows); j < rows; j += pieces * (kNarrowThreads / kRows)) {
-            float y[kNarrowCluster];
+        // rows p, p + pieces, ... of the batch, a warp each, four columns a lane: the
+        // pieces' sums in order
+        const int rows = min(BN, a.M - m0);
+        const int64_t n = n0 + 4 * lane;
+        const bool vec = a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.Y) % (4 * sizeof(TY)) == 0;
+        for (int j = p + pieces * warp; j < rows; j += pieces * (kNarrowThreads / 32)) {
+            float4 y[kNarrowCluster];
             #pragma unroll
             for (int k = 0; k < kNarrowCluster; ++k)
-                if (k < pieces) y[k] = cl.map_shared_rank(reinterpret_cast<float*>(smem), k)[j * kRows + r];
-            float sum = y[0];
+                if (k < pieces) y[k] = load4(cl.map_shared_rank(reinterpret_cast<const float*>(smem), k) + j * kRows + 4 * lane);
+            float4 sum = y[0];
             #pragma unroll
             for (int k = 1; k < kNarrowCluster; ++k)
-                if (k < pieces) sum += y[k];
-            if (n < a.N) static_cast<TY*>(a.Y)[(int64_t)(m0 + j) * a.N + n] = (TY)sum;
+                if (k < pieces) sum.x += y[k].x, sum.y += y[k].y, sum.z += y[k].z, sum.w += y[k].w;
+            TY* to = static_cast<TY*>(a.Y) + (int64_t)(m0 + j) * a.N + n;
+            if (vec && n < a.N) {  // then the four are inside
+                store4(to, sum);
+            } else {
+                if (n < a.N) to[0] = (TY)sum.x;
+                if (n + 1 < a.N) to[1] = (TY)sum.y;
+                if (n + 2 < a.N) to[2] = (TY)sum.z;
+                if (n + 3 < a.N) to[3] = (TY)sum.w;
+            }
         }
         cl.sync();  // no CTA leaves while its sums may be read
     }
@@ -634,9 +665,11 @@ cudaError_t launch_gemm(const uint8_t* Xf, const float* sa, int64_t M, int64_t K
     const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     a.tiles_a = (int)n_tiles;
     const int64_t ctas = n_tiles * ((M + bn - 1) / bn);
+    // Pieces of at least 4 blocks, as many as leave all CTAs resident (two a SM up to 64 rows; one a SM with
+    // twice the stages and half the pieces was slower behind another call, whose CTAs then
+    // leave no room to start in: 14.6 us a call instead of 13.5 at 1 x 3584 x 18944).
     const int64_t slots = (bn <= 64 ? 2 : 1) * (int64_t)sms;
     int pieces = 1;
-    // pieces of at least 4 blocks, as many as leave one wave
     while (pieces < kNarrowCluster && (pieces + 1) * ctas <= slots && a.kbs / (pieces + 1) >= 4) ++pieces;
     if (!code_map(&a.tm_a, Wf, N, K, kRows) || !code_map(&a.tm_b, Xf, M, K, bn)) return cudaErrorNotSupported;
     switch (bn) {
