@@ -14,14 +14,16 @@
 // Two launches.  The first reads every row once (what bounds the call): maximum,
 // its first place and the fp32 sum of weights, a row cut into slices for enough CTAs.
 // The second has a cluster of CTAs a sequence, which all walk the drafts on the
-// same numbers, and go over one row for the draw (over as many more as
-// there are refusals at the node with draft probabilities).
+// same numbers, and go over the last row once more for the draw.
 //
 // The draw compares a random number with sums over 10^5 weights: in fp32 their
-// roundings would decide between neighbours now and then.  The weights of the
-// draw are integers instead: w / 2^ceil(max) in units of 2^-40, each within a
-// few units of the exact value (the exponent's argument in two floats, a table of 2^(i/128), a
-// polynomial of four terms), so sums are exact, in any order and split.
+// roundings would decide between neighbours now and then.  So the fp32 sums only
+// decide where the number lies further from the token's two edges than they can be off: by
+// at most kOff Z, counted at its definition.  Otherwise the row's weights are taken as integers:
+// w / 2^ceil(max) in units of 2^-40, each within a few units of the exact value (the
+// exponent's argument in two floats, a table of 2^(i/128), a polynomial of four terms), so
+// that sums are exact, in any order and split.  That is 40 instructions a weight; on 24
+// rows of 152064 the draw took 34 us with integers alone.
 #include <cooperative_groups.h>
 
 #include "kernels.h"
@@ -36,11 +38,22 @@ __device__ unsigned g_verify_error;
 
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kDrawThreads = 512;  // of the second launch, at most
+constexpr int kDrawWarps = kDrawThreads / 32;
 constexpr int kVerifyCluster = 8;
-constexpr int kTile = 128;        // weights of a tile, 4 a lane
+constexpr int kTile = 128;        // weights of a warp's load, 4 a lane
+constexpr int kSeg = 512;         // of a segment, 16 a lane
 constexpr int kMaxDrafts = KVQ_MAX_TREE;
 constexpr int kMaxSlices = 32;    // of a row, in the first launch
 constexpr float kGreedyBelow = 0x1p-20f;
+
+// How far an fp32 sum over weights of a row may be off, relative to the row's whole sum Z, in units of
+// 2^-24: a weight exp2(t), t = (l - max) c with two roundings and half of one in c, is within
+// 2.5 |t| ln 2 + 4 (ex2.approx), and the mean of |t| over the distribution is at most log2(vocab) <=
+// 22: 42; the factors that bring sums of the first launch to one maximum the same: 42; additions of
+// 16 weights, over a warp, 8 warps and 32 slices, the others in 64 bits: 21; refused tokens'
+// weights taken off: 42.  147 in all, below 2^-16.
+constexpr float kOff = 0x1p-16f;
 
 struct RowPart {
     float top, sum;  // maximum; sum of exp2((l - top) c), NaN where a value is NaN or +infinity
@@ -57,7 +70,7 @@ struct VerifyArgs {
     const float *temp, *u;
     int32_t *keep, *out, *count;
     RowPart* parts;  // [tokens][slices]
-    int slices;
+    int slices, seg_count;
 };
 
 __device__ __forceinline__ float load1(const float* p) { return *p; }
@@ -92,12 +105,13 @@ struct Scale {
     bool greedy;
 };
 __device__ __forceinline__ Scale scale_of(const float* temp, int b) {
-    const float t = temp != nullptr ? temp[b] : 1.f;
+    constexpr float kLog2E = 1.44269502162933349609375f, kLog2ELo = 1.9259629911266175e-8f;
+    float t = temp != nullptr ? temp[b] : 1.f;
     Scale s;
     s.greedy = !(t >= kGreedyBelow);
-    const double c = 1.4426950408889634074 / (s.greedy ? 1.0 : (double)fminf(t, 0x1p60f));
-    s.hi = (float)c;
-    s.lo = (float)(c - (double)s.hi);
+    t = s.greedy ? 1.f : fminf(t, 0x1p60f);
+    s.hi = __fdiv_rn(kLog2E, t);
+    s.lo = __fdiv_rn(fmaf(-s.hi, t, kLog2E) + kLog2ELo, t);  // the remainder is exact
     return s;
 }
 
@@ -121,41 +135,49 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_rows_kernel(const Verif
     griddep_launch_dependents();
     griddep_wait();
     const int t = blockIdx.x;
-    const int b = kvq_find_seq(a.cu, a.seqs, t);
-    if (b < 0) return;
-    const float c = scale_of(a.temp, b).hi;
     const T* row = static_cast<const T*>(a.L) + t * a.ld_l;
     const bool wide = row_wide(row);
     const int runs = (a.vocab + 3) / 4, per = (runs + a.slices - 1) / a.slices;
     const int lo = blockIdx.y * per, hi = min(lo + per, runs);
-    RowPart p = {-INFINITY, 0.f, 0x7FFFFFFF, 0};
-    for (int r = lo + threadIdx.x; r < hi; r += U * kVerifyThreads) {
-        float v[U][4];
+    float v[U][4];
+    auto load = [&](int r) {
         #pragma unroll
         for (int k = 0; k < U; ++k) {
             const int q = r + k * kVerifyThreads;
             load_run(row, 4 * q, q < hi ? a.vocab : 0, wide, -INFINITY, v[k]);
         }
+    };
+    if (lo + (int)threadIdx.x < hi) load(lo + threadIdx.x);  // before the sequence is known
+    const int b = kvq_find_seq(a.cu, a.seqs, t);
+    if (b < 0) return;
+    const float c = scale_of(a.temp, b).hi;
+    RowPart p = {-INFINITY, 0.f, 0x7FFFFFFF, 0};
+    double all = 0.0;  // (a thread adds up to 2^22 / 4096 times)
+    for (int r = lo + threadIdx.x; r < hi; r += U * kVerifyThreads) {
         float m = p.top;
         #pragma unroll
         for (int k = 0; k < U; ++k) m = fmaxf(m, fmaxf(fmaxf(v[k][0], v[k][1]), fmaxf(v[k][2], v[k][3])));
         if (m > p.top) {
-            p.sum *= ex2((p.top - m) * c);  // (0 while there was none)
+            all *= ex2((p.top - m) * c);  // (0 while there was none)
             p.top = m;
             #pragma unroll
             for (int k = U * 4 - 1; k >= 0; --k)
                 if (v[k / 4][k % 4] == m) p.at = 4 * (r + k / 4 * kVerifyThreads) + k % 4;
         }
         if (m > -INFINITY) {
+            float sum = 0.f;
             #pragma unroll
             for (int k = 0; k < U; ++k)
-                p.sum += (ex2((v[k][0] - m) * c) + ex2((v[k][1] - m) * c)) + (ex2((v[k][2] - m) * c) + ex2((v[k][3] - m) * c));
+                sum += (ex2((v[k][0] - m) * c) + ex2((v[k][1] - m) * c)) + (ex2((v[k][2] - m) * c) + ex2((v[k][3] - m) * c));
+            all += sum;
         } else {  // all -infinity, or NaN
             #pragma unroll
             for (int k = 0; k < U * 4; ++k)
-                if (v[k / 4][k % 4] != v[k / 4][k % 4]) p.sum = NAN;
+                if (v[k / 4][k % 4] != v[k / 4][k % 4]) all = NAN;
         }
+        if (r + U * kVerifyThreads < hi) load(r + U * kVerifyThreads);
     }
+    p.sum = (float)all;
     #pragma unroll
     for (int o = 16; o >= 1; o /= 2) {
         const RowPart q = {__shfl_xor_sync(0xFFFFFFFFu, p.top, o), __shfl_xor_sync(0xFFFFFFFFu, p.sum, o),
@@ -189,7 +211,7 @@ struct Pow2Table {
         }
     }
 };
-__constant__ constexpr Pow2Table kPow2{};
+__device__ const Pow2Table kPow2{};  // (in constant memory its divergent reads came one by one)
 
 struct Unit {
     float hi, lo, ref;  // log2(e) / T, the whole power of two above the largest weight
@@ -237,6 +259,11 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
     for (int o = 16; o >= 1; o /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
+__device__ __forceinline__ float warp_sum(float v) {
+    #pragma unroll
+    for (int o = 16; o >= 1; o /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
 // Inclusive prefix over the warp.
 __device__ __forceinline__ uint64_t warp_prefix(uint64_t v) {
     const int lane = threadIdx.x % 32;
@@ -247,165 +274,245 @@ __device__ __forceinline__ uint64_t warp_prefix(uint64_t v) {
     }
     return v;
 }
+// fp32 weights in the draw's units (64-bit floating point is slow here).
+__device__ __forceinline__ uint64_t to_units(float w) { return __float2ull_rn(w * 0x1p40f); }
 
 struct DrawShared {
     uint64_t pow2[128];
     RowPart row[kMaxDrafts];
     float u[kMaxDrafts], w[kMaxDrafts], q[kMaxDrafts];  // of each draft at its parent
     int id[kMaxDrafts], parent[kMaxDrafts], taken[kMaxDrafts], refused[kMaxDrafts];
-    uint64_t cta_sum[2], warp[kVerifyWarps];
+    uint64_t cta_sum[2];
+    float q_warp[kDrawWarps], q_sum[2];
+    int verdict;  // the token that the fp32 sums give, -1 where they leave it open
 };
 
+// Sums over a row by the cluster, and the token where they pass a number.  Each CTA has
+// a run of segments and the sums of each in shared memory, in the draw's units.
 template <typename T>
 struct Draw {
     const VerifyArgs& a;
     DrawShared& s;
-    uint64_t* tile_sum;  // of this CTA's tiles
-    int tiles, per, t0, t1, rank, ctas, passes;
+    uint64_t* sums;
+    const Scale c;
+    int rank, s0, s1, passes;
     uint64_t before, total;  // of the CTAs ahead; of all
+    float q_total;
 
-    // The weights that a pass sums: of row t in unit `unit`, less q times `cut`
-    // (0: the weights themselves).
-    __device__ __forceinline__ float q_at(int64_t t, int j) const {
-        const int64_t i = t * a.ld_q + j;
-        return a.q_f16 ? __half2float(static_cast<const __half*>(a.Q)[i]) : static_cast<const float*>(a.Q)[i];
-    }
-    __device__ __forceinline__ uint64_t left(float l, float q, const Unit& unit, uint64_t cut) const {
-        const uint64_t w = weight(l, unit, s.pow2), c = cut != 0 ? part_of(q, cut) : 0;
-        return w > c ? w - c : 0;
-    }
-    __device__ __forceinline__ void load_tile(int64_t t, int tile, bool with_q, float* l, float* q) const {
-        const int j = tile * kTile + 4 * (threadIdx.x % 32);
-        const T* row = static_cast<const T*>(a.L) + t * a.ld_l;
-        load_run(row, j, a.vocab, row_wide(row), -INFINITY, l);
-        if (!with_q) return;
-        if (a.q_f16) {
-            const __half* r = static_cast<const __half*>(a.Q) + t * a.ld_q;
-            load_run(r, j, a.vocab, row_wide(r), 0.f, q);
+    // A lane's 16 of a segment, 4 runs of 4, 128 apart; past the end -infinity and 0.
+    template <typename X>
+    __device__ __forceinline__ void load_seg(const X* row, int seg, float past, float (&v)[16]) const {
+        const int j = seg * kSeg + 4 * (int)(threadIdx.x % 32);
+        if (row_wide(row) && (seg + 1) * kSeg <= a.vocab) {
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float4 x = load4(row + j + k * kTile);
+                v[4 * k] = x.x, v[4 * k + 1] = x.y, v[4 * k + 2] = x.z, v[4 * k + 3] = x.w;
+            }
         } else {
-            const float* r = static_cast<const float*>(a.Q) + t * a.ld_q;
-            load_run(r, j, a.vocab, row_wide(r), 0.f, q);
+            #pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = j + k / 4 * kTile + k % 4 < a.vocab ? load1(row + j + k / 4 * kTile + k % 4) : past;
         }
     }
+    __device__ __forceinline__ const T* row(int64_t t) const { return static_cast<const T*>(a.L) + t * a.ld_l; }
+    __device__ __forceinline__ void load_q(int64_t t, int seg, float (&v)[16]) const {
+        if (a.q_f16)
+            load_seg(static_cast<const __half*>(a.Q) + t * a.ld_q, seg, 0.f, v);
+        else
+            load_seg(static_cast<const float*>(a.Q) + t * a.ld_q, seg, 0.f, v);
+    }
 
-    // Sums of this CTA's tiles, of the CTAs before it and of all; the tokens in
-    // s.refused count 0.
-    __device__ void pass(int64_t t, const Unit& unit, uint64_t cut, int refused) {
-        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-        constexpr int U = 2;
-        for (int x = t0 + warp; x < t1; x += U * kVerifyWarps) {
-            float l[U][4], q[U][4];
-            #pragma unroll
-            for (int k = 0; k < U; ++k)
-                if (x + k * kVerifyWarps < t1) load_tile(t, x + k * kVerifyWarps, cut != 0, l[k], q[k]);
-            #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                if (x + k * kVerifyWarps >= t1) break;
-                uint64_t v = 0;
-                #pragma unroll
-                for (int i = 0; i < 4; ++i) v += left(l[k][i], cut != 0 ? q[k][i] : 0.f, unit, cut);
-                v = warp_sum(v);
-                if (lane == 0) tile_sum[x + k * kVerifyWarps - t0] = v;
-            }
+    // What is left of a weight: of logit l with draft probability q, in fp32 (relative to
+    // exp of the row's maximum, Z the row's sum; with_q: less q Z) ...
+    struct Fast {
+        float top, c, z;
+        bool with_q;
+        __device__ __forceinline__ float value(float l, float q) const {
+            const float w = l > -INFINITY ? ex2((l - top) * c) : 0.f;
+            return with_q ? fmaxf(w - (q > 0.f ? fminf(q, 1.f) : 0.f) * z, 0.f) : w;
         }
-        __syncthreads();
-        if (threadIdx.x == 0)
-            for (int i = 0; i < refused; ++i) {
-                const int x = s.refused[i] / kTile;
-                if (x >= t0 && x < t1)
-                    tile_sum[x - t0] -= weight(load1(static_cast<const T*>(a.L) + t * a.ld_l + s.refused[i]), unit, s.pow2);
+        __device__ __forceinline__ uint64_t units(float l, float q) const { return to_units(value(l, q)); }
+        __device__ __forceinline__ uint64_t lanes(const float (&l)[16], const float (&q)[16]) const {
+            float sum = 0.f;
+            #pragma unroll
+            for (int k = 0; k < 16; ++k) sum += value(l[k], q[k]);
+            return to_units(warp_sum(sum));
+        }
+    };
+    // ... and as integers (cut 0: without q), exact sums.
+    struct Exact {
+        Unit unit;
+        uint64_t cut;
+        const uint64_t* pow2;
+        bool with_q;
+        __device__ __forceinline__ uint64_t units(float l, float q) const {
+            const uint64_t w = weight(l, unit, pow2), x = with_q ? part_of(q, cut) : 0;
+            return w > x ? w - x : 0;
+        }
+        __device__ __forceinline__ uint64_t lanes(const float (&l)[16], const float (&q)[16]) const {
+            // four at a time, the others waiting in line: 16 copies of the code took longer to
+            // fetch than to run
+            uint64_t sum = 0;
+            float x[16], y[16];
+            #pragma unroll
+            for (int k = 0; k < 16; ++k) x[k] = l[k], y[k] = q[k];
+            #pragma unroll 1
+            for (int g = 0; g < 4; ++g) {
+                #pragma unroll
+                for (int k = 0; k < 4; ++k) sum += units(x[k], y[k]);
+                #pragma unroll
+                for (int k = 0; k < 12; ++k) x[k] = x[k + 4], y[k] = y[k + 4];
             }
-        __syncthreads();
-        uint64_t v = 0;
-        for (int x = threadIdx.x; x < t1 - t0; x += kVerifyThreads) v += tile_sum[x];
-        v = warp_sum(v);
-        if (lane == 0) s.warp[warp] = v;
+            return warp_sum(sum);
+        }
+    };
+
+    // The sums of row t, of the tokens in s.refused 0.
+    template <typename W>
+    __device__ void pass(int64_t t, const W& w, int refused) {
+        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+        float q_mine = 0.f;
+        const int warps = blockDim.x / 32;
+        for (int seg = s0 + warp; seg < s1; seg += warps) {
+            float l[16], q[16];
+            load_seg(row(t), seg, -INFINITY, l);
+            if (w.with_q) {
+                load_q(t, seg, q);
+                #pragma unroll
+                for (int k = 0; k < 16; ++k) q_mine += fminf(fabsf(q[k]), 1.f);
+            } else {
+                #pragma unroll
+                for (int k = 0; k < 16; ++k) q[k] = 0.f;
+            }
+            const uint64_t sum = w.lanes(l, q);
+            if (lane == 0) sums[seg - s0] = sum;
+        }
+        q_mine = warp_sum(q_mine);
+        if (lane == 0) s.q_warp[warp] = q_mine;
         __syncthreads();
         const int slot = passes++ & 1;  // one barrier a pass: the next but one writes here again
-        if (threadIdx.x == 0) {
-            v = 0;
-            for (int i = 0; i < kVerifyWarps; ++i) v += s.warp[i];
-            s.cta_sum[slot] = v;
+        if (warp == 0) {
+            for (int i = 0; i < refused; ++i) {
+                const int seg = s.refused[i] / kSeg;
+                if (lane == 0 && seg >= s0 && seg < s1) {
+                    const uint64_t x = w.units(load1(row(t) + s.refused[i]), 0.f);
+                    sums[seg - s0] -= x < sums[seg - s0] ? x : sums[seg - s0];
+                }
+            }
+            __syncwarp();
+            uint64_t v = 0;
+            for (int x = lane; x < s1 - s0; x += 32) v += sums[x];
+            v = warp_sum(v);
+            if (lane == 0) {
+                s.cta_sum[slot] = v;
+                float x = 0.f;
+                for (int i = 0; i < warps; ++i) x += s.q_warp[i];
+                s.q_sum[slot] = x;
+            }
         }
         cg::cluster_group cl = cg::this_cluster();
         cl.sync();
         before = total = 0;
-        for (int r = 0; r < ctas; ++r) {
-            const uint64_t c = *cl.map_shared_rank(&s.cta_sum[slot], r);
-            if (r < rank) before += c;
-            total += c;
+        q_total = 0.f;
+        #pragma unroll
+        for (int r = 0; r < kVerifyCluster; ++r) {
+            const uint64_t x = *cl.map_shared_rank(&s.cta_sum[slot], r);
+            q_total += *cl.map_shared_rank(&s.q_sum[slot], r);
+            if (r < rank) before += x;
+            total += x;
         }
     }
 
-    // The first token whose cumulative weight passes `target`, in the CTA and the
-    // warp that hold it; -1 elsewhere.
-    __device__ int find(int64_t t, const Unit& unit, uint64_t cut, int refused, uint64_t target) const {
+    // The first token whose cumulative sum passes `target` by more than `off`, the token before
+    // it staying behind by more than `off`, in one lane of the CTA and the warp that hold it;
+    // -1 elsewhere, and where it is closer.
+    template <typename W>
+    __device__ int find(int64_t t, const W& w, int refused, uint64_t target, uint64_t off) const {
         if (threadIdx.x >= 32 || target < before) return -1;
         const int lane = threadIdx.x;
         uint64_t run = before;
-        for (int x = t0; x < t1; x += 32) {
-            const uint64_t v = x + lane < t1 ? tile_sum[x - t0 + lane] : 0, up = run + warp_prefix(v);
+        for (int x = 0; x < s1 - s0; x += 32) {
+            const uint64_t v = x + lane < s1 - s0 ? sums[x + lane] : 0, up = run + warp_prefix(v);
             const unsigned hit = __ballot_sync(0xFFFFFFFFu, up > target);
             if (hit == 0) {
                 run = __shfl_sync(0xFFFFFFFFu, up, 31);
                 continue;
             }
-            const int first = __ffs(hit) - 1;
+            const int first = __ffs(hit) - 1, seg = s0 + x + first;
             run = __shfl_sync(0xFFFFFFFFu, up - v, first);
-            float l[4], q[4];
-            load_tile(t, x + first, cut != 0, l, q);
-            uint64_t w[4], sum = 0;
-            #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[i] = left(l[i], cut != 0 ? q[i] : 0.f, unit, cut);
-                for (int k = 0; k < refused; ++k)
-                    if (s.refused[k] == (x + first) * kTile + 4 * lane + i) w[i] = 0;
-                sum += w[i];
+            float l[16], q[16];
+            load_seg(row(t), seg, -INFINITY, l);
+            if (w.with_q) {
+                load_q(t, seg, q);
+            } else {
+                #pragma unroll
+                for (int k = 0; k < 16; ++k) q[k] = 0.f;
             }
-            const uint64_t end = run + warp_prefix(sum);
-            const unsigned in = __ballot_sync(0xFFFFFFFFu, end > target);
-            if (in == 0 || lane != __ffs(in) - 1) return -1;
-            uint64_t c = end - sum;
-            #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                c += w[i];
-                if (c > target) return (x + first) * kTile + 4 * lane + i;
+            #pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                uint64_t y[4], sum = 0;
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = w.units(l[i], q[i]);
+                #pragma unroll
+                for (int i = 0; i < 12; ++i) l[i] = l[i + 4], q[i] = q[i + 4];
+                for (int r = 0; r < refused; ++r) {
+                    const int off_lane = s.refused[r] - (seg * kSeg + k * kTile + 4 * lane);
+                    #pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (off_lane == i) y[i] = 0;
+                }
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) sum += y[i];
+                const uint64_t end = run + warp_prefix(sum);
+                const unsigned in = __ballot_sync(0xFFFFFFFFu, end > target);
+                if (in != 0) {
+                    if (lane != __ffs(in) - 1) return -1;
+                    uint64_t at = end - sum;
+                    #pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint64_t lo = at;
+                        at += y[i];
+                        if (at > target)
+                            return (off == 0 || (lo + off < target && target + off < at))
+                                       ? seg * kSeg + k * kTile + 4 * lane + i
+                                       : -1;
+                    }
+                }
+                run = __shfl_sync(0xFFFFFFFFu, end, 31);
             }
+            return -1;
         }
         return -1;
     }
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kVerifyThreads) verify_draw_kernel(const VerifyArgs a) {
-    extern __shared__ uint64_t tile_sum[];
+__global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const VerifyArgs a) {
+    extern __shared__ uint64_t seg_sums[];
     __shared__ DrawShared s;
     cg::cluster_group cl = cg::this_cluster();
-    if (threadIdx.x < 128) s.pow2[threadIdx.x] = kPow2.v[threadIdx.x];
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, rank = (int)cl.block_rank();
+    if (tid < 128) s.pow2[tid] = kPow2.v[tid];
+    if (tid == 0) s.verdict = -1;
     griddep_launch_dependents();
     griddep_wait();
     const int b = blockIdx.x / kVerifyCluster;
     const int first = a.cu[b], end = a.cu[b + 1], n = end - first;
     const bool sound = first >= 0 && n >= 0 && end <= a.tokens;
     if (!sound || n == 0 || n > kMaxDrafts) {  // the whole cluster
-        if (cl.block_rank() == 0) {
-            if (threadIdx.x == 0) {
+        if (rank == 0) {
+            if (tid == 0) {
                 a.count[b] = 0;
                 if (n != 0 || !sound) atomicOr(&g_verify_error, kErrCacheRange);
             }
             if (sound)
-                for (int i = threadIdx.x; i < n; i += kVerifyThreads) a.keep[first + i] = a.out[first + i] = -1;
+                for (int i = tid; i < n; i += blockDim.x) a.keep[first + i] = a.out[first + i] = -1;
         }
         return;
     }
     const Scale c = scale_of(a.temp, b);
-    const int tid = threadIdx.x;
     if (tid < n) {
         const int64_t t = first + tid;
-        RowPart p = a.parts[t * a.slices];
-        for (int i = 1; i < a.slices; ++i) join(p, a.parts[t * a.slices + i], c.hi);
-        if (!(p.top > -INFINITY)) p.sum = NAN;
-        s.row[tid] = p;
         s.u[tid] = a.u[t];
         s.id[tid] = a.ids[t];
         int up = tid - 1;
@@ -415,51 +522,67 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_draw_kernel(const Verif
         }
         s.parent[tid] = up;
     }
+    #pragma unroll 1
+    for (int r = warp; r < n; r += blockDim.x / 32) {  // a row's slices, one a lane
+        RowPart p = {-INFINITY, 0.f, 0x7FFFFFFF, 0};
+        if (lane < a.slices) p = a.parts[(int64_t)(first + r) * a.slices + lane];
+        #pragma unroll 1
+        for (int o = 16; o >= 1; o /= 2) {
+            const RowPart q = {__shfl_xor_sync(0xFFFFFFFFu, p.top, o), __shfl_xor_sync(0xFFFFFFFFu, p.sum, o),
+                               __shfl_xor_sync(0xFFFFFFFFu, p.at, o), 0};
+            join(p, q, c.hi);
+        }
+        if (lane == 0) {
+            if (!(p.top > -INFINITY)) p.sum = NAN;
+            s.row[r] = p;
+        }
+    }
     __syncthreads();
     if (tid > 0 && tid < n) {
         const int up = s.parent[tid], id = s.id[tid];
         float w = 0.f, q = 0.f;
         if (up >= 0 && id >= 0 && id < a.vocab) {
-            const float d = load1(static_cast<const T*>(a.L) + (first + up) * a.ld_l + id) - s.row[up].top;
-            const float x = d * c.hi, e = fmaf(d, c.lo, fmaf(d, c.hi, -x));
-            w = exp2f(x) * fmaf(e, 0.693147182f, 1.f);  // (NaN for a row of no use: every test fails)
-            if (!(d > -INFINITY)) w = 0.f;
+            const float l = load1(static_cast<const T*>(a.L) + (first + up) * a.ld_l + id);
             if (a.Q != nullptr) {
                 const int64_t i = (first + up) * a.ld_q + id;
                 q = a.q_f16 ? __half2float(static_cast<const __half*>(a.Q)[i]) : static_cast<const float*>(a.Q)[i];
             }
+            const float d = l - s.row[up].top;
+            const float x = d * c.hi, e = fmaf(d, c.lo, fmaf(d, c.hi, -x));
+            w = exp2f(x) * fmaf(e, 0.693147182f, 1.f);  // (NaN for a row of no use: every test fails)
+            if (!(d > -INFINITY)) w = 0.f;
         }
         s.w[tid] = w;
         s.q[tid] = q;
     }
     __syncthreads();
 
-    Draw<T> dr{a, s, tile_sum};
-    dr.tiles = (a.vocab + kTile - 1) / kTile;
-    dr.per = (dr.tiles + kVerifyCluster - 1) / kVerifyCluster;
-    dr.rank = (int)cl.block_rank();
-    dr.ctas = kVerifyCluster;
-    dr.t0 = min(dr.rank * dr.per, dr.tiles);
-    dr.t1 = min(dr.t0 + dr.per, dr.tiles);
+    const int seg_per = (a.seg_count + kVerifyCluster - 1) / kVerifyCluster;
+    Draw<T> dr{a, s, seg_sums, c};
+    dr.rank = rank;
+    dr.s0 = min(rank * seg_per, a.seg_count);
+    dr.s1 = min(dr.s0 + seg_per, a.seg_count);
     dr.passes = 0;
+    dr.total = 0;
 
     // Every thread of the cluster takes the same way through this: it depends on
     // shared values that all CTAs computed alike, and on the passes' totals.
     int node = 0, taken = 1, refused = 0, cuts = 0, todo = 0;  // cuts of todo made
     float gone = 0.f;                                          // weights of the refused
     uint64_t cut = 0;
-    auto unit_of = [&](int i) { return Unit{c.hi, c.lo, ceilf(s.row[i].top * c.hi)}; };
+    auto exact = [&](uint64_t by) {
+        return typename Draw<T>::Exact{{c.hi, c.lo, ceilf(s.row[node].top * c.hi)}, by, s.pow2, by != 0};
+    };
     auto make_cuts = [&]() {
-        const Unit unit = unit_of(node);
         while (cuts < todo) {
             if (cuts == 0) {
-                dr.pass(first + node, unit, 0, 0);
+                dr.pass(first + node, exact(0), 0);
                 cut = dr.total;
             } else {
                 cut += dr.total;
             }
             if (cut == 0) break;
-            dr.pass(first + node, unit, cut, 0);
+            dr.pass(first + node, exact(cut), 0);
             ++cuts;
         }
         cuts = todo;
@@ -488,9 +611,8 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_draw_kernel(const Verif
         } else {
             make_cuts();
             uint64_t w = 0;
-            if (id >= 0 && id < a.vocab)
-                w = dr.left(load1(static_cast<const T*>(a.L) + (first + node) * a.ld_l + id), s.q[i], unit_of(node), cut);
-            yes = (double)s.u[i] * s.q[i] * (double)dr.total < (double)w;
+            if (id >= 0 && id < a.vocab) w = exact(cut).units(load1(dr.row(first + node) + id), s.q[i]);
+            yes = s.u[i] * s.q[i] * (float)dr.total < (float)w;
             todo += !yes;
         }
         if (yes) {
@@ -504,38 +626,47 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_draw_kernel(const Verif
     }
     // the token after the last one taken
     const RowPart p = s.row[node];
+    const int64_t t = first + node;
+    const float u = s.u[0] < 1.f ? s.u[0] : 0x1.fffffep-1f;
     int next = -1;
-    bool mine = false;
-    if (p.sum != p.sum) {  // no distribution
-        mine = dr.rank == 0 && tid == 0;
-    } else if (c.greedy) {
+    bool mine = rank == 0 && tid == 0, shared = false;
+    if (p.sum == p.sum && c.greedy) {
         next = p.at;
-        mine = dr.rank == 0 && tid == 0;
-    } else {
-        const Unit unit = unit_of(node);
-        make_cuts();
-        if (todo == 0) dr.pass(first + node, unit, 0, refused);
-        if (dr.total == 0 && (todo != 0 || refused != 0)) {  // nothing left but roundings: the whole row
-            cut = 0;
-            refused = 0;
-            dr.pass(first + node, unit, 0, 0);
+    } else if (p.sum == p.sum) {
+        if (todo == 0 || (todo == 1 && cuts == 0)) {
+            // in fp32, after a refusal less q Z
+            const typename Draw<T>::Fast w = {p.top, c.hi, p.sum, todo == 1};
+            dr.pass(t, w, refused);
+            const uint64_t off = to_units(2.f * kOff * p.sum * (1.f + dr.q_total)) + 2;
+            const int x = dr.find(t, w, refused, part_of(u, dr.total), off);
+            if (x >= 0)
+                for (int r = 0; r < kVerifyCluster; ++r) *cl.map_shared_rank(&s.verdict, r) = x;
+            cl.sync();
+            next = s.verdict;
         }
-        const float u = s.u[0];
-        const uint64_t target = part_of(u < 1.f ? u : 0x1.fffffep-1f, dr.total);
-        next = dr.find(first + node, unit, cut, refused, target);
-        mine = next >= 0;
-        if (dr.total == 0) mine = dr.rank == 0 && tid == 0;
+        if (next < 0) {
+            shared = true;
+            make_cuts();
+            if (todo == 0) dr.pass(t, exact(0), refused);
+            if (dr.total == 0 && (todo != 0 || refused != 0)) {  // nothing left but roundings: the whole row
+                cut = 0;
+                refused = 0;
+                dr.pass(t, exact(0), 0);
+            }
+            next = dr.find(t, exact(cut), refused, part_of(u, dr.total), 0);
+            mine = next >= 0 || (dr.total == 0 && mine);
+        }
     }
-    __syncthreads();
+    __syncthreads();  // s.taken
     if (mine) a.out[first + taken - 1] = next;
-    if (dr.rank == 0) {
+    if (rank == 0) {
         if (tid == 0) a.count[b] = taken;
         if (tid < n) {
             a.keep[first + tid] = tid == 0 ? 0 : tid < taken ? s.taken[tid] : -1;
             if (tid != taken - 1) a.out[first + tid] = tid < taken - 1 ? s.id[s.taken[tid + 1]] : -1;
         }
     }
-    cl.sync();  // no CTA leaves while its sums may be read
+    if (shared) cl.sync();  // no CTA leaves while its sums may be read
 }
 
 int verify_slices(int64_t tokens, int64_t vocab, int sms) {
@@ -547,14 +678,16 @@ int verify_slices(int64_t tokens, int64_t vocab, int sms) {
 }
 
 template <typename T>
-cudaError_t launch_verify(const VerifyArgs& a, unsigned flags, cudaStream_t stream) {
+cudaError_t launch_verify(const VerifyArgs& a, int sms, unsigned flags, cudaStream_t stream) {
     cudaError_t e = layer_launch(verify_rows_kernel<T>, dim3((unsigned)a.tokens, (unsigned)a.slices), kVerifyThreads, 0, flags,
                                  stream, a);
     if (e != cudaSuccess) return e;
-    const int tiles = (a.vocab + kTile - 1) / kTile, per = (tiles + kVerifyCluster - 1) / kVerifyCluster;
+    const int per = (a.seg_count + kVerifyCluster - 1) / kVerifyCluster;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.seqs * kVerifyCluster));
-    cfg.blockDim = dim3(kVerifyThreads);
+    // (64 registers a thread: 2 CTAs of 512 or 4 of 256 threads an SM; all clusters resident
+    // comes first, then more warps for the passes)
+    cfg.blockDim = dim3((unsigned)(a.seqs * kVerifyCluster <= 2 * sms ? kDrawThreads : kDrawThreads / 2));
     cfg.dynamicSmemBytes = (size_t)per * sizeof(uint64_t);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -577,9 +710,10 @@ cudaError_t launch_draft_verify(const void* L, int l_f16, int64_t ld_l, int64_t 
                                 int64_t tokens, const int32_t* ids, const uint64_t* mask, const void* Q, int q_f16,
                                 int64_t ld_q, const float* temp, const float* u, int32_t* keep, int32_t* out,
                                 int32_t* count, void* ws, int sms, unsigned flags, cudaStream_t stream) {
+    const int slices = verify_slices(tokens, vocab, sms), segs = (int)((vocab + kSeg - 1) / kSeg);
     const VerifyArgs a = {L, Q, ld_l, ld_q, q_f16, (int)vocab, (int)tokens, (int)seqs, cu, ids, mask, temp, u, keep, out,
-                          count, static_cast<RowPart*>(ws), verify_slices(tokens, vocab, sms)};
-    return l_f16 ? launch_verify<__half>(a, flags, stream) : launch_verify<float>(a, flags, stream);
+                          count, static_cast<RowPart*>(ws), slices, segs};
+    return l_f16 ? launch_verify<__half>(a, sms, flags, stream) : launch_verify<float>(a, sms, flags, stream);
 }
 
 cudaError_t read_and_clear_verify_error(unsigned* flags, cudaStream_t stream) {
