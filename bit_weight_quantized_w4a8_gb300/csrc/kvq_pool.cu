@@ -54,6 +54,8 @@ struct PlanArgs {
     // pages held before, totals
     int32_t *back_at, *need_at, *old_held;
     PlanTotals* totals;
+    const int32_t *cu_at, *len_at;  // cu and lens as the look-ups read them
+    int wide;                       // pos, slot and seq on 16 bytes
 };
 
 struct Pair {
@@ -61,45 +63,48 @@ struct Pair {
     __device__ __forceinline__ Pair operator+(Pair o) const { return {a + o.a, b + o.b}; }
 };
 
-// Exclusive prefix of v over the threads of the cluster; *total over all.
-__device__ Pair cluster_scan(Pair v, Pair* warp_sum, Pair* cta_sum, Pair* total) {
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+struct ScanShared {
+    Pair warp[32], cta[2];
+};
+
+// Exclusive prefix of v over the threads of the cluster; *total over all.  The CTAs'
+// sums take turns in two places, so that one barrier a scan does: the next but one writes
+// there again.
+__device__ Pair cluster_scan(Pair v, ScanShared& sh, int& turn, Pair* total) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
     Pair x = v;
     #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
         const Pair y = {__shfl_up_sync(0xFFFFFFFFu, x.a, o), __shfl_up_sync(0xFFFFFFFFu, x.b, o)};
         if (lane >= o) x = x + y;
     }
-    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();  // the warps' sums of the scan before have been read
+    if (lane == 31) sh.warp[warp] = x;
     __syncthreads();
-    if (warp == 0) {
-        Pair w = warp_sum[lane], s = w;
-        #pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const Pair y = {__shfl_up_sync(0xFFFFFFFFu, s.a, o), __shfl_up_sync(0xFFFFFFFFu, s.b, o)};
-            if (lane >= o) s = s + y;
-        }
-        warp_sum[lane] = {s.a - w.a, s.b - w.b};
-        if (lane == 31) *cta_sum = s;
+    Pair base = {0, 0}, all = {0, 0};
+    Pair w = lane < warps ? sh.warp[lane] : Pair{0, 0};
+    #pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const Pair y = {__shfl_up_sync(0xFFFFFFFFu, w.a, o), __shfl_up_sync(0xFFFFFFFFu, w.b, o)};
+        if (lane >= o) w = w + y;
     }
+    if (warp > 0) base = {__shfl_sync(0xFFFFFFFFu, w.a, warp - 1), __shfl_sync(0xFFFFFFFFu, w.b, warp - 1)};
+    all = {__shfl_sync(0xFFFFFFFFu, w.a, 31), __shfl_sync(0xFFFFFFFFu, w.b, 31)};
     cg::cluster_group cl = cg::this_cluster();
-    Pair before = {0, 0};
-    *total = {0, 0};
+    *total = all;
     if (cl.num_blocks() > 1) {
+        if (threadIdx.x == 0) sh.cta[turn] = all;
         cl.sync();
-        for (unsigned r = 0; r < cl.num_blocks(); ++r) {
-            const Pair s = *cl.map_shared_rank(cta_sum, r);
-            if (r < cl.block_rank()) before = before + s;
+        *total = {0, 0};
+        #pragma unroll
+        for (unsigned r = 0; r < kPlanCluster; ++r) {
+            const Pair s = *cl.map_shared_rank(&sh.cta[turn], r);
+            if (r < cl.block_rank()) base = base + s;
             *total = *total + s;
         }
-        cl.sync();  // the sums are free for the next scan, and no CTA leaves while they are read
-    } else {
-        __syncthreads();
-        *total = *cta_sum;
+        turn ^= 1;
     }
-    const Pair base = warp_sum[warp];
-    __syncthreads();
-    return {before.a + base.a + x.a - v.a, before.b + base.b + x.b - v.b};
+    return {base.a + x.a - v.a, base.b + x.b - v.b};
 }
 
 // The last row b with at[b] <= k.
@@ -126,7 +131,8 @@ __device__ __forceinline__ int32_t page_out(const PlanArgs& a, const PlanTotals&
     return p < t.top ? a.stack[p] : page_back(a, (int64_t)t.top + t.back - 1 - p);
 }
 
-// Tokens, pages handed out and pages given back, by thread i of n.
+// Pages handed out, pages given back and tokens, by thread i of n; a thread takes
+// four tokens in a row, so that one search does for them and they leave in wide stores.
 __device__ void plan_fill(const PlanArgs& a, const PlanTotals& t, int64_t i, int64_t n) {
     for (int64_t k = i; k < t.need; k += n) {
         const int b = row_of(a.need_at, a.seqs, k);
@@ -137,39 +143,74 @@ __device__ void plan_fill(const PlanArgs& a, const PlanTotals& t, int64_t i, int
         if (p < a.pages) a.stack[p] = page_back(a, k);
     }
     if (a.pos == nullptr && a.slot == nullptr && a.seq == nullptr) return;
-    for (int64_t k = i; k < a.room; k += n) {
-        int pos = 0, row = -1;
-        int64_t slot = -1;
-        if (k < t.tokens) {
-            row = row_of(a.cu, a.seqs, k);
-            const int x = a.lens[row] + (int)(k - a.cu[row]);
-            pos = a.mask != nullptr ? a.lens[row] + __popcll(a.mask[k]) - 1 : x;
-            if (a.slot != nullptr) {
-                const int64_t j = x >> a.shift, old = a.old_held[row];
-                const int32_t page = j < old ? a.table[row * a.max_pages + j] : page_out(a, t, a.need_at[row] + j - old);
-                if (page >= 0 && page < a.pages) slot = ((int64_t)page << a.shift) + (x & ((1 << a.shift) - 1));
+    for (int64_t g = 4 * i; g < a.room; g += 4 * n) {
+        int pos[4], seq[4];
+        int64_t slot[4];
+        int row = g < t.tokens ? row_of(a.cu_at, a.seqs, g) : 0;
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t k = g + e;
+            pos[e] = 0;
+            slot[e] = seq[e] = -1;
+            if (k < t.tokens) {
+                while (a.cu_at[row + 1] <= k) ++row;
+                const int len = a.len_at[row], x = len + (int)(k - a.cu_at[row]);
+                pos[e] = a.mask != nullptr ? len + __popcll(a.mask[k]) - 1 : x;
+                seq[e] = row;
+                if (a.slot != nullptr) {
+                    const int64_t j = x >> a.shift, old = a.old_held[row];
+                    const int32_t page = j < old ? a.table[row * a.max_pages + j] : page_out(a, t, a.need_at[row] + j - old);
+                    if (page >= 0 && page < a.pages) slot[e] = ((int64_t)page << a.shift) + (x & ((1 << a.shift) - 1));
+                }
             }
         }
-        if (a.pos != nullptr) a.pos[k] = pos;
-        if (a.slot != nullptr) a.slot[k] = slot;
-        if (a.seq != nullptr) a.seq[k] = row;
+        if (a.wide && g + 4 <= a.room) {
+            if (a.pos != nullptr) *reinterpret_cast<int4*>(a.pos + g) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            if (a.seq != nullptr) *reinterpret_cast<int4*>(a.seq + g) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+            if (a.slot != nullptr) {
+                reinterpret_cast<longlong2*>(a.slot + g)[0] = make_longlong2(slot[0], slot[1]);
+                reinterpret_cast<longlong2*>(a.slot + g)[1] = make_longlong2(slot[2], slot[3]);
+            }
+        } else {
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (g + e >= a.room) break;
+                if (a.pos != nullptr) a.pos[g + e] = pos[e];
+                if (a.slot != nullptr) a.slot[g + e] = slot[e];
+                if (a.seq != nullptr) a.seq[g + e] = seq[e];
+            }
+        }
     }
 }
 
-template <bool FILL>
-__global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const PlanArgs a) {
-    __shared__ Pair warp_sum[32], cta_sum;
+// ITEMS: rows of a thread.  FILL: writes the step too; with one CTA (kOne) the look-ups stay
+// in shared memory.
+constexpr int kOneRows = 1024;
+template <int ITEMS, bool FILL, bool kOne>
+__global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const __grid_constant__ PlanArgs args) {
+    __shared__ ScanShared sh;
+    __shared__ int32_t rows_at[kOne ? 5 : 1][kOne ? kOneRows + 1 : 1];
+    PlanArgs a = args;
+    if constexpr (kOne) {
+        a.back_at = rows_at[0];
+        a.need_at = rows_at[1];
+        a.old_held = rows_at[2];
+        a.cu_at = rows_at[3];
+        a.len_at = rows_at[4];
+    }
     griddep_launch_dependents();
     griddep_wait();
-    const int ctas = gridDim.x, per = (a.seqs + ctas * kPlanThreads - 1) / (ctas * kPlanThreads);
-    const int r0 = (blockIdx.x * kPlanThreads + threadIdx.x) * per;
+    const int ctas = gridDim.x, threads = blockDim.x;
+    const int per = ITEMS == 1 ? 1 : (a.seqs + ctas * threads - 1) / (ctas * threads);
+    const int r0 = (blockIdx.x * threads + threadIdx.x) * per;
     const int rows = max(0, min(per, a.seqs - r0));
     bool bad = false;
-    int64_t len[kPlanItems], n[kPlanItems];
-    int held[kPlanItems], back[kPlanItems], back_sum = 0;
-    int64_t back_total = 0;
+    const int top_in = *a.top;
+    int64_t len[ITEMS], n[ITEMS];
+    int held[ITEMS], back[ITEMS];
+    int64_t back_sum = 0;
     #pragma unroll
-    for (int i = 0; i < kPlanItems; ++i) {
+    for (int i = 0; i < ITEMS; ++i) {
         len[i] = n[i] = 0;
         held[i] = back[i] = 0;
         if (i < rows) {
@@ -185,24 +226,21 @@ __global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const PlanArgs 
                 held[i] = 0;
                 len[i] = 0;
             }
-            back_total += back[i];
+            back_sum += back[i];
         }
     }
-    int top = *a.top;
-    const int top_in = (int)min((int64_t)max(top, 0), a.pages);
-    bad |= top_in != top;
-    top = top_in;
+    int turn = 0;
     Pair total;
-    const Pair bp = cluster_scan({back_total, 0}, warp_sum, &cta_sum, &total);
+    const Pair bp = cluster_scan({back_sum, 0}, sh, turn, &total);
     PlanTotals t;
-    t.top = top;
+    t.top = (int)min((int64_t)max(top_in, 0), a.pages);
     t.back = total.a;
-    t.mid = (int)min(top + total.a, a.pages);
-    bad |= top + total.a > a.pages;
+    t.mid = (int)min(t.top + total.a, a.pages);
+    bad |= t.top != top_in || t.top + total.a > a.pages;
 
-    int64_t need[kPlanItems], ask_p = 0, ask_n = 0;
+    int64_t need[ITEMS], ask_p = 0, ask_n = 0;
     #pragma unroll
-    for (int i = 0; i < kPlanItems; ++i) {
+    for (int i = 0; i < ITEMS; ++i) {
         need[i] = 0;
         if (n[i] > 0) {
             const int64_t end = len[i] + n[i], want = (end + (1 << a.shift) - 1) >> a.shift;
@@ -214,28 +252,34 @@ __global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const PlanArgs 
         ask_p += need[i];
         ask_n += n[i];
     }
-    Pair up = cluster_scan({ask_p, ask_n}, warp_sum, &cta_sum, &total);
-    int64_t got_p = 0, got_n = 0;
-    #pragma unroll
-    for (int i = 0; i < kPlanItems; ++i) {
-        up = up + Pair{need[i], n[i]};
-        if ((need[i] > 0 && up.a > t.mid) || up.b > a.room) need[i] = n[i] = 0;
-        got_p += need[i];
-        got_n += n[i];
+    Pair at = cluster_scan({ask_p, ask_n}, sh, turn, &total);
+    if (total.a > t.mid || total.b > a.room) {  // some have to wait: once more over those that go in
+        Pair up = at;
+        int64_t got_p = 0, got_n = 0;
+        #pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            up = up + Pair{need[i], n[i]};
+            if ((need[i] > 0 && up.a > t.mid) || up.b > a.room) need[i] = n[i] = 0;
+            got_p += need[i];
+            got_n += n[i];
+        }
+        at = cluster_scan({got_p, got_n}, sh, turn, &total);
     }
-    const Pair at = cluster_scan({got_p, got_n}, warp_sum, &cta_sum, &total);
     t.need = total.a;
     t.tokens = (int)total.b;
     int64_t b_at = bp.a, p_at = at.a, n_at = at.b;
     #pragma unroll
-    for (int i = 0; i < kPlanItems; ++i) {
+    for (int i = 0; i < ITEMS; ++i) {
         if (i < rows) {
             const int r = r0 + i;
             a.lens[r] = (int)len[i];
             a.held[r] = held[i] + (int)need[i];
             a.cu[r] = (int)n_at;
-            // a count of at most 65536 x 2^31 pages given back says nothing past 2^31: clamped, marked
-            a.back_at[r] = (int)min(b_at, (int64_t)0x7FFFFFFF);
+            if constexpr (kOne) {
+                rows_at[3][r] = (int)n_at;
+                rows_at[4][r] = (int)len[i];
+            }
+            a.back_at[r] = (int)min(b_at, (int64_t)0x7FFFFFFF);  // (more than that cannot be free pages)
             a.need_at[r] = (int)p_at;
             a.old_held[r] = held[i];
             b_at += back[i];
@@ -246,20 +290,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const PlanArgs 
     if (t.back > 0x7FFFFFFF) t.back = 0x7FFFFFFF, bad = true;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         a.cu[a.seqs] = t.tokens;
+        if constexpr (kOne) rows_at[3][a.seqs] = t.tokens;
         *a.top = t.mid - (int)t.need;
-        *a.totals = t;
+        if constexpr (!FILL) *a.totals = t;
     }
     if (bad) atomicOr(&g_pool_error, kErrCacheRange);
-    if constexpr (FILL) {
-        if (ctas > 1)
-            cg::this_cluster().sync();
-        else
-            __syncthreads();
-        plan_fill(a, t, blockIdx.x * kPlanThreads + threadIdx.x, (int64_t)ctas * kPlanThreads);
-    }
+    if (!kOne)  // (also: no CTA leaves while its sums may be read)
+        cg::this_cluster().sync();
+    else
+        __syncthreads();
+    if constexpr (FILL) plan_fill(a, t, blockIdx.x * threads + threadIdx.x, (int64_t)ctas * threads);
 }
 
-__global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(const PlanArgs a) {
+__global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(const __grid_constant__ PlanArgs a) {
     griddep_launch_dependents();
     griddep_wait();
     plan_fill(a, *a.totals, (int64_t)blockIdx.x * kFillThreads + threadIdx.x, (int64_t)gridDim.x * kFillThreads);
@@ -295,20 +338,32 @@ cudaError_t launch_kvq_plan(const kvq_pool_t& p, int32_t* lens, const int32_t* g
     a.back_at = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + 256);
     a.need_at = a.back_at + pad;
     a.old_held = a.need_at + pad;
-    const int ctas = p.seqs <= kPlanThreads && tokens <= 4096 && p.seqs * p.max_pages <= 1 << 17 ? 1 : kPlanCluster;
-    const bool two = tokens > 16384;
+    a.cu_at = cu;
+    a.len_at = lens;
+    a.wide = reinterpret_cast<uintptr_t>(pos) % 16 == 0 && reinterpret_cast<uintptr_t>(slot) % 16 == 0 &&
+             reinterpret_cast<uintptr_t>(seq) % 16 == 0;
+    // One CTA where rows, tokens and the pages that may come back are few; else a cluster, and
+    // for many tokens a second launch over all SMs.
+    const bool one = p.seqs <= kOneRows && tokens <= 4096 && p.seqs * p.max_pages <= 1 << 17;
+    const bool two = !one && tokens > 16384;
+    const int threads = one ? (int)((p.seqs > tokens / 4 ? p.seqs : tokens / 4) + 127) / 128 * 128 : kPlanThreads;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kPlanThreads);
+    cfg.gridDim = dim3(one ? 1u : (unsigned)kPlanCluster);
+    cfg.blockDim = dim3((unsigned)(threads < kPlanThreads ? threads : kPlanThreads));
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {(unsigned)ctas, 1, 1};
+    attr[0].val.clusterDim = {cfg.gridDim.x, 1, 1};
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = flags & 1u ? 2 : 1;
-    cudaError_t e = two ? cudaLaunchKernelEx(&cfg, plan_scan_kernel<false>, a) : cudaLaunchKernelEx(&cfg, plan_scan_kernel<true>, a);
+    const bool few = p.seqs <= (int64_t)kPlanCluster * kPlanThreads;  // one row a thread
+    const cudaError_t e = one   ? cudaLaunchKernelEx(&cfg, plan_scan_kernel<1, true, true>, a)
+                          : two ? (few ? cudaLaunchKernelEx(&cfg, plan_scan_kernel<1, false, false>, a)
+                                       : cudaLaunchKernelEx(&cfg, plan_scan_kernel<kPlanItems, false, false>, a))
+                                : (few ? cudaLaunchKernelEx(&cfg, plan_scan_kernel<1, true, false>, a)
+                                       : cudaLaunchKernelEx(&cfg, plan_scan_kernel<kPlanItems, true, false>, a));
     if (e != cudaSuccess || !two) return e;
     return layer_launch(plan_fill_kernel, dim3((unsigned)(4 * sms)), kFillThreads, 0, 1u, stream, a);
 }
