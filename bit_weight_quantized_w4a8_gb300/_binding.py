@@ -914,23 +914,50 @@ def kvq_attention(Q, cache, batch, mask=None, scale: float = None, out=None, ws=
 # a serving step around the layers
 # --------------------------------------------------------------------------
 
-def _one_device(first, *others):
-    """The tensors' device; raises where they lie on different ones or it is not
-    the current one, on whose stream the call would run."""
-    d = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != d:
-            raise ValueError("all tensors must be on one device")
-    if d != torch.cuda.current_device():
-        raise ValueError("the tensors are on cuda:%d, the current device is cuda:%d" % (d, torch.cuda.current_device()))
-    return first.device
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _scratch(ws, nbytes, device):
-    """The caller's workspace, or one of this call's own: the allocator hands it on in
-    the stream's order (in a captured graph: within the graph)."""
+def _device_of(t, name):
+    """The index of the tensor's device, which has to be the current one: the call runs
+    on its current stream."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    d = t.get_device()
+    if d < 0:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if d != _current_device():
+        raise ValueError("%s is on cuda:%d, the current device is cuda:%d" % (name, d, _current_device()))
+    return d
+
+
+def _arg(t, dtype, shape, name, dev):
+    """The address of a contiguous tensor of that type, shape and device."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape and \
+            t.is_contiguous():
+        return t.data_ptr()
+    _want(t, dtype, name, shape)
+    raise ValueError("all tensors must be on one device (%s is on %s)" % (name, t.device))
+
+
+def _optional(t, dtype, shape, name, dev):
+    return None if t is None else _arg(t, dtype, shape, name, dev)
+
+
+def _out(t, dtype, shape, name, dev, like):
+    """(tensor, address) of an output: the caller's, or a new one beside `like`."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+        return t, t.data_ptr()
+    return t, _arg(t, dtype, shape, name, dev)
+
+
+def _scratch(ws, nbytes, like):
+    """The caller's workspace as (tensor, bytes), or one of this call's own: the allocator
+    hands it on in the stream's order (in a captured graph: within the graph)."""
     if ws is None:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device), nbytes
+    if not isinstance(ws, torch.Tensor) or ws.get_device() != like.get_device():
+        raise ValueError("ws must be a tensor on the device of the others")
     return ws, ws.numel() * ws.element_size()
 
 
@@ -949,20 +976,22 @@ def kvq_pool(seqs: int, max_pages: int, pages: int, device="cuda") -> KVQPool:
     return KVQPool(table, held, stack, torch.full((1,), pages, dtype=torch.int32, device=device))
 
 
-def _pool_arg(p, page):
+def _pool_arg(p, page, dev):
     """(kvq_pool_t as bytes, seqs)"""
     table, held, stack, top = p
-    for t, name in ((table, "table"), (held, "held"), (stack, "stack"), (top, "top")):
-        _want(t, torch.int32, name)
-    if table.dim() != 2 or held.shape != table.shape[:1] or stack.dim() != 1 or top.shape != (1,):
+    if not isinstance(table, torch.Tensor) or not isinstance(stack, torch.Tensor):
+        raise TypeError("the pool's arrays must be torch tensors")
+    if table.dim() != 2 or stack.dim() != 1:
         raise ValueError("the pool must be table [seqs][max_pages], held [seqs], stack [pages], top [1]")
-    seqs, width = table.shape
-    return _pack_pool(table.data_ptr(), held.data_ptr(), stack.data_ptr(), top.data_ptr(), seqs, width, stack.shape[0],
+    (seqs, width), pages = table.shape, stack.shape[0]
+    i32 = torch.int32
+    return _pack_pool(_arg(table, i32, (seqs, width), "table", dev), _arg(held, i32, (seqs,), "held", dev),
+                      _arg(stack, i32, (pages,), "stack", dev), _arg(top, i32, (1,), "top", dev), seqs, width, pages,
                       page), seqs
 
 
 def kvq_plan_workspace_bytes(pool, page: int) -> int:
-    return int(lib().kvq_plan_workspace_bytes(_pool_arg(pool, page)[0]))
+    return int(lib().kvq_plan_workspace_bytes(_pool_arg(pool, page, _device_of(pool[0], "table"))[0]))
 
 
 def kvq_plan(pool, page: int, lens, add, tokens: int, grow=None, mask=None, cu=None, pos=None, slot=None, seq=None,
@@ -973,35 +1002,26 @@ def kvq_plan(pool, page: int, lens, add, tokens: int, grow=None, mask=None, cu=N
     (KVQBatch(cu, lens, pool.table), pos, slot, seq): positions int32 (with mask
     [tokens] int64: by depth in the drafted tree), rows of the pool int64 and
     rows of the batch int32 of the step's tokens."""
-    pa, seqs = _pool_arg(pool, page)
-    _want(lens, torch.int32, "lens", (seqs,))
-    _want(add, torch.int32, "add", (seqs,))
-    if grow is not None:
-        _want(grow, torch.int32, "grow", (seqs,))
-    if mask is not None:
-        _want(mask, torch.int64, "mask", (tokens,))
-    dev = _one_device(lens, *pool, add, grow, mask, cu, pos, slot, seq, ws)
-    cu = torch.empty((seqs + 1,), dtype=torch.int32, device=dev) if cu is None else cu
-    pos = torch.empty((tokens,), dtype=torch.int32, device=dev) if pos is None else pos
-    slot = torch.empty((tokens,), dtype=torch.int64, device=dev) if slot is None else slot
-    seq = torch.empty((tokens,), dtype=torch.int32, device=dev) if seq is None else seq
-    _want(cu, torch.int32, "cu", (seqs + 1,))
-    _want(pos, torch.int32, "pos", (tokens,))
-    _want(slot, torch.int64, "slot", (tokens,))
-    _want(seq, torch.int32, "seq", (tokens,))
+    dev = _device_of(lens, "lens")
+    pa, seqs = _pool_arg(pool, page, dev)
+    i32, n = torch.int32, (seqs,)
+    lp, ap, gp = _arg(lens, i32, n, "lens", dev), _arg(add, i32, n, "add", dev), _optional(grow, i32, n, "grow", dev)
+    n = (tokens,)
+    mp = _optional(mask, torch.int64, n, "mask", dev)
+    cu, cp = _out(cu, i32, (seqs + 1,), "cu", dev, lens)
+    pos, pp = _out(pos, i32, n, "pos", dev, lens)
+    slot, tp = _out(slot, torch.int64, n, "slot", dev, lens)
+    seq, qp = _out(seq, i32, n, "seq", dev, lens)
     L = lib()
-    ws, wsb = _scratch(ws, L.kvq_plan_workspace_bytes(pa), dev)
-    _check(L.kvq_plan(pa, lens.data_ptr(), _ptr(grow), add.data_ptr(), _ptr(mask), tokens, cu.data_ptr(), pos.data_ptr(),
-                      slot.data_ptr(), seq.data_ptr(), ws.data_ptr(), wsb, flags, _stream(lens)))
+    ws, wsb = _scratch(ws, L.kvq_plan_workspace_bytes(pa), lens)
+    _check(L.kvq_plan(pa, lp, gp, ap, mp, tokens, cp, pp, tp, qp, ws.data_ptr(), wsb, flags, _stream(lens)))
     return KVQBatch(cu, lens, pool[0]), pos, slot, seq
 
 
-def _want_rows(t, name, shape):
+def _want_rows(t, name, shape, dev):
     """[rows][cols] with contiguous columns, rows at any distance; returns the distance."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch tensor" % name)
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.get_device() != dev:
+        raise ValueError("%s must be on the device of the others" % name)
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     n, v = shape
@@ -1030,33 +1050,24 @@ def draft_verify(logits, cu, ids, u, mask=None, q=None, temp=None, keep=None, ou
     lt = _want_type(logits, "logits")
     if logits.dim() != 2:
         raise ValueError("logits must be [tokens][vocab]")
+    dev = _device_of(logits, "logits")
     n, v = logits.shape
-    ld = _want_rows(logits, "logits", (n, v))
-    _want(cu, torch.int32, "cu")
-    if cu.dim() != 1 or cu.shape[0] < 2:
-        raise ValueError("cu must be [seqs + 1]")
-    seqs = cu.shape[0] - 1
-    _want(ids, torch.int32, "ids", (n,))
-    _want(u, torch.float32, "u", (n,))
-    if mask is not None:
-        _want(mask, torch.int64, "mask", (n,))
-    if temp is not None:
-        _want(temp, torch.float32, "temp", (seqs,))
+    ld = _want_rows(logits, "logits", (n, v), dev)
+    if not isinstance(cu, torch.Tensor) or cu.dim() != 1 or cu.shape[0] < 2:
+        raise ValueError("cu must be a tensor [seqs + 1]")
+    seqs, i32, f32 = cu.shape[0] - 1, torch.int32, torch.float32
+    cp, ip, up = _arg(cu, i32, (seqs + 1,), "cu", dev), _arg(ids, i32, (n,), "ids", dev), _arg(u, f32, (n,), "u", dev)
+    mp, tp = _optional(mask, torch.int64, (n,), "mask", dev), _optional(temp, f32, (seqs,), "temp", dev)
     qt = ld_q = 0
     if q is not None:
         qt = _want_type(q, "q")
-        ld_q = _want_rows(q, "q", (n, v))
-    dev = _one_device(logits, cu, ids, u, mask, q, temp, keep, out, count, ws)
-    keep = torch.empty((n,), dtype=torch.int32, device=dev) if keep is None else keep
-    out = torch.empty((n,), dtype=torch.int32, device=dev) if out is None else out
-    count = torch.empty((seqs,), dtype=torch.int32, device=dev) if count is None else count
-    _want(keep, torch.int32, "keep", (n,))
-    _want(out, torch.int32, "out", (n,))
-    _want(count, torch.int32, "count", (seqs,))
+        ld_q = _want_rows(q, "q", (n, v), dev)
+    keep, kp = _out(keep, i32, (n,), "keep", dev, ids)
+    out, op = _out(out, i32, (n,), "out", dev, ids)
+    count, np = _out(count, i32, (seqs,), "count", dev, ids)
     L = lib()
-    ws, wsb = _scratch(ws, L.draft_verify_workspace_bytes(n, v), dev)
-    _check(L.draft_verify(logits.data_ptr(), lt, ld, v, cu.data_ptr(), seqs, n, ids.data_ptr(), _ptr(mask), _ptr(q), qt,
-                          ld_q, _ptr(temp), u.data_ptr(), keep.data_ptr(), out.data_ptr(), count.data_ptr(),
+    ws, wsb = _scratch(ws, L.draft_verify_workspace_bytes(n, v), ids)
+    _check(L.draft_verify(logits.data_ptr(), lt, ld, v, cp, seqs, n, ip, mp, _ptr(q), qt, ld_q, tp, up, kp, op, np,
                           ws.data_ptr(), wsb, flags, _stream(logits)))
     return keep, out, count
 
@@ -1074,50 +1085,54 @@ def _f8_blocks(n: int) -> int:
 
 def f8_quantize_weights(W, Wf=None, sw=None):
     """W [N][K] fp32 -> (Wf [N][K] uint8 (e4m3), sw [ceil(N/128)][ceil(K/128)] fp32)."""
-    _want(W, torch.float32, "W")
+    dev = _device_of(W, "W")
     if W.dim() != 2:
         raise ValueError("W must have two dimensions")
     N, K = W.shape
-    dev = _one_device(W, Wf, sw)
-    Wf = torch.empty((N, K), dtype=torch.uint8, device=dev) if Wf is None else Wf
-    sw = torch.empty((_f8_blocks(N), _f8_blocks(K)), dtype=torch.float32, device=dev) if sw is None else sw
-    _want(Wf, torch.uint8, "Wf", (N, K))
-    _want(sw, torch.float32, "sw", (_f8_blocks(N), _f8_blocks(K)))
-    _check(lib().f8_quantize_weights(W.data_ptr(), N, K, Wf.data_ptr(), sw.data_ptr(), _stream(W)))
+    wp = _arg(W, torch.float32, (N, K), "W", dev)
+    blocks = (_f8_blocks(N), _f8_blocks(K))
+    Wf, fp = _out(Wf, torch.uint8, (N, K), "Wf", dev, W)
+    sw, sp = _out(sw, torch.float32, blocks, "sw", dev, W)
+    _check(lib().f8_quantize_weights(wp, N, K, fp, sp, _stream(W)))
     return Wf, sw
+
+
+def _f8_rows(X):
+    """(type, M, K, address, device)"""
+    xt = _want_type(X, "X")
+    if X.dim() != 2:
+        raise ValueError("X must have two dimensions")
+    dev = _device_of(X, "X")
+    M, K = X.shape
+    return xt, M, K, _arg(X, X.dtype, (M, K), "X", dev), dev
 
 
 def f8_quantize_rows(X, Xf=None, sa=None, flags: int = 0):
     """X [M][K] fp32 or fp16 -> (Xf [M][K] uint8 (e4m3), sa [ceil(K/128)][M] fp32)."""
-    xt = _want_type(X, "X")
-    _want(X, X.dtype, "X")
-    if X.dim() != 2:
-        raise ValueError("X must have two dimensions")
-    M, K = X.shape
-    dev = _one_device(X, Xf, sa)
-    Xf = torch.empty((M, K), dtype=torch.uint8, device=dev) if Xf is None else Xf
-    sa = torch.empty((_f8_blocks(K), M), dtype=torch.float32, device=dev) if sa is None else sa
-    _want(Xf, torch.uint8, "Xf", (M, K))
-    _want(sa, torch.float32, "sa", (_f8_blocks(K), M))
-    _check(lib().f8_quantize_rows(X.data_ptr(), xt, M, K, Xf.data_ptr(), sa.data_ptr(), flags, _stream(X)))
+    xt, M, K, xp, dev = _f8_rows(X)
+    scales = (_f8_blocks(K), M)
+    Xf, fp = _out(Xf, torch.uint8, (M, K), "Xf", dev, X)
+    sa, sp = _out(sa, torch.float32, scales, "sa", dev, X)
+    _check(lib().f8_quantize_rows(xp, xt, M, K, fp, sp, flags, _stream(X)))
     return Xf, sa
 
 
-def _f8_weights(Wf, sw, K):
-    _want(Wf, torch.uint8, "Wf")
-    if Wf.dim() != 2 or Wf.shape[1] != K:
-        raise ValueError("Wf must be [N][%d]" % K)
+def _f8_weights(Wf, sw, K, dev):
+    """(N, address of Wf, address of sw)"""
+    if not isinstance(Wf, torch.Tensor) or Wf.dim() != 2 or Wf.shape[1] != K:
+        raise ValueError("Wf must be a tensor [N][%d]" % K)
     N = Wf.shape[0]
-    _want(sw, torch.float32, "sw", (_f8_blocks(N), _f8_blocks(K)))
-    return N
+    return N, _arg(Wf, torch.uint8, (N, K), "Wf", dev), _arg(sw, torch.float32, (_f8_blocks(N), _f8_blocks(K)), "sw", dev)
 
 
-def _f8_out(Y, shape, dtype, device):
-    if Y is None:
-        Y = torch.empty(shape, dtype=dtype, device=device)
-    yt = _want_type(Y, "Y")
-    _want(Y, Y.dtype, "Y", shape)
-    return Y, yt
+def _f8_out(Y, shape, dtype, like, dev):
+    """(Y, type, address)"""
+    if Y is not None:
+        dtype = Y.dtype if isinstance(Y, torch.Tensor) else None
+    if dtype not in _TYPES:
+        raise TypeError("Y must be float32 or float16, got %s" % dtype)
+    Y, yp = _out(Y, dtype, shape, "Y", dev, like)
+    return Y, _TYPES[dtype], yp
 
 
 def f8_linear_workspace_bytes(M: int, K: int, N: int) -> int:
@@ -1127,34 +1142,26 @@ def f8_linear_workspace_bytes(M: int, K: int, N: int) -> int:
 def f8_gemm(Xf, sa, Wf, sw, dtype=torch.float32, Y=None, flags: int = 0):
     """Y [M][N] (fp32 or fp16): the product of e4m3 codes with a scale for each row
     and 128 values of X and each 128 x 128 block of W."""
-    _want(Xf, torch.uint8, "Xf")
+    dev = _device_of(Xf, "Xf")
     if Xf.dim() != 2:
         raise ValueError("Xf must have two dimensions")
     M, K = Xf.shape
-    _want(sa, torch.float32, "sa", (_f8_blocks(K), M))
-    N = _f8_weights(Wf, sw, K)
-    dev = _one_device(Xf, sa, Wf, sw, Y)
-    Y, yt = _f8_out(Y, (M, N), dtype, dev)
-    _check(lib().f8_gemm(Xf.data_ptr(), sa.data_ptr(), M, K, Wf.data_ptr(), sw.data_ptr(), N, Y.data_ptr(), yt, flags,
-                         _stream(Xf)))
+    xp, ap = _arg(Xf, torch.uint8, (M, K), "Xf", dev), _arg(sa, torch.float32, (_f8_blocks(K), M), "sa", dev)
+    N, wp, sp = _f8_weights(Wf, sw, K, dev)
+    Y, yt, yp = _f8_out(Y, (M, N), dtype, Xf, dev)
+    _check(lib().f8_gemm(xp, ap, M, K, wp, sp, N, yp, yt, flags, _stream(Xf)))
     return Y
 
 
 def f8_linear(X, Wf, sw, dtype=torch.float32, Y=None, ws=None, flags: int = 0):
     """f8_quantize_rows and f8_gemm in one call: X [M][K] fp32 or fp16, any number
     of rows; Y [M][N] fp32 or fp16."""
-    xt = _want_type(X, "X")
-    _want(X, X.dtype, "X")
-    if X.dim() != 2:
-        raise ValueError("X must have two dimensions")
-    M, K = X.shape
-    N = _f8_weights(Wf, sw, K)
-    dev = _one_device(X, Wf, sw, Y, ws)
-    Y, yt = _f8_out(Y, (M, N), dtype, dev)
+    xt, M, K, xp, dev = _f8_rows(X)
+    N, wp, sp = _f8_weights(Wf, sw, K, dev)
+    Y, yt, yp = _f8_out(Y, (M, N), dtype, X, dev)
     L = lib()
-    ws, wsb = _scratch(ws, L.f8_linear_workspace_bytes(M, K, N), dev)
-    _check(L.f8_linear(X.data_ptr(), xt, M, K, Wf.data_ptr(), sw.data_ptr(), N, Y.data_ptr(), yt, ws.data_ptr(), wsb,
-                       flags, _stream(X)))
+    ws, wsb = _scratch(ws, L.f8_linear_workspace_bytes(M, K, N), X)
+    _check(L.f8_linear(xp, xt, M, K, wp, sp, N, yp, yt, ws.data_ptr(), wsb, flags, _stream(X)))
     return Y
 
 
