@@ -20,7 +20,7 @@
 // roundings would decide between neighbours now and then.  So the fp32 sums only
 // decide where the number lies further from the token's two edges than they can be off: by
 // at most kOff Z, counted at its definition.  Otherwise the row's weights are taken as integers:
-// w / 2^ceil(max) in units of 2^-40, each within a few units of the exact value (the
+// w in units of 2^-40 of the largest, each within a few units of the exact value (the
 // exponent's argument in two floats, a table of 2^(i/128), a polynomial of four terms), so
 // that sums are exact, in any order and split.  That is 40 instructions a weight; on 24
 // rows of 152064 the draw took 34 us with integers alone.
@@ -214,16 +214,17 @@ struct Pow2Table {
 __device__ const Pow2Table kPow2{};  // (in constant memory its divergent reads came one by one)
 
 struct Unit {
-    float hi, lo, ref;  // log2(e) / T, the whole power of two above the largest weight
+    float hi, lo, top;  // log2(e) / T, the row's maximum
 };
 
-// exp2(l c - ref) in units of 2^-40, 0 below half a unit.
+// exp((l - top) / T) in units of 2^-40, 0 below half a unit.
 __device__ __forceinline__ uint64_t weight(float l, const Unit& s, const uint64_t* pow2) {
     constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
-    const float p = l * s.hi;
-    const float e = fmaf(l, s.lo, fmaf(l, s.hi, -p));
-    const float d = p - s.ref;  // exact where it is above -41
+    // the difference in two floats, before it is scaled: logits near the type's ends must not overflow
+    const float dh = l - s.top, b = dh - l, dl = (l - (dh - b)) - (s.top + b);
+    const float d = dh * s.hi;
     if (!(d > -41.f)) return 0;
+    const float e = fmaf(dl, s.hi, fmaf(dh, s.lo, fmaf(dh, s.hi, -d)));
     const float t = fmaf(d, 128.f, kMagic);
     const int k = __float_as_int(t) - __float_as_int(kMagic);  // nearest 1/128
     const float r = fmaf(t - kMagic, -1.f / 128.f, d);         // exact, |r| <= 1/256
@@ -571,7 +572,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
     float gone = 0.f;                                          // weights of the refused
     uint64_t cut = 0;
     auto exact = [&](uint64_t by) {
-        return typename Draw<T>::Exact{{c.hi, c.lo, ceilf(s.row[node].top * c.hi)}, by, s.pow2, by != 0};
+        return typename Draw<T>::Exact{{c.hi, c.lo, s.row[node].top}, by, s.pow2, by != 0};
     };
     auto make_cuts = [&]() {
         while (cuts < todo) {

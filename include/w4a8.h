@@ -728,7 +728,7 @@ int kvq_plan(const kvq_pool_t* pool, int32_t* lens, const int32_t* grow, const i
  *     sequence's cache grows by (kvq_plan's grow); 0 for a sequence without tokens.
  * Rows of tokens that no sequence holds are left as they are.
  * Arithmetic: tests in fp32 (sums of fp32 weights over the vocabulary, relative error below
- * 2^-18); the draw on integer weights in units of 2^-40 of the largest weight's power of two, each within 4
+ * 2^-18); the draw on integer weights in units of 2^-40 of the largest weight, each within 4
  * units, whose sums are exact: the same call gives the same tokens.
  * -infinity takes a token out; a row that holds a NaN, +infinity or nothing but -infinity has
  * no distribution: its children are refused, the token drawn is -1.  A draft outside the vocabulary
