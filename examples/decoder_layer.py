@@ -1,6 +1,8 @@
 """One decoder layer on the quantized linears, from residual to residual:
-decoding token by token, and verifying a tree of drafted tokens whose accepted
-branch stays in the cache.
+decoding token by token, verifying a tree of drafted tokens whose accepted
+branch stays in the cache, and serving several requests: prompts with images on
+the linears for many rows, then drafted steps whose pages, positions and accepted tokens
+never leave the GPU.
 
     python examples/decoder_layer.py [--hidden 3584 --heads 28 --kv-heads 4 --inner 18944]
 
@@ -24,13 +26,18 @@ import bit_weight_quantized_w4a8_gb300 as w4  # noqa: E402
 class DecoderLayer:
     """norm, q/k/v, rotary positions and cache, attention, o, norm, gated MLP."""
 
-    def __init__(self, hidden, heads, kv_heads, dim, inner, base=1e6, seed=0, device="cuda"):
+    def __init__(self, hidden, heads, kv_heads, dim, inner, base=1e6, seed=0, device="cuda", prompts=False):
+        """prompts: keeps the weights as e4m3 blocks too, for calls of more than 64 rows."""
         self.heads, self.kv_heads, self.dim = heads, kv_heads, dim
         g = torch.Generator(device=device)
         g.manual_seed(seed)
+        self.f8 = []  # q, k, v, o, gate, up, down
 
         def weight(n, k):
-            return w4.w4_quantize_weights(torch.randn((n, k), generator=g, device=device) * k ** -0.5)
+            w = torch.randn((n, k), generator=g, device=device) * k ** -0.5
+            if prompts:
+                self.f8.append(w4.f8_quantize_weights(w))
+            return w4.w4_quantize_weights(w)
 
         self.qkv = [weight(n * dim, hidden) for n in (heads, kv_heads, kv_heads)]
         self.o = weight(hidden, heads * dim)
@@ -38,6 +45,21 @@ class DecoderLayer:
         self.down = weight(hidden, inner)
         self.norm1, self.norm2 = (1 + 0.1 * torch.randn(hidden, generator=g, device=device) for _ in range(2))
         self.freqs, self.mscale = w4.rope_frequencies(dim, base, device=device)
+
+    def prompt(self, r, y, cache, batch, pos, axis=None, trace=None):
+        """step for any number of rows, on the e4m3 weights; with axis, pos is [axes][M]."""
+        M = r.shape[0]
+        r1, x1 = w4.add_norm(r, self.norm1, y=y)
+        q, k, v = (w4.f8_linear(x1, *w).view(M, -1, self.dim) for w in self.f8[:3])
+        qr = w4.kvq_write(cache, batch, k, v, Q=q, pos=pos, freqs=self.freqs, mscale=self.mscale, axis=axis)
+        a = w4.kvq_attention(qr, cache, batch)
+        yo = w4.f8_linear(a.view(M, -1), *self.f8[3])
+        r2, x2 = w4.add_norm(r1, self.norm2, y=yo)
+        h = w4.w4a8_silu_mul(*(w4.f8_linear(x2, *w) for w in self.f8[4:6]))
+        yd = w4.f8_linear(h, *self.f8[6])
+        if trace is not None:
+            trace.update(r1=r1, x1=x1, q=q, k=k, v=v, qr=qr, a=a, yo=yo, r2=r2, x2=x2, h=h, yd=yd)
+        return r2, yd
 
     def step(self, r, y, cache, batch, pos, mask=None, trace=None):
         """r [M][hidden] fp32 residual, y the block before's output (or None), M <=
@@ -90,6 +112,56 @@ def verify_tree(layer, cache, table, context, parents, accepted, r):
     return r2, y, context + len(accepted)
 
 
+class Server:
+    """Requests decoded together: each call plans its step from the lengths, runs the layer
+    and leaves on the device what the next call goes on from."""
+
+    def __init__(self, layer, vocab, seqs, max_pages, pages, page=64, bits=8, seed=1, device="cuda"):
+        g = torch.Generator(device=device)
+        g.manual_seed(seed)
+        hidden = layer.norm1.shape[0]
+        self.layer, self.page = layer, page
+        self.embed = torch.randn((vocab, hidden), generator=g, device=device)
+        self.head = w4.w4_quantize_weights(torch.randn((vocab, hidden), generator=g, device=device) * 3 * hidden ** -0.5)
+        self.norm = torch.ones(hidden, device=device)
+        self.cache = w4.kvq_cache(pages, page, layer.kv_heads, layer.dim, bits, device)
+        self.pool = w4.kvq_pool(seqs, max_pages, pages, device)
+        self.lens, self.grow = (torch.zeros(seqs, dtype=torch.int32, device=device) for _ in range(2))
+
+    def logits(self, r, y):
+        return w4.w4a8_linear(w4.add_norm(r, self.norm, y=y)[1], *self.head)
+
+    def prompt(self, add, x, pos, axis):
+        """x [tokens][hidden]: the rows of add [seqs] new tokens each (0: none, -1: the
+        request ended), pos [axes][tokens].  Returns the logits of each request's last token."""
+        batch, *_ = w4.kvq_plan(self.pool, self.page, self.lens, add, x.shape[0], grow=self.grow)
+        r, y = self.layer.prompt(x, None, self.cache, batch, pos, axis)
+        self.grow = (batch.cu[1:] - batch.cu[:-1]).contiguous()  # a request that had to wait has grown by nothing
+        last = (batch.cu[1:] - 1).clamp_min(0).long()
+        return self.logits(r[last], y[last])
+
+    def step(self, add, ids, mask, u, temp, trace=None):
+        """ids [tokens]: of each request its last token, then its drafts, a tree by mask.
+        Returns what draft_verify does."""
+        batch, pos, slot, seq = w4.kvq_plan(self.pool, self.page, self.lens, add, ids.shape[0], grow=self.grow, mask=mask)
+        r, y = self.layer.step(self.embed[ids.long()], None, self.cache, batch, pos, mask)
+        logits = self.logits(r, y)
+        keep, out, count = w4.draft_verify(logits, batch.cu, ids, u, mask=mask, temp=temp)
+        if trace is not None:
+            trace.update(batch=batch, pos=pos, slot=slot, seq=seq, logits=logits, before=w4.kvq_read(self.cache, batch, ids.shape[0]))
+        w4.kvq_keep(self.cache, batch, keep)
+        self.grow = count
+        return keep, out, count
+
+
+def image_positions(rows, cols, text):
+    """Positions of an image's rows x cols tokens and `text` tokens behind it on three axes
+    (time, height, width): the text goes on from the largest one on all of them."""
+    h, w = (t.reshape(-1) for t in torch.meshgrid(torch.arange(rows), torch.arange(cols), indexing="ij"))
+    image = torch.stack((torch.zeros_like(h), h, w))
+    return torch.cat((image, (max(rows, cols) + torch.arange(text)).expand(3, text)), 1).to(torch.int32)
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--hidden", type=int, default=3584)
@@ -129,6 +201,29 @@ def main():
     r2, y, context = verify_tree(layer, cache, table, a.tokens, parents, [0, 2, 5], rt)
     assert torch.isfinite(y).all() and w4.w4a8_device_error() == 0
     print("a tree of %d tokens verified, 3 accepted: %d tokens cached" % (len(parents), context))
+    # three requests: prompts with an image, then steps of a tree of drafts each
+    layer = DecoderLayer(a.hidden, a.heads, a.kv_heads, a.dim, a.inner, prompts=True)
+    seqs, sizes = 3, (100, 164, 72)
+    server = Server(layer, 1000, seqs, 16, 48, bits=a.bits)
+    add = torch.tensor(sizes, dtype=torch.int32, device="cuda")
+    pos = torch.cat([image_positions(8, 8, n - 64) for n in sizes], 1).cuda()
+    pairs = a.dim // 2
+    axis = w4.rope_axes((pairs - 2 * (3 * pairs // 8), 3 * pairs // 8, 3 * pairs // 8))
+    logits = server.prompt(add, torch.randn((sum(sizes), a.hidden), device="cuda"), pos, axis)
+    roots = logits.argmax(1)
+    parents = [-1, 0, 0, 1, 1, 2]
+    mask = tree_mask(parents).cuda().repeat(seqs)
+    add.fill_(len(parents))
+    temp = torch.full((seqs,), 0.8, device="cuda")
+    said = 0
+    for _ in range(4):
+        ids = torch.randint(0, 1000, (seqs, len(parents)), device="cuda", dtype=torch.int32)
+        ids[:, 0] = roots
+        keep, out, count = server.step(add, ids.reshape(-1), mask, torch.rand(ids.numel(), device="cuda"), temp)
+        roots = out.view(seqs, -1).gather(1, (count.long() - 1)[:, None])[:, 0]
+        said += int(count.sum())
+    assert w4.w4a8_device_error() == 0
+    print("%d requests served: %d tokens of prompts, %d tokens said in 4 steps" % (seqs, sum(sizes), said))
 
 
 if __name__ == "__main__":
