@@ -132,8 +132,9 @@ template <typename T>
 __global__ void __launch_bounds__(kVerifyThreads) verify_rows_kernel(const VerifyArgs a) {
     constexpr int U = 4;  // runs of 4 under way
     __shared__ RowPart part[kVerifyWarps];
-    griddep_launch_dependents();
+    // in this order: when the second launch starts, what the caller's kernels wrote is there
     griddep_wait();
+    griddep_launch_dependents();
     const int t = blockIdx.x;
     const T* row = static_cast<const T*>(a.L) + t * a.ld_l;
     const bool wide = row_wide(row);
@@ -239,16 +240,18 @@ __device__ __forceinline__ uint64_t weight(float l, const Unit& s, const uint64_
     return ((uint64_t)v + ((uint64_t)1 << n >> 1)) >> n;
 }
 
-// floor(f a) for f in [0, 1]; 0 for a negative f or NaN.
+// f a for f in [0, 1], to nearest (cut off instead, 10^5 weights less q A would all lean to one
+// side, and their sum by as many halves of a unit); from f = 2^-8 on within 2^-32 of it.
+// 0 for a negative f or NaN.
 __device__ __forceinline__ uint64_t part_of(float f, uint64_t a) {
     if (!(f > 0.f)) return 0;
     if (f >= 1.f) return a;
     const uint32_t bits = __float_as_uint(f);
     const int ex = bits >> 23;  // f = m 2^-sh
-    const uint64_t m = (bits & 0x7FFFFFu) | (ex != 0 ? 0x800000u : 0u);
+    const uint32_t m = (bits & 0x7FFFFFu) | (ex != 0 ? 0x800000u : 0u);
     const int sh = 150 - (ex != 0 ? ex : 1);  // 24 .. 149
-    const uint64_t hi = __umul64hi(a, m), lo = a * m;
-    return sh < 64 ? hi << (64 - sh) | lo >> sh : sh < 128 ? hi >> (sh - 64) : 0;
+    const uint64_t p = ((uint64_t)(uint32_t)(a >> 32) * m << 1) + ((uint64_t)(uint32_t)a * m >> 31);  // a m 2^-31
+    return sh < 32 ? p << (31 - sh) : sh < 90 ? ((p >> (sh - 32)) + 1) >> 1 : 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -297,6 +300,7 @@ struct Draw {
     uint64_t* sums;
     const Scale c;
     int rank, s0, s1, passes;
+    bool open;               // another CTA may still read this one's sums
     uint64_t before, total;  // of the CTAs ahead; of all
     float q_total;
 
@@ -422,6 +426,7 @@ struct Draw {
             if (r < rank) before += x;
             total += x;
         }
+        open = true;
     }
 
     // The first token whose cumulative sum passes `target` by more than `off`, the token before
@@ -493,14 +498,15 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
     __shared__ DrawShared s;
     cg::cluster_group cl = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, rank = (int)cl.block_rank();
+    // All that does not come from the first launch is fetched while that one runs: offsets, drafts
+    // and their logits at their parents.
     if (tid < 128) s.pow2[tid] = kPow2.v[tid];
     if (tid == 0) s.verdict = -1;
-    griddep_launch_dependents();
-    griddep_wait();
     const int b = blockIdx.x / kVerifyCluster;
     const int first = a.cu[b], end = a.cu[b + 1], n = end - first;
     const bool sound = first >= 0 && n >= 0 && end <= a.tokens;
     if (!sound || n == 0 || n > kMaxDrafts) {  // the whole cluster
+        griddep_wait();  // (the next kernel must not overtake the first launch)
         if (rank == 0) {
             if (tid == 0) {
                 a.count[b] = 0;
@@ -512,26 +518,38 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
         return;
     }
     const Scale c = scale_of(a.temp, b);
+    int up = tid - 1, id = -1;
+    float l = -INFINITY, q = 0.f;
     if (tid < n) {
         const int64_t t = first + tid;
+        id = a.ids[t];
         s.u[tid] = a.u[t];
-        s.id[tid] = a.ids[t];
-        int up = tid - 1;
+        s.id[tid] = id;
         if (a.mask != nullptr) {  // the ancestor drafted last
             const uint64_t below = a.mask[t] & (((uint64_t)1 << tid) - 1);
             up = 63 - __clzll((long long)below);  // -1: none
         }
         s.parent[tid] = up;
+        if (tid == 0 || up < 0 || id < 0 || id >= a.vocab) id = -1;
+        if (id >= 0) {
+            l = load1(static_cast<const T*>(a.L) + (first + up) * a.ld_l + id);
+            if (a.Q != nullptr) {
+                const int64_t i = (first + up) * a.ld_q + id;
+                q = a.q_f16 ? __half2float(static_cast<const __half*>(a.Q)[i]) : static_cast<const float*>(a.Q)[i];
+            }
+        }
     }
+    griddep_launch_dependents();
+    griddep_wait();
     #pragma unroll 1
     for (int r = warp; r < n; r += blockDim.x / 32) {  // a row's slices, one a lane
         RowPart p = {-INFINITY, 0.f, 0x7FFFFFFF, 0};
         if (lane < a.slices) p = a.parts[(int64_t)(first + r) * a.slices + lane];
         #pragma unroll 1
         for (int o = 16; o >= 1; o /= 2) {
-            const RowPart q = {__shfl_xor_sync(0xFFFFFFFFu, p.top, o), __shfl_xor_sync(0xFFFFFFFFu, p.sum, o),
+            const RowPart x = {__shfl_xor_sync(0xFFFFFFFFu, p.top, o), __shfl_xor_sync(0xFFFFFFFFu, p.sum, o),
                                __shfl_xor_sync(0xFFFFFFFFu, p.at, o), 0};
-            join(p, q, c.hi);
+            join(p, x, c.hi);
         }
         if (lane == 0) {
             if (!(p.top > -INFINITY)) p.sum = NAN;
@@ -540,14 +558,8 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
     }
     __syncthreads();
     if (tid > 0 && tid < n) {
-        const int up = s.parent[tid], id = s.id[tid];
-        float w = 0.f, q = 0.f;
-        if (up >= 0 && id >= 0 && id < a.vocab) {
-            const float l = load1(static_cast<const T*>(a.L) + (first + up) * a.ld_l + id);
-            if (a.Q != nullptr) {
-                const int64_t i = (first + up) * a.ld_q + id;
-                q = a.q_f16 ? __half2float(static_cast<const __half*>(a.Q)[i]) : static_cast<const float*>(a.Q)[i];
-            }
+        float w = 0.f;
+        if (id >= 0) {
             const float d = l - s.row[up].top;
             const float x = d * c.hi, e = fmaf(d, c.lo, fmaf(d, c.hi, -x));
             w = exp2f(x) * fmaf(e, 0.693147182f, 1.f);  // (NaN for a row of no use: every test fails)
@@ -564,6 +576,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
     dr.s0 = min(rank * seg_per, a.seg_count);
     dr.s1 = min(dr.s0 + seg_per, a.seg_count);
     dr.passes = 0;
+    dr.open = false;
     dr.total = 0;
 
     // Every thread of the cluster takes the same way through this: it depends on
@@ -580,7 +593,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
                 dr.pass(first + node, exact(0), 0);
                 cut = dr.total;
             } else {
-                cut += dr.total;
+                cut = cut + dr.total < cut ? ~(uint64_t)0 : cut + dr.total;
             }
             if (cut == 0) break;
             dr.pass(first + node, exact(cut), 0);
@@ -630,7 +643,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
     const int64_t t = first + node;
     const float u = s.u[0] < 1.f ? s.u[0] : 0x1.fffffep-1f;
     int next = -1;
-    bool mine = rank == 0 && tid == 0, shared = false;
+    bool mine = rank == 0 && tid == 0;
     if (p.sum == p.sum && c.greedy) {
         next = p.at;
     } else if (p.sum == p.sum) {
@@ -643,10 +656,10 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
             if (x >= 0)
                 for (int r = 0; r < kVerifyCluster; ++r) *cl.map_shared_rank(&s.verdict, r) = x;
             cl.sync();
+            dr.open = false;
             next = s.verdict;
         }
         if (next < 0) {
-            shared = true;
             make_cuts();
             if (todo == 0) dr.pass(t, exact(0), refused);
             if (dr.total == 0 && (todo != 0 || refused != 0)) {  // nothing left but roundings: the whole row
@@ -667,7 +680,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
             if (tid != taken - 1) a.out[first + tid] = tid < taken - 1 ? s.id[s.taken[tid + 1]] : -1;
         }
     }
-    if (shared) cl.sync();  // no CTA leaves while its sums may be read
+    if (dr.open) cl.sync();  // no CTA leaves while its sums may be read
 }
 
 int verify_slices(int64_t tokens, int64_t vocab, int sms) {

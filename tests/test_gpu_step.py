@@ -1,6 +1,8 @@
 """A serving step's operators on the GPU against plain 64-bit references
 (step_ref.py): within bounds counted from their roundings, and equal where what
 comes out is whole numbers.  Outputs lie between guard bytes."""
+import math
+
 import numpy as np
 import pytest
 
@@ -414,6 +416,56 @@ def test_draft_verify_bad_offsets(w4):
     for cu in ([0, 7], [-1, 3], [4, 2], [0, 2 ** 31 - 1]):
         got = run_verify(w4, logits, np.array(cu, I32), ids, u)
         assert got[2][0] == 0 and w4.w4a8_device_error() == RANGE
+
+
+def test_draft_verify_refusals_before_a_row_of_no_use(w4):
+    """Two siblings refused over the whole row, then a third taken whose own row holds no distribution:
+    the next token is -1."""
+    rng = np.random.default_rng(18)
+    seqs, v = 24, 20000
+    logits = rng.standard_normal((4 * seqs, v)).astype(F32)
+    q = np.exp(rng.standard_normal((4 * seqs, v)))
+    q[:, 7] = 0
+    q = (q / q.sum(1, keepdims=True)).astype(F32)
+    ids, u = np.zeros(4 * seqs, I32), rng.random(4 * seqs).astype(F32)
+    for b in range(seqs):
+        ids[4 * b + 1:4 * b + 3] = np.argsort(q[4 * b] / sref.distribution(logits[4 * b], 1.0))[-2:]
+        ids[4 * b + 3] = 7
+    logits[3::4] = np.nan
+    u[1::4] = u[2::4] = 0.999
+    mask = np.tile(np.array([1, 3, 5, 9], np.uint64).view(I64), seqs)
+    cu = np.arange(0, 4 * seqs + 1, 4, dtype=I32)
+    got = run_verify(w4, logits, cu, ids, u, mask, q)
+    same(got, sref.verify(logits, cu, ids, u, mask, q))
+    assert np.all(got[2] == 2) and np.all(got[1].reshape(seqs, 4)[:, :2] == [7, -1])
+
+
+def test_draft_verify_roundings_of_a_long_tail_do_not_add_up(w4):
+    """A draw among 2^20 tokens that hold 2^-29 of the largest weight each, of which the draft's
+    probabilities leave about half: some 2^10 of the units of 2^-40 that the sums are made of.  A weight is
+    the difference of two numbers rounded to nearest, off by at most a unit and by 0.41 in the root mean
+    square, so that a sum over 2^20 is off by about 420 units, half a token; six times that are less than 3
+    tokens.  Numbers all cut off on one side would be off by up to 2^19 units, hundreds of tokens."""
+    g = torch.Generator(device="cuda").manual_seed(19)
+    seqs, v = 16, 2 ** 20
+    logits = -20 + 0.1 * torch.randn((2 * seqs, v), device="cuda", generator=g)
+    logits[:, 0] = 0
+    logits[:, v - 1] = -20 + math.log(v)
+    p = torch.softmax(logits.double(), 1)
+    q = p * (0.3 + 0.4 * torch.rand((2 * seqs, v), device="cuda", generator=g))
+    q[:, v - 1] = 0
+    q[:, 0] = 0
+    q[:, 0] = 1 - q.sum(1)
+    q = q.float()
+    u = torch.full((2 * seqs,), 0.99999, device="cuda")
+    u[::2] = torch.linspace(0.01, 0.3, seqs, device="cuda")
+    cu = torch.arange(0, 2 * seqs + 1, 2, dtype=torch.int32, device="cuda")
+    keep, out, count = w4.draft_verify(logits, cu, torch.zeros(2 * seqs, dtype=torch.int32, device="cuda"), u, q=q)
+    run = (p[::2] - q[::2].double()).clamp_min(0).cumsum(1)
+    want = torch.searchsorted(run, u[::2, None].double() * run[:, -1:], right=True)[:, 0]
+    assert bool((count == 1).all()) and bool((want < v - 1).all())
+    off = (out[::2].long() - want).abs().max()
+    assert int(off) <= 3, off
 
 
 def test_draft_verify_follows_the_target(w4):
