@@ -10,54 +10,49 @@ namespace {
 
 constexpr int kF8Threads = 256;
 
-// Sixteen lanes a (row, block of 128), 8 values a lane; a CTA has 8 rows x 2 U blocks, so that
-// the scales, a block's of all rows side by side, leave in runs of 32 bytes.
+// Sixteen lanes a (row, block of 128), 8 values a lane; a CTA has 8 rows x 2 blocks, so that the
+// scales, a block's of all rows side by side, leave in runs of 32 bytes.  One launch in a graph: 1 x 3584
+// 2.2 us, 777 x 4096 4.3, 8192 x 3584 23.5 (3.8 TB/s; a warp a row and block, with the scales one by one, 38);
+// four blocks a group of lanes gain 3% there and cost 16 rows half as much again.  What bounds it is the two roundings of
+// each value, to both sides of its quotient.
 constexpr int kRowsTile = 8;
-template <typename T, int U>
+template <typename T>
 __global__ void __launch_bounds__(kF8Threads) f8_rows_kernel(const T* X, int M, int K, int kbs, uint8_t* Xf, float* sa) {
-    constexpr int STEP = kF8Threads / 16 / kRowsTile;
-    __shared__ float scales[STEP * U][kRowsTile];
+    constexpr int BLOCKS = kF8Threads / 16 / kRowsTile;
+    __shared__ float scales[BLOCKS][kRowsTile];
     griddep_launch_dependents();
     griddep_wait();
     const int g = threadIdx.x / 16, l = threadIdx.x % 16;
     const int r = g % kRowsTile, m = blockIdx.x * kRowsTile + r;
-    const int kb0 = blockIdx.y * STEP * U + g / kRowsTile;
-    float4 a[U], b[U];
-    #pragma unroll
-    for (int i = 0; i < U; ++i) {
-        const int k = (kb0 + STEP * i) * kF8Block + 8 * l;
-        a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (m < M && k < K) {  // K is a multiple of 16
-            const T* x = X + (int64_t)m * K + k;
-            if constexpr (sizeof(T) == 2) {
-                const uint4 u = *reinterpret_cast<const uint4*>(x);
-                const __half2* h = reinterpret_cast<const __half2*>(&u);
-                const float2 p = __half22float2(h[0]), q = __half22float2(h[1]), s = __half22float2(h[2]), t = __half22float2(h[3]);
-                a[i] = make_float4(p.x, p.y, q.x, q.y);
-                b[i] = make_float4(s.x, s.y, t.x, t.y);
-            } else {
-                a[i] = load4(x);
-                b[i] = load4(x + 4);
-            }
+    const int kb = blockIdx.y * BLOCKS + g / kRowsTile, k = kb * kF8Block + 8 * l;
+    float4 a, b;
+    a = b = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (m < M && k < K) {  // K is a multiple of 16
+        const T* x = X + (int64_t)m * K + k;
+        if constexpr (sizeof(T) == 2) {
+            const uint4 u = *reinterpret_cast<const uint4*>(x);
+            const __half2* h = reinterpret_cast<const __half2*>(&u);
+            const float2 p = __half22float2(h[0]), q = __half22float2(h[1]), s = __half22float2(h[2]), t = __half22float2(h[3]);
+            a = make_float4(p.x, p.y, q.x, q.y);
+            b = make_float4(s.x, s.y, t.x, t.y);
+        } else {
+            a = load4(x);
+            b = load4(x + 4);
         }
     }
+    float top = max_nan(absmax4_nan(a), absmax4_nan(b));
     #pragma unroll
-    for (int i = 0; i < U; ++i) {
-        const int kb = kb0 + STEP * i, k = kb * kF8Block + 8 * l;
-        float top = max_nan(absmax4_nan(a[i]), absmax4_nan(b[i]));
-        #pragma unroll
-        for (int o = 8; o >= 1; o /= 2) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        const float s = f8_scale(top);
-        float lo, hi;
-        quant_bracket(s, &lo, &hi);
-        if (m < M && k < K)
-            *reinterpret_cast<uint2*>(Xf + (int64_t)m * K + k) = make_uint2(f8_codes4(a[i], s, lo, hi), f8_codes4(b[i], s, lo, hi));
-        if (l == 0) scales[g / kRowsTile + STEP * i][r] = s;
-    }
+    for (int o = 8; o >= 1; o /= 2) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const float s = f8_scale(top);
+    float lo, hi;
+    quant_bracket(s, &lo, &hi);
+    if (m < M && k < K)
+        *reinterpret_cast<uint2*>(Xf + (int64_t)m * K + k) = make_uint2(f8_codes4(a, s, lo, hi), f8_codes4(b, s, lo, hi));
+    if (l == 0) scales[g / kRowsTile][r] = s;
     __syncthreads();
-    if (threadIdx.x < STEP * U * kRowsTile) {
-        const int kb = blockIdx.y * STEP * U + threadIdx.x / kRowsTile, row = blockIdx.x * kRowsTile + threadIdx.x % kRowsTile;
-        if (kb < kbs && row < M) sa[(int64_t)kb * M + row] = scales[threadIdx.x / kRowsTile][threadIdx.x % kRowsTile];
+    if (threadIdx.x < BLOCKS * kRowsTile) {
+        const int block = blockIdx.y * BLOCKS + threadIdx.x / kRowsTile, row = blockIdx.x * kRowsTile + threadIdx.x % kRowsTile;
+        if (block < kbs && row < M) sa[(int64_t)block * M + row] = scales[threadIdx.x / kRowsTile][threadIdx.x % kRowsTile];
     }
 }
 
@@ -106,19 +101,11 @@ cudaError_t launch_f8_quantize_weights(const float* W, int64_t N, int64_t K, uin
 cudaError_t launch_f8_quantize_rows(const void* X, int x_f16, int64_t M, int64_t K, uint8_t* Xf, float* sa, unsigned flags,
                                     cudaStream_t stream) {
     const int kbs = f8_blocks(K);
-    // many pairs: four to a group of lanes, their loads under way together; few: one (16 rows
-    // of 3584 took 3.9 us with four, 2.5 with one, 8192 rows ROWS1 us with one, 23 with four)
-    const int u = M * kbs >= 64 * 1024 ? 4 : 1;
-    const dim3 grid((unsigned)((M + kRowsTile - 1) / kRowsTile), (unsigned)((kbs + 2 * u - 1) / (2 * u)));
-    auto go = [&](auto* kernel, auto* x) {
-        return layer_launch(kernel, grid, kF8Threads, 0, flags, stream, x, (int)M, (int)K, kbs, Xf, sa);
-    };
-    if (x_f16) {
-        const __half* x = static_cast<const __half*>(X);
-        return u == 4 ? go(f8_rows_kernel<__half, 4>, x) : go(f8_rows_kernel<__half, 1>, x);
-    }
-    const float* x = static_cast<const float*>(X);
-    return u == 4 ? go(f8_rows_kernel<float, 4>, x) : go(f8_rows_kernel<float, 1>, x);
+    const dim3 grid((unsigned)((M + kRowsTile - 1) / kRowsTile), (unsigned)((kbs + 1) / 2));
+    return x_f16 ? layer_launch(f8_rows_kernel<__half>, grid, kF8Threads, 0, flags, stream, static_cast<const __half*>(X),
+                                (int)M, (int)K, kbs, Xf, sa)
+                 : layer_launch(f8_rows_kernel<float>, grid, kF8Threads, 0, flags, stream, static_cast<const float*>(X),
+                                (int)M, (int)K, kbs, Xf, sa);
 }
 
 }  // namespace w4a8
