@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
     if (tid < n) {
         const int64_t t = first + tid;
         id = a.ids[t];
-        s.u[tid] = a.u[t];
+        s.u[tid] = fminf(fmaxf(a.u[t], 0.f), 0x1.fffffep-1f);  // (NaN: 0)
         s.id[tid] = id;
         if (a.mask != nullptr) {  // the ancestor drafted last
             const uint64_t below = a.mask[t] & (((uint64_t)1 << tid) - 1);
@@ -536,6 +536,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
             if (a.Q != nullptr) {
                 const int64_t i = (first + up) * a.ld_q + id;
                 q = a.q_f16 ? __half2float(static_cast<const __half*>(a.Q)[i]) : static_cast<const float*>(a.Q)[i];
+                q = fminf(fmaxf(q, 0.f), 1.f);
             }
         }
     }
@@ -641,7 +642,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
     // the token after the last one taken
     const RowPart p = s.row[node];
     const int64_t t = first + node;
-    const float u = s.u[0] < 1.f ? s.u[0] : 0x1.fffffep-1f;
+    const float u = s.u[0];
     int next = -1;
     bool mine = rank == 0 && tid == 0;
     if (p.sum == p.sum && c.greedy) {

@@ -732,8 +732,8 @@ int kvq_plan(const kvq_pool_t* pool, int32_t* lens, const int32_t* grow, const i
  * units, whose sums are exact: the same call gives the same tokens.
  * -infinity takes a token out; a row that holds a NaN, +infinity or nothing but -infinity has
  * no distribution: its children are refused, the token drawn is -1.  A draft outside the vocabulary
- * is refused.  If refusals left nothing but roundings, the draw takes the whole row.  u outside [0, 1) counts
- * as the nearest number inside, temp that is negative or NaN as 0.
+ * is refused.  If refusals left nothing but roundings, the draw takes the whole row.  u outside [0, 1)
+ * and Q outside [0, 1] count as the nearest number inside, NaN as 0, temp that is negative or NaN as 0.
  *   L [tokens][vocab] l_type, rows ld_l elements apart; Q [tokens][vocab] q_type, ld_q, or NULL;
  *   ids [tokens] int32 (the root's is not read); temp [seqs] fp32 or NULL (1); u [tokens] fp32.
  *   ws, ws_bytes: draft_verify_workspace_bytes, 256-byte aligned (need not be

@@ -202,6 +202,18 @@ def test_rope_axes_strides_and_one_axis(w4):
     assert torch.equal(x, plain) and torch.equal(fused[:, :64], before[:, :64]) and torch.equal(fused[:, 384:], before[:, 384:])
 
 
+def test_rope_axis_is_a_sequence_of_numbers(w4):
+    x, pos = torch.zeros((2, 2, 64), device="cuda"), torch.zeros((3, 2), dtype=torch.int32, device="cuda")
+    freqs = torch.ones(32, dtype=torch.float64, device="cuda")
+    with pytest.raises(TypeError):  # not a count of them
+        w4.rope_rotate(x, pos, freqs, axis=32)
+    with pytest.raises(ValueError, match="32 pairs, got 4"):  # entries are counted, not an array's bytes
+        w4.rope_rotate(x, pos, freqs, axis=np.zeros(4, np.int64))
+    with pytest.raises(ValueError):
+        w4.rope_rotate(x, pos, freqs, axis=[-1] * 32)
+    w4.rope_rotate(x, pos, freqs, axis=np.full(32, 2, np.int64))
+
+
 @pytest.mark.parametrize("bits", [8, 4])
 def test_kvq_write_axes(w4, bits):
     """Keys and queries turned by several axes in the cache's write: the write of keys
@@ -371,6 +383,33 @@ def test_draft_verify_random_numbers_outside(w4):
     logits = np.zeros((4, 1000), F32)
     got = run_verify(w4, logits, np.arange(5, dtype=I32), np.zeros(4, I32), np.array([1.0, 7.0, -3.0, np.nan], F32))
     assert list(got[1][:3]) == [999, 999, 0] and 0 <= got[1][3] < 1000 and list(got[2]) == [1] * 4
+
+
+def test_draft_verify_tests_with_numbers_outside(w4):
+    """The same of a draft's random number and probability: a token without weight is never taken, a token
+    with all of it always."""
+    rng = np.random.default_rng(22)
+    v = 700
+    logits = rng.standard_normal((16, v)).astype(F32)
+    logits[::2, :350] = -np.inf
+    logits[8, 400:] = logits[8, :399] = -np.inf  # token 399 has it all
+    ids = np.full(16, 5, I32)
+    ids[[9, 11]] = 399, 500
+    u = np.full(16, 0.5, F32)
+    u[1::2] = [-1, -np.inf, np.nan, 0, 1, np.nan, 0, 0]
+    cu = np.arange(0, 17, 2, dtype=I32)
+    got = run_verify(w4, logits, cu, ids, u)
+    inside = u.copy()
+    inside[1::2] = [0, 0, 0, 0, 1 - 2.0 ** -24, 0, 0, 0]
+    same(got, sref.verify(logits, cu, ids, inside))
+    assert list(got[2]) == [1, 1, 1, 1, 2, 2, 1, 1]
+    q = np.exp(rng.standard_normal((16, v)))
+    q = (q / q.sum(1, keepdims=True)).astype(F32)
+    wild = q.copy()
+    wild[0, 5], wild[2, 5], wild[4, 5], wild[8, 399], wild[10, 500] = -0.5, np.nan, np.inf, 3.0, -np.inf
+    wild[6, 400:440], wild[12, 500:], wild[14, 350:] = -2.0, np.nan, np.inf
+    got = run_verify(w4, logits, cu, ids, u, None, wild)
+    same(got, sref.verify(logits, cu, ids, inside, None, np.where(np.isnan(wild), 0, np.clip(wild, 0, 1)).astype(F32)))
 
 
 @pytest.mark.parametrize("temp", [2.0 ** -20, 1e-3, 30.0, 1e30, np.inf])
