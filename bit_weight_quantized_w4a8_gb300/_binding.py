@@ -694,7 +694,7 @@ def _want_rope(pos, freqs, tokens, axis=None):
         _want(pos, torch.int32, "pos", (tokens,))
         return 2 * pairs, None
     if not isinstance(axis, bytes):
-        axis = bytes(axis)
+        axis = bytes(int(a) for a in axis)
     if len(axis) != pairs:
         raise ValueError("axis must have one entry for each of the %d pairs, got %d" % (pairs, len(axis)))
     _want(pos, torch.int32, "pos")
