@@ -189,10 +189,8 @@ int f8_linear(const void* X, int x_type, int64_t M, int64_t K, const uint8_t* Wf
     if ((st = check_workspace("f8_linear", ws, ws_bytes, linear_bytes(M, K))) != W4A8_OK) return st;
     uint8_t* Xf = static_cast<uint8_t*>(ws);
     float* sa = reinterpret_cast<float*>(Xf + linear_scales_at(M, K));
-    cudaError_t e = w4a8::launch_f8_quantize_rows(X, x_type, M, K, Xf, sa, flags, st_of(stream));
-    if (e == cudaSuccess)
-        e = w4a8::launch_f8_gemm(Xf, sa, M, K, Wf, sw, N, Y, y_type, sms, W4A8_LAUNCH_PDL, st_of(stream));
-    return w4a8::status_done(e, "f8_linear launch");
+    return w4a8::status_done(
+        w4a8::launch_f8_linear(X, x_type, M, K, Wf, sw, N, Y, y_type, Xf, sa, sms, flags, st_of(stream)), "f8_linear launch");
 }
 
 }  // extern "C"

@@ -25,29 +25,11 @@ __global__ void __launch_bounds__(kF8Threads) f8_rows_kernel(const T* X, int M, 
     const int g = threadIdx.x / 16, l = threadIdx.x % 16;
     const int r = g % kRowsTile, m = blockIdx.x * kRowsTile + r;
     const int kb = blockIdx.y * BLOCKS + g / kRowsTile, k = kb * kF8Block + 8 * l;
-    float4 a, b;
-    a = b = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (m < M && k < K) {  // K is a multiple of 16
-        const T* x = X + (int64_t)m * K + k;
-        if constexpr (sizeof(T) == 2) {
-            const uint4 u = *reinterpret_cast<const uint4*>(x);
-            const __half2* h = reinterpret_cast<const __half2*>(&u);
-            const float2 p = __half22float2(h[0]), q = __half22float2(h[1]), s = __half22float2(h[2]), t = __half22float2(h[3]);
-            a = make_float4(p.x, p.y, q.x, q.y);
-            b = make_float4(s.x, s.y, t.x, t.y);
-        } else {
-            a = load4(x);
-            b = load4(x + 4);
-        }
-    }
-    float top = max_nan(absmax4_nan(a), absmax4_nan(b));
-    #pragma unroll
-    for (int o = 8; o >= 1; o /= 2) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const float s = f8_scale(top);
-    float lo, hi;
-    quant_bracket(s, &lo, &hi);
-    if (m < M && k < K)
-        *reinterpret_cast<uint2*>(Xf + (int64_t)m * K + k) = make_uint2(f8_codes4(a, s, lo, hi), f8_codes4(b, s, lo, hi));
+    Eight<T> v;
+    v.load(X + (int64_t)m * K + k, m < M && k < K);  // K is a multiple of 16
+    float s;
+    const uint2 codes = f8_row_codes(v, &s);
+    if (m < M && k < K) *reinterpret_cast<uint2*>(Xf + (int64_t)m * K + k) = codes;
     if (l == 0) scales[g / kRowsTile][r] = s;
     __syncthreads();
     if (threadIdx.x < BLOCKS * kRowsTile) {

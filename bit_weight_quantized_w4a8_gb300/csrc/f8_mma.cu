@@ -23,6 +23,7 @@
 #include <cudaTypedefs.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "f8.cuh"
 #include "kernels.h"
@@ -46,6 +47,8 @@ struct F8Args {
     void* Y;
     int64_t N;
     int M, kbs, tiles_a, tiles;
+    const void* X;  // values of X, where the product makes the codes itself
+    int K;
 };
 
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
@@ -366,6 +369,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) f8_wide_kernel(const __grid_c
 constexpr int kNarrowThreads = kProducerThreads + 128;
 constexpr int kNarrowCluster = 8;  // pieces of K, at most
 constexpr int kNarrowAhead = 8;    // blocks whose scales have been asked for
+constexpr int kOwnRows = 2;        // up to which the kernel makes X's codes itself
 
 template <int BN>
 struct Narrow {
@@ -377,26 +381,34 @@ struct Narrow {
     static_assert(kStages * kStage >= BN * kRows * 4, "the sums have to fit");
 };
 
-template <int BN, typename TY>
+// TX: type of X's values, of which warps 2 and 3 make the codes and scales where the tensor
+// core and the consumers read them; void: codes and scales come from memory.
+template <int BN, typename TY, typename TX>
 __global__ void __launch_bounds__(kNarrowThreads, Narrow<BN>::kCtas) f8_narrow_kernel(const __grid_constant__ F8Args a) {
     using C = Narrow<BN>;
+    constexpr bool kOwn = !std::is_void_v<TX>;
+    // the values are at most kStages blocks in front of the MMAs, these two in front of the sums
+    static_assert(!kOwn || (kOwnRows <= 2 && C::kStages + 2 <= kNarrowAhead), "a row half a warp; the ring of scales");
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars<C::kStages, 2> sh;
     __shared__ __align__(16) float scale[2][BN];
     __shared__ float2 scale_ring[kNarrowAhead][BN];  // of X's rows and of W on their way
+    __shared__ uint64_t scale_full[kOwn ? kNarrowAhead : 1];  // X's are there
     cg::cluster_group cl = cg::this_cluster();
     uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(smem_u32(&sh.full[i]), 1);
+            mbar_init(smem_u32(&sh.full[i]), kOwn ? 2 : 1);
             mbar_init(smem_u32(&sh.empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.d_full[i]), 1);
             mbar_init(smem_u32(&sh.d_empty[i]), 4);
         }
+        if constexpr (kOwn)
+            for (int i = 0; i < kNarrowAhead; ++i) mbar_init(smem_u32(&scale_full[i]), 1);
         sh.abort = 0;
         fence_mbar_init();
     }
@@ -416,17 +428,17 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<BN>::kCtas) f8_narrow_k
         const uint64_t once = l2_evict_first_policy(), keep = l2_evict_last_policy();
         auto load_w = [&](int i, int s) {
             if (!elect_one()) return;
-            mbar_arrive_expect_tx(smem_u32(&sh.full[s]), C::kStage);
+            mbar_arrive_expect_tx(smem_u32(&sh.full[s]), kOwn ? kABytes : C::kStage);
             tma_load_2d_hint(sbase + s * C::kStage, &a.tm_a, (kb0 + i) * kKBytes, (int)n0, smem_u32(&sh.full[s]), once);
         };
         auto load_x = [&](int i, int s) {
-            if (elect_one())
+            if (!kOwn && elect_one())
                 tma_load_2d_hint(sbase + s * C::kStage + kABytes, &a.tm_b, (kb0 + i) * kKBytes, m0, smem_u32(&sh.full[s]), keep);
         };
         // the weights do not come from the kernel before
         const int ahead = min(steps, C::kStages);
         for (int i = 0; i < ahead; ++i) load_w(i, i);
-        griddep_wait();
+        if constexpr (!kOwn) griddep_wait();
         for (int i = 0; i < ahead; ++i) load_x(i, i);
         issued = ahead;
         int s = 0;
@@ -461,7 +473,40 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<BN>::kCtas) f8_narrow_k
         }
         if (issued > 0 && lane == 0) drain(smem_u32(&sh.d_full[(issued - 1) & 1]), ((issued - 1) / 2) & 1);
         __syncwarp();
-    } else if (warp >= 4) {
+    } else if (warp < 4) {
+        if constexpr (kOwn) {
+            // one block the one warp, the next the other, sixteen lanes a row, values two blocks ahead
+            // (both warps on each block: 17.7 us instead of 15.1 at 1 x 3584 x 18944, a block took as
+            // long as its weights).  Rows from M on stay as they are: they only meet columns of the
+            // sums that nobody writes.
+            griddep_wait();
+            const int l = lane % 16, r = lane / 16;
+            const TX* x = static_cast<const TX*>(a.X) + (int64_t)min(r, a.M - 1) * a.K + kb0 * kF8Block + 8 * l;
+            Eight<TX> now, next[2];
+            auto load = [&](int i, Eight<TX>& v) { v.load(x + i * kF8Block, i < steps && (kb0 + i) * kF8Block + 8 * l < a.K); };
+            load(warp - 2, next[0]);
+            load(warp, next[1]);
+            for (int i = warp - 2; i < steps; i += 2) {
+                now = next[0], next[0] = next[1];
+                load(i + 4, next[1]);
+                const int s = i % C::kStages, round = i / C::kStages;
+                float sx;
+                const uint2 codes = f8_row_codes(now, &sx);
+                if (round > 0 && !__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.empty[s]), (round & 1) ^ 1, &sh.abort))) break;
+                if (r < a.M) {
+                    // the 128-byte swizzle: 16-byte chunk c of row r lies at c ^ (r % 8)
+                    *reinterpret_cast<uint2*>(smem + s * C::kStage + kABytes + r * kKBytes + ((l / 2) ^ r) * 16 + l % 2 * 8) = codes;
+                    if (l == 0) scale_ring[i % kNarrowAhead][r].x = sx;
+                }
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&sh.full[s]));
+                    mbar_arrive(smem_u32(&scale_full[i % kNarrowAhead]));
+                }
+            }
+        }
+    } else {
         griddep_wait();
         const int q = warp % 4, t = tid - kProducerThreads;  // t: the thread's column for scales, its lane for sums
         const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
@@ -472,7 +517,7 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<BN>::kCtas) f8_narrow_k
         auto ask = [&](int i) {
             if (i < steps && t < BN) {
                 const uint32_t at = smem_u32(&scale_ring[i % kNarrowAhead][t]);
-                cp_async_4(at, sa + (int64_t)i * a.M);
+                if constexpr (!kOwn) cp_async_4(at, sa + (int64_t)i * a.M);
                 cp_async_4(at + 4, sw + i);
             }
             cp_async_commit();
@@ -485,6 +530,9 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<BN>::kCtas) f8_narrow_k
         Ring<2> d;
         for (int i = 0; i < steps; ++i, d.next()) {
             cp_async_wait<kNarrowAhead - 2>();
+            if constexpr (kOwn)
+                if (ok && t < 32)
+                    ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&scale_full[i % kNarrowAhead]), i / kNarrowAhead & 1, &sh.abort));
             if (t < BN) {
                 const float2 s = scale_ring[i % kNarrowAhead][t];
                 scale[d.at][t] = s.x * s.y;
@@ -635,33 +683,46 @@ cudaError_t launch_wide(F8Args& a, int sms, unsigned flags, cudaStream_t stream)
     return cluster_launch(f8_wide_kernel<TY>, dim3((unsigned)(2 * pairs)), 2, kWideThreads, kWideSmem, flags, stream, a);
 }
 
-template <int BN, typename TY>
+template <int BN, typename TY, typename TX = void>
 cudaError_t launch_narrow(F8Args& a, int pieces, unsigned flags, cudaStream_t stream) {
     static std::atomic<uint64_t> ready{0};
-    const cudaError_t e = layer_smem(f8_narrow_kernel<BN, TY>, Narrow<BN>::kSmem, ready);
+    const cudaError_t e = layer_smem(f8_narrow_kernel<BN, TY, TX>, Narrow<BN>::kSmem, ready);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)pieces, (unsigned)a.tiles_a, (unsigned)((a.M + BN - 1) / BN));
-    return cluster_launch(f8_narrow_kernel<BN, TY>, grid, pieces, kNarrowThreads, Narrow<BN>::kSmem, flags, stream, a);
+    return cluster_launch(f8_narrow_kernel<BN, TY, TX>, grid, pieces, kNarrowThreads, Narrow<BN>::kSmem, flags, stream, a);
 }
 
+// Where the narrow kernel makes X's codes itself: a launch less, 7.0 us instead of 7.9 at 1 x 3584 x
+// 3584, 15.1 instead of 15.6 at 1 x 3584 x 18944 (2 rows the same; 4 rows 16.4 instead of 15.2 at
+// 18944 x 3584, dependent launches).  Not where CTAs come in several waves, each with the values'
+// way to go again: 88.7 us instead of 87.0 at 1 x 3584 x 152064.
+bool makes_codes(int64_t M, int64_t N, int sms) { return M <= kOwnRows && (N + kRows - 1) / kRows <= 2 * (int64_t)sms; }
+bool goes_wide(int64_t M, int64_t N, int sms) {
+    const int64_t wide = (M + 2 * kRows - 1) / (2 * kRows) * ((N + kWideCols - 1) / kWideCols);
+    return (M > 128 && 3 * wide >= sms) || (N + kRows - 1) / kRows > 65535;
+}
+
+// Xf and sa, or, with X, up to kOwnRows rows of values of type x_f16.
 template <typename TY>
-cudaError_t launch_gemm(const uint8_t* Xf, const float* sa, int64_t M, int64_t K, const uint8_t* Wf, const float* sw,
-                        int64_t N, void* Y, int sms, unsigned flags, cudaStream_t stream) {
+cudaError_t launch_gemm(const uint8_t* Xf, const float* sa, const void* X, int x_f16, int64_t M, int64_t K, const uint8_t* Wf,
+                        const float* sw, int64_t N, void* Y, int sms, unsigned flags, cudaStream_t stream) {
     F8Args a = {};
     a.sa = sa;
     a.sw = sw;
     a.Y = Y;
     a.N = N;
     a.M = (int)M;
+    a.K = (int)K;
+    a.X = X;
     a.kbs = (int)((K + kF8Block - 1) / kF8Block);
-    const int64_t m_tiles = (M + 2 * kRows - 1) / (2 * kRows), wide = m_tiles * ((N + kWideCols - 1) / kWideCols);
-    const int64_t n_tiles = (N + kRows - 1) / kRows;
-    if ((M > 128 && 3 * wide >= sms) || n_tiles > 65535) {
+    if (goes_wide(M, N, sms)) {
+        const int64_t m_tiles = (M + 2 * kRows - 1) / (2 * kRows);
         a.tiles_a = (int)m_tiles;
-        a.tiles = (int)wide;
+        a.tiles = (int)(m_tiles * ((N + kWideCols - 1) / kWideCols));
         if (!code_map(&a.tm_a, Xf, M, K, kRows) || !code_map(&a.tm_b, Wf, N, K, kWideCols / 2)) return cudaErrorNotSupported;
         return launch_wide<TY>(a, sms, flags, stream);
     }
+    const int64_t n_tiles = (N + kRows - 1) / kRows;
     const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     a.tiles_a = (int)n_tiles;
     const int64_t ctas = n_tiles * ((M + bn - 1) / bn);
@@ -671,7 +732,11 @@ cudaError_t launch_gemm(const uint8_t* Xf, const float* sa, int64_t M, int64_t K
     const int64_t slots = (bn <= 64 ? 2 : 1) * (int64_t)sms;
     int pieces = 1;
     while (pieces < kNarrowCluster && (pieces + 1) * ctas <= slots && a.kbs / (pieces + 1) >= 4) ++pieces;
-    if (!code_map(&a.tm_a, Wf, N, K, kRows) || !code_map(&a.tm_b, Xf, M, K, bn)) return cudaErrorNotSupported;
+    if (!code_map(&a.tm_a, Wf, N, K, kRows)) return cudaErrorNotSupported;
+    if (X != nullptr)
+        return x_f16 ? launch_narrow<16, TY, __half>(a, pieces, flags, stream)
+                     : launch_narrow<16, TY, float>(a, pieces, flags, stream);
+    if (!code_map(&a.tm_b, Xf, M, K, bn)) return cudaErrorNotSupported;
     switch (bn) {
         case 16: return launch_narrow<16, TY>(a, pieces, flags, stream);
         case 32: return launch_narrow<32, TY>(a, pieces, flags, stream);
@@ -684,8 +749,18 @@ cudaError_t launch_gemm(const uint8_t* Xf, const float* sa, int64_t M, int64_t K
 
 cudaError_t launch_f8_gemm(const uint8_t* Xf, const float* sa, int64_t M, int64_t K, const uint8_t* Wf, const float* sw,
                            int64_t N, void* Y, int y_f16, int sms, unsigned flags, cudaStream_t stream) {
-    return y_f16 ? launch_gemm<__half>(Xf, sa, M, K, Wf, sw, N, Y, sms, flags, stream)
-                 : launch_gemm<float>(Xf, sa, M, K, Wf, sw, N, Y, sms, flags, stream);
+    return y_f16 ? launch_gemm<__half>(Xf, sa, nullptr, 0, M, K, Wf, sw, N, Y, sms, flags, stream)
+                 : launch_gemm<float>(Xf, sa, nullptr, 0, M, K, Wf, sw, N, Y, sms, flags, stream);
+}
+
+cudaError_t launch_f8_linear(const void* X, int x_f16, int64_t M, int64_t K, const uint8_t* Wf, const float* sw, int64_t N,
+                             void* Y, int y_f16, uint8_t* Xf, float* sa, int sms, unsigned flags, cudaStream_t stream) {
+    if (makes_codes(M, N, sms))
+        return y_f16 ? launch_gemm<__half>(nullptr, nullptr, X, x_f16, M, K, Wf, sw, N, Y, sms, flags, stream)
+                     : launch_gemm<float>(nullptr, nullptr, X, x_f16, M, K, Wf, sw, N, Y, sms, flags, stream);
+    const cudaError_t e = launch_f8_quantize_rows(X, x_f16, M, K, Xf, sa, flags, stream);
+    // (the product may start under the quantizer, whatever the caller's flags)
+    return e != cudaSuccess ? e : launch_f8_gemm(Xf, sa, M, K, Wf, sw, N, Y, y_f16, sms, 1u, stream);
 }
 
 cudaError_t read_and_clear_f8_error(unsigned* flags, cudaStream_t stream) {

@@ -152,6 +152,9 @@ cudaError_t launch_f8_quantize_rows(const void* X, int x_f16, int64_t M, int64_t
                                     unsigned flags, cudaStream_t stream);
 cudaError_t launch_f8_gemm(const uint8_t* Xf, const float* sa, int64_t M, int64_t K, const uint8_t* Wf, const float* sw,
                            int64_t N, void* Y, int y_f16, int sms, unsigned flags, cudaStream_t stream);
+// Both in turn (codes in Xf, scales in sa), or in one launch for few rows.
+cudaError_t launch_f8_linear(const void* X, int x_f16, int64_t M, int64_t K, const uint8_t* Wf, const float* sw, int64_t N,
+                             void* Y, int y_f16, uint8_t* Xf, float* sa, int sms, unsigned flags, cudaStream_t stream);
 cudaError_t read_and_clear_f8_error(unsigned* flags, cudaStream_t stream);
 
 }  // namespace w4a8

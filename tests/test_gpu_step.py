@@ -156,6 +156,33 @@ def test_f8_linear(w4, M, K, N, xt, yt):
         w4.f8_linear(dev(x), wf, sw, ws=ws2)
 
 
+@pytest.mark.parametrize("M", [1, 2, 3])
+@pytest.mark.parametrize("K,N", [(16, 5), (128, 128), (144, 130), (640, 200), (1040, 4000), (18944, 384), (272, 40000)])
+@pytest.mark.parametrize("xt", [F32, F16])
+def test_f8_linear_single_tokens(w4, M, K, N, xt):
+    """Few rows take one launch, or two where the weights are many: the bits of the two steps, zero, tiny and
+    not finite blocks among them, and nothing of the rows behind the last."""
+    rng = np.random.default_rng(K + N)
+    x = rng.standard_normal((M + 1, K)).astype(xt)
+    x[0, :min(K, 128)] = np.round(8 * x[0, :min(K, 128)]) / 8  # quotients near ties
+    x[M - 1, 256:384] = 0
+    x[M - 1, 128:256] *= xt(1e-6)
+    x[M, :] = np.nan
+    wf, sw = w4.f8_quantize_weights(dev((0.05 * rng.standard_normal((N, K))).astype(F32)))
+    for odd in (None, np.nan, np.inf):
+        if odd is not None:
+            x[0, K // 2] = odd
+        a = dev(x)[:M]
+        y = guards.out((M, N), torch.float32)
+        for flags in (0, w4.LAUNCH_PDL):
+            y.t.zero_()
+            w4.f8_linear(a, wf, sw, Y=y.t, flags=flags)
+            guards.check_all(y)
+            want = w4.f8_gemm(*w4.f8_quantize_rows(a), wf, sw)
+            assert np.array_equal(np_(y.t), np_(want), equal_nan=True)
+        assert np.isnan(np_(y.t)[0]).all() == (odd is not None) and np.isfinite(np_(y.t)[1:]).all()
+
+
 def test_f8_linear_not_finite(w4):
     """An infinity or a NaN stays in its row of X (and its rows of W)."""
     rng = np.random.default_rng(0)
