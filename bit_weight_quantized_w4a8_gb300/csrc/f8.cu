@@ -11,10 +11,11 @@ namespace {
 constexpr int kF8Threads = 256;
 
 // Sixteen lanes a (row, block of 128), 8 values a lane; a CTA has 8 rows x 2 blocks, so that the
-// scales, a block's of all rows side by side, leave in runs of 32 bytes.  One launch in a graph: 1 x 3584
-// 2.2 us, 777 x 4096 4.3, 8192 x 3584 23.5 (3.8 TB/s; a warp a row and block, with the scales one by one, 38);
-// four blocks a group of lanes gain 3% there and cost 16 rows half as much again.  What bounds it is the two roundings of
-// each value, to both sides of its quotient.
+// scales, a block's of all rows side by side, leave in runs of 32 bytes.  One launch in a graph, from
+// fp16: 16 x 3584 2.7 us, 777 x 4096 4.6, 8192 x 3584 21.4 (4.1 TB/s; a warp a row and block, with the
+// scales one by one, 38; codes made outside the branch that stores them 24.6).  Four blocks a group of
+// lanes gain 3% there and cost 16 rows half as much again.  What bounds it is the two roundings of each
+// value, to both sides of its quotient.
 constexpr int kRowsTile = 8;
 template <typename T>
 __global__ void __launch_bounds__(kF8Threads) f8_rows_kernel(const T* X, int M, int K, int kbs, uint8_t* Xf, float* sa) {
@@ -25,11 +26,15 @@ __global__ void __launch_bounds__(kF8Threads) f8_rows_kernel(const T* X, int M, 
     const int g = threadIdx.x / 16, l = threadIdx.x % 16;
     const int r = g % kRowsTile, m = blockIdx.x * kRowsTile + r;
     const int kb = blockIdx.y * BLOCKS + g / kRowsTile, k = kb * kF8Block + 8 * l;
+    const bool in = m < M && k < K;  // K is a multiple of 16
     Eight<T> v;
-    v.load(X + (int64_t)m * K + k, m < M && k < K);  // K is a multiple of 16
-    float s;
-    const uint2 codes = f8_row_codes(v, &s);
-    if (m < M && k < K) *reinterpret_cast<uint2*>(Xf + (int64_t)m * K + k) = codes;
+    if (in) v.load(X + (int64_t)m * K + k);
+    float4 a, b;
+    v.get(a, b);
+    const float s = f8_row_scale(a, b);
+    float lo, hi;
+    quant_bracket(s, &lo, &hi);
+    if (in) *reinterpret_cast<uint2*>(Xf + (int64_t)m * K + k) = make_uint2(f8_codes4(a, s, lo, hi), f8_codes4(b, s, lo, hi));
     if (l == 0) scales[g / kRowsTile][r] = s;
     __syncthreads();
     if (threadIdx.x < BLOCKS * kRowsTile) {

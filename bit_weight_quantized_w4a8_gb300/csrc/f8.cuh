@@ -51,15 +51,13 @@ __device__ __forceinline__ uint32_t f8_codes4(float4 v, float s, float lo, float
     return a == b ? a : f8_codes4_exact(v, s);
 }
 
-// Eight values of a row as they are in memory; past the end zeros.
+// Eight values of a row as they are in memory.
 template <typename T>
 struct Eight;
 template <>
 struct Eight<__half> {
-    uint4 u;
-    __device__ __forceinline__ void load(const __half* p, bool in) {
-        u = in ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
-    }
+    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+    __device__ __forceinline__ void load(const __half* p) { u = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void get(float4& a, float4& b) const {
         const __half2* h = reinterpret_cast<const __half2*>(&u);
         const float2 p = __half22float2(h[0]), q = __half22float2(h[1]), s = __half22float2(h[2]), t = __half22float2(h[3]);
@@ -69,26 +67,17 @@ struct Eight<__half> {
 };
 template <>
 struct Eight<float> {
-    float4 x, y;
-    __device__ __forceinline__ void load(const float* p, bool in) {
-        x = in ? load4(p) : make_float4(0.f, 0.f, 0.f, 0.f);
-        y = in ? load4(p + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = make_float4(0.f, 0.f, 0.f, 0.f);
+    __device__ __forceinline__ void load(const float* p) { x = load4(p), y = load4(p + 4); }
     __device__ __forceinline__ void get(float4& a, float4& b) const { a = x, b = y; }
 };
 
-// The codes of 8 of a block's 128 values, whose other lanes are the sixteen side by side; *s their scale.
-template <typename T>
-__device__ __forceinline__ uint2 f8_row_codes(const Eight<T>& v, float* s) {
-    float4 a, b;
-    v.get(a, b);
+// The scale of a block of 128 values, 8 in each of sixteen lanes side by side.
+__device__ __forceinline__ float f8_row_scale(const float4& a, const float4& b) {
     float top = max_nan(absmax4_nan(a), absmax4_nan(b));
     #pragma unroll
     for (int o = 8; o >= 1; o /= 2) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    *s = f8_scale(top);
-    float lo, hi;
-    quant_bracket(*s, &lo, &hi);
-    return make_uint2(f8_codes4(a, *s, lo, hi), f8_codes4(b, *s, lo, hi));
+    return f8_scale(top);
 }
 
 }  // namespace w4a8

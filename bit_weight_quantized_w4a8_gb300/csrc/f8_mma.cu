@@ -483,15 +483,22 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<BN>::kCtas) f8_narrow_k
             const int l = lane % 16, r = lane / 16;
             const TX* x = static_cast<const TX*>(a.X) + (int64_t)min(r, a.M - 1) * a.K + kb0 * kF8Block + 8 * l;
             Eight<TX> now, next[2];
-            auto load = [&](int i, Eight<TX>& v) { v.load(x + i * kF8Block, i < steps && (kb0 + i) * kF8Block + 8 * l < a.K); };
+            auto load = [&](int i, Eight<TX>& v) {
+                v = Eight<TX>();
+                if (i < steps && (kb0 + i) * kF8Block + 8 * l < a.K) v.load(x + i * kF8Block);
+            };
             load(warp - 2, next[0]);
             load(warp, next[1]);
             for (int i = warp - 2; i < steps; i += 2) {
                 now = next[0], next[0] = next[1];
                 load(i + 4, next[1]);
                 const int s = i % C::kStages, round = i / C::kStages;
-                float sx;
-                const uint2 codes = f8_row_codes(now, &sx);
+                float4 u, v;
+                now.get(u, v);
+                const float sx = f8_row_scale(u, v);
+                float lo, hi;
+                quant_bracket(sx, &lo, &hi);
+                const uint2 codes = make_uint2(f8_codes4(u, sx, lo, hi), f8_codes4(v, sx, lo, hi));
                 if (round > 0 && !__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.empty[s]), (round & 1) ^ 1, &sh.abort))) break;
                 if (r < a.M) {
                     // the 128-byte swizzle: 16-byte chunk c of row r lies at c ^ (r % 8)
