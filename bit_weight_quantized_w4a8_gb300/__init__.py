@@ -2,7 +2,9 @@
 group-wise INT4 scales) and W8A16; the MLP's gated product between the
 gate/up and down projections; the rest of the decoder layer (residual and
 norms, rotary positions, a quantized paged key/value cache and attention over
-it); and the IndexSoftmax integer softmax.
+it); a serving step around the layers (pages and positions planned on the
+device, drafted tokens verified); a linear with e4m3 blocks for any number of
+rows; and the IndexSoftmax integer softmax.
 
 The compute lives in libw4a8.so (CUDA kernels behind the C ABI of
 include/w4a8.h); this package is its thin Python binding.

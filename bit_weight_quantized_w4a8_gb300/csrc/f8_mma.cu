@@ -10,13 +10,20 @@
 // registers hold a tile's sums until its last block, so TMEM belongs to the next tile
 // while a tile is written.
 //
-// Two kernels:
+// Two kernels (figures: launches one after another in a graph, weights not in L2):
 //  wide    256 rows of X x 256 of W by a pair of CTAs, 128 rows of X and half of W's in the
 //          shared memory of each: a thread has one row of X and 128 columns, so one
-//          scale a block.  For many rows.
+//          scale a block.  For many rows: 8192 x 3584 x 18944 473 us (2.35 PFLOP/s), 777 x 4096 x
+//          4608 21.  A block takes 690 cycles of the tensor core's 512, and two buffers of 256
+//          columns are all TMEM has: it waits for the sums' way to registers (128 x 128 a warp
+//          group, loads 32 columns at a time) rather than for operands.  Tiles of 160
+//          columns with three buffers took 554 us, halves of 128 494, 16 consumer warps 478.
 //  narrow  128 rows of W x 16 .. 128 of X: the weights fill the tensor core's 128 rows
 //          whatever the batch, K is cut over a cluster whose sums are joined through
-//          distributed shared memory in the order of the pieces.  For few rows.
+//          distributed shared memory in the order of the pieces.  For few rows: 1 x 3584 x 18944
+//          15.1 us (10.1 at the copy rate), 49 x 18944 x 3584 19, 1 x 3584 x 152064 87 (81): launch,
+//          the first bytes' way and the join are 4 to 5 us, the rest streams.
+//  goes_wide chooses between them.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -690,11 +697,46 @@ cudaError_t launch_wide(F8Args& a, int sms, unsigned flags, cudaStream_t stream)
     return cluster_launch(f8_wide_kernel<TY>, dim3((unsigned)(2 * pairs)), 2, kWideThreads, kWideSmem, flags, stream, a);
 }
 
+// How many clusters of a size the GPU holds at once, with one CTA an SM: fewer than SMs / size, as a
+// cluster stays within a group of SMs (46 of 3 and 15 of 7 on 152 SMs).
+int max_clusters(int size) {
+    constexpr int kDevices = 16;
+    static std::atomic<uint64_t> ready{0};
+    static std::atomic<int> known[kDevices][kNarrowCluster + 1];
+    auto* f = f8_narrow_kernel<128, float, void>;
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || layer_smem(f, Narrow<128>::kSmem, ready) != cudaSuccess) return 0;
+    if (dev < kDevices && (n = known[dev][size].load(std::memory_order_relaxed)) != 0) return n - 1;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {(unsigned)size, 1, 1};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)size);
+    cfg.blockDim = dim3(kNarrowThreads);
+    cfg.dynamicSmemBytes = Narrow<128>::kSmem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, f, &cfg) != cudaSuccess) {
+        cudaGetLastError();  // (one piece then)
+        return 0;
+    }
+    if (dev < kDevices) known[dev][size].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
 template <int BN, typename TY, typename TX = void>
-cudaError_t launch_narrow(F8Args& a, int pieces, unsigned flags, cudaStream_t stream) {
+cudaError_t launch_narrow(F8Args& a, unsigned flags, cudaStream_t stream) {
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = layer_smem(f8_narrow_kernel<BN, TY, TX>, Narrow<BN>::kSmem, ready);
     if (e != cudaSuccess) return e;
+    const int64_t tiles = a.tiles_a * (int64_t)((a.M + BN - 1) / BN);
+    // Pieces of at least 4 blocks, as many as leave all clusters resident: 16 tiles in pieces of 7, counted by
+    // SMs, took 21.2 us, of 6 15.0 (512 x 3584 x 512).  Two CTAs an SM up to 64 rows; one with
+    // twice the stages and half the pieces was slower behind another call, whose CTAs then
+    // leave no room to start in: 14.6 us a call instead of 13.5 at 1 x 3584 x 18944.
+    int pieces = 1;
+    for (int p = 2; p <= kNarrowCluster && a.kbs / p >= 4 && tiles <= Narrow<BN>::kCtas * (int64_t)max_clusters(p); ++p)
+        pieces = p;
     const dim3 grid((unsigned)pieces, (unsigned)a.tiles_a, (unsigned)((a.M + BN - 1) / BN));
     return cluster_launch(f8_narrow_kernel<BN, TY, TX>, grid, pieces, kNarrowThreads, Narrow<BN>::kSmem, flags, stream, a);
 }
@@ -704,9 +746,12 @@ cudaError_t launch_narrow(F8Args& a, int pieces, unsigned flags, cudaStream_t st
 // 18944 x 3584, dependent launches).  Not where CTAs come in several waves, each with the values'
 // way to go again: 88.7 us instead of 87.0 at 1 x 3584 x 152064.
 bool makes_codes(int64_t M, int64_t N, int sms) { return M <= kOwnRows && (N + kRows - 1) / kRows <= 2 * (int64_t)sms; }
-bool goes_wide(int64_t M, int64_t N, int sms) {
-    const int64_t wide = (M + 2 * kRows - 1) / (2 * kRows) * ((N + kWideCols - 1) / kWideCols);
-    return (M > 128 && 3 * wide >= sms) || (N + kRows - 1) / kRows > 65535;
+// More than 128 rows whose narrow tiles leave K in one piece go wide: 512 x 3584 x 3584 (112 tiles) 21.2 us
+// there, 25.2 narrow, 384 x 18944 x 3584 (84) 69.5 and 82.6; 256 x 18944 x 3584 (56, two pieces) 70 and
+// 47.8, 1500 x 3584 x 512 (48) 21.2 and 19.1.  (Each call on its own, L2 flushed, fp16 out.)
+bool goes_wide(int64_t M, int64_t N) {
+    const int64_t n_tiles = (N + kRows - 1) / kRows;
+    return n_tiles > 65535 || (M > 128 && n_tiles * ((M + kRows - 1) / kRows) > max_clusters(2));
 }
 
 // Xf and sa, or, with X, up to kOwnRows rows of values of type x_f16.
@@ -722,7 +767,7 @@ cudaError_t launch_gemm(const uint8_t* Xf, const float* sa, const void* X, int x
     a.K = (int)K;
     a.X = X;
     a.kbs = (int)((K + kF8Block - 1) / kF8Block);
-    if (goes_wide(M, N, sms)) {
+    if (goes_wide(M, N)) {
         const int64_t m_tiles = (M + 2 * kRows - 1) / (2 * kRows);
         a.tiles_a = (int)m_tiles;
         a.tiles = (int)(m_tiles * ((N + kWideCols - 1) / kWideCols));
@@ -732,23 +777,16 @@ cudaError_t launch_gemm(const uint8_t* Xf, const float* sa, const void* X, int x
     const int64_t n_tiles = (N + kRows - 1) / kRows;
     const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     a.tiles_a = (int)n_tiles;
-    const int64_t ctas = n_tiles * ((M + bn - 1) / bn);
-    // Pieces of at least 4 blocks, as many as leave all CTAs resident (two a SM up to 64 rows; one a SM with
-    // twice the stages and half the pieces was slower behind another call, whose CTAs then
-    // leave no room to start in: 14.6 us a call instead of 13.5 at 1 x 3584 x 18944).
-    const int64_t slots = (bn <= 64 ? 2 : 1) * (int64_t)sms;
-    int pieces = 1;
-    while (pieces < kNarrowCluster && (pieces + 1) * ctas <= slots && a.kbs / (pieces + 1) >= 4) ++pieces;
     if (!code_map(&a.tm_a, Wf, N, K, kRows)) return cudaErrorNotSupported;
     if (X != nullptr)
-        return x_f16 ? launch_narrow<16, TY, __half>(a, pieces, flags, stream)
-                     : launch_narrow<16, TY, float>(a, pieces, flags, stream);
+        return x_f16 ? launch_narrow<16, TY, __half>(a, flags, stream)
+                     : launch_narrow<16, TY, float>(a, flags, stream);
     if (!code_map(&a.tm_b, Xf, M, K, bn)) return cudaErrorNotSupported;
     switch (bn) {
-        case 16: return launch_narrow<16, TY>(a, pieces, flags, stream);
-        case 32: return launch_narrow<32, TY>(a, pieces, flags, stream);
-        case 64: return launch_narrow<64, TY>(a, pieces, flags, stream);
-        default: return launch_narrow<128, TY>(a, pieces, flags, stream);
+        case 16: return launch_narrow<16, TY>(a, flags, stream);
+        case 32: return launch_narrow<32, TY>(a, flags, stream);
+        case 64: return launch_narrow<64, TY>(a, flags, stream);
+        default: return launch_narrow<128, TY>(a, flags, stream);
     }
 }
 

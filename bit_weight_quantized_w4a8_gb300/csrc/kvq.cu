@@ -45,7 +45,8 @@ struct RopeArg {
     float mscale;
     int64_t ld_pos;
     uint32_t axis[8];  // of each pair, two bits: in the launch's constants, so that no load stands in front of
-                       // the position's (with one axis all are 0)
+                       // the position's (with one axis all are 0).  8191 x 32 x 128 with three axes 33.2 us
+                       // (30.1 at the copy rate), with one 30.8: three positions a token instead of one
 };
 
 struct WriteArgs {

@@ -16,7 +16,9 @@
 //
 // One cluster of CTAs scans (a thread has up to 8 rows, so 65536 rows take one
 // pass) and, for short steps, writes all; for long ones a second launch writes
-// with the whole GPU.
+// with the whole GPU.  In a graph 48 requests take 4.3 us, 4093 requests of which half are
+// exchanged (two calls) 29.5: nothing but latency, of the scan's two to three prefix sums (10 us a call under
+// ncu) and of a look-up's search through the offsets, 12 loads one after the other (10 to 16).
 #include <cooperative_groups.h>
 
 #include "kernels.h"
