@@ -14,9 +14,9 @@
 //  wide    256 rows of X x 256 of W by a pair of CTAs, 128 rows of X and half of W's in the
 //          shared memory of each: a thread has one row of X and 128 columns, so one
 //          scale a block.  For many rows: 8192 x 3584 x 18944 473 us (2.35 PFLOP/s), 777 x 4096 x
-//          4608 21.  A block takes 690 cycles of the tensor core's 512, and two buffers of 256
-//          columns are all TMEM has: it waits for the sums' way to registers (128 x 128 a warp
-//          group, loads 32 columns at a time) rather than for operands.  Tiles of 160
+//          4608 21.  A block takes about 1000 cycles; its four MMAs alone take 690 (512 at the nominal
+//          rate).  The rest is the sums' way out of TMEM (128 x 128 a warp group, 32 columns at a
+//          time): two buffers of 256 columns are all it has, so the products wait for it.  Tiles of 160
 //          columns with three buffers took 554 us, halves of 128 494, 16 consumer warps 478.
 //  narrow  128 rows of W x 16 .. 128 of X: the weights fill the tensor core's 128 rows
 //          whatever the batch, K is cut over a cluster whose sums are joined through
