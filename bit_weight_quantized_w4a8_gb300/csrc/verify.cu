@@ -245,18 +245,31 @@ __device__ __forceinline__ uint64_t weight(float l, const Unit& s, const uint64_
     return ((uint64_t)v + ((uint64_t)1 << n >> 1)) >> n;
 }
 
-// f a for f in [0, 1], to nearest (cut off instead, 10^5 weights less q A would all lean to one
-// side, and their sum by as many halves of a unit); from f = 2^-8 on within 2^-32 of it.
-// 0 for a negative f or NaN.
-__device__ __forceinline__ uint64_t part_of(float f, uint64_t a) {
-    if (!(f > 0.f)) return 0;
-    if (f >= 1.f) return a;
+// f = m 2^-sh for f in (0, 1]; sh 23 .. 149.
+__device__ __forceinline__ int split(float f, uint32_t& m) {
     const uint32_t bits = __float_as_uint(f);
-    const int ex = bits >> 23;  // f = m 2^-sh
-    const uint32_t m = (bits & 0x7FFFFFu) | (ex != 0 ? 0x800000u : 0u);
-    const int sh = 150 - (ex != 0 ? ex : 1);  // 24 .. 149
+    const int ex = bits >> 23;
+    m = (bits & 0x7FFFFFu) | (ex != 0 ? 0x800000u : 0u);
+    return 150 - (ex != 0 ? ex : 1);
+}
+// floor(u a), u in [0, 1).
+__device__ __forceinline__ uint64_t target_of(float u, uint64_t a) {
+    uint32_t m;
+    const int sh = split(u, m);
+    const uint64_t hi = __umul64hi(a, m), lo = a * m;
+    return sh < 64 ? hi << (64 - sh) | lo >> sh : sh < 128 ? hi >> (sh - 64) : 0;
+}
+// 16 q a, to nearest (cut off instead, 10^5 weights less q A would all lean to one side, and their
+// sum by as many halves of a unit); from q = 2^-12 on within 2^-32 of it, above 64 bits their
+// largest number.  q outside [0, 1]: the nearest inside; NaN: 0.
+constexpr int kCutShift = 4;  // sums of up to 2^22 weights, 63 times, in 64 bits
+__device__ __forceinline__ uint64_t part_of(float q, uint64_t a) {
+    if (!(q > 0.f)) return 0;
+    uint32_t m;
+    const int sh = split(fminf(q, 1.f), m) - kCutShift;
     const uint64_t p = ((uint64_t)(uint32_t)(a >> 32) * m << 1) + ((uint64_t)(uint32_t)a * m >> 31);  // a m 2^-31
-    return sh < 32 ? p << (31 - sh) : sh < 90 ? ((p >> (sh - 32)) + 1) >> 1 : 0;
+    if (sh < 32) return p >> (32 + sh) >> 1 != 0 ? ~(uint64_t)0 : p << (31 - sh);
+    return sh < 90 ? ((p >> (sh - 32)) + 1) >> 1 : 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -349,7 +362,7 @@ struct Draw {
             return to_units(warp_sum(sum));
         }
     };
-    // ... and as integers (cut 0: without q), exact sums.
+    // ... and as integers, exact sums (cut: A in 16 units; 0: without q).
     struct Exact {
         Unit unit;
         uint64_t cut;
@@ -597,10 +610,8 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
         while (cuts < todo) {
             if (cuts == 0) {
                 dr.pass(first + node, exact(0), 0);
-                cut = dr.total;
-            } else {
-                cut = cut + dr.total < cut ? ~(uint64_t)0 : cut + dr.total;
             }
+            cut += (dr.total + (1 << kCutShift >> 1)) >> kCutShift;
             if (cut == 0) break;
             dr.pass(first + node, exact(cut), 0);
             ++cuts;
@@ -658,7 +669,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
             const typename Draw<T>::Fast w = {p.top, c.hi, p.sum, todo == 1};
             dr.pass(t, w, refused);
             const uint64_t off = to_units(2.f * kOff * p.sum * (1.f + dr.q_total)) + 2;
-            const int x = dr.find(t, w, refused, part_of(u, dr.total), off);
+            const int x = dr.find(t, w, refused, target_of(u, dr.total), off);
             if (x >= 0)
                 for (int r = 0; r < kVerifyCluster; ++r) *cl.map_shared_rank(&s.verdict, r) = x;
             cl.sync();
@@ -673,7 +684,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
                 refused = 0;
                 dr.pass(t, exact(0), 0);
             }
-            next = dr.find(t, exact(cut), refused, part_of(u, dr.total), 0);
+            next = dr.find(t, exact(cut), refused, target_of(u, dr.total), 0);
             mine = next >= 0 || (dr.total == 0 && mine);
         }
     }

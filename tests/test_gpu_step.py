@@ -126,6 +126,23 @@ def test_f8_gemm(w4, M, K, N, yt):
     close(y.t, want, err + ref.out_round(want, yt), "Y")
 
 
+@pytest.mark.parametrize("M,K,N", [(1, 16, 65535 * 128 + 129), (2, 131072, 130), (20, 131072, 300), (300, 131072, 40),
+                                   (70001, 32, 64)])
+def test_f8_gemm_ends_of_the_sizes(w4, M, K, N):
+    """Small whole numbers and scales of 1, sums below 2^24: exact."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    small = dev(sref.e4m3_codes(np.arange(-2, 3).astype(np.float64)))
+    pick = lambda *s: torch.randint(0, 5, s, device="cuda", generator=g)  # noqa: E731
+    x, w = pick(M, K), pick(N, K)
+    kb = -(-K // 128)
+    y = guards.out((M, N), torch.float32)
+    w4.f8_gemm(small[x], torch.ones((kb, M), device="cuda"), small[w], torch.ones((-(-N // 128), kb), device="cuda"), Y=y.t)
+    guards.check_all(y)
+    for n in range(0, N, 1 << 22):
+        want = (x.double() - 2) @ (w[n:n + (1 << 22)].double() - 2).T
+        assert torch.equal(y.t[:, n:n + (1 << 22)].double(), want)
+
+
 @pytest.mark.parametrize("M,K,N", [(1, 4096, 200), (40, 2064, 300), (100, 1024, 256), (600, 1296, 6001)])
 def test_f8_gemm_whole_numbers(w4, M, K, N):
     """Small whole numbers and scales that are powers of two: every sum is exact."""
@@ -505,6 +522,27 @@ def test_draft_verify_refusals_before_a_row_of_no_use(w4):
     got = run_verify(w4, logits, cu, ids, u, mask, q)
     same(got, sref.verify(logits, cu, ids, u, mask, q))
     assert np.all(got[2] == 2) and np.all(got[1].reshape(seqs, 4)[:, :2] == [7, -1])
+
+
+def test_draft_verify_largest_vocabulary_many_refusals(w4):
+    """2^22 equal weights and eight refusals of one token at the root: what is taken off adds up to 2^66 of
+    the units of 2^-40.  Roundings: half a unit a weight and a refusal's, 2^-20 of a weight after 2^22."""
+    rng = np.random.default_rng(23)
+    v, kids = 2 ** 22, 8
+    logits = np.zeros((kids + 1, v), F32)
+    q = rng.random(v)
+    q[77] = 0
+    q *= 0.4 / q.sum()
+    q[77] = 0.6
+    q = np.tile(q.astype(F32), (kids + 1, 1))
+    ids = np.full(kids + 1, 77, I32)
+    u = np.full(kids + 1, 0.99, F32)
+    mask = np.array([1] + [1 | 1 << i for i in range(1, kids + 1)], np.uint64).view(I64)
+    cu = np.array([0, kids + 1], I32)
+    for u0 in (0.0, 0.123, 0.5, 0.987):
+        u[0] = u0
+        got, want = run_verify(w4, logits, cu, ids, u, mask, q), sref.verify(logits, cu, ids, u, mask, q)
+        assert got[2][0] == 1 and abs(int(got[1][0]) - int(want[1][0])) <= 1
 
 
 def test_draft_verify_roundings_of_a_long_tail_do_not_add_up(w4):
