@@ -11,8 +11,8 @@
 // while a tile is written.
 //
 // Two kernels (figures: launches one after another in a graph, weights not in L2):
-//  wide    256 rows of X x 256 of W by a pair of CTAs, 128 rows of X and half of W's in the
-//          shared memory of each: a thread has one row of X and 128 columns, so one
+//  wide    256 rows of X x 256 (or 128: half_tiles) of W by a pair of CTAs, 128 rows of X and half of
+//          W's in the shared memory of each: a thread has one row of X and half of the columns, so one
 //          scale a block.  For many rows: 8192 x 3584 x 18944 473 us (2.35 PFLOP/s), 777 x 4096 x
 //          4608 21.  A block takes about 1000 cycles; its four MMAs alone take 690 (512 at the nominal
 //          rate).  The rest is the sums' way out of TMEM (128 x 128 a warp group, 32 columns at a
@@ -137,18 +137,21 @@ __device__ __forceinline__ void issue_block(uint32_t d, uint32_t a, uint32_t b, 
 // wide
 // ---------------------------------------------------------------------------
 
-constexpr int kWideCols = 256;
-constexpr int kWideBufs = 2;  // of 256 columns in TMEM
-constexpr int kWideStages = 5;
-constexpr int kWideWarps = 8;  // consumers: warp w has lanes 32 (w % 4) .., columns 128 (w / 4) ..
-constexpr int kWarpCols = kWideCols / 2;
+constexpr int kWideWarps = 8;  // consumers: warp w has lanes 32 (w % 4) .., half w / 4 of the columns
 constexpr int kWideThreads = kProducerThreads + 32 * kWideWarps;
-constexpr int kWideStage = kABytes + kWideCols / 2 * kKBytes;  // of one CTA
 constexpr int kWideOut = 32 * 64;  // a warp's outputs on their way: 32 rows of 16 columns
 constexpr int kWideAhead = 4;      // blocks whose scales of X a warp has or has asked for
 constexpr int kWideSa = kWideAhead * 32 * 4;
-constexpr int kWideSmem = kWideStages * kWideStage + kWideWarps * (kWideOut + kWideSa) + 1024;
-static_assert(kWideBufs * kWideCols <= 512 && kWideStage % 1024 == 0, "TMEM columns, operands on 1024 bytes");
+
+template <int COLS>
+struct Wide {
+    static constexpr int kBufs = 512 / COLS;  // of COLS columns in TMEM
+    static constexpr int kStages = COLS == 256 ? 5 : 8;
+    static constexpr int kWarpCols = COLS / 2;
+    static constexpr int kStage = kABytes + COLS / 2 * kKBytes;  // of one CTA
+    static constexpr int kSmem = kStages * kStage + kWideWarps * (kWideOut + kWideSa) + 1024;
+    static_assert(kStage % 1024 == 0 && kSmem <= 227 * 1024, "operands on 1024 bytes, one CTA's shared memory");
+};
 
 // A warp's buffer of 32 rows of 16 outputs in 16-byte chunks, swapped about so that
 // 8 lanes with 8 rows, or with all chunks of a few, meet all banks.
@@ -195,23 +198,25 @@ __device__ __forceinline__ void store_cols16(uint8_t* buf, const float* x, TY* Y
     __syncwarp();
 }
 
-template <typename TY>
+template <int COLS, typename TY>
 __global__ void __launch_bounds__(kWideThreads, 1) f8_wide_kernel(const __grid_constant__ F8Args a) {
     // of the pair's barriers, full and d_empty count in the even CTA, which issues
     // the MMAs; empty and d_full are told to both
+    using C = Wide<COLS>;
+    constexpr int kWarpCols = C::kWarpCols;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ Bars<kWideStages, kWideBufs> sh;
+    __shared__ Bars<C::kStages, C::kBufs> sh;
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank();
     uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (tid == 0) {
-        for (int i = 0; i < kWideStages; ++i) {
+        for (int i = 0; i < C::kStages; ++i) {
             mbar_init(smem_u32(&sh.full[i]), 1);
             mbar_init(smem_u32(&sh.empty[i]), 1);
         }
-        for (int i = 0; i < kWideBufs; ++i) {
+        for (int i = 0; i < C::kBufs; ++i) {
             mbar_init(smem_u32(&sh.d_full[i]), 1);
             mbar_init(smem_u32(&sh.d_empty[i]), 2 * kWideWarps);
         }
@@ -236,47 +241,47 @@ __global__ void __launch_bounds__(kWideThreads, 1) f8_wide_kernel(const __grid_c
         const uint64_t keep = l2_evict_last_policy();
         const uint32_t full0 = cluster_addr(smem_u32(&sh.full[0]), 0);
         int kb = 0, tile = first;
-        Ring<kWideStages> st;
+        Ring<C::kStages> st;
         for (int i = 0; i < steps; ++i, st.next()) {
-            if (i >= kWideStages &&
+            if (i >= C::kStages &&
                 !__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.empty[st.at]), st.phase ^ 1, &sh.abort)))
                 break;
             if (elect_one()) {
-                const uint32_t at = sbase + st.at * kWideStage, bar = full0 + 8 * st.at;
-                if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh.full[st.at]), 2 * kWideStage);
+                const uint32_t at = sbase + st.at * C::kStage, bar = full0 + 8 * st.at;
+                if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh.full[st.at]), 2 * C::kStage);
                 tma_load_2d_pair(at, &a.tm_a, kb * kKBytes, (tile % a.tiles_a * 2 + rank) * kRows, bar, keep);
-                tma_load_2d_pair(at + kABytes, &a.tm_b, kb * kKBytes, (tile / a.tiles_a * 2 + rank) * (kWideCols / 2), bar, keep);
+                tma_load_2d_pair(at + kABytes, &a.tm_b, kb * kKBytes, (tile / a.tiles_a * 2 + rank) * (COLS / 2), bar, keep);
             }
             issued = i + 1;
             if (++kb == a.kbs) kb = 0, tile += pairs;
         }
         // nothing may come to this CTA after it has gone: copies (all have landed when
         // their stage is told to be empty; both CTAs' count in the even one) and what is told to it
-        for (int i = max(0, issued - kWideStages); lane == 0 && i < issued; ++i) {
+        for (int i = max(0, issued - C::kStages); lane == 0 && i < issued; ++i) {
             if (!*(volatile int*)&sh.abort)
-                drain(smem_u32(&sh.empty[i % kWideStages]), (i / kWideStages) & 1);
+                drain(smem_u32(&sh.empty[i % C::kStages]), (i / C::kStages) & 1);
             else if (rank == 0)
-                drain(smem_u32(&sh.full[i % kWideStages]), (i / kWideStages) & 1);
+                drain(smem_u32(&sh.full[i % C::kStages]), (i / C::kStages) & 1);
         }
         __syncwarp();
     } else if (warp == 1) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (rank == 0) {
-            const uint32_t idesc = e4m3_idesc(2 * kRows, kWideCols);
-            Ring<kWideStages> st;
-            Ring<kWideBufs> d;
+            const uint32_t idesc = e4m3_idesc(2 * kRows, COLS);
+            Ring<C::kStages> st;
+            Ring<C::kBufs> d;
             for (int i = 0; i < steps; ++i, st.next(), d.next()) {
-                if (i >= kWideBufs &&
+                if (i >= C::kBufs &&
                     !__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.d_empty[d.at]), d.phase ^ 1, &sh.abort)))
                     break;
                 if (!__all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.full[st.at]), st.phase, &sh.abort))) break;
                 tc_fence_after_sync();
                 if (elect_one()) {
-                    const uint32_t at = sbase + st.at * kWideStage;
+                    const uint32_t at = sbase + st.at * C::kStage;
                     const uint64_t ad = sw128_desc(at), bd = sw128_desc(at + kABytes);
                     #pragma unroll
                     for (int k = 0; k < kKBytes / 32; ++k)
-                        tc_mma_e4m3_pair(tmem + kWideCols * d.at, ad + 2 * k, bd + 2 * k, idesc, k > 0);
+                        tc_mma_e4m3_pair(tmem + COLS * d.at, ad + 2 * k, bd + 2 * k, idesc, k > 0);
                     tc_commit_pair(smem_u32(&sh.d_full[d.at]));
                     tc_commit_pair(smem_u32(&sh.empty[st.at]));
                 }
@@ -284,7 +289,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) f8_wide_kernel(const __grid_c
             }
             // every MMA is done before TMEM is given back
             if (issued > 0 && lane == 0)
-                drain(smem_u32(&sh.d_full[(issued - 1) % kWideBufs]), ((issued - 1) / kWideBufs) & 1);
+                drain(smem_u32(&sh.d_full[(issued - 1) % C::kBufs]), ((issued - 1) / C::kBufs) & 1);
             __syncwarp();
         }
     } else if (warp < 4) {
@@ -292,14 +297,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) f8_wide_kernel(const __grid_c
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int cw = warp - 4, q = warp % 4, g = cw / 4;
-        uint8_t* buf = smem + kWideStages * kWideStage + cw * kWideOut;
+        uint8_t* buf = smem + C::kStages * C::kStage + cw * kWideOut;
         const bool vec = a.N % (16 / sizeof(TY)) == 0 && reinterpret_cast<uintptr_t>(a.Y) % 16 == 0;
         const int64_t nbs = (a.N + kF8Block - 1) / kF8Block;
         const uint32_t d_empty = cluster_addr(smem_u32(&sh.d_empty[0]), 0);
         // The row's scales come by asynchronous copies, each lane's for itself, those of W
         // 32 blocks at a time, one a lane: loads into registers that far ahead all had to be
         // waited for with the nearest one.
-        float* sa_ring = reinterpret_cast<float*>(smem + kWideStages * kWideStage + kWideWarps * kWideOut + cw * kWideSa) + lane;
+        float* sa_ring = reinterpret_cast<float*>(smem + C::kStages * C::kStage + kWideWarps * kWideOut + cw * kWideSa) + lane;
         const float* ask_at = nullptr;
         int ask_tile = first, ask_left = 0, ask_i = 0;
         auto ask = [&]() {
@@ -319,10 +324,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) f8_wide_kernel(const __grid_c
         for (int k = 0; k < kWideAhead - 1; ++k) ask();
         int i = 0;
         bool ok = true;
-        Ring<kWideBufs> d;
+        Ring<C::kBufs> d;
         for (int tile = first; ok && tile < a.tiles; tile += pairs) {
             const int m0 = (tile % a.tiles_a * 2 + rank) * kRows + 32 * q;
-            const int64_t n0 = (int64_t)(tile / a.tiles_a) * kWideCols + kWarpCols * g;
+            const int64_t n0 = (int64_t)(tile / a.tiles_a) * COLS + kWarpCols * g;
             const float* sw = a.sw + min(n0 / kF8Block, nbs - 1) * a.kbs;
             float acc[kWarpCols];
             #pragma unroll
@@ -338,7 +343,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) f8_wide_kernel(const __grid_c
                 ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&sh.d_full[d.at]), d.phase, &sh.abort));
                 if (!ok) break;
                 tc_fence_after_sync();
-                const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + kWideCols * d.at + kWarpCols * g;
+                const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + COLS * d.at + kWarpCols * g;
                 uint32_t v[2][32];
                 tmem_ld32(lanes, v[0]);
                 #pragma unroll
@@ -688,13 +693,17 @@ cudaError_t cluster_launch(F* f, dim3 grid, int cluster, int threads, int smem, 
     return cudaLaunchKernelEx(&cfg, f, a);
 }
 
-template <typename TY>
-cudaError_t launch_wide(F8Args& a, int sms, unsigned flags, cudaStream_t stream) {
+template <int COLS, typename TY>
+cudaError_t launch_wide(F8Args& a, int64_t m_tiles, const uint8_t* Xf, int64_t K, const uint8_t* Wf, int sms, unsigned flags,
+                        cudaStream_t stream) {
     static std::atomic<uint64_t> ready{0};
-    const cudaError_t e = layer_smem(f8_wide_kernel<TY>, kWideSmem, ready);
+    const cudaError_t e = layer_smem(f8_wide_kernel<COLS, TY>, Wide<COLS>::kSmem, ready);
     if (e != cudaSuccess) return e;
+    a.tiles_a = (int)m_tiles;
+    a.tiles = (int)(m_tiles * ((a.N + COLS - 1) / COLS));
+    if (!code_map(&a.tm_a, Xf, a.M, K, kRows) || !code_map(&a.tm_b, Wf, a.N, K, COLS / 2)) return cudaErrorNotSupported;
     const int pairs = a.tiles < sms / 2 ? a.tiles : sms / 2;
-    return cluster_launch(f8_wide_kernel<TY>, dim3((unsigned)(2 * pairs)), 2, kWideThreads, kWideSmem, flags, stream, a);
+    return cluster_launch(f8_wide_kernel<COLS, TY>, dim3((unsigned)(2 * pairs)), 2, kWideThreads, Wide<COLS>::kSmem, flags, stream, a);
 }
 
 // How many clusters of a size the GPU holds at once, with one CTA an SM: fewer than SMs / size, as a
@@ -746,12 +755,21 @@ cudaError_t launch_narrow(F8Args& a, unsigned flags, cudaStream_t stream) {
 // 18944 x 3584, dependent launches).  Not where CTAs come in several waves, each with the values'
 // way to go again: 88.7 us instead of 87.0 at 1 x 3584 x 152064.
 bool makes_codes(int64_t M, int64_t N, int sms) { return M <= kOwnRows && (N + kRows - 1) / kRows <= 2 * (int64_t)sms; }
-// More than 128 rows whose narrow tiles leave K in one piece go wide: 512 x 3584 x 3584 (112 tiles) 21.2 us
-// there, 25.2 narrow, 384 x 18944 x 3584 (84) 69.5 and 82.6; 256 x 18944 x 3584 (56, two pieces) 70 and
-// 47.8, 1500 x 3584 x 512 (48) 21.2 and 19.1.  (Each call on its own, L2 flushed, fp16 out.)
+// More than 128 rows whose narrow tiles leave K in one piece go wide: 512 x 3584 x 3584 (112 tiles) 17.1 us
+// there, 25.2 narrow, 384 x 18944 x 3584 (84) 53.9 and 82.6.  With two pieces the two are within 12% of each
+// other: 256 x 18944 x 3584 (56) 53.9 and 47.8, 1500 x 3584 x 512 (48) 17.1 and 19.1; with more, narrow
+// wins: 777 x 3584 x 512 (28) 17.1 and 15.0.  (Each call on its own, L2 flushed, fp16 out.)
 bool goes_wide(int64_t M, int64_t N) {
     const int64_t n_tiles = (N + kRows - 1) / kRows;
     return n_tiles > 65535 || (M > 128 && n_tiles * ((M + kRows - 1) / kRows) > max_clusters(2));
+}
+
+// Tiles of 128 columns instead of 256 where the pairs of SMs go round as often: a block takes 0.77 of the
+// time.  512 x 18944 x 3584 (one round) 70.3 -> 53.9 us, 512 x 4096 x 4608 23.2 -> 19.1; with a round more,
+// 640 x 18944 x 3584 (two instead of one) 70.2 and 99, 1500 (three, two) 130 and 142.
+bool half_tiles(int64_t m_tiles, int64_t N, int sms) {
+    const int64_t pairs = sms / 2, full = m_tiles * ((N + 255) / 256), half = m_tiles * ((N + 127) / 128);
+    return (half + pairs - 1) / pairs == (full + pairs - 1) / pairs;
 }
 
 // Xf and sa, or, with X, up to kOwnRows rows of values of type x_f16.
@@ -769,10 +787,8 @@ cudaError_t launch_gemm(const uint8_t* Xf, const float* sa, const void* X, int x
     a.kbs = (int)((K + kF8Block - 1) / kF8Block);
     if (goes_wide(M, N)) {
         const int64_t m_tiles = (M + 2 * kRows - 1) / (2 * kRows);
-        a.tiles_a = (int)m_tiles;
-        a.tiles = (int)(m_tiles * ((N + kWideCols - 1) / kWideCols));
-        if (!code_map(&a.tm_a, Xf, M, K, kRows) || !code_map(&a.tm_b, Wf, N, K, kWideCols / 2)) return cudaErrorNotSupported;
-        return launch_wide<TY>(a, sms, flags, stream);
+        return half_tiles(m_tiles, N, sms) ? launch_wide<128, TY>(a, m_tiles, Xf, K, Wf, sms, flags, stream)
+                                           : launch_wide<256, TY>(a, m_tiles, Xf, K, Wf, sms, flags, stream);
     }
     const int64_t n_tiles = (N + kRows - 1) / kRows;
     const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;

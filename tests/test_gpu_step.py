@@ -106,7 +106,8 @@ def test_f8_quantize_weights(w4, N, K):
 SHAPES = [(1, 16, 1), (1, 128, 128), (1, 1024, 129), (2, 112, 257), (16, 3584, 512), (17, 144, 130), (32, 2048, 127),
           (33, 4096, 384), (64, 1040, 1000), (65, 256, 300), (128, 1152, 640), (129, 512, 128), (300, 640, 513),
           (130, 256, 26000), (1000, 1040, 9001), (513, 128, 20480), (257, 272, 20001),
-          (512, 3584, 512), (1500, 3584, 512), (400, 1024, 3584), (256, 1024, 4608)]
+          (512, 3584, 512), (1500, 3584, 512), (400, 1024, 3584), (256, 1024, 4608), (500, 2064, 4601), (257, 128, 3585),
+          (2560, 640, 500)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
