@@ -44,9 +44,8 @@ struct RopeArg {
     int rot, inter;
     float mscale;
     int64_t ld_pos;
-    uint32_t axis[8];  // of each pair, two bits: in the launch's constants, so that no load stands in front of
-                       // the position's (with one axis all are 0).  8191 x 32 x 128 with three axes 33.2 us
-                       // (30.1 at the copy rate), with one 30.8: three positions a token instead of one
+    int axes;          // that the pairs use
+    uint32_t axis[8];  // of each pair, two bits, in the launch's constants
 };
 
 struct WriteArgs {
@@ -142,8 +141,12 @@ struct PairWalk {
 // queries under way.  Queries come first, on their own: with the keys' slots, a chain of
 // loads, in front of every load and both kinds in one loop, 8190 tokens of 32 +
 // 2 heads took 44 us instead of 36.5 (a floor of 33).
-template <typename TX, typename TYO, int DIM, int BITS, bool HAS_KV>
-__global__ void __launch_bounds__(kLayerThreads) rope_write_kernel(const WriteArgs a) {
+// AXES: positions of more than one axis, in a variant of its own (the look-up of a pair's axis costs the
+// calls without one 6%: 8191 x 32 x 128 34.9 us a call instead of 32.8), held to the 48 registers of
+// the other: with 56, hence four CTAs an SM, 33.2 us in a graph instead of 31.9, as with one axis.  All
+// axes' positions loaded side by side with the look-up: 34.
+template <typename TX, typename TYO, int DIM, int BITS, bool HAS_KV, bool AXES>
+__global__ void __launch_bounds__(kLayerThreads, AXES ? 5 : 0) rope_write_kernel(const WriteArgs a) {
     constexpr int LPV = DIM / 8;
     extern __shared__ float2 cs[];  // [tokens_per_cta][rot / 2]
     __shared__ int64_t slot_row[16];
@@ -192,8 +195,12 @@ __global__ void __launch_bounds__(kLayerThreads) rope_write_kernel(const WriteAr
     // the last threads, whose warps have no look-up to make, first
     for (int e = kLayerThreads - 1 - (int)threadIdx.x; e < nt * pairs; e += kLayerThreads) {
         const int t = e / pairs, i = e - t * pairs;
-        const int64_t axis = a.rope.axis[i >> 4] >> (2 * (i & 15)) & 3;
-        cs[e] = turn_cos_sin(turn_fraction(a.rope.freqs[i]), a.rope.pos[axis * a.rope.ld_pos + t0 + t], a.rope.mscale);
+        if constexpr (AXES) {
+            const int64_t axis = a.rope.axis[i >> 4] >> (2 * (i & 15)) & 3;
+            cs[e] = turn_cos_sin(turn_fraction(a.rope.freqs[i]), a.rope.pos[axis * a.rope.ld_pos + t0 + t], a.rope.mscale);
+        } else {
+            cs[e] = turn_cos_sin(turn_fraction(a.rope.freqs[i]), a.rope.pos[t0 + t], a.rope.mscale);
+        }
     }
     __syncthreads();
     if (a.heads_q > 0) {
@@ -277,8 +284,11 @@ __global__ void __launch_bounds__(kLayerThreads) rope_write_kernel(const WriteAr
 // axis: host array of rot / 2 entries below 4, or NULL (one axis).
 RopeArg rope_arg(const int32_t* pos, int64_t tokens, const uint8_t* axis, const double* freqs, int rot, int inter,
                  float mscale) {
-    RopeArg r = {pos, freqs, rot, inter, mscale, tokens, {}};
-    for (int i = 0; axis != nullptr && i < rot / 2; ++i) r.axis[i / 16] |= (uint32_t)axis[i] << (2 * (i % 16));
+    RopeArg r = {pos, freqs, rot, inter, mscale, tokens, 1, {}};
+    for (int i = 0; axis != nullptr && i < rot / 2; ++i) {
+        r.axes = r.axes > axis[i] ? r.axes : axis[i] + 1;
+        r.axis[i / 16] |= (uint32_t)axis[i] << (2 * (i % 16));
+    }
     return r;
 }
 
@@ -294,10 +304,13 @@ cudaError_t launch_write(const WriteArgs& a0, int dim, int sms, unsigned flags, 
     while (ctas * gy < 2 * sms && gy * groups < vecs * a.tokens_per_cta) gy *= 2;
     const dim3 grid((unsigned)ctas, (unsigned)gy);
     const int smem = a.tokens_per_cta * (a.rope.rot / 2) * (int)sizeof(float2);
+    auto go = [&](auto* one, auto* several) {
+        return layer_launch(a.rope.axes > 1 ? several : one, grid, kLayerThreads, smem, flags, stream, a);
+    };
     switch (dim) {
-        case 64: return layer_launch(rope_write_kernel<TX, TYO, 64, BITS, HAS_KV>, grid, kLayerThreads, smem, flags, stream, a);
-        case 128: return layer_launch(rope_write_kernel<TX, TYO, 128, BITS, HAS_KV>, grid, kLayerThreads, smem, flags, stream, a);
-        case 256: return layer_launch(rope_write_kernel<TX, TYO, 256, BITS, HAS_KV>, grid, kLayerThreads, smem, flags, stream, a);
+        case 64: return go(rope_write_kernel<TX, TYO, 64, BITS, HAS_KV, false>, rope_write_kernel<TX, TYO, 64, BITS, HAS_KV, true>);
+        case 128: return go(rope_write_kernel<TX, TYO, 128, BITS, HAS_KV, false>, rope_write_kernel<TX, TYO, 128, BITS, HAS_KV, true>);
+        case 256: return go(rope_write_kernel<TX, TYO, 256, BITS, HAS_KV, false>, rope_write_kernel<TX, TYO, 256, BITS, HAS_KV, true>);
         default: return cudaErrorInvalidValue;
     }
 }
