@@ -781,7 +781,7 @@ int f8_gemm(const uint8_t* Xf, const float* sa, int64_t M, int64_t K, const uint
 
 /* f8_quantize_rows and f8_gemm in one call, the codes in the workspace
  * (f8_linear_workspace_bytes, 256-byte aligned, need not be zeroed, one call at a
- * time): the same Y. */
+ * time; what it holds afterwards is unspecified): the same Y. */
 size_t f8_linear_workspace_bytes(int64_t M, int64_t K, int64_t N);
 int f8_linear(const void* X, int x_type, int64_t M, int64_t K, const uint8_t* Wf, const float* sw, int64_t N, void* Y,
               int y_type, void* ws, size_t ws_bytes, unsigned flags, void* stream);
