@@ -67,7 +67,7 @@ typedef enum {
 
 /* Launch flag: allow the kernel to start while the previous kernel on the
    stream is still running (programmatic dependent launch).  The kernel then
-   streams Wq/Wq8 and the weight scales before waiting for the previous
+   streams Wq/Wq8/Wf and the weight scales before waiting for the previous
    kernel, so those weight buffers must NOT be written by the kernel launched
    immediately before it on the same stream.  Activations, outputs and the
    workspace are only touched after the wait. */
