@@ -621,10 +621,11 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
     for (int i = 1; i < n; ++i) {
         if (s.parent[i] != node) continue;
         const RowPart& p = s.row[node];
+        if (p.sum != p.sum) continue;  // no distribution: no child is taken, and no pass made for one
         const int id = s.id[i];
         bool yes;
         if (c.greedy) {
-            yes = id == p.at && p.sum == p.sum;
+            yes = id == p.at;
         } else if (a.Q == nullptr) {
             bool again = false;
             for (int k = 0; k < refused; ++k) again |= s.refused[k] == id;
