@@ -126,7 +126,8 @@ class Server:
         self.norm = torch.ones(hidden, device=device)
         self.cache = w4.kvq_cache(pages, page, layer.kv_heads, layer.dim, bits, device)
         self.pool = w4.kvq_pool(seqs, max_pages, pages, device)
-        self.lens, self.grow = (torch.zeros(seqs, dtype=torch.int32, device=device) for _ in range(2))
+        # shift: the next rotary position of each request less its cached tokens (an image's tokens share positions)
+        self.lens, self.grow, self.shift = (torch.zeros(seqs, dtype=torch.int32, device=device) for _ in range(3))
 
     def logits(self, r, y):
         return w4.w4a8_linear(w4.add_norm(r, self.norm, y=y)[1], *self.head)
@@ -134,9 +135,13 @@ class Server:
     def prompt(self, add, x, pos, axis):
         """x [tokens][hidden]: the rows of add [seqs] new tokens each (0: none, -1: the
         request ended), pos [axes][tokens].  Returns the logits of each request's last token."""
-        batch, *_ = w4.kvq_plan(self.pool, self.page, self.lens, add, x.shape[0], grow=self.grow)
+        batch, _, _, seq = w4.kvq_plan(self.pool, self.page, self.lens, add, x.shape[0], grow=self.grow)
         r, y = self.layer.prompt(x, None, self.cache, batch, pos, axis)
         self.grow = (batch.cu[1:] - batch.cu[:-1]).contiguous()  # a request that had to wait has grown by nothing
+        top = torch.full((add.shape[0] + 1,), -1, dtype=torch.int32, device=pos.device)  # largest positions: of no row, of each
+        top.scatter_reduce_(0, seq.long() + 1, pos.amax(0), "amax")
+        ended = self.shift.masked_fill(add < 0, 0)
+        self.shift.copy_(torch.where(self.grow > 0, top[1:] + 1 - self.lens - self.grow, ended))
         last = (batch.cu[1:] - 1).clamp_min(0).long()
         return self.logits(r[last], y[last])
 
@@ -144,7 +149,9 @@ class Server:
         """ids [tokens]: of each request its last token, then its drafts, a tree by mask.
         Returns what draft_verify does."""
         batch, pos, slot, seq = w4.kvq_plan(self.pool, self.page, self.lens, add, ids.shape[0], grow=self.grow, mask=mask)
-        r, y = self.layer.step(self.embed[ids.long()], None, self.cache, batch, pos, mask)
+        self.shift.masked_fill_(add < 0, 0)
+        at = pos + self.shift[seq.clamp_min(0).long()]  # slots count all tokens, positions go on from the prompt's
+        r, y = self.layer.step(self.embed[ids.long()], None, self.cache, batch, at, mask)
         logits = self.logits(r, y)
         keep, out, count = w4.draft_verify(logits, batch.cu, ids, u, mask=mask, temp=temp)
         if trace is not None:
