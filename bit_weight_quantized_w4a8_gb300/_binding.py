@@ -1001,7 +1001,9 @@ def kvq_plan(pool, page: int, lens, add, tokens: int, grow=None, mask=None, cu=N
     pages they lack (or wait, if these or the tokens do not reach).  Returns
     (KVQBatch(cu, lens, pool.table), pos, slot, seq): positions int32 (with mask
     [tokens] int64: by depth in the drafted tree), rows of the pool int64 and
-    rows of the batch int32 of the step's tokens."""
+    rows of the batch int32 of the step's tokens.  mask lies as add asks, those
+    that wait included; token t of row b is at[b] + t - cu[b] of such a layout, at =
+    the sums of max(add, 0) before each row."""
     dev = _device_of(lens, "lens")
     pa, seqs = _pool_arg(pool, page, dev)
     i32, n = torch.int32, (seqs,)

@@ -53,8 +53,8 @@ struct PlanArgs {
     int32_t *cu, *pos, *seq;
     int64_t* slot;
     // workspace: first page of each row among those given back and handed out,
-    // pages held before, totals
-    int32_t *back_at, *need_at, *old_held;
+    // pages held before, first word of its tree (with mask), totals
+    int32_t *back_at, *need_at, *old_held, *ask_at;
     PlanTotals* totals;
     const int32_t *cu_at, *len_at;  // cu and lens as the look-ups read them
     int wide;                       // pos, slot and seq on 16 bytes
@@ -157,7 +157,7 @@ __device__ void plan_fill(const PlanArgs& a, const PlanTotals& t, int64_t i, int
             if (k < t.tokens) {
                 while (a.cu_at[row + 1] <= k) ++row;
                 const int len = a.len_at[row], x = len + (int)(k - a.cu_at[row]);
-                pos[e] = a.mask != nullptr ? len + __popcll(a.mask[k]) - 1 : x;
+                pos[e] = a.mask != nullptr ? len + __popcll(a.mask[a.ask_at[row] + (x - len)]) - 1 : x;
                 seq[e] = row;
                 if (a.slot != nullptr) {
                     const int64_t j = x >> a.shift, old = a.old_held[row];
@@ -191,7 +191,7 @@ constexpr int kOneRows = 1024;
 template <int ITEMS, bool FILL, bool kOne>
 __global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const __grid_constant__ PlanArgs args) {
     __shared__ ScanShared sh;
-    __shared__ int32_t rows_at[kOne ? 5 : 1][kOne ? kOneRows + 1 : 1];
+    __shared__ int32_t rows_at[kOne ? 6 : 1][kOne ? kOneRows + 1 : 1];
     PlanArgs a = args;
     if constexpr (kOne) {
         a.back_at = rows_at[0];
@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const __grid_co
         a.old_held = rows_at[2];
         a.cu_at = rows_at[3];
         a.len_at = rows_at[4];
+        a.ask_at = rows_at[5];
     }
     griddep_launch_dependents();
     griddep_wait();
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const __grid_co
     const int top_in = *a.top;
     int64_t len[ITEMS], n[ITEMS];
     int held[ITEMS], back[ITEMS];
-    int64_t back_sum = 0;
+    int64_t back_sum = 0, ask_sum = 0;
     #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
         len[i] = n[i] = 0;
@@ -229,24 +230,29 @@ __global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const __grid_co
                 len[i] = 0;
             }
             back_sum += back[i];
+            ask_sum += n[i];
         }
     }
     int turn = 0;
     Pair total;
-    const Pair bp = cluster_scan({back_sum, 0}, sh, turn, &total);
+    const Pair bp = cluster_scan({back_sum, ask_sum}, sh, turn, &total);
     PlanTotals t;
     t.top = (int)min((int64_t)max(top_in, 0), a.pages);
     t.back = total.a;
     t.mid = (int)min(t.top + total.a, a.pages);
     bad |= t.top != top_in || t.top + total.a > a.pages;
 
-    int64_t need[ITEMS], ask_p = 0, ask_n = 0;
+    // trees' words lie as all rows ask for tokens, whether they go in or wait: the caller
+    // lays them out before the call
+    int64_t need[ITEMS], ask_p = 0, ask_n = 0, words = bp.b;
     #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
         need[i] = 0;
+        if (a.mask != nullptr && i < rows) a.ask_at[r0 + i] = (int)min(words, (int64_t)a.room);
         if (n[i] > 0) {
             const int64_t end = len[i] + n[i], want = (end + (1 << a.shift) - 1) >> a.shift;
-            if (want > a.max_pages || end > kKvqMaxSlots)
+            words += n[i];
+            if (want > a.max_pages || end > kKvqMaxSlots || (a.mask != nullptr && words > a.room))
                 n[i] = 0;
             else
                 need[i] = max(want - held[i], (int64_t)0);
@@ -312,7 +318,7 @@ __global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(const __grid_co
 
 }  // namespace
 
-size_t kvq_plan_workspace(const kvq_pool_t& p) { return 256 + 3 * (size_t)((p.seqs + 63) / 64 * 64) * 4; }
+size_t kvq_plan_workspace(const kvq_pool_t& p) { return 256 + 4 * (size_t)((p.seqs + 63) / 64 * 64) * 4; }
 
 cudaError_t launch_kvq_plan(const kvq_pool_t& p, int32_t* lens, const int32_t* grow, const int32_t* add,
                             const uint64_t* mask, int64_t tokens, int32_t* cu, int32_t* pos, int64_t* slot,
@@ -340,6 +346,7 @@ cudaError_t launch_kvq_plan(const kvq_pool_t& p, int32_t* lens, const int32_t* g
     a.back_at = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + 256);
     a.need_at = a.back_at + pad;
     a.old_held = a.need_at + pad;
+    a.ask_at = a.old_held + pad;
     a.cu_at = cu;
     a.len_at = lens;
     a.wide = reinterpret_cast<uintptr_t>(pos) % 16 == 0 && reinterpret_cast<uintptr_t>(slot) % 16 == 0 &&

@@ -685,10 +685,15 @@ typedef struct {
  *   add[b] = 0: no tokens, nothing changes.
  * Outputs: cu [seqs + 1]; lens is the batch's start; for token t of row b,
  * slot s = lens[b] + t - cu[b]: pos [tokens] = s (with mask: lens[b] + the number
- * of bits of mask[t] - 1, the depth in a drafted tree whose words hold ancestors and self),
+ * of bits of its word - 1, the depth in a drafted tree whose words hold ancestors and self),
  * slot [tokens] int64 = page * (the row's page of s) + s % page, the row of
  * the pool in kvq_cache_t, -1 where that page is outside the pool, seq [tokens] = b;
  * from cu[seqs] on pos 0, slot -1, seq -1.  pos, slot, seq: NULL to skip.
+ * mask [tokens] lies as the rows ask, which a caller knows before the call: the words of row b
+ * begin at at[b] = the sum of max(add, 0) of the rows before it, whether these go in or wait; a row
+ * whose words do not lie within `tokens` waits.  Where rows may have to wait, what else the caller laid
+ * out by add (ids, random numbers, activations, and the mask itself) is gathered before the calls that
+ * take the batch: token t of row b is number at[b] + t - cu[b] of it.
  * Counters out of range (held, lens, top, pages coming back onto a full stack)
  * are cut to it and set bit 3 of the device error word; no address outside the arrays is
  * touched as long as page numbers are only moved, which is all this call does.

@@ -49,3 +49,54 @@ def test_no_child_of_a_row_with_a_nan_is_taken(w4):  # noqa: F811
     same(got, sref.verify(logits, cu, ids, u, mask, q))
     bad = np.arange(seqs) % 3 < 2
     assert np.all(got[2][bad] == 1) and np.all(got[1][::5][bad] == -1) and np.all(got[2][~bad] > 1)
+
+
+# -- the plan of a step ----------------------------------------------------------------
+
+def plan_with_trees(host, add, tokens, mask, grow):
+    """sref.Pool.plan with the mask laid out as `add` asks; a row whose words lie past the mask waits."""
+    asked = np.maximum(np.asarray(add, np.int64), 0)
+    at = np.cumsum(asked) - asked
+    cu, pos, slot, seq = host.plan(np.where(at + asked > tokens, np.minimum(add, 0), add), tokens, grow)
+    n = cu[-1]
+    s = seq[:n]
+    word = mask.view(np.uint64)[at[s] + np.arange(n) - cu[s]]
+    pos[:n] = host.lens[s] + np.array([bin(int(x)).count("1") for x in word], np.int64) - 1
+    return cu, pos, slot, seq
+
+
+@pytest.mark.parametrize("seqs,width", [(40, 4), (1000, 3), (1500, 4), (9000, 3), (6000, 40)])
+def test_kvq_plan_reads_trees_where_they_were_asked(w4, seqs, width):  # noqa: F811
+    """Rows that wait, for pages or for good, between rows that go in: each row's positions come from its own tree,
+    whose words the caller laid out before it could know."""
+    rng = np.random.default_rng(seqs + width)
+    page = 16
+    lens = rng.integers(0, width * page // 2, seqs)
+    pages = int((-(-lens // page)).sum()) + seqs // 40
+    host = make_pool(rng, seqs, width, pages, page, lens)
+    pool = w4.KVQPool(*(dev(np.asarray(a).astype(I32)) for a in (host.table, host.held, host.stack, [host.top])))
+    dl = dev(lens.astype(I32))
+    add = rng.integers(0, 5, seqs)
+    add[rng.random(seqs) < 0.2] = 0
+    if width <= 4:
+        add[rng.random(seqs) < 0.05] = -1
+    add[rng.random(seqs) < 0.05] = 64  # too long for a narrow table
+    grow = rng.integers(0, 2, seqs)
+    trees = [tree_words(int(a), rng) for a in add if a > 0]
+    asked = int(np.maximum(add, 0).sum())
+    waits = 0
+    for tokens in (asked + 3, asked - asked // 3):
+        mask = np.concatenate(trees + [np.zeros(3, I64)])[:tokens]
+        outs = [guards.out((seqs + 1,), torch.int32), guards.out((tokens,), torch.int32), guards.out((tokens,), torch.int64),
+                guards.out((tokens,), torch.int32)]
+        ws = guards.out((w4.kvq_plan_workspace_bytes(pool, page),), torch.uint8)
+        w4.kvq_plan(pool, page, dl, dev(add.astype(I32)), tokens, grow=dev(grow.astype(I32)), mask=dev(mask), cu=outs[0].t,
+                    pos=outs[1].t, slot=outs[2].t, seq=outs[3].t, ws=ws.t)
+        guards.check_all(*outs, ws)
+        want = plan_with_trees(host, add, tokens, mask, grow)
+        for o, x, name in zip(outs, want, ("cu", "pos", "slot", "seq")):
+            assert np.array_equal(np_(o.t), x), name
+        assert np.array_equal(np_(dl), host.lens) and int(pool.top[0]) == host.top
+        inside = np.diff(want[0]) > 0
+        waits += int((~inside & (add > 0))[:np.flatnonzero(inside)[-1]].sum())
+    assert waits >= 2
