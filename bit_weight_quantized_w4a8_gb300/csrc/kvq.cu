@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kLayerThreads, AXES ? 5 : 0) rope_write_kernel
                 const int64_t slot = kvq_token_slot(a.b.cu, a.b.start, b, i);
                 if (slot >= 0) row = kvq_slot_row(a.b.table, a.b.max_pages, a.c.pages, a.c.shift, b, slot);
             }
-            if (row < 0) atomicOr(&g_kvq_error, kErrCacheRange);
+            if (row < 0 && (b >= 0 || !kvq_behind(a.b.cu, a.b.seqs, i))) atomicOr(&g_kvq_error, kErrCacheRange);
             slot_row[threadIdx.x] = row;
         }
     }
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kLayerThreads) kvq_read_kernel(const KvqCacheA
         int64_t row = -1;
         const int s = kvq_find_seq(b.cu, b.seqs, i);
         if (s >= 0) row = kvq_slot_row(b.table, b.max_pages, c.pages, c.shift, s, kvq_token_slot(b.cu, b.start, s, i));
-        if (row < 0) atomicOr(&g_kvq_error, kErrCacheRange);
+        if (row < 0 && (s >= 0 || !kvq_behind(b.cu, b.seqs, i))) atomicOr(&g_kvq_error, kErrCacheRange);
         slot_row[threadIdx.x] = row;
     }
     __syncthreads();

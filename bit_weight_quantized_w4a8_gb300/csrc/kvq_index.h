@@ -30,6 +30,9 @@ KVQ_HD int kvq_find_seq(const int32_t* cu, int seqs, int i) {
     return cu[lo] >= 0 && cu[lo] <= i && i < cu[lo + 1] ? lo : -1;
 }
 
+// Whether token i lies behind the last sequence: a step planned for more tokens than went in.
+KVQ_HD bool kvq_behind(const int32_t* cu, int seqs, int i) { return cu[seqs] >= 0 && i >= cu[seqs]; }
+
 // Slot of token i of the sequence b that kvq_find_seq gives, or -1 where its start is negative.
 KVQ_HD int64_t kvq_token_slot(const int32_t* cu, const int32_t* start, int b, int i) {
     const int64_t s = start[b];

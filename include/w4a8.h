@@ -561,7 +561,8 @@ typedef struct {
 /* The tokens of a call, sequence by sequence (all device arrays of int32, so
  * that a captured graph follows them):
  *   cu [seqs + 1]: tokens cu[b] .. cu[b + 1] - 1 are sequence b's (none is
- *     fine); cu[0] = 0, not decreasing, cu[seqs] = tokens;
+ *     fine); cu[0] = 0, not decreasing, cu[seqs] <= tokens; tokens from cu[seqs] on
+ *     are no sequence's and left out (a planned step in which requests wait);
  *   start [seqs]: token cu[b] + i sits in (goes to, comes from) the
  *     sequence's slot start[b] + i;
  *   table [seqs][max_pages]: slot s lies in page table[b][s / page].

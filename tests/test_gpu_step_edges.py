@@ -100,3 +100,32 @@ def test_kvq_plan_reads_trees_where_they_were_asked(w4, seqs, width):  # noqa: F
         inside = np.diff(want[0]) > 0
         waits += int((~inside & (add > 0))[:np.flatnonzero(inside)[-1]].sum())
     assert waits >= 2
+
+
+def test_tokens_behind_a_batch_with_a_waiting_row_are_no_error(w4):  # noqa: F811
+    """A step planned for more tokens than went in: the cache's write and read leave the others out, and the error
+    word stays 0; offsets that are not in order, or negative, set it as ever."""
+    g = torch.Generator(device="cuda").manual_seed(37)
+    page, heads, dim, n = 16, 2, 64, 40
+    i32 = dict(dtype=torch.int32, device="cuda")
+    pool = w4.kvq_pool(3, 2, 2)
+    lens = torch.zeros(3, **i32)
+    batch, pos, slot, seq = w4.kvq_plan(pool, page, lens, torch.tensor([10, 20, 5], **i32), n)
+    assert batch.cu.tolist() == [0, 10, 10, 10]
+    cache = w4.kvq_cache(2, page, heads, dim, 8)
+    cache.ks.fill_(-3)
+    q, k, v = (torch.randn((n, h, dim), device="cuda", generator=g) for h in (4, heads, heads))
+    f = torch.ones(dim // 2, dtype=torch.float64, device="cuda")
+    qr = w4.kvq_write(cache, batch, k, v, Q=q, pos=pos, freqs=f)
+    out = torch.full((n, heads, dim), 7.0, device="cuda")
+    w4.kvq_read(cache, batch, n, K=out, V=torch.empty_like(out))
+    w4.kvq_attention(qr, cache, batch)
+    w4.kvq_keep(cache, batch, torch.zeros(n, **i32))
+    assert w4.w4a8_device_error() == 0
+    turned = w4.rope_rotate(k, pos, f)
+    assert float((out[:10] - turned[:10]).abs().max()) <= float(turned[:10].abs().max()) / 127 * 0.51
+    assert bool((out[10:] == 7).all()) and bool((cache.ks[1, :, :10] >= 0).all())
+    assert bool((cache.ks[0] == -3).all()) and bool((cache.ks[1, :, 10:] == -3).all())
+    for cu in ([2, 10, 10, 10], [0, 10, 5, 40], [0, -1, -1, -1], [0, 10, 10, -5]):
+        w4.kvq_write(cache, w4.KVQBatch(torch.tensor(cu, **i32), lens, pool.table), k, v)
+        assert w4.w4a8_device_error() == 8, cu
