@@ -132,10 +132,22 @@ class Server:
     def logits(self, r, y):
         return w4.w4a8_linear(w4.add_norm(r, self.norm, y=y)[1], *self.head)
 
+    def asked(self, add, batch, seq):
+        """Of each token of the batch its number among those that `add` asks for: rows that wait
+        leave theirs out.  (0 for those behind the last.)"""
+        ask = add.clamp_min(0)
+        at = ask.cumsum(0) - ask - batch.cu[:-1]
+        n = seq.shape[0]
+        number = at[seq.clamp_min(0).long()] + torch.arange(n, device=seq.device)
+        return torch.where(seq < 0, 0, number).clamp_(0, n - 1)
+
     def prompt(self, add, x, pos, axis):
         """x [tokens][hidden]: the rows of add [seqs] new tokens each (0: none, -1: the
-        request ended), pos [axes][tokens].  Returns the logits of each request's last token."""
+        request ended), pos [axes][tokens].  Returns the logits of each request's last token; a
+        request that had to wait (grow 0) is to ask again and has none."""
         batch, _, _, seq = w4.kvq_plan(self.pool, self.page, self.lens, add, x.shape[0], grow=self.grow)
+        number = self.asked(add, batch, seq)
+        x, pos = x[number], pos[:, number]
         r, y = self.layer.prompt(x, None, self.cache, batch, pos, axis)
         self.grow = (batch.cu[1:] - batch.cu[:-1]).contiguous()  # a request that had to wait has grown by nothing
         top = torch.full((add.shape[0] + 1,), -1, dtype=torch.int32, device=pos.device)  # largest positions: of no row, of each
@@ -146,9 +158,12 @@ class Server:
         return self.logits(r[last], y[last])
 
     def step(self, add, ids, mask, u, temp, trace=None):
-        """ids [tokens]: of each request its last token, then its drafts, a tree by mask.
-        Returns what draft_verify does."""
+        """ids [tokens]: of each request its last token, then its drafts, a tree by mask, as
+        add asks for them.  Returns what draft_verify does, in the same places: -1, and count 0, for a
+        request that had to wait."""
         batch, pos, slot, seq = w4.kvq_plan(self.pool, self.page, self.lens, add, ids.shape[0], grow=self.grow, mask=mask)
+        number = self.asked(add, batch, seq)
+        ids, mask, u = ids[number], mask[number], u[number]
         self.shift.masked_fill_(add < 0, 0)
         at = pos + self.shift[seq.clamp_min(0).long()]  # slots count all tokens, positions go on from the prompt's
         r, y = self.layer.step(self.embed[ids.long()], None, self.cache, batch, at, mask)
@@ -158,6 +173,8 @@ class Server:
             trace.update(batch=batch, pos=pos, slot=slot, seq=seq, logits=logits, before=w4.kvq_read(self.cache, batch, ids.shape[0]))
         w4.kvq_keep(self.cache, batch, keep)
         self.grow = count
+        places = torch.where(seq < 0, ids.shape[0], number)  # (one more for the tokens that no row holds)
+        keep, out = (t.new_full((ids.shape[0] + 1,), -1).index_copy_(0, places, t)[:-1] for t in (keep, out))
         return keep, out, count
 
 
@@ -227,7 +244,8 @@ def main():
         ids = torch.randint(0, 1000, (seqs, len(parents)), device="cuda", dtype=torch.int32)
         ids[:, 0] = roots
         keep, out, count = server.step(add, ids.reshape(-1), mask, torch.rand(ids.numel(), device="cuda"), temp)
-        roots = out.view(seqs, -1).gather(1, (count.long() - 1)[:, None])[:, 0]
+        said_last = out.view(seqs, -1).gather(1, (count.long() - 1).clamp_min(0)[:, None])[:, 0]
+        roots = torch.where(count > 0, said_last, roots)  # a request that had to wait asks again
         said += int(count.sum())
     assert w4.w4a8_device_error() == 0
     print("%d requests served: %d tokens of prompts, %d tokens said in 4 steps" % (seqs, sum(sizes), said))
