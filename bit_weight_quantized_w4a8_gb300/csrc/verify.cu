@@ -20,7 +20,7 @@
 // roundings would decide between neighbours now and then.  So the fp32 sums only
 // decide where the number lies further from the token's two edges than they can be off: by
 // at most kOff Z, counted at its definition.  Otherwise the row's weights are taken as integers:
-// w in units of 2^-40 of the largest, each within a few units of the exact value (the
+// w in units of 2^-40 of the largest, each within 3 units of the exact value (the
 // exponent's argument in two floats, a table of 2^(i/128), a polynomial of four terms), so
 // that sums are exact, in any order and split.  That is 40 instructions a weight: a CTA's
 // 19008 weights of a row of 152064 take 8.4 us, 14.5 with the draft's probabilities, in fp32 2.7.
@@ -223,7 +223,10 @@ struct Unit {
     float hi, lo, top;  // log2(e) / T, the row's maximum
 };
 
-// exp((l - top) / T) in units of 2^-40, 0 below half a unit.
+// exp((l - top) / T) in units of 2^-40, 0 below half a unit.  With y = yh + yl what is left of the exponent
+// after the table's 2^(k/128), |y| <= 2^-8.5: exp(y) - 1 = yh + (yl + yh yl + yh^2 (1/2 + yh/6 + yh^2/24)), of which
+// the term yh yl (yl holds the rounding of the scaled difference) makes up to 150 units and yh^5 / 120 less
+// than 1/100.  Worst of 10^8 logits at temperatures from 0.1 to 7: 2.6 units.
 __device__ __forceinline__ uint64_t weight(float l, const Unit& s, const uint64_t* pow2) {
     constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
     // the difference in two floats, before it is scaled: logits near the type's ends must not overflow
@@ -237,7 +240,7 @@ __device__ __forceinline__ uint64_t weight(float l, const Unit& s, const uint64_
     constexpr float kLn2 = 0.693147182464599609375f, kLn2Lo = -1.90465429995776e-9f;
     const float yh = r * kLn2;
     const float yl = fmaf(r, kLn2, -yh) + fmaf(r, kLn2Lo, e * kLn2);
-    const float q = yh * yh * fmaf(yh, fmaf(yh, 1.f / 24.f, 1.f / 6.f), 0.5f);
+    const float q = fmaf(yh, yl, yh * yh * fmaf(yh, fmaf(yh, 1.f / 24.f, 1.f / 6.f), 0.5f));
     const int z = __float2int_rn(yh * 0x1p39f) + __float2int_rn((yl + q) * 0x1p39f);  // exp(y) - 1
     const uint64_t w = pow2[k & 127];
     const int64_t v = (int64_t)w + ((int64_t)(uint32_t)(w >> 9) * z >> 30);

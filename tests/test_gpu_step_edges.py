@@ -51,6 +51,37 @@ def test_no_child_of_a_row_with_a_nan_is_taken(w4):  # noqa: F811
     assert np.all(got[2][bad] == 1) and np.all(got[1][::5][bad] == -1) and np.all(got[2][~bad] > 1)
 
 
+def test_weights_of_a_draw_are_within_four_units(w4):  # noqa: F811
+    """The first token has the largest weight, 2^40 units; four others are chosen to weigh as much together,
+    18 units more or less, to a unit.  With each of them within 4 units of its exact weight, half the sum passes the
+    first token or not as the exact sums say."""
+    rng = np.random.default_rng(32)
+    n, one = 6000, 2.0 ** 40
+    temp = rng.uniform(0.3, 3, n).astype(F32)
+    t = temp.astype(np.float64)
+    top = np.where(rng.random(n) < 0.5, 0, rng.uniform(-20, 20, n)).astype(F32)
+    logits = np.zeros((n, 5), F32)
+    logits[:, 0] = top
+    side = np.where(rng.random(n) < 0.5, 18.0, -18.0)
+    left = one + side
+
+    def weight(l):
+        return np.exp((l.astype(np.float64) - top.astype(np.float64)) / t) * one
+
+    for k in (1, 2, 3, 4):
+        want = left * rng.uniform(0.2, 0.8, n) if k == 1 else left
+        l = (top + t * np.log(np.maximum(want, 0.4) / one)).astype(F32)
+        for _ in range(4):  # from below
+            l = np.where(weight(l) > want, np.nextafter(l, NEG), l)
+        logits[:, k] = l
+        left = left - weight(l)
+    assert np.all(np.abs(left) < 1)
+    got = run_verify(w4, logits, np.arange(n + 1, dtype=I32), np.zeros(n, I32), np.full(n, 0.5, F32), None, None, temp)
+    assert np.all(got[2] == 1)
+    wrong = (got[1] == 0) != (side < 0)
+    assert not wrong.any(), "%d of %d" % (wrong.sum(), n)
+
+
 # -- the plan of a step ----------------------------------------------------------------
 
 def plan_with_trees(host, add, tokens, mask, grow):
