@@ -262,17 +262,29 @@ __device__ __forceinline__ uint64_t target_of(float u, uint64_t a) {
     const uint64_t hi = __umul64hi(a, m), lo = a * m;
     return sh < 64 ? hi << (64 - sh) | lo >> sh : sh < 128 ? hi >> (sh - 64) : 0;
 }
-// 16 q a, to nearest (cut off instead, 10^5 weights less q A would all lean to one side, and their
-// sum by as many halves of a unit); from q = 2^-12 on within 2^-32 of it, above 64 bits their
-// largest number.  q outside [0, 1]: the nearest inside; NaN: 0.
-constexpr int kCutShift = 4;  // sums of up to 2^22 weights, 63 times, in 64 bits
-__device__ __forceinline__ uint64_t part_of(float q, uint64_t a) {
+// What refusals take off in all, A = m 2^sh: sh is 0 until the sum passes 64 bits (2^22 weights, 63 times, reach
+// 2^68), then each step cuts off less than 2^-63 of it.
+struct Cut {
+    uint64_t m;
+    int sh;
+    __device__ __forceinline__ void add(uint64_t x) {
+        m += x >>= sh;
+        if (m < x) m = m >> 1 | (uint64_t)1 << 63, ++sh;
+    }
+};
+// q A to nearest (cut off instead, 10^5 weights less q A would all lean to one side, and their
+// sum by as many halves of a unit), above 64 bits their largest number.  q outside [0, 1]: the
+// nearest inside; NaN: 0.
+__device__ __forceinline__ uint64_t part_of(float q, const Cut& a) {
     if (!(q > 0.f)) return 0;
-    uint32_t m;
-    const int sh = split(fminf(q, 1.f), m) - kCutShift;
-    const uint64_t p = ((uint64_t)(uint32_t)(a >> 32) * m << 1) + ((uint64_t)(uint32_t)a * m >> 31);  // a m 2^-31
-    if (sh < 32) return p >> (32 + sh) >> 1 != 0 ? ~(uint64_t)0 : p << (31 - sh);
-    return sh < 90 ? ((p >> (sh - 32)) + 1) >> 1 : 0;
+    uint32_t f;
+    const int sh = split(fminf(q, 1.f), f) - a.sh;  // q A = f m 2^-sh, sh 19 .. 149
+    const uint64_t hi = (uint64_t)(uint32_t)(a.m >> 32) * f, lo = (uint64_t)(uint32_t)a.m * f;  // each below 2^56
+    if (sh <= 32) {
+        const uint64_t x = hi << (32 - sh), y = x + ((lo + (1u << (sh - 1))) >> sh);
+        return hi >> 32 >> sh != 0 || y < x ? ~(uint64_t)0 : y;
+    }
+    return sh < 92 ? (hi + (lo >> 32) + ((uint64_t)1 << (sh - 33))) >> (sh - 32) : 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -365,10 +377,10 @@ struct Draw {
             return to_units(warp_sum(sum));
         }
     };
-    // ... and as integers, exact sums (cut: A in 16 units; 0: without q).
+    // ... and as integers, exact sums (cut: A).
     struct Exact {
         Unit unit;
-        uint64_t cut;
+        Cut cut;
         const uint64_t* pow2;
         bool with_q;
         __device__ __forceinline__ uint64_t units(float l, float q) const {
@@ -605,18 +617,18 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
     // shared values that all CTAs computed alike, and on the passes' totals.
     int node = 0, taken = 1, refused = 0, cuts = 0, todo = 0;  // cuts of todo made
     float gone = 0.f;                                          // weights of the refused
-    uint64_t cut = 0;
-    auto exact = [&](uint64_t by) {
-        return typename Draw<T>::Exact{{c.hi, c.lo, s.row[node].top}, by, s.pow2, by != 0};
+    Cut cut = {0, 0};
+    auto exact = [&](bool less) {
+        return typename Draw<T>::Exact{{c.hi, c.lo, s.row[node].top}, cut, s.pow2, less};
     };
     auto make_cuts = [&]() {
         while (cuts < todo) {
-            if (cuts == 0) {
-                dr.pass(first + node, exact(0), 0);
-            }
-            cut += (dr.total + (1 << kCutShift >> 1)) >> kCutShift;
-            if (cut == 0) break;
-            dr.pass(first + node, exact(cut), 0);
+            if (cuts == 0)
+                dr.pass(first + node, exact(false), 0);
+            else if (dr.total == 0)
+                break;  // nothing is left, and nothing more is taken off
+            cut.add(dr.total);
+            dr.pass(first + node, exact(true), 0);
             ++cuts;
         }
         cuts = todo;
@@ -646,7 +658,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
         } else {
             make_cuts();
             uint64_t w = 0;
-            if (id >= 0 && id < a.vocab) w = exact(cut).units(load1(dr.row(first + node) + id), s.q[i]);
+            if (id >= 0 && id < a.vocab) w = exact(true).units(load1(dr.row(first + node) + id), s.q[i]);
             yes = s.u[i] * s.q[i] * (float)dr.total < (float)w;
             todo += !yes;
         }
@@ -656,7 +668,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
             node = i;
             refused = cuts = todo = 0;
             gone = 0.f;
-            cut = 0;
+            cut = {0, 0};
         }
     }
     // the token after the last one taken
@@ -682,13 +694,14 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
         }
         if (next < 0) {
             make_cuts();
-            if (todo == 0) dr.pass(t, exact(0), refused);
-            if (dr.total == 0 && (todo != 0 || refused != 0)) {  // nothing left but roundings: the whole row
-                cut = 0;
+            bool less = todo != 0;
+            if (!less) dr.pass(t, exact(false), refused);
+            if (dr.total == 0 && (less || refused != 0)) {  // nothing left but roundings: the whole row
+                less = false;
                 refused = 0;
-                dr.pass(t, exact(0), 0);
+                dr.pass(t, exact(false), 0);
             }
-            next = dr.find(t, exact(cut), refused, target_of(u, dr.total), 0);
+            next = dr.find(t, exact(less), refused, target_of(u, dr.total), 0);
             mine = next >= 0 || (dr.total == 0 && mine);
         }
     }

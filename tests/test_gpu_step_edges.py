@@ -82,6 +82,36 @@ def test_weights_of_a_draw_are_within_four_units(w4):  # noqa: F811
     assert not wrong.any(), "%d of %d" % (wrong.sum(), n)
 
 
+def test_what_a_refusal_takes_off_is_rounded_once(w4):  # noqa: F811
+    """A refused draft whose probabilities leave k 2^-24 of a weight of 2^40 units (the row's largest), and two tokens
+    that weigh as much as what is left, 24 units more or less.  Each of the two weights may be 4 units off, hence the
+    row's sum 8, and what is taken off half a unit more: less than 17 in all."""
+    rng = np.random.default_rng(33)
+    n, one = 3000, 2.0 ** 40
+    k = rng.integers(1, 1 << rng.integers(2, 20, n))
+    q0 = 1 - k * 2.0 ** -24
+    side = np.where(rng.random(n) < 0.5, 24.0, -24.0)
+    logits, q = np.full((2 * n, 4), NEG, F32), np.zeros((2 * n, 4), F32)
+    logits[::2, 0], logits[1::2] = 0, 0
+    q[::2, 0], q[::2, 1] = q0, k * 2.0 ** -25
+    assert np.all(q[::2, 0].astype(np.float64) == q0)
+    # rest = 2^40 - q0 (2^40 + rest) + side
+    rest = left = (k * 2.0 ** 16 + side) / (1 + q0)
+    for c in (2, 3):
+        l = np.log(np.maximum(left, 1) / one).astype(F32)
+        for _ in range(4):
+            l = np.where(np.exp(l.astype(np.float64)) * one > left, np.nextafter(l, NEG), l)
+        logits[::2, c] = np.where(left > 1, l, NEG)
+        left = left - np.exp(logits[::2, c].astype(np.float64)) * one
+    assert np.all(np.abs(left) < 4) and np.all(rest > 2.0 ** 14)
+    ids = np.ones(2 * n, I32)  # a token without weight: refused
+    u = np.full(2 * n, 0.5, F32)
+    got = run_verify(w4, logits, np.arange(0, 2 * n + 1, 2, dtype=I32), ids, u, None, q)
+    assert np.all(got[2] == 1)
+    wrong = (got[1][::2] == 0) != (side < 0)
+    assert not wrong.any(), "%d of %d" % (wrong.sum(), n)
+
+
 # -- the plan of a step ----------------------------------------------------------------
 
 def plan_with_trees(host, add, tokens, mask, grow):
