@@ -240,8 +240,8 @@ __device__ __forceinline__ uint64_t weight(float l, const Unit& s, const uint64_
     constexpr float kLn2 = 0.693147182464599609375f, kLn2Lo = -1.90465429995776e-9f;
     const float yh = r * kLn2;
     const float yl = fmaf(r, kLn2, -yh) + fmaf(r, kLn2Lo, e * kLn2);
-    const float q = fmaf(yh, yl, yh * yh * fmaf(yh, fmaf(yh, 1.f / 24.f, 1.f / 6.f), 0.5f));
-    const int z = __float2int_rn(yh * 0x1p39f) + __float2int_rn((yl + q) * 0x1p39f);  // exp(y) - 1
+    const float q = fmaf(yh, fmaf(yh, fmaf(yh, fmaf(yh, 1.f / 24.f, 1.f / 6.f), 0.5f), yl), yl);
+    const int z = __float2int_rn(yh * 0x1p39f) + __float2int_rn(q * 0x1p39f);  // exp(y) - 1
     const uint64_t w = pow2[k & 127];
     const int64_t v = (int64_t)w + ((int64_t)(uint32_t)(w >> 9) * z >> 30);
     const int n = -(k >> 7);  // 0 .. 41
