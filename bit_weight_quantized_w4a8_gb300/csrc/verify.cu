@@ -53,11 +53,11 @@ constexpr int kMaxSlices = 32;    // of a row, in the first launch
 constexpr float kGreedyBelow = 0x1p-20f;
 
 // How far an fp32 sum over weights of a row may be off, relative to the row's whole sum Z, in units of
-// 2^-24: a weight exp2(t), t = (l - max) c with two roundings and half of one in c, is within
-// 2.5 |t| ln 2 + 4 (ex2.approx), and the mean of |t| over the distribution is at most log2(vocab) <=
-// 22: 42; the factors that bring sums of the first launch to one maximum the same: 42; additions of
-// 16 weights, over a warp, 8 warps and 32 slices, the others in 64 bits: 21; refused tokens'
-// weights taken off: 42.  147 in all, below 2^-16.
+// 2^-24: a weight exp2(t), t = (l - max) c with two roundings and 1.2 in c (a rounded quotient of a rounded
+// constant), is within 3.2 |t| ln 2 + 4 (ex2.approx), and the mean of |t| over the distribution is at most
+// log2(vocab) <= 22: 53; the factors that bring sums of the first launch to one maximum the same: 53; additions of
+// 16 weights, over a warp, 8 warps and 32 slices, the others in 64 bits: 21 (the first launch's sum
+// Z: 127); refused tokens' weights taken off: 53.  180 in all, below 2^-16.
 constexpr float kOff = 0x1p-16f;
 
 struct RowPart {
@@ -621,46 +621,54 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
     auto exact = [&](bool less) {
         return typename Draw<T>::Exact{{c.hi, c.lo, s.row[node].top}, cut, s.pow2, less};
     };
-    auto make_cuts = [&]() {
-        while (cuts < todo) {
-            if (cuts == 0)
-                dr.pass(first + node, exact(false), 0);
-            else if (dr.total == 0)
-                break;  // nothing is left, and nothing more is taken off
+    // The sums of what is left at the node, by the integers.
+    auto exact_sums = [&]() {
+        if (cuts == 0) dr.pass(first + node, exact(false), refused);
+        for (; cuts < todo && dr.total != 0; ++cuts) {  // (0: nothing more is taken off)
             cut.add(dr.total);
             dr.pass(first + node, exact(true), 0);
-            ++cuts;
         }
         cuts = todo;
     };
+    #pragma unroll 1
     for (int i = 1; i < n; ++i) {
         if (s.parent[i] != node) continue;
         const RowPart& p = s.row[node];
         if (p.sum != p.sum) continue;  // no distribution: no child is taken, and no pass made for one
         const int id = s.id[i];
+        const float w = s.w[i];  // (0 for tokens outside the vocabulary)
         bool yes;
         if (c.greedy) {
             yes = id == p.at;
-        } else if (a.Q == nullptr) {
-            bool again = false;
-            for (int k = 0; k < refused; ++k) again |= s.refused[k] == id;
-            yes = !again && s.u[i] * (p.sum - gone) < s.w[i];
-            if (!yes && !again && id >= 0 && id < a.vocab && s.w[i] > 0.f) {
-                gone += s.w[i];
+        } else {
+            float u = s.u[i];
+            bool weighs = w > 0.f, open;
+            if (a.Q == nullptr) {
+                #pragma unroll 1
+                for (int k = 0; k < refused; ++k) weighs &= s.refused[k] != id;
+                // The fp32 sum of what is left is off by up to kOff Z, whatever is left: near enough to the
+                // border (2^-20 of w: its own roundings) the integers decide.
+                const float side = u * (p.sum - gone) - w;
+                yes = weighs && side < 0.f;
+                open = weighs && refused > 0 && !(fabsf(side) > u * kOff * p.sum + 0x1p-20f * w);
+            } else {
+                u *= s.q[i];
+                yes = todo == 0 && u * p.sum < w;
+                open = todo > 0 && weighs;
+            }
+            if (open) {
+                exact_sums();
+                yes = target_of(u, dr.total) < exact(todo > 0).units(load1(dr.row(first + node) + id), s.q[i]);
+            }
+            if (!yes && a.Q != nullptr) {
+                ++todo;
+            } else if (!yes && weighs) {
+                gone += w;
                 __syncthreads();
                 if (tid == 0) s.refused[refused] = id;
                 __syncthreads();
                 ++refused;
             }
-        } else if (todo == 0) {
-            yes = s.u[i] * s.q[i] * p.sum < s.w[i];
-            todo += !yes;
-        } else {
-            make_cuts();
-            uint64_t w = 0;
-            if (id >= 0 && id < a.vocab) w = exact(true).units(load1(dr.row(first + node) + id), s.q[i]);
-            yes = s.u[i] * s.q[i] * (float)dr.total < (float)w;
-            todo += !yes;
         }
         if (yes) {
             if (tid == 0) s.taken[taken] = i;
@@ -693,15 +701,12 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
             next = s.verdict;
         }
         if (next < 0) {
-            make_cuts();
-            bool less = todo != 0;
-            if (!less) dr.pass(t, exact(false), refused);
-            if (dr.total == 0 && (less || refused != 0)) {  // nothing left but roundings: the whole row
-                less = false;
-                refused = 0;
-                dr.pass(t, exact(false), 0);
+            for (;;) {
+                exact_sums();
+                if (dr.total != 0 || (todo == 0 && refused == 0)) break;
+                todo = cuts = refused = 0;  // nothing left but roundings: the whole row
             }
-            next = dr.find(t, exact(less), refused, target_of(u, dr.total), 0);
+            next = dr.find(t, exact(todo > 0), refused, target_of(u, dr.total), 0);
             mine = next >= 0 || (dr.total == 0 && mine);
         }
     }

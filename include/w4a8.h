@@ -733,9 +733,11 @@ int kvq_plan(const kvq_pool_t* pool, int32_t* lens, const int32_t* grow, const i
  *   count [seqs]: how many are kept (1 + taken), which is how many are said and what the
  *     sequence's cache grows by (kvq_plan's grow); 0 for a sequence without tokens.
  * Rows of tokens that no sequence holds are left as they are.
- * Arithmetic: tests in fp32 (sums of fp32 weights over the vocabulary, relative error below
- * 2^-18); the draw on integer weights in units of 2^-40 of the largest weight, each within 4
- * units, whose sums are exact: the same call gives the same tokens.
+ * Arithmetic: the first test at a token in fp32 (a row's sum of fp32 weights is within 2^-16 of itself).
+ * Behind refusals with Q, and behind refusals of given drafts where fp32 could take the wrong side (what
+ * is left may be little: the error of its fp32 sum is 2^-16 of the whole row's), the tests, and always the draw,
+ * are those of integer weights in units of 2^-40 of the largest weight, each within 4 units, less what
+ * refusals take off (rounded once more), whose sums are exact: the same call gives the same tokens.
  * -infinity takes a token out; a row that holds a NaN, +infinity or nothing but -infinity has
  * no distribution: its children are refused, the token drawn is -1.  A draft outside the vocabulary
  * is refused.  If refusals left nothing but roundings, the draw takes the whole row.  u outside [0, 1)

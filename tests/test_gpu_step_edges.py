@@ -112,6 +112,37 @@ def test_what_a_refusal_takes_off_is_rounded_once(w4):  # noqa: F811
     assert not wrong.any(), "%d of %d" % (wrong.sum(), n)
 
 
+def test_tests_after_refusals_that_leave_next_to_nothing(w4):  # noqa: F811
+    """Sixteen refused tokens hold all but 2^-25 of the weight; what is left lies in six tokens, in shares of
+    1/40.  The random numbers are odd multiples of 1/128, so that u times a sum of at most 40 shares
+    is 2^-13 of it at least from a whole number of shares; the weights' roundings (half a unit of 2^-40 each,
+    a share is 2^13.7 units) are a twentieth of that.  Drafts without weight are never taken."""
+    rng = np.random.default_rng(34)
+    seqs, v, big = 48, 900, 16
+    shares = np.array([13, 11, 7, 5, 3, 1])
+    par = [-1] + [0] * (big + 6)
+    n = len(par)
+    logits = np.full((n * seqs, v), NEG, F32)
+    ids, u = np.zeros(n * seqs, I32), np.full(n * seqs, ALMOST_ONE, F32)
+    for b in range(seqs):
+        place = rng.permutation(v)
+        row = logits[n * b]
+        row[place[:big]] = 0
+        row[place[big:big + 6]] = np.log(shares / 40 * 2.0 ** -21)
+        logits[n * b + 1:n * (b + 1)] = rng.standard_normal((n - 1, v))
+        ids[n * b + 1:n * b + 1 + big] = place[:big]
+        tail = list(rng.permutation(place[big:big + 6])[:4]) + [place[700], -1]  # one without weight, one outside
+        ids[n * b + 1 + big:n * (b + 1)] = rng.permutation(tail)
+        u[n * b + 1 + big:n * (b + 1)] = (2 * rng.integers(0, 64, 6) + 1) / 128
+        u[n * b] = (2 * rng.integers(0, 64) + 1) / 128
+    mask = np.tile(words(*par), seqs)
+    cu = np.arange(0, n * seqs + 1, n, dtype=I32)
+    got, want = run_verify(w4, logits, cu, ids, u, mask), sref.verify(logits, cu, ids, u, mask)
+    same(got[2:], want[2:], "count")
+    same(got, want)
+    assert 4 < (want[2] == 1).sum() < seqs - 4
+
+
 # -- the plan of a step ----------------------------------------------------------------
 
 def plan_with_trees(host, add, tokens, mask, grow):
