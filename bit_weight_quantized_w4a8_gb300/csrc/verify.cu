@@ -692,7 +692,8 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
             // in fp32, after a refusal less q Z
             const typename Draw<T>::Fast w = {p.top, c.hi, p.sum, todo == 1};
             dr.pass(t, w, refused);
-            const uint64_t off = to_units(2.f * kOff * p.sum * (1.f + dr.q_total)) + 2;
+            // (probabilities may sum to the vocabulary's size: at most 2^21 weights, half of the largest sum)
+            const uint64_t off = to_units(fminf(2.f * kOff * p.sum * (1.f + dr.q_total), 0x1p21f)) + 2;
             const int x = dr.find(t, w, refused, target_of(u, dr.total), off);
             if (x >= 0)
                 for (int r = 0; r < kVerifyCluster; ++r) *cl.map_shared_rank(&s.verdict, r) = x;

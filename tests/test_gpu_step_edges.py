@@ -143,6 +143,36 @@ def test_tests_after_refusals_that_leave_next_to_nothing(w4):  # noqa: F811
     assert 4 < (want[2] == 1).sum() < seqs - 4
 
 
+def test_draws_with_probabilities_that_sum_to_a_million(w4):  # noqa: F811
+    """Draft probabilities need not sum to 1: the bound on the fp32 sums grows with them, past 64 bits, and leaves the
+    draw to the integers.  Half of 2^22 tokens are left, in two runs of 2^20 equal weights each; the random numbers
+    put the target 2^-10 to 2^-7 of a token from the next one.  A weight is off by at most 4 units of 2^-40, 2^20 of them by
+    2^-18 of a token; the fp32 weights of the second run, each off by the same up to 2^-22, by up to a quarter."""
+    seqs, v = 48, 2 ** 22
+    rng = np.random.default_rng(35)
+    low = -rng.random(seqs).astype(F32)
+    w = np.exp(low.astype(np.float64))
+    total = (v // 4) * (1 + w)
+    u = np.full(2 * seqs, 0.99, F32)
+    for b in range(seqs):
+        cand = (rng.random(20000) * 0.3 + 0.2).astype(F32)  # targets in the first run
+        at = cand.astype(np.float64) * total[b]
+        edge = np.abs(at - np.round(at))
+        u[2 * b] = cand[np.flatnonzero((edge > 2.0 ** -10) & (edge < 2.0 ** -7))[0]]
+    assert np.all(u[::2].astype(np.float64) * total < v // 4 - 1)
+    want = 2 * np.floor(u[::2].astype(np.float64) * total).astype(I64)  # the even tokens are left
+    logits = torch.zeros((2 * seqs, v), device="cuda")
+    logits[::2, v // 2:] = dev(low)[:, None]
+    q = torch.zeros((2 * seqs, v), dtype=torch.float16, device="cuda")
+    q[:, 1::2] = 1
+    ids = torch.ones(2 * seqs, dtype=torch.int32, device="cuda")
+    cu = torch.arange(0, 2 * seqs + 1, 2, dtype=torch.int32, device="cuda")
+    keep, out, count = w4.draft_verify(logits, cu, ids, dev(u), q=q)
+    assert bool((count == 1).all())
+    got = np_(out)[::2]
+    assert np.array_equal(got, want), "%d of %d" % ((got != want).sum(), seqs)
+
+
 # -- the plan of a step ----------------------------------------------------------------
 
 def plan_with_trees(host, add, tokens, mask, grow):
