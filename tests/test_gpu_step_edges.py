@@ -251,3 +251,37 @@ def test_tokens_behind_a_batch_with_a_waiting_row_are_no_error(w4):  # noqa: F81
     for cu in ([2, 10, 10, 10], [0, 10, 5, 40], [0, -1, -1, -1], [0, 10, 10, -5]):
         w4.kvq_write(cache, w4.KVQBatch(torch.tensor(cu, **i32), lens, pool.table), k, v)
         assert w4.w4a8_device_error() == 8, cu
+
+
+def graph_us(call, reps=5):
+    call()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    times = []
+    for _ in range(reps):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        g.replay()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(1000 * a.elapsed_time(b))
+    return min(times)
+
+
+@pytest.mark.parametrize("seqs,tokens", [(1000, 8), (8000, 8), (65536, 8), (65536, 20000)])
+def test_kvq_plan_does_not_walk_over_idle_rows(w4, seqs, tokens):  # noqa: F811
+    """Two tokens in seats far apart: the step of two neighbours, and about its time (a walk over 65534 idle
+    rows takes a hundred times as long)."""
+    us = []
+    for second in (1, seqs // 2, seqs - 1):
+        pool = w4.kvq_pool(seqs, 1, 16)
+        lens = torch.zeros(seqs, dtype=torch.int32, device="cuda")
+        add = torch.zeros(seqs, dtype=torch.int32, device="cuda")
+        add[0] = 1
+        add[second] = 2
+        batch, pos, slot, seq = w4.kvq_plan(pool, 16, lens, add, tokens)
+        assert seq[:4].tolist() == [0, second, second, -1] and slot[:4].tolist() == [15 * 16, 14 * 16, 14 * 16 + 1, -1]
+        assert pos[:4].tolist() == [0, 0, 1, 0] and batch.cu[second:second + 2].tolist() == [1, 3]
+        us.append(graph_us(lambda: w4.kvq_plan(pool, 16, lens, add, tokens)))
+    assert max(us) < 4 * us[0] + 20, us
