@@ -24,9 +24,15 @@ __device__ __forceinline__ float f8_scale(float amax) { return __fmul_rn(amax, 1
 
 // The code of the quotient x / s itself.  Rounding it to fp32 first can only make
 // a difference where the rounded quotient is a tie between two codes and the
-// exact one is not: the remainder, which an fma gives exactly, then tells the side.
+// exact one is not: the remainder, which an fma gives exactly, then tells the side.  (At a tie it is a multiple of
+// 2^-10 units in the last place of s: small scales and their values, of at most 448 s, go up together, so that it
+// is no less than the smallest number.)
 static __device__ __noinline__ uint32_t f8_codes4_exact(float4 v, float s) {
     if (s == 0.f) return 0u;
+    if (s < 0x1p-64f) {
+        constexpr float kUp = 0x1p64f;
+        s *= kUp, v.x *= kUp, v.y *= kUp, v.z *= kUp, v.w *= kUp;
+    }
     const float x[4] = {v.x, v.y, v.z, v.w};
     float q[4];
     #pragma unroll

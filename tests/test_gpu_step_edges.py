@@ -285,3 +285,30 @@ def test_kvq_plan_does_not_walk_over_idle_rows(w4, seqs, tokens):  # noqa: F811
         assert pos[:4].tolist() == [0, 0, 1, 0] and batch.cu[second:second + 2].tolist() == [1, 3]
         us.append(graph_us(lambda: w4.kvq_plan(pool, 16, lens, add, tokens)))
     assert max(us) < 4 * us[0] + 20, us
+
+
+# -- the linear with e4m3 blocks -------------------------------------------------------
+
+def test_f8_quotients_next_to_ties_of_the_smallest_scales(w4):  # noqa: F811
+    """Subnormal scales of many bits, and values whose quotient rounds to a tie between two codes without being one: what is
+    left over is less than the smallest number, and still tells the side."""
+    rng = np.random.default_rng(36)
+    ties = np.concatenate([(2 * np.arange(8) + 1) / 1024, *[(2 * np.arange(8, 16) + 1) * 2.0 ** (e - 4) for e in range(-6, 5)]])
+    rows = []
+    while len(rows) < 400:
+        k = int(rng.integers(1 << 21, (1 << 23) - 1))
+        top = F32(448 * k * 2.0 ** -149)
+        k = int(np.float64(sref.f8_scale(np.array([top]))[0]) * 2.0 ** 149)
+        x = np.round(ties * k)
+        near = (x != ties * k) & ((x / k).astype(F32) == ties.astype(F32))
+        if near.sum() < 4:
+            continue
+        row = np.zeros(128, F32)
+        row[0] = top
+        row[1:1 + near.sum()] = (x[near] * 2.0 ** -149 * rng.choice([-1, 1], near.sum())).astype(F32)
+        rows.append(row)
+    x = np.array(rows)
+    xf, sa = w4.f8_quantize_rows(dev(x))
+    codes, scales = sref.f8_rows(x)
+    assert np.array_equal(np_(sa), scales) and np.all(scales < 2.0 ** -126)
+    assert np.array_equal(sref.E4M3[np_(xf)], sref.E4M3[codes])
