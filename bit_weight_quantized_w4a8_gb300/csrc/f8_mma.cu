@@ -58,17 +58,25 @@ struct F8Args {
     int K;
 };
 
+// (Of a kernel launched dependently, warps that do not wait for the one before may wait here for those that do:
+// its time does not count.)
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
     #pragma unroll 1
     for (int i = 0; i < 64; ++i)
         if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer_ns();
+    unsigned long long t0 = globaltimer_ns();
+    bool alone = false;
     for (;;) {
         #pragma unroll 1
         for (int i = 0; i < 64; ++i)
             if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            if (!alone) {
+                griddep_wait();
+                alone = true, t0 = globaltimer_ns();
+                continue;
+            }
             *abort_flag = 1;
             atomicOr(&g_f8_error, kErrFullWait);
             return false;
@@ -462,6 +470,7 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<BN>::kCtas) f8_narrow_k
             issued = i + 1;
             if (++s == C::kStages) s = 0, phase ^= 1;
         }
+        griddep_wait();  // (a full stage holds codes of X, which come behind the kernel before)
         for (int i = max(0, issued - C::kStages); lane == 0 && i < issued; ++i)
             drain(smem_u32(&sh.full[i % C::kStages]), (i / C::kStages) & 1);
         __syncwarp();
