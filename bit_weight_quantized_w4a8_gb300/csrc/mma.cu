@@ -122,15 +122,23 @@ struct MmaArgs {
     int pre_pieces;
 };
 
+// (Of a kernel launched dependently, warps that do not wait for the one before may wait here for those that do:
+// its time does not count.)
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
     if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer_ns();
+    unsigned long long t0 = globaltimer_ns();
+    bool alone = false;
     for (;;) {
         #pragma unroll 1
         for (int i = 0; i < 32; ++i)
             if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            if (!alone) {
+                griddep_wait();
+                alone = true, t0 = globaltimer_ns();
+                continue;
+            }
             *abort_flag = 1;
             atomicOr(&g_mma_error, kErrFullWait);
             return false;

@@ -75,3 +75,20 @@ def test_f8_linear_behind_a_long_kernel(w4, pause, M, K, N):
     w4.f8_linear(x, *w, Y=y, ws=ws, flags=w4.LAUNCH_PDL)
     assert w4.w4a8_device_error() == 0
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("M,K,N", [(16, 3584, 512), (40, 18944, 300), (64, 4096, 4096)])
+def test_w4a8_linear_behind_a_long_kernel(w4, pause, M, K, N):
+    """The tensor-core kernel, whose weights' way through its stages waits for the activation's."""
+    rng = np.random.default_rng(M)
+    x = torch.from_numpy(rng.standard_normal((M, K)).astype(np.float16)).cuda()
+    w = w4.w4_quantize_weights(torch.from_numpy((0.05 * rng.standard_normal((N, K))).astype(np.float32)).cuda())
+    assert w4.w4a8_plan_info(M, K, N)["kernel"] == 1
+    ws = torch.zeros(w4.w4a8_workspace_bytes(M, K, N), dtype=torch.uint8, device="cuda")
+    want = w4.w4a8_linear(x, *w, ws=ws)
+    y = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    pause()
+    w4.w4a8_linear(x, *w, Y=y, ws=ws, flags=w4.LAUNCH_PDL)
+    assert w4.w4a8_device_error() == 0
+    assert torch.equal(y, want)
