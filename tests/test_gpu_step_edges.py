@@ -312,3 +312,89 @@ def test_f8_quotients_next_to_ties_of_the_smallest_scales(w4):  # noqa: F811
     codes, scales = sref.f8_rows(x)
     assert np.array_equal(np_(sa), scales) and np.all(scales < 2.0 ** -126)
     assert np.array_equal(sref.E4M3[np_(xf)], sref.E4M3[codes])
+
+
+# -- calls launched dependently behind what they read ------------------------------------
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("with_q", [False, True])
+def test_a_step_of_dependent_launches(w4, captured, with_q):  # noqa: F811
+    """A step in which each call reads what the one before writes, every launch dependent: the bits of the same step
+    launched one after the other, step by step, buffers spoiled in between."""
+    hidden, heads, dim, v, page = 512, 4, 64, 32000, 16
+    seqs, n = 6, 48
+    g = torch.Generator(device="cuda").manual_seed(38)
+    rand = lambda *s: torch.randn(s, device="cuda", generator=g)  # noqa: E731
+    i32 = dict(dtype=torch.int32, device="cuda")
+    wk, wl = (w4.f8_quantize_weights(rand(m, hidden) * 0.1) for m in (heads * dim, v))
+    gamma, freqs = torch.ones(hidden, device="cuda"), torch.rand(dim // 2, dtype=torch.float64, device="cuda", generator=g)
+    axis = w4.rope_axes((8, 12, 12))
+    mask = dev(np.tile(words(-1, 0, 0, 1, 1, 2, 0, 3), seqs))
+    steps = [(rand(n, hidden) * 2, torch.randint(0, v, (n,), device="cuda", generator=g, dtype=torch.int32),
+              torch.rand(n, device="cuda", generator=g) * 1e-3, torch.randint(0, 500, (3, n), device="cuda", generator=g,
+                                                                              dtype=torch.int32)) for _ in range(8)]
+    q = torch.softmax(rand(n, v), 1) if with_q else None
+    add = torch.full((seqs,), 8, **i32)
+
+    class State:
+        def __init__(self):
+            self.r, self.ids, self.u, self.pos = (torch.empty_like(t) for t in steps[0])
+            self.pool, self.cache = w4.kvq_pool(seqs, 4, 24), w4.kvq_cache(24, page, heads, dim, 8)
+            self.lens, self.count = torch.zeros(seqs, **i32), torch.zeros(seqs, **i32)
+            self.cu, self.at, self.seq = torch.zeros(seqs + 1, **i32), torch.zeros(n, **i32), torch.zeros(n, **i32)
+            self.slot = torch.zeros(n, dtype=torch.int64, device="cuda")
+            self.x = torch.zeros((n, hidden), dtype=torch.float16, device="cuda")
+            self.xf, self.sa = torch.zeros((n, hidden), dtype=torch.uint8, device="cuda"), torch.zeros((4, n), device="cuda")
+            self.k, self.logits = torch.zeros((n, heads * dim), device="cuda"), torch.zeros((n, v), device="cuda")
+            self.qr, self.kr = (torch.zeros((n, heads, dim), dtype=t, device="cuda") for t in (torch.float16, torch.float32))
+            self.keep, self.out = torch.zeros(n, **i32), torch.zeros(n, **i32)
+
+        def spoil(self):
+            for t in (self.x, self.sa, self.k, self.logits, self.qr, self.kr):
+                t.fill_(float("nan"))
+            for t in (self.xf, self.cu, self.at, self.seq, self.slot, self.keep, self.out):
+                t.fill_(3)
+
+        def run(self, flags):
+            f = dict(flags=flags)
+            batch, *_ = w4.kvq_plan(self.pool, page, self.lens, add, n, grow=self.count, mask=mask, cu=self.cu, pos=self.at,
+                                    slot=self.slot, seq=self.seq, **f)
+            w4.add_norm(self.r, gamma, X=self.x, **f)
+            w4.f8_quantize_rows(self.x, Xf=self.xf, sa=self.sa, **f)
+            w4.f8_gemm(self.xf, self.sa, *wk, Y=self.k, **f)
+            k = self.k.view(n, heads, dim)
+            w4.rope_rotate(k, self.pos, freqs, Y=self.kr, axis=axis, **f)
+            w4.kvq_write(self.cache, batch, self.kr, k, Q=k, pos=self.pos, freqs=freqs, axis=axis, Q_out=self.qr, **f)
+            w4.f8_linear(self.x, *wl, Y=self.logits, **f)
+            w4.draft_verify(self.logits, self.cu, self.ids, self.u, mask=mask, q=q, keep=self.keep, out=self.out,
+                            count=self.count, **f)
+            w4.kvq_keep(self.cache, batch, self.keep, **f)
+
+        def all(self):
+            return [self.lens, self.count, self.cu, self.at, self.seq, self.slot, self.x, self.k, self.logits, self.qr, self.kr,
+                    self.keep, self.out, *self.pool, *self.cache]
+
+    want, got = State(), State()
+    graph = None
+    if captured:
+        got.run(w4.LAUNCH_PDL)
+        torch.cuda.synchronize()
+        got = State()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got.run(w4.LAUNCH_PDL)
+    taken = 0
+    for step in steps:
+        for s in (want, got):
+            s.spoil()
+            for t, x in zip((s.r, s.ids, s.u, s.pos), step):
+                t.copy_(x)
+        want.run(0)
+        if graph is None:
+            got.run(w4.LAUNCH_PDL)
+        else:
+            graph.replay()
+        for i, (a, b) in enumerate(zip(want.all(), got.all())):
+            assert np.array_equal(np_(a), np_(b), equal_nan=a.dtype.is_floating_point), i
+        taken += int(want.count.sum()) - seqs
+    assert taken > 0 and w4.w4a8_device_error() == 0
