@@ -16,9 +16,11 @@
 //
 // One cluster of CTAs scans (a thread has up to 8 rows, so 65536 rows take one
 // pass) and, for short steps, writes all; for long ones a second launch writes
-// with the whole GPU.  In a graph 48 requests take 4.3 us, 4093 requests of which half are
-// exchanged (two calls) 29.5: nothing but latency, of the scan's two to three prefix sums (10 us a call under
-// ncu) and of a look-up's search through the offsets, 12 loads one after the other (10 to 16).
+// with the whole GPU.  In a graph 48 requests take 4.2 us, 4093 requests of which half are
+// exchanged (two calls) 27.7 to 29.4: latency, of the scan's two to three prefix sums (10 us a call under
+// ncu) and of a look-up's search through the offsets, 12 loads one after the other (10 to 16).  Two requests in
+// a pool of 1000, 8000 and 65536 rows: 10, 18 and 51 us, wherever they sit.  (8 rows a thread, from 8193 rows on, spill
+// 400 bytes.)
 #include <cooperative_groups.h>
 
 #include <type_traits>

@@ -25,10 +25,11 @@
 // that sums are exact, in any order and split.  That is 40 instructions a weight: a CTA's
 // 19008 weights of a row of 152064 take 8.4 us, 14.5 with the draft's probabilities, in fp32 2.7.
 //
-// With 152064 tokens, in a graph: one greedy chain of 5 6.5 us; 24 trees of up to 12 54 to 58 (bytes at
+// With 152064 tokens, in a graph: one greedy chain of 5 6.2 to 6.7 us; 24 trees of up to 12 56 to 59 (bytes at
 // the copy rate: 23), of which the first launch takes 30 (5.1 TB/s: its start and end are as long as a
 // third of it) and the second 36, some sequence always being left open by the fp32 sums; 61
-// chains with probabilities 91 to 115 (36), by how many of them are left open on the same SMs: 39 and 60 to 75.
+// chains with probabilities 91 to 111 (36), by how many of them are left open on the same SMs: 39 and 60 to 75.
+// The second launch is held to 64 registers (two CTAs of 512 threads an SM) and spills 76 to 96 bytes.
 #include <cooperative_groups.h>
 
 #include "kernels.h"

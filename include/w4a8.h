@@ -69,7 +69,9 @@ typedef enum {
    stream is still running (programmatic dependent launch).  The kernel then
    streams Wq/Wq8/Wf and the weight scales before waiting for the previous
    kernel, so those weight buffers must NOT be written by the kernel launched
-   immediately before it on the same stream.  Activations, outputs and the
+   immediately before it on the same stream, nor, in a row of launches with this
+   flag, by any of the row or by the one in front of it (each may start under the one
+   before, all of them while the first still runs).  Activations, outputs and the
    workspace are only touched after the wait. */
 #define W4A8_LAUNCH_PDL 1u
 
@@ -740,8 +742,10 @@ int kvq_plan(const kvq_pool_t* pool, int32_t* lens, const int32_t* grow, const i
  * refusals take off (rounded once more), whose sums are exact: the same call gives the same tokens.
  * -infinity takes a token out; a row that holds a NaN, +infinity or nothing but -infinity has
  * no distribution: its children are refused, the token drawn is -1.  A draft outside the vocabulary
- * is refused.  If refusals left nothing but roundings, the draw takes the whole row.  u outside [0, 1)
- * and Q outside [0, 1] count as the nearest number inside, NaN as 0, temp that is negative or NaN as 0.
+ * is refused (with Q like any other: p = max(p - Q, 0); a place without a draft is one whose word
+ * names no ancestor, hence nobody's child).  If refusals left nothing but roundings, the draw takes the whole row.  u outside [0, 1)
+ * and Q outside [0, 1] count as the nearest number inside, NaN as 0, temp that is negative or NaN as 0,
+ * above 2^60 as 2^60.
  *   L [tokens][vocab] l_type, rows ld_l elements apart; Q [tokens][vocab] q_type, ld_q, or NULL;
  *   ids [tokens] int32 (the root's is not read); temp [seqs] fp32 or NULL (1); u [tokens] fp32.
  *   ws, ws_bytes: draft_verify_workspace_bytes, 256-byte aligned (need not be
