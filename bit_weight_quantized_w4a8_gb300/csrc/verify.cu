@@ -25,11 +25,13 @@
 // that sums are exact, in any order and split.  That is 40 instructions a weight: a CTA's
 // 19008 weights of a row of 152064 take 8.4 us, 14.5 with the draft's probabilities, in fp32 2.7.
 //
-// With 152064 tokens, in a graph: one greedy chain of 5 6.2 to 6.7 us; 24 trees of up to 12 56 to 59 (bytes at
+// With 152064 tokens, in a graph: one greedy chain of 5 6.2 us; 24 trees of up to 12 52 to 55 (bytes at
 // the copy rate: 23), of which the first launch takes 30 (5.1 TB/s: its start and end are as long as a
-// third of it) and the second 36, some sequence always being left open by the fp32 sums; 61
-// chains with probabilities 91 to 111 (36), by how many of them are left open on the same SMs: 39 and 60 to 75.
-// The second launch is held to 64 registers (two CTAs of 512 threads an SM) and spills 76 to 96 bytes.
+// third of it) and the second 33, some sequence always being left open by the fp32 sums; 61
+// chains with probabilities 88 to 111 (36), by how many of them are left open on the same SMs: 39 and 60 to 75.
+// The second launch is held to 64 registers (two CTAs of 512 threads an SM).  Drafts with and without
+// probabilities have variants of their own: in one, which spilled 76 to 96 bytes, 24 trees took 57.5 us and 61 chains
+// 2 more; with probabilities 28 to 40 bytes are left.
 #include <cooperative_groups.h>
 
 #include "kernels.h"
@@ -326,8 +328,8 @@ struct DrawShared {
 };
 
 // Sums over a row by the cluster, and the token where they pass a number.  Each CTA has
-// a run of segments and the sums of each in shared memory, in the draw's units.
-template <typename T>
+// a run of segments and the sums of each in shared memory, in the draw's units.  Q: drafts with probabilities.
+template <typename T, bool Q>
 struct Draw {
     const VerifyArgs& a;
     DrawShared& s;
@@ -368,7 +370,7 @@ struct Draw {
         bool with_q;
         __device__ __forceinline__ float value(float l, float q) const {
             const float w = l > -INFINITY ? ex2((l - top) * c) : 0.f;
-            return with_q ? fmaxf(w - (q > 0.f ? fminf(q, 1.f) : 0.f) * z, 0.f) : w;
+            return Q && with_q ? fmaxf(w - (q > 0.f ? fminf(q, 1.f) : 0.f) * z, 0.f) : w;
         }
         __device__ __forceinline__ uint64_t units(float l, float q) const { return to_units(value(l, q)); }
         __device__ __forceinline__ uint64_t lanes(const float (&l)[16], const float (&q)[16]) const {
@@ -385,7 +387,7 @@ struct Draw {
         const uint64_t* pow2;
         bool with_q;
         __device__ __forceinline__ uint64_t units(float l, float q) const {
-            const uint64_t w = weight(l, unit, pow2), x = with_q ? part_of(q, cut) : 0;
+            const uint64_t w = weight(l, unit, pow2), x = Q && with_q ? part_of(q, cut) : 0;
             return w > x ? w - x : 0;
         }
         __device__ __forceinline__ uint64_t lanes(const float (&l)[16], const float (&q)[16]) const {
@@ -415,7 +417,7 @@ struct Draw {
         for (int seg = s0 + warp; seg < s1; seg += warps) {
             float l[16], q[16];
             load_seg(row(t), seg, -INFINITY, l);
-            if (w.with_q) {
+            if (Q && w.with_q) {
                 load_q(t, seg, q);
                 #pragma unroll
                 for (int k = 0; k < 16; ++k) q_mine += fminf(fabsf(q[k]), 1.f);
@@ -482,7 +484,7 @@ struct Draw {
             run = __shfl_sync(0xFFFFFFFFu, up - v, first);
             float l[16], q[16];
             load_seg(row(t), seg, -INFINITY, l);
-            if (w.with_q) {
+            if (Q && w.with_q) {
                 load_q(t, seg, q);
             } else {
                 #pragma unroll
@@ -526,7 +528,7 @@ struct Draw {
     }
 };
 
-template <typename T>
+template <typename T, bool Q>
 __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const VerifyArgs a) {
     extern __shared__ uint64_t seg_sums[];
     __shared__ DrawShared s;
@@ -567,7 +569,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
         if (tid == 0 || up < 0 || id < 0 || id >= a.vocab) id = -1;
         if (id >= 0) {
             l = load1(static_cast<const T*>(a.L) + (first + up) * a.ld_l + id);
-            if (a.Q != nullptr) {
+            if (Q) {
                 const int64_t i = (first + up) * a.ld_q + id;
                 q = a.q_f16 ? __half2float(static_cast<const __half*>(a.Q)[i]) : static_cast<const float*>(a.Q)[i];
                 q = fminf(fmaxf(q, 0.f), 1.f);
@@ -606,7 +608,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
     __syncthreads();
 
     const int seg_per = (a.seg_count + kVerifyCluster - 1) / kVerifyCluster;
-    Draw<T> dr{a, s, seg_sums, c};
+    Draw<T, Q> dr{a, s, seg_sums, c};
     dr.rank = rank;
     dr.s0 = min(rank * seg_per, a.seg_count);
     dr.s1 = min(dr.s0 + seg_per, a.seg_count);
@@ -620,7 +622,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
     float gone = 0.f;                                          // weights of the refused
     Cut cut = {0, 0};
     auto exact = [&](bool less) {
-        return typename Draw<T>::Exact{{c.hi, c.lo, s.row[node].top}, cut, s.pow2, less};
+        return typename Draw<T, Q>::Exact{{c.hi, c.lo, s.row[node].top}, cut, s.pow2, less};
     };
     // The sums of what is left at the node, by the integers.
     auto exact_sums = [&]() {
@@ -644,7 +646,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
         } else {
             float u = s.u[i];
             bool weighs = w > 0.f, open;
-            if (a.Q == nullptr) {
+            if (!Q) {
                 #pragma unroll 1
                 for (int k = 0; k < refused; ++k) weighs &= s.refused[k] != id;
                 // The fp32 sum of what is left is off by up to kOff Z, whatever is left: near enough to the
@@ -661,7 +663,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
                 exact_sums();
                 yes = target_of(u, dr.total) < exact(todo > 0).units(load1(dr.row(first + node) + id), s.q[i]);
             }
-            if (!yes && a.Q != nullptr) {
+            if (!yes && Q) {
                 ++todo;
             } else if (!yes && weighs) {
                 gone += w;
@@ -691,7 +693,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
     } else if (p.sum == p.sum) {
         if (todo == 0 || (todo == 1 && cuts == 0)) {
             // in fp32, after a refusal less q Z
-            const typename Draw<T>::Fast w = {p.top, c.hi, p.sum, todo == 1};
+            const typename Draw<T, Q>::Fast w = {p.top, c.hi, p.sum, todo == 1};
             dr.pass(t, w, refused);
             // (probabilities may sum to the vocabulary's size: at most 2^21 weights, half of the largest sum)
             const uint64_t off = to_units(fminf(2.f * kOff * p.sum * (1.f + dr.q_total), 0x1p21f)) + 2;
@@ -752,7 +754,8 @@ cudaError_t launch_verify(const VerifyArgs& a, int sms, unsigned flags, cudaStre
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, verify_draw_kernel<T>, a);
+    return a.Q != nullptr ? cudaLaunchKernelEx(&cfg, verify_draw_kernel<T, true>, a)
+                          : cudaLaunchKernelEx(&cfg, verify_draw_kernel<T, false>, a);
 }
 
 }  // namespace
